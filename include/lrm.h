@@ -41,7 +41,8 @@
  *  - Each entry point opens an NVTX range of its own name around its host work when the
  *    environment variable LRM_NVTX is 1 at the library's first call (off otherwise).
  *  - The kernels of lrm_score, lrm_select, lrm_select_static, lrm_compact,
- *    lrm_grouped_backward (tensor-core path) and lrm_scatter_dx use programmatic dependent launch: each waits (griddepcontrol.wait) for the
+ *    lrm_grouped_backward (tensor-core path), lrm_scatter_dx, lrm_sort_tokens, lrm_combine, lrm_linear
+ *    and the gradients of the last two use programmatic dependent launch: each waits (griddepcontrol.wait) for the
  *    work queued before it on the stream to complete before it touches memory, and lets the
  *    next launch on the stream start early.  Ordinary stream order therefore holds for every
  *    caller; a caller kernel that is itself launched with programmatic stream serialization
@@ -323,6 +324,109 @@ lrm_status lrm_swiglu_forward(const void* h, int64_t P, int32_t I, lrm_dtype dt,
  */
 lrm_status lrm_score_norms(const float* alpha, const void* g, const float* phi_sq, int64_t T, int32_t k,
                            int32_t H, lrm_dtype dt, float* scores, int32_t* dev_status, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * The layer's forward around the experts, and its unpruned gradients: tokens sorted by expert and
+ * back, and the products with bias, activation and residual.  With these a whole MoE layer runs
+ * through the library: lrm_route, lrm_sort_tokens, lrm_linear (SwiGLU), lrm_linear, lrm_combine,
+ * and back: lrm_combine_backward, lrm_linear_backward, lrm_act_backward, lrm_linear_backward,
+ * lrm_scatter_dx (the gradient of lrm_sort_tokens).  The pages name these steps ("forward completo")
+ * but give no form for them.
+ * ------------------------------------------------------------------------------------------- */
+
+/*
+ * Tokens sorted by expert.  Pair u = t*k + j goes to row row_of_pair[u] of its expert's segment,
+ * pairs of one expert in ascending u (stable):
+ *   seg_offsets [E+1] int32   out: segment e is rows seg_offsets[e] .. seg_offsets[e+1]-1
+ *   pair_of_row [T*k] int32   out: the pair of each row, -1 for rows >= seg_offsets[E]
+ *   row_of_pair [T*k] int32   out: the row of each pair, -1 if it is not routed
+ *   x_s [T*k, H] dt           out: x_s[r] = x[pair_of_row[r] / k], zeros for rows >= seg_offsets[E].
+ *                             May be NULL (then x may be, too): only the three index arrays.
+ *   topk_idx [T*k] int32      expert ids; -1: the pair is not routed (padding, a masked token).  Any
+ *                             other id outside [0, E) sets LRM_ERR_BAD_INDEX and counts as -1.
+ *   ws: scratch of at least lrm_workspace_size bytes.
+ * Deterministic.  Its gradient is lrm_scatter_dx with cap = T*k: dx[t] = sum_j dx_s[row_of_pair[t*k+j]].
+ * Errors: LRM_ERR_INVALID_ARG, LRM_ERR_SHAPE, LRM_ERR_DTYPE, LRM_ERR_WORKSPACE, LRM_ERR_CUDA.
+ */
+lrm_status lrm_sort_tokens(const int32_t* topk_idx, const void* x, int64_t T, int32_t k, int32_t E, int32_t H,
+                           lrm_dtype dt, int32_t* seg_offsets, int32_t* pair_of_row, int32_t* row_of_pair, void* x_s,
+                           void* ws, size_t ws_bytes, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Back to tokens with the routing weights:  y[t] = residual[t] + sum over j = 0..k-1, in that order,
+ * of alpha[t*k+j] * y_s[row_of_pair[t*k+j]], summed in fp32 (the residual last) and rounded once.
+ * A token none of whose pairs is routed gets its residual (0 without one).
+ *   row_of_pair [T*k] int32, alpha [T*k] fp32, y_s [cap,H] dt, residual [T,H] dt or NULL -> y [T,H] dt.
+ * y may be the residual's buffer.  A row outside [-1, cap) is not followed (the pair adds nothing) and
+ * sets LRM_ERR_BAD_INDEX.  Deterministic: no atomics.
+ */
+lrm_status lrm_combine(const int32_t* row_of_pair, const float* alpha, const void* y_s, const void* residual, int64_t T,
+                       int32_t k, int32_t H, lrm_dtype dt, int64_t cap, void* y, int32_t* dev_status,
+                       cudaStream_t stream);
+
+/*
+ * Gradient of lrm_combine (the residual's is dy itself).  For every pair u = t*k + j with row r:
+ *   dy_s[r] = round_dt(alpha_u * dy_t),   dalpha[u] = dy_t . y_s[r]   (fp32; 0 for an unrouted pair)
+ *   dy [T,H] dt, y_s [cap,H] dt  ->  dy_s [cap,H] dt, dalpha [T*k] fp32.
+ * Rows of dy_s that no pair names are not written.  With dalpha NULL y_s is not read (and may be NULL).
+ * row_of_pair as in lrm_combine; no two pairs may name one row (as lrm_sort_tokens writes it).
+ */
+lrm_status lrm_combine_backward(const int32_t* row_of_pair, const float* alpha, const void* dy, const void* y_s,
+                                int64_t T, int32_t k, int32_t H, lrm_dtype dt, int64_t cap, void* dy_s, float* dalpha,
+                                int32_t* dev_status, cudaStream_t stream);
+
+/* Activations of lrm_linear. */
+typedef enum lrm_act {
+  LRM_ACT_NONE = 0,
+  LRM_ACT_RELU = 1,   /* max(z, 0)                                            */
+  LRM_ACT_GELU = 2,   /* z Phi(z), Phi by the error function                  */
+  LRM_ACT_SILU = 3,   /* z sigmoid(z)                                         */
+  LRM_ACT_SWIGLU = 4  /* SiLU(z_gate) * z_up: w and bias hold N gate rows, then N up rows */
+} lrm_act;
+
+/* Bytes of scratch `ws` that lrm_linear, lrm_act_backward and lrm_linear_backward need for a product of
+ * R rows (one buffer serves all three).  N: columns of y; for lrm_linear_backward alone, those of dz with
+ * LRM_ACT_NONE.  Host-only.  Errors: LRM_ERR_INVALID_ARG, LRM_ERR_SHAPE, LRM_ERR_DTYPE. */
+lrm_status lrm_linear_workspace_size(int64_t R, int32_t E, int32_t N, int32_t K, lrm_act act, lrm_dtype dt,
+                                     size_t* bytes);
+
+/*
+ * Product with bias, activation and residual in its epilogue, dense or one weight per expert:
+ *   z = x W[e]^T + b[e],   y = act(z) + residual
+ * over the rows of each segment (seg_offsets [E+1], as lrm_sort_tokens writes it; checked on the device,
+ * LRM_ERR_BAD_SEGMENTS: nothing is computed), or over all R rows with one weight (seg_offsets NULL, E = 1).
+ *   x [R,K] dt, w [E,N',K] dt, bias [E,N'] dt or NULL, residual [R,N] (type of y) or NULL
+ *   -> y [R,N], z [R,N'] dt or NULL (the pre-activation, for lrm_act_backward); N' = 2N for SwiGLU, else N.
+ * dt LRM_BF16 or LRM_F32; out_dt is the type of y: dt, or LRM_F32 from bf16 inputs (a router's logits;
+ * no residual then).  Sums, bias, activation and residual are in fp32, each output is rounded once.
+ * Rows >= seg_offsets[E] are not written.  N and K are multiples of 8, up to 2^24; R <= INT32_MAX.
+ * ws: scratch of at least lrm_linear_workspace_size bytes.  flags: LRM_GEMM_DEFAULT or
+ * LRM_GEMM_FORCE_SIMT (products on the CUDA cores).
+ */
+lrm_status lrm_linear(const int32_t* seg_offsets, const void* x, const void* w, const void* bias, const void* residual,
+                      int64_t R, int32_t E, int32_t N, int32_t K, lrm_act act, lrm_dtype dt, lrm_dtype out_dt, void* y,
+                      void* z, void* ws, size_t ws_bytes, int32_t flags, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Gradient of lrm_linear's activation and bias:
+ *   dz = round_dt(dy * act'(z)),  db[e] = sum over the segment's rows of dz before rounding (fp32)
+ *   dy [R,N] dt, z [R,N'] dt (not read for LRM_ACT_NONE)  ->  dz [R,N'] dt, db [E,N'] fp32 or NULL.
+ * An expert without rows gets db = 0.  Rows >= seg_offsets[E] are not written.  Without db no ws is
+ * needed.  Deterministic: the sums are taken in a fixed order.
+ */
+lrm_status lrm_act_backward(const int32_t* seg_offsets, const void* dy, const void* z, int64_t R, int32_t E, int32_t N,
+                            lrm_act act, lrm_dtype dt, void* dz, float* db, void* ws, size_t ws_bytes,
+                            int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Gradients of lrm_linear's product from dz [R,N] (lrm_act_backward's; N counts all columns of dz):
+ *   dx = dz W[e]   [R,K] dt (NULL skips it),   dw[e] = dz^T x over the segment's rows   [E,N,K] fp32
+ *   (NULL skips it); an expert without rows gets dw = 0.
+ * The residual's gradient is dy itself.  Segments, ws, flags and limits as for lrm_linear.
+ */
+lrm_status lrm_linear_backward(const int32_t* seg_offsets, const void* dz, const void* x, const void* w, int64_t R,
+                               int32_t E, int32_t N, int32_t K, lrm_dtype dt, void* dx, float* dw, void* ws,
+                               size_t ws_bytes, int32_t flags, int32_t* dev_status, cudaStream_t stream);
 
 /*
  * Self-test of failure detection (no counterpart in the pages; part of this library's fault

@@ -19,6 +19,7 @@ LRM_BF16, LRM_F32 = 0, 1
 LRM_QUOTA_RATIO, LRM_QUOTA_CAP, LRM_QUOTA_EXPLICIT = 0, 1, 2
 LRM_GEMM_DEFAULT, LRM_GEMM_FORCE_SIMT = 0, 1
 LRM_SCORE_LRM, LRM_SCORE_GRAD_SQ, LRM_SCORE_GRAD_ABS = 0, 1, 2
+LRM_ACT_NONE, LRM_ACT_RELU, LRM_ACT_GELU, LRM_ACT_SILU, LRM_ACT_SWIGLU = 0, 1, 2, 3, 4
 LRM_MAX_EXPERTS, LRM_MAX_TOPK = 1024, 16
 
 _p, _i32, _i64, _sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
@@ -43,6 +44,14 @@ SIGNATURES = {
     "lrm_recompute_forward": (C.c_int, [_p, _p, _p, _i32, _i32, _i32, C.c_int, _i64, _p, _p, _p, _sz, _i32, _p,
                                         _p]),
     "lrm_selftest_wait_timeout": (C.c_int, [_p, _i64, _p]),
+    "lrm_sort_tokens": (C.c_int, [_p, _p, _i64, _i32, _i32, _i32, C.c_int, _p, _p, _p, _p, _p, _sz, _p, _p]),
+    "lrm_combine": (C.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, C.c_int, _i64, _p, _p, _p]),
+    "lrm_combine_backward": (C.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, C.c_int, _i64, _p, _p, _p, _p]),
+    "lrm_linear_workspace_size": (C.c_int, [_i64, _i32, _i32, _i32, C.c_int, C.c_int, C.POINTER(_sz)]),
+    "lrm_linear": (C.c_int, [_p, _p, _p, _p, _p, _i64, _i32, _i32, _i32, C.c_int, C.c_int, C.c_int, _p, _p, _p, _sz,
+                             _i32, _p, _p]),
+    "lrm_act_backward": (C.c_int, [_p, _p, _p, _i64, _i32, _i32, C.c_int, C.c_int, _p, _p, _p, _sz, _p, _p]),
+    "lrm_linear_backward": (C.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, _i32, C.c_int, _p, _p, _p, _sz, _i32, _p, _p]),
     "lrm_score_mode": (C.c_int, [_p, _p, _p, _i64, _i32, _i32, _i32, C.c_int, C.c_int, _p, _p, _p]),
 }
 

@@ -287,6 +287,204 @@ def lrm_scatter_dx(row_of_pair, dx_c, T, k, dx=None, cap=None, dev_status=None):
     return dx
 
 
+def _same(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def lrm_sort_tokens(topk_idx, x, E, seg_offsets=None, pair_of_row=None, row_of_pair=None, x_s=None, ws=None,
+                    dev_status=None):
+    """Tokens sorted by expert.  topk_idx int32 [T,k] (-1: not routed), x [T,H] or None (indices only).
+    Returns seg_offsets [E+1], pair_of_row [T*k], row_of_pair [T*k] (int32) and x_s [T*k,H].
+    Its gradient is lrm_scatter_dx(row_of_pair, dx_s, T, k)."""
+    T, k = topk_idx.shape
+    dev = topk_idx.device
+    if x is not None and (x.dim() != 2 or x.shape[0] != T):
+        raise ValueError(f"x must be [T,H] with T = {T}, got {list(x.shape)}")
+    H = x.shape[1] if x is not None else 8
+    i32 = dict(dtype=torch.int32, device=dev)
+    seg_offsets = torch.empty(E + 1, **i32) if seg_offsets is None else seg_offsets
+    pair_of_row = torch.empty(T * k, **i32) if pair_of_row is None else pair_of_row
+    row_of_pair = torch.empty(T * k, **i32) if row_of_pair is None else row_of_pair
+    if x is not None and x_s is None:
+        x_s = torch.empty(T * k, H, dtype=x.dtype, device=dev)
+    _same(seg_offsets, (E + 1,), "seg_offsets")
+    _same(pair_of_row, (T * k,), "pair_of_row")
+    _same(row_of_pair, (T * k,), "row_of_pair")
+    _same(x_s, (T * k, H), "x_s")
+    if ws is None:
+        ws = torch.empty(lrm_workspace_size(T, k, E, 8, 8, torch.float32), dtype=torch.uint8, device=dev)
+    _ok(L.load().lrm_sort_tokens(_cuda(topk_idx, "topk_idx", torch.int32), _opt(x, "x"), T, k, E, H,
+                                 L.LRM_BF16 if x is None else _dt(x), _cuda(seg_offsets, "seg_offsets", torch.int32),
+                                 _cuda(pair_of_row, "pair_of_row", torch.int32),
+                                 _cuda(row_of_pair, "row_of_pair", torch.int32),
+                                 _opt(x_s, "x_s", None if x is None else x.dtype), _cuda(ws, "ws"), ws.numel(),
+                                 _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_sort_tokens")
+    return seg_offsets, pair_of_row, row_of_pair, x_s
+
+
+def lrm_combine(row_of_pair, alpha, y_s, residual=None, y=None, dev_status=None):
+    """y [T,H] = residual + sum_j alpha[t,j] * y_s[row_of_pair[t,j]]; alpha fp32 [T,k], y_s [rows,H]."""
+    T, k = alpha.shape
+    H = y_s.shape[1]
+    if row_of_pair.numel() != T * k:
+        raise ValueError(f"row_of_pair must hold T*k = {T * k} rows, got {row_of_pair.numel()}")
+    y = torch.empty(T, H, dtype=y_s.dtype, device=y_s.device) if y is None else y
+    _same(y, (T, H), "y")
+    _same(residual, (T, H), "residual")
+    _ok(L.load().lrm_combine(_cuda(row_of_pair, "row_of_pair", torch.int32), _cuda(alpha, "alpha", torch.float32),
+                             _cuda(y_s, "y_s"), _opt(residual, "residual", y_s.dtype), T, k, H, _dt(y_s),
+                             y_s.shape[0], _cuda(y, "y", y_s.dtype), _opt(dev_status, "dev_status", torch.int32),
+                             _stream()), "lrm_combine")
+    return y
+
+
+def lrm_combine_backward(row_of_pair, alpha, dy, y_s, dy_s=None, dalpha=None, dev_status=None):
+    """Gradient of lrm_combine: dy_s [rows,H] and dalpha fp32 [T,k].  y_s None: dy_s alone (it must then
+    be given, it fixes the row count)."""
+    T, k = alpha.shape
+    H = dy.shape[1]
+    if y_s is None and dy_s is None:
+        raise ValueError("dy_s must be given when y_s is not")
+    rows = (y_s if y_s is not None else dy_s).shape[0]
+    if row_of_pair.numel() != T * k:
+        raise ValueError(f"row_of_pair must hold T*k = {T * k} rows, got {row_of_pair.numel()}")
+    dy_s = torch.empty(rows, H, dtype=dy.dtype, device=dy.device) if dy_s is None else dy_s
+    if y_s is not None and dalpha is None:
+        dalpha = torch.empty(T, k, dtype=torch.float32, device=dy.device)
+    elif y_s is None:
+        dalpha = None
+    _same(dy, (T, H), "dy")
+    _same(y_s, (rows, H), "y_s")
+    _same(dy_s, (rows, H), "dy_s")
+    if dalpha is not None and dalpha.numel() != T * k:
+        raise ValueError(f"dalpha must hold T*k = {T * k} values, got {dalpha.numel()}")
+    _ok(L.load().lrm_combine_backward(_cuda(row_of_pair, "row_of_pair", torch.int32),
+                                      _cuda(alpha, "alpha", torch.float32), _cuda(dy, "dy"), _opt(y_s, "y_s", dy.dtype),
+                                      T, k, H, _dt(dy), rows, _cuda(dy_s, "dy_s", dy.dtype),
+                                      _opt(dalpha, "dalpha", torch.float32),
+                                      _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_combine_backward")
+    return dy_s, dalpha
+
+
+_ACTS = {"none": L.LRM_ACT_NONE, "relu": L.LRM_ACT_RELU, "gelu": L.LRM_ACT_GELU, "silu": L.LRM_ACT_SILU,
+         "swiglu": L.LRM_ACT_SWIGLU}
+
+
+def _act_code(act: str) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    return _ACTS[act]
+
+
+def _experts(w, seg_offsets, name):
+    """(E, rows, columns) of a weight [rows, columns], or [E, rows, columns] with segments."""
+    if seg_offsets is None:
+        if w.dim() != 2:
+            raise ValueError(f"{name} must be [N,K] without seg_offsets, got {list(w.shape)}")
+        return (1, *w.shape)
+    if w.dim() != 3:
+        raise ValueError(f"{name} must be [E,N,K] with seg_offsets, got {list(w.shape)}")
+    _same(seg_offsets, (w.shape[0] + 1,), "seg_offsets")
+    return tuple(w.shape)
+
+
+def lrm_linear_workspace_size(R: int, E: int, N: int, K: int, act: str, dtype: torch.dtype) -> int:
+    """Scratch bytes of lrm_linear, lrm_act_backward and lrm_linear_backward (N: columns of y)."""
+    out = C.c_size_t(0)
+    dt = L.LRM_BF16 if dtype == torch.bfloat16 else L.LRM_F32
+    _ok(L.load().lrm_linear_workspace_size(R, E, N, K, _act_code(act), dt, C.byref(out)), "lrm_linear_workspace_size")
+    return int(out.value)
+
+
+def lrm_linear(x, w, bias=None, residual=None, act="none", seg_offsets=None, save_z=False, out_dtype=None, y=None,
+               z=None, ws=None, flags=L.LRM_GEMM_DEFAULT, dev_status=None):
+    """y = act(x w^T + bias) + residual; act "none", "relu", "gelu", "silu" or "swiglu" (w: gate rows, then
+    up rows).  x [R,K]; w [N',K] and bias [N'], or, with seg_offsets (rows sorted by expert), w [E,N',K] and
+    bias [E,N'].  save_z also returns the pre-activation z [R,N'].  out_dtype torch.float32 gives an fp32 y
+    from bf16 inputs.  Returns (y, z or None)."""
+    R, K = x.shape
+    E, NP, Kw = _experts(w, seg_offsets, "w")
+    code = _act_code(act)
+    if Kw != K:
+        raise ValueError(f"x has {K} columns, w {Kw}")
+    if act == "swiglu" and NP % 2:
+        raise ValueError(f"w has {NP} rows: gate and up rows in equal number expected")
+    N = NP // 2 if act == "swiglu" else NP
+    dev, out_dtype = x.device, x.dtype if out_dtype is None else out_dtype
+    if bias is not None and bias.numel() != E * NP:
+        raise ValueError(f"bias must hold {E * NP} values, got {bias.numel()}")
+    y = torch.empty(R, N, dtype=out_dtype, device=dev) if y is None else y
+    if save_z and z is None:
+        z = torch.empty(R, NP, dtype=x.dtype, device=dev)
+    _same(y, (R, N), "y")
+    _same(z, (R, NP), "z")
+    _same(residual, (R, N), "residual")
+    if ws is None:
+        ws = torch.empty(lrm_linear_workspace_size(R, E, N, K, act, x.dtype), dtype=torch.uint8, device=dev)
+    _ok(L.load().lrm_linear(_opt(seg_offsets, "seg_offsets", torch.int32), _cuda(x, "x"), _cuda(w, "w", x.dtype),
+                            _opt(bias, "bias", x.dtype), _opt(residual, "residual", y.dtype), R, E, N, K, code, _dt(x),
+                            _dt(y), _cuda(y, "y"), _opt(z, "z", x.dtype), _cuda(ws, "ws"), ws.numel(), int(flags),
+                            _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_linear")
+    return y, z
+
+
+def lrm_act_backward(dy, z, act="none", seg_offsets=None, bias_grad=True, dz=None, db=None, ws=None,
+                     dev_status=None):
+    """dz = dy * act'(z) [R,N'] and db fp32 [N'] ([E,N'] with seg_offsets), the column sums of dz, unless
+    bias_grad is False.  z may be None for act "none"."""
+    R, N = dy.shape
+    code = _act_code(act)
+    NP = 2 * N if act == "swiglu" else N
+    E = 1 if seg_offsets is None else seg_offsets.numel() - 1
+    dev = dy.device
+    dz = torch.empty(R, NP, dtype=dy.dtype, device=dev) if dz is None else dz
+    if bias_grad and db is None:
+        db = torch.empty((NP,) if seg_offsets is None else (E, NP), dtype=torch.float32, device=dev)
+    if not bias_grad:
+        db = None
+    if db is not None and db.numel() != E * NP:
+        raise ValueError(f"db must hold {E * NP} values, got {db.numel()}")
+    if act != "none" and z is None:
+        raise ValueError(f"z is needed for act {act!r}")
+    _same(z, (R, NP), "z")
+    _same(dz, (R, NP), "dz")
+    if ws is None and db is not None:
+        ws = torch.empty(lrm_linear_workspace_size(R, E, N, 8, act, dy.dtype), dtype=torch.uint8, device=dev)
+    _ok(L.load().lrm_act_backward(_opt(seg_offsets, "seg_offsets", torch.int32), _cuda(dy, "dy"),
+                                  _opt(z, "z", dy.dtype), R, E, N, code, _dt(dy), _cuda(dz, "dz", dy.dtype),
+                                  _opt(db, "db", torch.float32), _opt(ws, "ws"), 0 if ws is None else ws.numel(),
+                                  _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_act_backward")
+    return dz, db
+
+
+def lrm_linear_backward(dz, x, w, seg_offsets=None, need_dx=True, need_dw=True, dx=None, dw=None, ws=None,
+                        flags=L.LRM_GEMM_DEFAULT, dev_status=None):
+    """Gradients of lrm_linear's product from dz [R,N]: dx [R,K] = dz w and dw fp32 [N,K] = dz^T x ([E,N,K]
+    with seg_offsets).  Returns (dx or None, dw or None)."""
+    R, N = dz.shape
+    E, Nw, K = _experts(w, seg_offsets, "w")
+    if Nw != N:
+        raise ValueError(f"dz has {N} columns, w {Nw} rows")
+    dev = dz.device
+    if need_dx and dx is None:
+        dx = torch.empty(R, K, dtype=dz.dtype, device=dev)
+    if need_dw and dw is None:
+        dw = torch.empty(w.shape, dtype=torch.float32, device=dev)
+    dx, dw = (dx if need_dx else None), (dw if need_dw else None)
+    _same(x, (R, K), "x")
+    _same(dx, (R, K), "dx")
+    _same(dw, w.shape, "dw")
+    if ws is None:
+        ws = torch.empty(lrm_linear_workspace_size(R, E, N, K, "none", dz.dtype), dtype=torch.uint8, device=dev)
+    _ok(L.load().lrm_linear_backward(_opt(seg_offsets, "seg_offsets", torch.int32), _cuda(dz, "dz"),
+                                     _cuda(x, "x", dz.dtype), _cuda(w, "w", dz.dtype), R, E, N, K, _dt(dz),
+                                     _opt(dx, "dx", dz.dtype), _opt(dw, "dw", torch.float32), _cuda(ws, "ws"),
+                                     ws.numel(), int(flags), _opt(dev_status, "dev_status", torch.int32), _stream()),
+        "lrm_linear_backward")
+    return dx, dw
+
+
 class PrunedBackward:
     """The whole pruned expert backward for one fixed problem size, with every buffer
     allocated once (device memory from torch).  `run` queues score -> select -> compact ->
@@ -391,6 +589,63 @@ class PrunedBackward:
                 "phi_c": self.phi_c, "dh_c": self.dh_c, "dx_c": self.dx_c, "dw_gate_up": self.dw_gate_up,
                 "dw_down": self.dw_down, "dx": self.dx, "dev_status": self.dev_status,
                 "row_dot": self.row_dot, "dalpha": self.dalpha}
+
+
+class MoeLayer:
+    """The expert layer around the routing, forward and unpruned backward, for one fixed problem size with
+    every buffer allocated once.  forward: sort by expert, SwiGLU product, down product, weighted way back;
+    backward: the gradients of x, alpha and both weights.  Everything is queued on the current stream; no
+    host synchronisation.  train=False keeps no state for the backward (serving)."""
+
+    def __init__(self, T, k, E, H, I, dtype=torch.bfloat16, device="cuda", flags=L.LRM_GEMM_DEFAULT, train=True):
+        self.T, self.k, self.E, self.H, self.I = T, k, E, H, I
+        self.dtype, self.flags, self.train = dtype, flags, train
+        dev, P = torch.device(device), T * k
+        i32 = dict(dtype=torch.int32, device=dev)
+        new = dict(dtype=dtype, device=dev)
+        self.seg_offsets = torch.empty(E + 1, **i32)
+        self.pair_of_row = torch.empty(P, **i32)
+        self.row_of_pair = torch.empty(P, **i32)
+        self.x_s, self.phi_s = torch.empty(P, H, **new), torch.empty(P, I, **new)
+        self.y_s, self.y = torch.empty(P, H, **new), torch.empty(T, H, **new)
+        self.dev_status = torch.zeros(1, **i32)
+        ws = max(lrm_workspace_size(T, k, E, 8, 8, torch.float32),
+                 lrm_linear_workspace_size(P, E, I, H, "swiglu", dtype),
+                 lrm_linear_workspace_size(P, E, H, I, "none", dtype))
+        if train:
+            self.h_s, self.dh_s = torch.empty(P, 2 * I, **new), torch.empty(P, 2 * I, **new)
+            self.dy_s, self.dphi_s = torch.empty(P, H, **new), torch.empty(P, I, **new)
+            self.dx_s, self.dx = torch.empty(P, H, **new), torch.empty(T, H, **new)
+            self.dalpha = torch.empty(T, k, dtype=torch.float32, device=dev)
+            self.dw_gate_up = torch.empty(E, 2 * I, H, dtype=torch.float32, device=dev)
+            self.dw_down = torch.empty(E, H, I, dtype=torch.float32, device=dev)
+            ws = max(ws, lrm_linear_workspace_size(P, E, 2 * I, H, "none", dtype))
+        self.ws = torch.empty(ws, dtype=torch.uint8, device=dev)
+
+    def forward(self, x, topk_idx, alpha, w_gate_up, w_down, residual=None):
+        """y [T,H] = residual + sum_j alpha[t,j] * w_down[e] SwiGLU(w_gate_up[e] x_t), e = topk_idx[t,j] (-1: none)."""
+        lrm_sort_tokens(topk_idx, x, self.E, seg_offsets=self.seg_offsets, pair_of_row=self.pair_of_row,
+                        row_of_pair=self.row_of_pair, x_s=self.x_s, ws=self.ws, dev_status=self.dev_status)
+        lrm_linear(self.x_s, w_gate_up, act="swiglu", seg_offsets=self.seg_offsets, y=self.phi_s,
+                   z=self.h_s if self.train else None, ws=self.ws, flags=self.flags, dev_status=self.dev_status)
+        lrm_linear(self.phi_s, w_down, seg_offsets=self.seg_offsets, y=self.y_s, ws=self.ws, flags=self.flags,
+                   dev_status=self.dev_status)
+        return lrm_combine(self.row_of_pair, alpha, self.y_s, residual=residual, y=self.y, dev_status=self.dev_status)
+
+    def backward(self, dy, alpha, w_gate_up, w_down):
+        """Gradients of the last forward: dx [T,H], dalpha [T,k], dw_gate_up, dw_down (the residual's is dy)."""
+        if not self.train:
+            raise ValueError("MoeLayer(train=False) keeps no state for a backward")
+        seg, kw = self.seg_offsets, dict(ws=self.ws, dev_status=self.dev_status)
+        lrm_combine_backward(self.row_of_pair, alpha, dy, self.y_s, dy_s=self.dy_s, dalpha=self.dalpha,
+                             dev_status=self.dev_status)
+        lrm_linear_backward(self.dy_s, self.phi_s, w_down, seg_offsets=seg, dx=self.dphi_s, dw=self.dw_down,
+                            flags=self.flags, **kw)
+        lrm_act_backward(self.dphi_s, self.h_s, act="swiglu", seg_offsets=seg, bias_grad=False, dz=self.dh_s, **kw)
+        lrm_linear_backward(self.dh_s, self.x_s, w_gate_up, seg_offsets=seg, dx=self.dx_s, dw=self.dw_gate_up,
+                            flags=self.flags, **kw)
+        lrm_scatter_dx(self.row_of_pair, self.dx_s, self.T, self.k, dx=self.dx, dev_status=self.dev_status)
+        return self.dx, self.dalpha, self.dw_gate_up, self.dw_down
 
 
 class HostPipeline:

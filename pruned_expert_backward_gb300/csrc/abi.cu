@@ -27,6 +27,34 @@ lrm_status check_dims(int64_t T, int32_t k, int32_t E, int32_t H, int32_t I) {
 }
 lrm_status check_dt(lrm_dtype dt) { return (dt == LRM_BF16 || dt == LRM_F32) ? LRM_OK : LRM_ERR_DTYPE; }
 
+// Sizes of lrm_linear and its gradients: R rows, E weights of N (2N for SwiGLU) x K.
+lrm_status check_linear(int64_t R, int32_t E, int32_t N, int32_t K, lrm_act act, lrm_dtype dt) {
+  if (R < 0 || E < 1 || N < 1 || K < 1) return LRM_ERR_INVALID_ARG;
+  if (act < LRM_ACT_NONE || act > LRM_ACT_SWIGLU) return LRM_ERR_INVALID_ARG;
+  if (R > INT32_MAX || E > LRM_MAX_EXPERTS || N > (1 << 24) || K > (1 << 24)) return LRM_ERR_SHAPE;
+  if (N % 8 != 0 || K % 8 != 0) return LRM_ERR_SHAPE;
+  return check_dt(dt);
+}
+
+// Scratch of lrm_sort_tokens: the counts of each chunk of pairs and the buckets' sizes.
+struct SortWs {
+  size_t counts, loads, total;
+};
+SortWs sort_layout(int64_t T, int32_t k, int32_t E) {
+  const int64_t ct = sort_chunk_tokens(k), nc = (T + ct - 1) / ct;
+  SortWs w{};
+  w.loads = up(sizeof(int32_t) * (size_t)(nc > 0 ? nc : 1) * (E + 1));
+  w.total = w.loads + up(sizeof(int32_t) * (size_t)(E + 1));
+  return w;
+}
+
+// Scratch of the products and of the bias gradient (NP: rows of w, columns of dz).
+size_t linear_ws_bytes(int64_t, int32_t, int32_t, int32_t, lrm_dtype) { return 256; }
+size_t linear_grad_ws_bytes(int64_t, int32_t, int32_t, int32_t, lrm_dtype) { return 256; }
+size_t act_grad_ws_bytes(int64_t R, int32_t E, int32_t NP) {
+  return up(sizeof(float) * act_backward_part_rows(R, E) * NP);
+}
+
 lrm_status after_launch() {
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? LRM_OK : LRM_ERR_CUDA;
@@ -101,7 +129,9 @@ lrm_status lrm_workspace_size(int64_t T, int32_t k, int32_t E, int32_t H, int32_
   if (st) return st;
   if ((st = check_dt(dt))) return st;
   const size_t sel = workspace_layout(T * k, E).total, grp = grouped_ws_bytes(T * k, E, I, true);
+  const size_t srt = sort_layout(T, k, E).total;
   *bytes = sel > grp ? sel : grp;
+  if (*bytes < srt) *bytes = srt;
   return LRM_OK;
 }
 
@@ -372,6 +402,135 @@ lrm_status lrm_router_grad(const int32_t* row_of_pair, const float* alpha, const
   if (T > 0 && (!row_of_pair || !alpha || !dalpha)) return LRM_ERR_INVALID_ARG;
   if (T > 0 && cap > 0 && !row_dot) return LRM_ERR_INVALID_ARG;
   launch_router_grad(row_of_pair, alpha, row_dot, T * k, cap, dalpha, stream);
+  return after_launch();
+}
+
+lrm_status lrm_sort_tokens(const int32_t* topk_idx, const void* x, int64_t T, int32_t k, int32_t E, int32_t H,
+                           lrm_dtype dt, int32_t* seg_offsets, int32_t* pair_of_row, int32_t* row_of_pair, void* x_s,
+                           void* ws, size_t ws_bytes, int32_t* dev_status, cudaStream_t stream) {
+  LRM_NVTX_RANGE();
+  lrm_status st = check_dims(T, k, E, H, 8);
+  if (st) return st;
+  if ((st = check_dt(dt))) return st;
+  if (!seg_offsets) return LRM_ERR_INVALID_ARG;
+  if (T > 0 && (!topk_idx || !pair_of_row || !row_of_pair || (x_s && !x))) return LRM_ERR_INVALID_ARG;
+  if (!al16(x) || !al16(x_s)) return LRM_ERR_INVALID_ARG;
+  const SortWs w = sort_layout(T, k, E);
+  if (!ws || ws_bytes < w.total) return LRM_ERR_WORKSPACE;
+  char* b = static_cast<char*>(ws);
+  const SortArgs a{topk_idx, x, T, k, E, H, seg_offsets, pair_of_row, row_of_pair, x_s,
+                   reinterpret_cast<int32_t*>(b + w.counts), reinterpret_cast<int32_t*>(b + w.loads), dev_status};
+  return launch_sort_tokens(a, dt, stream);
+}
+
+lrm_status lrm_combine(const int32_t* row_of_pair, const float* alpha, const void* y_s, const void* residual, int64_t T,
+                       int32_t k, int32_t H, lrm_dtype dt, int64_t cap, void* y, int32_t* dev_status,
+                       cudaStream_t stream) {
+  LRM_NVTX_RANGE();
+  lrm_status st = check_dims(T, k, 1, H, 8);
+  if (st) return st;
+  if ((st = check_dt(dt))) return st;
+  if (cap < 0 || cap > INT32_MAX) return LRM_ERR_INVALID_ARG;
+  if (T > 0 && (!row_of_pair || !alpha || !y || (cap > 0 && !y_s))) return LRM_ERR_INVALID_ARG;
+  if (!al16(y_s) || !al16(residual) || !al16(y)) return LRM_ERR_INVALID_ARG;
+  if (T == 0) return LRM_OK;
+  launch_combine(row_of_pair, alpha, y_s, residual, T, k, H, dt, cap, y, dev_status, stream);
+  return after_launch();
+}
+
+lrm_status lrm_combine_backward(const int32_t* row_of_pair, const float* alpha, const void* dy, const void* y_s,
+                                int64_t T, int32_t k, int32_t H, lrm_dtype dt, int64_t cap, void* dy_s, float* dalpha,
+                                int32_t* dev_status, cudaStream_t stream) {
+  LRM_NVTX_RANGE();
+  lrm_status st = check_dims(T, k, 1, H, 8);
+  if (st) return st;
+  if ((st = check_dt(dt))) return st;
+  if (cap < 0 || cap > INT32_MAX) return LRM_ERR_INVALID_ARG;
+  if (T > 0 && (!row_of_pair || !alpha || !dy)) return LRM_ERR_INVALID_ARG;
+  if (T > 0 && cap > 0 && (!dy_s || (dalpha && !y_s))) return LRM_ERR_INVALID_ARG;
+  if (!al16(dy) || !al16(y_s) || !al16(dy_s)) return LRM_ERR_INVALID_ARG;
+  if (T == 0) return LRM_OK;
+  launch_combine_backward(row_of_pair, alpha, dy, dalpha ? y_s : nullptr, T, k, H, dt, cap, dy_s, dalpha, dev_status,
+                          stream);
+  return after_launch();
+}
+
+lrm_status lrm_linear_workspace_size(int64_t R, int32_t E, int32_t N, int32_t K, lrm_act act, lrm_dtype dt,
+                                     size_t* bytes) {
+  LRM_NVTX_RANGE();
+  if (!bytes) return LRM_ERR_INVALID_ARG;
+  lrm_status st = check_linear(R, E, N, K, act, dt);
+  if (st) return st;
+  const int32_t NP = act == LRM_ACT_SWIGLU ? 2 * N : N;
+  const size_t need[] = {linear_ws_bytes(R, E, NP, K, dt), act_grad_ws_bytes(R, E, NP),
+                         linear_grad_ws_bytes(R, E, NP, K, dt)};
+  size_t most = 0;
+  for (const size_t n : need) most = n > most ? n : most;
+  *bytes = most;
+  return LRM_OK;
+}
+
+lrm_status lrm_linear(const int32_t* seg_offsets, const void* x, const void* w, const void* bias, const void* residual,
+                      int64_t R, int32_t E, int32_t N, int32_t K, lrm_act act, lrm_dtype dt, lrm_dtype out_dt, void* y,
+                      void* z, void* ws, size_t ws_bytes, int32_t flags, int32_t* dev_status, cudaStream_t stream) {
+  LRM_NVTX_RANGE();
+  lrm_status st = check_linear(R, E, N, K, act, dt);
+  if (st) return st;
+  if ((st = check_dt(out_dt))) return st;
+  if (dt == LRM_F32 && out_dt != LRM_F32) return LRM_ERR_DTYPE;
+  if (out_dt != dt && residual) return LRM_ERR_DTYPE;  // the residual has the type of y and of x
+  if (flags != LRM_GEMM_DEFAULT && flags != LRM_GEMM_FORCE_SIMT) return LRM_ERR_INVALID_ARG;
+  if (!w || (!seg_offsets && E != 1)) return LRM_ERR_INVALID_ARG;
+  if (R > 0 && (!x || !y)) return LRM_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, w, bias, residual, y, z};
+  for (const void* p : ptrs)
+    if (!al16(p)) return LRM_ERR_INVALID_ARG;
+  const int32_t NP = act == LRM_ACT_SWIGLU ? 2 * N : N;
+  if (!ws || ws_bytes < linear_ws_bytes(R, E, NP, K, dt)) return LRM_ERR_WORKSPACE;
+  if (R == 0) return LRM_OK;
+  const LinearArgs a{seg_offsets, x, w, bias, residual, R, E, N, K, act, y, z, dev_status};
+  launch_linear_simt(a, dt, out_dt, stream);
+  return after_launch();
+}
+
+lrm_status lrm_act_backward(const int32_t* seg_offsets, const void* dy, const void* z, int64_t R, int32_t E, int32_t N,
+                            lrm_act act, lrm_dtype dt, void* dz, float* db, void* ws, size_t ws_bytes,
+                            int32_t* dev_status, cudaStream_t stream) {
+  LRM_NVTX_RANGE();
+  lrm_status st = check_linear(R, E, N, 8, act, dt);
+  if (st) return st;
+  if (!seg_offsets && E != 1) return LRM_ERR_INVALID_ARG;
+  if (R > 0 && (!dy || !dz || (act != LRM_ACT_NONE && !z))) return LRM_ERR_INVALID_ARG;
+  const void* ptrs[] = {dy, z, dz, db};
+  for (const void* p : ptrs)
+    if (!al16(p)) return LRM_ERR_INVALID_ARG;
+  const int32_t NP = act == LRM_ACT_SWIGLU ? 2 * N : N;
+  if (db && (!ws || ws_bytes < act_grad_ws_bytes(R, E, NP))) return LRM_ERR_WORKSPACE;
+  if (R == 0 && !db) return LRM_OK;
+  const ActGradArgs a{seg_offsets, dy, z, R, E, N, act, dz, db, static_cast<float*>(ws), dev_status};
+  launch_act_backward(a, dt, stream);
+  return after_launch();
+}
+
+lrm_status lrm_linear_backward(const int32_t* seg_offsets, const void* dz, const void* x, const void* w, int64_t R,
+                               int32_t E, int32_t N, int32_t K, lrm_dtype dt, void* dx, float* dw, void* ws,
+                               size_t ws_bytes, int32_t flags, int32_t* dev_status, cudaStream_t stream) {
+  LRM_NVTX_RANGE();
+  lrm_status st = check_linear(R, E, N, K, LRM_ACT_NONE, dt);
+  if (st) return st;
+  if (flags != LRM_GEMM_DEFAULT && flags != LRM_GEMM_FORCE_SIMT) return LRM_ERR_INVALID_ARG;
+  if ((!seg_offsets && E != 1) || (!dx && !dw)) return LRM_ERR_INVALID_ARG;
+  if (R > 0 && (!dz || (dx && !w) || (dw && !x))) return LRM_ERR_INVALID_ARG;
+  const void* ptrs[] = {dz, x, w, dx, dw};
+  for (const void* p : ptrs)
+    if (!al16(p)) return LRM_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < linear_grad_ws_bytes(R, E, N, K, dt)) return LRM_ERR_WORKSPACE;
+  if (R == 0) {  // no rows anywhere: every dW is zero
+    if (dw && cudaMemsetAsync(dw, 0, sizeof(float) * (size_t)E * N * K, stream) != cudaSuccess) return LRM_ERR_CUDA;
+    return LRM_OK;
+  }
+  const LinearGradArgs a{seg_offsets, dz, x, w, R, E, N, K, dx, dw, dev_status};
+  launch_linear_backward_simt(a, dt, stream);
   return after_launch();
 }
 

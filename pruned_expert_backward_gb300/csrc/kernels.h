@@ -113,4 +113,59 @@ void launch_recompute_simt(const RecomputeArgs& a, lrm_dtype dt, cudaStream_t s)
 lrm_status launch_grouped_tc(const GroupedArgs& a, const GemmWs& ws, cudaStream_t s);
 lrm_status launch_wait_selftest(int32_t* status, int64_t limit_ns, cudaStream_t s);
 
+// Tokens sorted by expert (lrm_sort_tokens), and the weighted way back with its gradient.
+struct SortArgs {
+  const int32_t* topk_idx;
+  const void* x;
+  int64_t T;
+  int32_t k, E, H;
+  int32_t *seg_offsets, *pair_of_row, *row_of_pair;
+  void* x_s;        // optional
+  int32_t* counts;  // scratch [chunks][E + 1]
+  int32_t* loads;   // scratch [E + 1]
+  int32_t* status;
+};
+int sort_chunk_tokens(int32_t k);  // tokens of a chunk of the multi-launch form
+lrm_status launch_sort_tokens(const SortArgs& a, lrm_dtype dt, cudaStream_t s);
+void launch_combine(const int32_t* row_of_pair, const float* alpha, const void* y_s, const void* residual, int64_t T,
+                    int32_t k, int32_t H, lrm_dtype dt, int64_t cap, void* y, int32_t* status, cudaStream_t s);
+void launch_combine_backward(const int32_t* row_of_pair, const float* alpha, const void* dy, const void* y_s, int64_t T,
+                             int32_t k, int32_t H, lrm_dtype dt, int64_t cap, void* dy_s, float* dalpha,
+                             int32_t* status, cudaStream_t s);
+
+// lrm_linear and its gradients.  seg_offsets is NULL for one dense product (E = 1).
+struct LinearArgs {
+  const int32_t* seg_offsets;
+  const void *x, *w, *bias, *residual;  // bias, residual optional
+  int64_t R;
+  int32_t E, N, K;  // N: columns of y (w has 2N rows per expert for SwiGLU)
+  lrm_act act;
+  void *y, *z;  // z optional: the pre-activation
+  int32_t* status;
+};
+void launch_linear_simt(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, cudaStream_t s);
+struct LinearGradArgs {
+  const int32_t* seg_offsets;
+  const void *dz, *x, *w;
+  int64_t R;
+  int32_t E, N, K;  // N: columns of dz (rows of w)
+  void* dx;         // optional
+  float* dw;        // optional
+  int32_t* status;
+};
+void launch_linear_backward_simt(const LinearGradArgs& a, lrm_dtype dt, cudaStream_t s);
+struct ActGradArgs {
+  const int32_t* seg_offsets;
+  const void *dy, *z;
+  int64_t R;
+  int32_t E, N;
+  lrm_act act;
+  void* dz;
+  float* db;    // optional
+  float* part;  // scratch [act_backward_part_rows][columns of dz], only with db
+  int32_t* status;
+};
+size_t act_backward_part_rows(int64_t R, int32_t E);
+void launch_act_backward(const ActGradArgs& a, lrm_dtype dt, cudaStream_t s);
+
 }  // namespace lrm

@@ -1,0 +1,454 @@
+// Tokens sorted by expert (lrm_sort_tokens) and the weighted way back (lrm_combine) with its
+// gradient (lrm_combine_backward).
+//
+// Pair u = (t, j) of expert e = topk_idx[u] goes to row
+//     row(u) = #{v : expert(v) < e} + #{v < u : expert(v) = e},
+// a stable counting sort; unrouted pairs (expert -1) form one more bucket behind the last expert's
+// whose rows are zeroed.  The way back is y_t = residual_t + sum_j alpha_tj y_s[row(tj)].
+// All three move each byte once and are bound by HBM at training size and by launch latency for a
+// few tokens.
+//
+// sort: up to kSmallPairs pairs one launch does everything: every CTA ranks all pairs for itself
+// (a few hundred nanoseconds in shared memory) and copies the rows of its own tokens.  Beyond that
+// three launches: counts of each chunk of pairs, the scan of every expert's counts down the chunks,
+// and a third that ranks a chunk's pairs and copies its tokens' rows (a token's row is read once and
+// written k times).
+// No atomics on anything that decides an order: all results are deterministic.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace lrm {
+
+namespace {
+
+// One launch up to this many pairs and experts: each of 32 warps keeps a count per bucket in shared memory.
+constexpr int kSmallPairs = 2048;
+constexpr int kSmallExperts = 256;
+constexpr int kChunkThreads = 256;  // multi-launch form: pairs of a chunk (whole tokens), at most one per thread
+
+// Bucket of a pair: its expert, or E when it is not routed (-1) or its id is out of range (recorded).
+__device__ __forceinline__ int bucket_of(int32_t id, int E, int32_t* status) {
+  if (id >= 0 && id < E) return id;
+  if (id != -1) set_status(status, LRM_ERR_BAD_INDEX);
+  return E;
+}
+
+// Exclusive block-wide prefix sum of one int per thread (blockDim.x a multiple of 32); sm: 33 ints.
+__device__ __forceinline__ int block_prefix(int v, int* sm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sm[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    int w = lane < nw ? sm[lane] : 0;
+    const int own = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    if (lane < nw) sm[lane] = w - own;
+    if (lane == 31) sm[32] = w;
+  }
+  __syncthreads();
+  const int res = sm[warp] + incl - v;
+  __syncthreads();
+  return res;
+}
+
+// Copies x rows of `ntok` tokens from t0 into their pairs' rows: s_dst[i * k + j] >= 0 is the row of
+// pair (t0 + i, j); a negative entry -1 - r zeroes row r (an unrouted pair's place).  (token, 16-byte
+// column) items are dealt to the threads, four tokens' loads in flight.
+template <typename T>
+__device__ __forceinline__ void copy_rows(const T* __restrict__ x, T* __restrict__ x_s, const int* s_dst, int64_t t0,
+                                          int ntok, int k, int H) {
+  constexpr int VN = VecTraits<T>::N;
+  const int nv = H / VN;
+  const int n = ntok * nv, step = blockDim.x;
+  for (int i0 = threadIdx.x; i0 < n; i0 += 4 * step) {
+    uint4 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + q * step;
+      if (i < n) v[q] = ld_stream16(x + t0 * H + (int64_t)i * VN);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + q * step;
+      if (i >= n) break;
+      const int tok = i / nv, col = (i - tok * nv) * VN;
+      for (int j = 0; j < k; ++j) {
+        const int r = s_dst[tok * k + j];
+        st16(x_s + (int64_t)(r >= 0 ? r : -1 - r) * H + col, r >= 0 ? v[q] : make_uint4(0, 0, 0, 0));
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- one launch ---------
+// Warp w ranks pairs [w * ppw, (w + 1) * ppw), 32 at a time in order, with __match_any_sync; counts
+// are [warp][bucket] in shared memory, scanned down the warps and then across the buckets.
+template <typename T>
+__global__ void __launch_bounds__(1024) sort_small_kernel(const int32_t* __restrict__ idx, const T* __restrict__ x,
+                                                          int n_tok, int k, int E, int H, int32_t* __restrict__ seg,
+                                                          int32_t* __restrict__ pair_of_row,
+                                                          int32_t* __restrict__ row_of_pair, T* __restrict__ x_s,
+                                                          int32_t* __restrict__ status) {
+  chain_wait();
+  extern __shared__ int sh[];
+  const int B = E + 1, nw = blockDim.x >> 5, P = n_tok * k;
+  int* s_cnt = sh;             // [nw][B] counts, then the warps' exclusive offsets
+  int* s_start = s_cnt + nw * B;  // [B] bucket starts
+  int* s_row = s_start + B;    // [P] rows (-1 - r where the pair is not routed)
+  int* s_scan = s_row + P;     // [33]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < nw * B; i += blockDim.x) s_cnt[i] = 0;
+  __syncthreads();
+  const int ppw = ((P + nw - 1) / nw + 31) / 32 * 32;
+  int* cnt = s_cnt + warp * B;
+  for (int u0 = warp * ppw; u0 < min(P, (warp + 1) * ppw); u0 += 32) {
+    const int u = u0 + lane;
+    const bool in = u < P;
+    const int e = in ? bucket_of(idx[u], E, blockIdx.x == 0 ? status : nullptr) : B;
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    const int before = in ? cnt[e] : 0;
+    if (in) s_row[u] = before + __popc(same & ((1u << lane) - 1u)) + (e << 16);  // rank < 2^16, bucket
+    __syncwarp();
+    if (in && (same >> lane) == 1u) cnt[e] = before + __popc(same);  // the last lane of a group
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int b0 = 0, run = 0; b0 < B; b0 += blockDim.x) {
+    const int e = b0 + threadIdx.x;
+    int tot = 0;
+    if (e < B)
+      for (int w = 0; w < nw; ++w) {
+        const int c = s_cnt[w * B + e];
+        s_cnt[w * B + e] = tot;
+        tot += c;
+      }
+    const int ex = block_prefix(tot, s_scan);
+    if (e < B) s_start[e] = run + ex;
+    run += s_scan[32];
+    __syncthreads();
+  }
+  for (int u = threadIdx.x; u < P; u += blockDim.x) {
+    const int e = s_row[u] >> 16, r = s_start[e] + s_cnt[(u / ppw) * B + e] + (s_row[u] & 0xffff);
+    s_row[u] = e < E ? r : -1 - r;
+    if (blockIdx.x == 0) {
+      row_of_pair[u] = e < E ? r : -1;
+      pair_of_row[r] = e < E ? u : -1;
+    }
+  }
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e < B; e += blockDim.x) seg[e] = s_start[e];
+  __syncthreads();
+  if (x_s != nullptr)
+    for (int t = blockIdx.x; t < n_tok; t += gridDim.x) copy_rows(x, x_s, s_row + t * k, t, 1, k, H);
+}
+
+// ---------------------------------------------------------------- three launches -----
+__global__ void __launch_bounds__(kChunkThreads) sort_count_kernel(const int32_t* __restrict__ idx, int64_t P, int E,
+                                                                   int chunk, int32_t* __restrict__ counts,
+                                                                   int32_t* __restrict__ status) {
+  chain_wait();
+  extern __shared__ int hist[];  // [E + 1]
+  const int B = E + 1;
+  for (int e = threadIdx.x; e < B; e += blockDim.x) hist[e] = 0;
+  __syncthreads();
+  const int64_t c = blockIdx.x, u = c * chunk + threadIdx.x;
+  if (threadIdx.x < chunk && u < P) atomicAdd(&hist[bucket_of(idx[u], E, status)], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e < B; e += blockDim.x) counts[c * B + e] = hist[e];
+}
+
+// One CTA per bucket: exclusive scan down its column of chunk counts; loads[e] = the bucket's size.
+__global__ void __launch_bounds__(1024) sort_colscan_kernel(int32_t* __restrict__ counts, int64_t n_chunks, int B,
+                                                            int32_t* __restrict__ loads) {
+  chain_wait();
+  __shared__ int sm[33];
+  const int e = blockIdx.x;
+  int run = 0;
+  for (int64_t c0 = 0; c0 < n_chunks; c0 += blockDim.x) {
+    const int64_t c = c0 + threadIdx.x;
+    const int v = c < n_chunks ? counts[c * B + e] : 0;
+    const int ex = block_prefix(v, sm);
+    if (c < n_chunks) counts[c * B + e] = run + ex;
+    run += sm[32];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) loads[e] = run;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kChunkThreads) sort_rows_kernel(
+    const int32_t* __restrict__ idx, const T* __restrict__ x, int64_t n_tok, int k, int E, int H, int chunk_tok,
+    const int32_t* __restrict__ counts, const int32_t* __restrict__ loads, int32_t* __restrict__ seg,
+    int32_t* __restrict__ pair_of_row, int32_t* __restrict__ row_of_pair, T* __restrict__ x_s) {
+  chain_wait();
+  constexpr int kWarps = kChunkThreads / 32;
+  extern __shared__ int sh[];
+  const int B = E + 1;
+  int* s_start = sh;                // [B] this chunk's first row of each bucket
+  int* s_cnt = s_start + B;         // [kWarps][B]
+  int* s_row = s_cnt + kWarps * B;  // [kChunkThreads]
+  __shared__ int s_scan[33];
+  const int64_t c = blockIdx.x, t0 = c * chunk_tok;
+  const int ntok = (int)min((int64_t)chunk_tok, n_tok - t0), np = ntok * k;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < kWarps * B; i += blockDim.x) s_cnt[i] = 0;
+  for (int b0 = 0, run = 0; b0 < B; b0 += blockDim.x) {
+    const int e = b0 + threadIdx.x;
+    const int ex = block_prefix(e < B ? loads[e] : 0, s_scan);
+    if (e < B) {
+      s_start[e] = run + ex + counts[c * B + e];
+      if (c == 0) seg[e] = run + ex;
+    }
+    run += s_scan[32];
+    __syncthreads();
+  }
+  const bool in = threadIdx.x < np;
+  const int64_t u = t0 * k + threadIdx.x;
+  const int e = in ? bucket_of(idx[u], E, nullptr) : B;
+  const unsigned same = __match_any_sync(0xffffffffu, e);
+  if (in && (same >> lane) == 1u) s_cnt[warp * B + e] = __popc(same);
+  __syncthreads();
+  if (in) {
+    int r = s_start[e] + __popc(same & ((1u << lane) - 1u));
+    for (int w = 0; w < warp; ++w) r += s_cnt[w * B + e];
+    s_row[threadIdx.x] = e < E ? r : -1 - r;
+    row_of_pair[u] = e < E ? r : -1;
+    pair_of_row[r] = e < E ? (int32_t)u : -1;
+  }
+  __syncthreads();
+  if (x_s != nullptr) copy_rows(x, x_s, s_row, t0, ntok, k, H);
+}
+
+// ---------------------------------------------------------------- the way back -------
+// A CTA covers TOK tokens and blockDim.x 16-byte columns (times a loop); each thread walks the CTA's
+// routed pairs with 8 row loads in flight and adds each token's in j order in fp32.
+constexpr int kCombineLoads = 8;
+
+template <typename T, int TOK>
+__global__ void __launch_bounds__(256) combine_kernel(const int32_t* __restrict__ row_of_pair,
+                                                      const float* __restrict__ alpha, const T* __restrict__ y_s,
+                                                      const T* residual, int64_t n_tok, int k, int H, int64_t cap,
+                                                      T* y, int32_t* __restrict__ status) {
+  // y may be the residual's buffer: each 16 bytes are read and then written by one thread
+  chain_wait();
+  constexpr int VN = VecTraits<T>::N;
+  constexpr int L = kCombineLoads;
+  __shared__ int2 s_item[TOK * LRM_MAX_TOPK];  // (token within the CTA, row), routed pairs in order
+  __shared__ float s_w[TOK * LRM_MAX_TOPK];
+  __shared__ int s_n;
+  const int64_t t0 = (int64_t)blockIdx.x * TOK;
+  const int ntok = (int)min((int64_t)TOK, n_tok - t0);
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int base = 0;
+    for (int q0 = 0; q0 < ntok * k; q0 += 32) {
+      const int q = q0 + lane;
+      const int r = q < ntok * k ? (int)checked_row(row_of_pair[t0 * k + q], cap, status) : -1;
+      const unsigned m = __ballot_sync(0xffffffffu, r >= 0);
+      if (r >= 0) {
+        const int at = base + __popc(m & ((1u << lane) - 1u));
+        s_item[at] = make_int2(q / k, r);
+        s_w[at] = alpha[t0 * k + q];
+      }
+      base += __popc(m);
+    }
+    if (lane == 0) s_n = base;
+  }
+  __syncthreads();
+  const int n = s_n, nv = H / VN;
+  for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < nv; v += gridDim.y * blockDim.x) {
+    float acc[VN];
+#pragma unroll
+    for (int q = 0; q < VN; ++q) acc[q] = 0.f;
+    int cur = 0;  // the token acc belongs to; tokens before it are written
+    auto flush = [&]() {
+      const int64_t at = (t0 + cur) * H + (int64_t)v * VN;
+      if (residual != nullptr) {
+        float f[VN];
+        unpack(*reinterpret_cast<const uint4*>(residual + at), f);
+#pragma unroll
+        for (int q = 0; q < VN; ++q) acc[q] += f[q];
+      }
+      st16(y + at, pack(acc));
+#pragma unroll
+      for (int q = 0; q < VN; ++q) acc[q] = 0.f;
+      ++cur;
+    };
+    for (int b0 = 0; b0 < n; b0 += L) {
+      uint4 vals[L];
+#pragma unroll
+      for (int m = 0; m < L; ++m)
+        if (b0 + m < n) vals[m] = ld_stream16(y_s + (int64_t)s_item[b0 + m].y * H + (int64_t)v * VN);
+#pragma unroll
+      for (int m = 0; m < L; ++m) {
+        if (b0 + m >= n) break;
+        const int tok = s_item[b0 + m].x;
+        const float w = s_w[b0 + m];
+        while (cur < tok) flush();
+        float f[VN];
+        unpack(vals[m], f);
+#pragma unroll
+        for (int q = 0; q < VN; ++q) acc[q] = fmaf(w, f[q], acc[q]);
+      }
+    }
+    while (cur < ntok) flush();
+  }
+}
+
+// One CTA per token: dy_t is read once; every routed pair's y_s row is read for its dot product with
+// dy_t and its dy_s row written, KB pairs at a time (their loads in flight together).
+template <typename T, int KB>
+__global__ void __launch_bounds__(256) combine_backward_kernel(const int32_t* __restrict__ row_of_pair,
+                                                               const float* __restrict__ alpha,
+                                                               const T* __restrict__ dy, const T* __restrict__ y_s,
+                                                               int k, int H, int64_t cap, T* __restrict__ dy_s,
+                                                               float* __restrict__ dalpha,
+                                                               int32_t* __restrict__ status) {
+  chain_wait();
+  constexpr int VN = VecTraits<T>::N;
+  __shared__ int64_t s_row[LRM_MAX_TOPK];
+  __shared__ float s_w[LRM_MAX_TOPK];
+  __shared__ float s_dot[8][LRM_MAX_TOPK];
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  if (threadIdx.x < k) {
+    s_row[threadIdx.x] = checked_row(row_of_pair[t * k + threadIdx.x], cap, status);
+    s_w[threadIdx.x] = alpha[t * k + threadIdx.x];
+  }
+  __syncthreads();
+  const int nv = H / VN;
+  for (int j0 = 0; j0 < k; j0 += KB) {
+    float dot[KB];
+#pragma unroll
+    for (int j = 0; j < KB; ++j) dot[j] = 0.f;
+    for (int v = threadIdx.x; v < nv; v += blockDim.x) {
+      const uint4 d4 = ldg16(dy + t * H + (int64_t)v * VN);
+      uint4 rows[KB];
+      if (y_s != nullptr)
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+          if (j0 + j < k && s_row[j0 + j] >= 0) rows[j] = ld_stream16(y_s + s_row[j0 + j] * H + (int64_t)v * VN);
+      float d[VN];
+      unpack(d4, d);
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        if (j0 + j >= k || s_row[j0 + j] < 0) continue;
+        float f[VN];
+        if (y_s != nullptr) {
+          unpack(rows[j], f);
+#pragma unroll
+          for (int q = 0; q < VN; ++q) dot[j] = fmaf(d[q], f[q], dot[j]);
+        }
+#pragma unroll
+        for (int q = 0; q < VN; ++q) f[q] = s_w[j0 + j] * d[q];
+        st16(dy_s + s_row[j0 + j] * H + (int64_t)v * VN, pack(f));
+      }
+    }
+    if (dalpha != nullptr)
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        dot[j] = warp_sum(dot[j]);
+        if (lane == 0 && j0 + j < k) s_dot[warp][j0 + j] = dot[j];
+      }
+  }
+  if (dalpha == nullptr) return;
+  __syncthreads();
+  if (threadIdx.x < k) {
+    float s = 0.f;
+    for (int w = 0; w < nw; ++w) s += s_dot[w][threadIdx.x];
+    dalpha[t * k + threadIdx.x] = s_row[threadIdx.x] >= 0 ? s : 0.f;
+  }
+}
+
+template <typename T>
+lrm_status sort_all(const SortArgs& a, cudaStream_t s) {
+  const int64_t P = a.T * a.k;
+  const int B = a.E + 1;
+  if (P <= kSmallPairs && a.E <= kSmallExperts) {
+    // a warp for every 64 pairs, at least as many threads as a row has 16-byte columns (up to 256)
+    int threads = (int)((P + 63) / 64) * 32;
+    const int cols = (a.H / VecTraits<T>::N + 31) / 32 * 32;
+    threads = threads < cols ? (cols < 256 ? cols : 256) : threads;
+    threads = threads < 32 ? 32 : threads;
+    const int nw = threads / 32;
+    const size_t smem = sizeof(int) * ((size_t)(nw + 1) * B + (size_t)P + 33);
+    const int64_t blocks = a.x_s != nullptr && a.T > 0 ? a.T : 1;
+    launch_chained(sort_small_kernel<T>, dim3((unsigned)(blocks < 608 ? blocks : 608)), dim3(threads), smem, s,
+                   a.topk_idx, (const T*)a.x, (int)a.T, a.k, a.E, a.H, a.seg_offsets, a.pair_of_row, a.row_of_pair,
+                   (T*)a.x_s, a.status);
+  } else {
+    const int chunk_tok = sort_chunk_tokens(a.k);
+    const int64_t nc = a.T > 0 ? (a.T + chunk_tok - 1) / chunk_tok : 1;
+    launch_chained(sort_count_kernel, dim3((unsigned)nc), dim3(kChunkThreads), sizeof(int) * B, s, a.topk_idx, P, a.E,
+                   chunk_tok * a.k, a.counts, a.status);
+    launch_chained(sort_colscan_kernel, dim3(B), dim3(nc > 256 ? 1024 : 256), 0, s, a.counts, nc, B, a.loads);
+    const size_t smem = sizeof(int) * ((size_t)B * (1 + kChunkThreads / 32) + kChunkThreads);
+    launch_chained(sort_rows_kernel<T>, dim3((unsigned)nc), dim3(kChunkThreads), smem, s, a.topk_idx, (const T*)a.x,
+                   a.T, a.k, a.E, a.H, chunk_tok, (const int32_t*)a.counts, (const int32_t*)a.loads, a.seg_offsets,
+                   a.pair_of_row, a.row_of_pair, (T*)a.x_s);
+  }
+  return cudaGetLastError() == cudaSuccess ? LRM_OK : LRM_ERR_CUDA;
+}
+
+template <typename T>
+void combine_all(const int32_t* row_of_pair, const float* alpha, const void* y_s, const void* residual, int64_t n_tok,
+                 int32_t k, int32_t H, int64_t cap, void* y, int32_t* status, cudaStream_t s) {
+  const int nv = H / VecTraits<T>::N;
+  // few tokens: one token and 64 columns per CTA, so that the rows spread over the GPU
+  if (n_tok < 2048) {
+    launch_chained(combine_kernel<T, 1>, dim3((unsigned)n_tok, (unsigned)((nv + 63) / 64)), dim3(64), 0, s,
+                   row_of_pair, alpha, (const T*)y_s, (const T*)residual, n_tok, k, H, cap, (T*)y, status);
+    return;
+  }
+  int threads = (nv + 31) / 32 * 32;
+  if (threads > 256) threads = 256;
+  launch_chained(combine_kernel<T, 8>, dim3((unsigned)((n_tok + 7) / 8)), dim3(threads), 0, s, row_of_pair, alpha,
+                 (const T*)y_s, (const T*)residual, n_tok, k, H, cap, (T*)y, status);
+}
+
+template <typename T>
+void combine_backward_all(const int32_t* row_of_pair, const float* alpha, const void* dy, const void* y_s, int64_t n_tok,
+                          int32_t k, int32_t H, int64_t cap, void* dy_s, float* dalpha, int32_t* status,
+                          cudaStream_t s) {
+  int threads = (H / VecTraits<T>::N + 31) / 32 * 32;
+  if (threads > 256) threads = 256;
+  launch_chained(combine_backward_kernel<T, 8>, dim3((unsigned)n_tok), dim3(threads), 0, s, row_of_pair, alpha,
+                 (const T*)dy, (const T*)y_s, k, H, cap, (T*)dy_s, dalpha, status);
+}
+
+}  // namespace
+
+int sort_chunk_tokens(int32_t k) { return kChunkThreads / k; }
+
+lrm_status launch_sort_tokens(const SortArgs& a, lrm_dtype dt, cudaStream_t s) {
+  return dt == LRM_BF16 ? sort_all<__nv_bfloat16>(a, s) : sort_all<float>(a, s);
+}
+
+void launch_combine(const int32_t* row_of_pair, const float* alpha, const void* y_s, const void* residual, int64_t T,
+                    int32_t k, int32_t H, lrm_dtype dt, int64_t cap, void* y, int32_t* status, cudaStream_t s) {
+  if (dt == LRM_BF16)
+    combine_all<__nv_bfloat16>(row_of_pair, alpha, y_s, residual, T, k, H, cap, y, status, s);
+  else
+    combine_all<float>(row_of_pair, alpha, y_s, residual, T, k, H, cap, y, status, s);
+}
+
+void launch_combine_backward(const int32_t* row_of_pair, const float* alpha, const void* dy, const void* y_s, int64_t T,
+                             int32_t k, int32_t H, lrm_dtype dt, int64_t cap, void* dy_s, float* dalpha,
+                             int32_t* status, cudaStream_t s) {
+  if (dt == LRM_BF16)
+    combine_backward_all<__nv_bfloat16>(row_of_pair, alpha, dy, y_s, T, k, H, cap, dy_s, dalpha, status, s);
+  else
+    combine_backward_all<float>(row_of_pair, alpha, dy, y_s, T, k, H, cap, dy_s, dalpha, status, s);
+}
+
+}  // namespace lrm
