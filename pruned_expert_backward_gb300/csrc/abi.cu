@@ -49,8 +49,15 @@ SortWs sort_layout(int64_t T, int32_t k, int32_t E) {
 }
 
 // Scratch of the products and of the bias gradient (NP: rows of w, columns of dz).
-size_t linear_ws_bytes(int64_t, int32_t, int32_t, int32_t, lrm_dtype) { return 256; }
-size_t linear_grad_ws_bytes(int64_t, int32_t, int32_t, int32_t, lrm_dtype) { return 256; }
+size_t linear_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
+  if (dt != LRM_F32) return kAlign;
+  return up(linear_planes_bytes(R, K)) + up(linear_planes_bytes((int64_t)E * NP, K));
+}
+size_t linear_grad_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
+  if (dt != LRM_F32) return kAlign + linear_plan_bytes(E);  // kAlign: the maps start on a 128-byte boundary
+  return kAlign + linear_plan_bytes(E) + up(linear_planes_bytes(R, NP)) + up(linear_planes_bytes(R, K)) +
+         up(linear_planes_bytes((int64_t)E * NP, K));
+}
 size_t act_grad_ws_bytes(int64_t R, int32_t E, int32_t NP) {
   return up(sizeof(float) * act_backward_part_rows(R, E) * NP);
 }
@@ -489,6 +496,7 @@ lrm_status lrm_linear(const int32_t* seg_offsets, const void* x, const void* w, 
   if (!ws || ws_bytes < linear_ws_bytes(R, E, NP, K, dt)) return LRM_ERR_WORKSPACE;
   if (R == 0) return LRM_OK;
   const LinearArgs a{seg_offsets, x, w, bias, residual, R, E, N, K, act, y, z, dev_status};
+  if (flags == LRM_GEMM_DEFAULT) return launch_linear_tc(a, dt, out_dt, ws, stream);
   launch_linear_simt(a, dt, out_dt, stream);
   return after_launch();
 }
@@ -530,6 +538,7 @@ lrm_status lrm_linear_backward(const int32_t* seg_offsets, const void* dz, const
     return LRM_OK;
   }
   const LinearGradArgs a{seg_offsets, dz, x, w, R, E, N, K, dx, dw, dev_status};
+  if (flags == LRM_GEMM_DEFAULT) return launch_linear_backward_tc(a, dt, ws, stream);
   launch_linear_backward_simt(a, dt, stream);
   return after_launch();
 }

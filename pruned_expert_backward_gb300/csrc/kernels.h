@@ -144,6 +144,9 @@ struct LinearArgs {
   int32_t* status;
 };
 void launch_linear_simt(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, cudaStream_t s);
+lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, void* ws, cudaStream_t s);
+size_t linear_planes_bytes(int64_t rows, int64_t cols);  // an fp32 operand as three bf16 planes
+size_t linear_plan_bytes(int32_t E);                     // plan and expert maps of the weights' gradient
 struct LinearGradArgs {
   const int32_t* seg_offsets;
   const void *dz, *x, *w;
@@ -154,6 +157,7 @@ struct LinearGradArgs {
   int32_t* status;
 };
 void launch_linear_backward_simt(const LinearGradArgs& a, lrm_dtype dt, cudaStream_t s);
+lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void* ws, cudaStream_t s);
 struct ActGradArgs {
   const int32_t* seg_offsets;
   const void *dy, *z;

@@ -1,0 +1,790 @@
+// lrm_linear and lrm_linear_backward on the tensor cores of sm_103a (tcgen05, TMEM, TMA).
+//
+//   FWD  y  = act(x W[e]^T + b[e]) + residual   (M = the segment's rows, N columns, K = hidden)
+//   DX   dx = dz W[e]                           (M = the segment's rows, N = hidden, K = columns of dz)
+//   DW   dW[e] = dz^T x                         (M = columns of dz, N = hidden, K = the segment's rows)
+//
+// CTAs run in pairs (a cluster of two) over a persistent grid; a pair computes a 256 x BN tile with
+// tcgen05.mma.cta_group::2: each CTA stages its own 128 rows of A and half of the BN columns of B per
+// 64-deep K slice and holds 128 rows of the fp32 accumulator in TMEM, twice, so that one tile's
+// epilogue runs under the next tile's products.  Warp 0 issues the TMA loads, warp 1 of the leader the
+// MMAs, warps 2-9 are the epilogue: two per 32-row TMEM quarter, each taking half of the columns.
+// A SwiGLU tile's columns are BN / 2 gate columns (the leader's half of B) and the BN / 2 up columns
+// that go with them (the other CTA's).
+//
+// Rows of a segment's last tile that belong to the next expert are computed and not stored: full
+// 32-row blocks leave by TMA from a ring of swizzled 2 KB boxes, partial ones by per-lane stores.  The
+// row-tile prefix of the segments is formed by every CTA for itself in shared memory (E <= 1024 sums,
+// below a microsecond), so FWD and DX are one launch without scratch.  DW reduces over rows, which
+// must not run into the next segment: its operands come through per-expert tensor maps whose row
+// extent ends at the segment's end (a small launch before it writes them), so TMA fills with zeros.
+//
+// fp32 accumulation.  The tensor core adds into its fp32 accumulator by truncation: against 64 bits a
+// sum of 2048 products is 2e-6 off (5.6e-6 when all have one sign), one of 32768 3.8e-5 (1.8e-4).
+// That is far below one bf16 rounding, so bf16 results are taken as they are.  For fp32 results
+// (PROMOTE) the accumulator is moved out of TMEM every `pk` K slices and added up in registers,
+// rounding to nearest.
+//
+// fp32 inputs are split into three bf16 planes, x = x0 + x1 + x2 (24 bits), and the six products of
+// weight 2^-16 and more are summed, the smallest first: x2 w0, x0 w2, x1 w1, x1 w0, x0 w1, x0 w0.  Only
+// the producer knows: it walks the K range once per term with the planes as the outer coordinate of
+// the operand maps.  What is left out is below 2^-24 of |x||w|.
+#include "kernels.h"
+#include "linear.cuh"
+#include "tc_host.h"
+#include "tc_ptx.cuh"
+
+namespace lrm {
+
+namespace {
+
+constexpr int kBM = 128;  // rows per CTA; a pair tile has 256
+constexpr int kBK = 64;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kABytes = kBM * kBK * 2;
+constexpr int kBoxBytes = 2048;  // 32 rows x 64 bytes, 64-byte swizzle: 32 bf16 or 16 fp32 columns
+constexpr int kBoxes = 3;        // boxes of an epilogue warp, used in turn
+
+enum Kind { FWD = 0, DX = 1, DW = 2 };
+
+template <int BN>
+struct Cfg {
+  static constexpr int kBBytes = BN / 2 * kBK * 2;  // this CTA's half of the columns
+  static constexpr int kStage = kABytes + kBBytes;
+  static constexpr int kStages = BN == 256 ? 5 : (BN == 128 ? 6 : 8);
+  static constexpr uint32_t kEpi = kStages * kStage;
+  static constexpr uint32_t kBars = kEpi + kEpiWarps * kBoxes * kBoxBytes;
+  static constexpr int kNBars = 2 * kStages + 5;  // full, empty, accumulator full[2] and empty[2], drain
+  static constexpr int kTmem = BN == 64 ? 128 : 2 * BN;
+  static constexpr size_t smem() { return 1024 + kBars + kNBars * 8 + 16 + 4 * (LRM_MAX_EXPERTS + 2) + 4 * 16; }
+};
+static_assert(Cfg<256>::smem() <= 232448 && Cfg<128>::smem() <= 232448 && Cfg<64>::smem() <= 232448, "shared memory");
+
+struct Params {
+  int E;
+  int64_t R;
+  int N;          // columns of the output (FWD: of y)
+  int M;          // DW: rows of dW[e]
+  int red;        // FWD, DX: length of the reduction
+  int tiles_n;
+  int tiles_m;    // DW: pair tiles along M
+  int terms;      // 1, or 6 for fp32 inputs in three planes
+  int pk;         // K slices per accumulator (PROMOTE)
+  const int32_t* seg;       // NULL: one dense problem
+  const int32_t* plan;      // DW with segments: [0] 1 if they are valid, [1 ..] experts, longest first
+  const CUtensorMap* maps;  // DW with segments: [2][E] operand maps cut at the segment's end
+  int act;
+  const void *bias, *residual;
+  void *y, *z;
+  int32_t* status;
+};
+
+// Term i of the split product: which plane of A and of B (the smallest products first).
+__device__ __forceinline__ int plane_a(int term) { return (0x001102 >> (4 * term)) & 15; }
+__device__ __forceinline__ int plane_b(int term) { return (0x010120 >> (4 * term)) & 15; }
+
+template <int BN>
+__host__ __device__ constexpr uint32_t instr_desc(uint32_t a_mn, uint32_t b_mn) {  // D fp32, A and B bf16, M = 256
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn << 15) | (b_mn << 16) | ((uint32_t)(BN >> 3) << 17) |
+         ((uint32_t)((2 * kBM) >> 4) << 24);
+}
+
+__device__ __forceinline__ void bulk_wait_read_boxes() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBoxes - 1) : "memory");
+}
+
+struct Tile {
+  int e;
+  int row0, row_end;  // FWD, DX: this CTA's output rows; DW: the rows summed over
+  int m0, n0;         // DW: this CTA's first output row; n0: first output column
+  int slices;         // K slices of one term
+  bool has_rows;
+};
+
+template <int KIND, int BN, bool GLU>
+__device__ __forceinline__ Tile decode(const Params& p, const int* prefix, int t, int rank) {
+  Tile d;
+  const int mg = t / p.tiles_n, nt = t - mg * p.tiles_n;
+  d.n0 = nt * (GLU ? BN / 2 : BN);
+  if (KIND == DW) {
+    const int ei = mg / p.tiles_m;
+    d.e = p.seg != nullptr ? __ldg(p.plan + 1 + ei) : 0;
+    d.m0 = (2 * (mg - ei * p.tiles_m) + rank) * kBM;
+    d.row0 = p.seg != nullptr ? __ldg(p.seg + d.e) : 0;
+    d.row_end = p.seg != nullptr ? __ldg(p.seg + d.e + 1) : (int)p.R;
+    d.slices = (d.row_end - d.row0 + kBK - 1) / kBK;
+    d.has_rows = d.m0 < p.M;
+    return d;
+  }
+  d.m0 = 0;
+  d.e = 0;
+  int end = (int)p.R;
+  if (p.seg != nullptr) {
+    int lo = 0, hi = p.E;  // the last e with prefix[e] <= mg
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= mg) lo = mid; else hi = mid;
+    }
+    d.e = lo;
+    end = __ldg(p.seg + lo + 1);
+    d.row0 = __ldg(p.seg + lo) + (mg - prefix[lo]) * (2 * kBM) + rank * kBM;
+  } else {
+    d.row0 = mg * (2 * kBM) + rank * kBM;
+  }
+  d.row_end = min(end, d.row0 + kBM);
+  d.slices = (p.red + kBK - 1) / kBK;
+  d.has_rows = d.row0 < end;
+  return d;
+}
+
+// 32 columns of one row per lane go out: whole 32-row blocks through the warp's next box(es) and TMA
+// (which clips columns past the tensor), others by each live lane.
+struct Out {
+  uint8_t* boxes;
+  uint32_t boxes_s;
+  int next;
+  __device__ __forceinline__ void box(const uint4 (&q)[4], const CUtensorMap* map, int lane, int n, int row, int e) {
+    if (lane == 0) bulk_wait_read_boxes();  // the store that used this box has read it
+    __syncwarp();
+    uint8_t* line = boxes + next * kBoxBytes + lane * 64;
+    const int swz = (lane >> 1) & 3;  // 64-byte swizzle: piece j of row r sits at j ^ ((r >> 1) & 3)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(line + ((j ^ swz) << 4)) = q[j];
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) tma_store_3d(map, boxes_s + next * kBoxBytes, n, row, e);
+    next = next + 1 == kBoxes ? 0 : next + 1;
+  }
+  template <typename T>
+  __device__ __forceinline__ void put(const float (&v)[32], const CUtensorMap* map, int lane, int n, int cols, int row,
+                                      int e, bool whole, bool live, T* row_ptr) {
+    constexpr int VN = VecTraits<T>::N;
+    constexpr int PC = 4 * VN;  // columns of a box
+#pragma unroll
+    for (int h = 0; h < 32 / PC; ++h) {
+      uint4 q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float f[VN];
+#pragma unroll
+        for (int i = 0; i < VN; ++i) f[i] = v[h * PC + j * VN + i];
+        q[j] = pack(f);
+      }
+      const int c0 = n + h * PC;
+      if (whole) {
+        if (c0 < cols) box(q, map, lane, c0, row, e);  // warp-uniform
+      } else if (live) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c0 + j * VN < cols) st16(row_ptr + c0 + j * VN, q[j]);
+      }
+    }
+  }
+};
+
+// v += 32 values of a row of T at column n (columns past `cols` are left alone).
+template <typename T>
+__device__ __forceinline__ void add_row(float (&v)[32], const T* row, int n, int cols) {
+  constexpr int VN = VecTraits<T>::N;
+#pragma unroll
+  for (int j = 0; j < 32 / VN; ++j)
+    if (n + j * VN < cols) {
+      float f[VN];
+      unpack(*reinterpret_cast<const uint4*>(row + n + j * VN), f);
+#pragma unroll
+      for (int i = 0; i < VN; ++i) v[j * VN + i] += f[i];
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ void act32(float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = act_value<ACT>(v[i]);
+}
+
+template <int KIND, int BN, bool GLU, bool PROMOTE, typename TI, typename TO>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ, const Params p) {
+  using C = Cfg<BN>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::kNBars);
+  int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
+  int* prefix = abort_flag + 3;                   // [E + 1] row tiles before each expert
+  int* scan = prefix + LRM_MAX_EXPERTS + 2;       // [kThreads / 32]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + S);
+  const uint32_t accf0 = smem_u32(bars + 2 * S), acce0 = smem_u32(bars + 2 * S + 2);
+  const uint32_t drain = smem_u32(bars + 2 * S + 4);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full0 + 8 * s, 2);   // leader's: both producers arrive with their byte counts
+      mbar_init(empty0 + 8 * s, 1);  // the leader's commit, multicast to the pair
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(accf0 + 8 * i, 1);
+      mbar_init(acce0 + 8 * i, 2 * kEpiWarps);  // leader's: the epilogue warps of both CTAs
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_holder), C::kTmem);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist before any remote operation targets them
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  chain_wait();  // the set-up above touches no global memory
+
+  int n_tiles;
+  if (KIND == DW) {
+    n_tiles = p.seg == nullptr || __ldg(p.plan) == 1 ? p.E * p.tiles_m * p.tiles_n : 0;
+  } else if (p.seg == nullptr) {
+    n_tiles = (int)((p.R + 2 * kBM - 1) / (2 * kBM)) * p.tiles_n;
+  } else {
+    // each thread sums a run of experts; a scan over the threads gives the prefix
+    const int per = (p.E + kThreads - 1) / kThreads, e0 = threadIdx.x * per, e1 = min(p.E, e0 + per);
+    int sum = 0, ok = 1;
+    for (int e = e0; e < e1; ++e) {
+      const int a = __ldg(p.seg + e), b = __ldg(p.seg + e + 1);
+      ok &= a <= b ? 1 : 0;
+      sum += (b - a + 2 * kBM - 1) / (2 * kBM);
+    }
+    if (threadIdx.x == 0) ok &= __ldg(p.seg) == 0 && (int64_t)__ldg(p.seg + p.E) <= p.R ? 1 : 0;
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) scan[warp] = incl;
+    const bool valid = __syncthreads_and(ok) != 0;
+    int run = incl - sum;
+    for (int w = 0; w < warp; ++w) run += scan[w];
+    for (int e = e0; e < e1; ++e) {
+      prefix[e] = run;
+      run += (__ldg(p.seg + e + 1) - __ldg(p.seg + e) + 2 * kBM - 1) / (2 * kBM);
+    }
+    if (e0 < p.E && e1 == p.E) prefix[p.E] = run;
+    __syncthreads();
+    n_tiles = valid ? prefix[p.E] * p.tiles_n : 0;
+    if (!valid && threadIdx.x == 0) set_status(p.status, LRM_ERR_BAD_SEGMENTS);
+  }
+
+  volatile int* abortv = abort_flag;
+  const uint32_t full_lead = cluster_addr(full0, 0), acce_lead = cluster_addr(acce0, 0);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer ----
+    if (lane == 0) {
+      uint32_t it = 0, st = 0, sph = 0;
+      bool ok = true;
+      int last_e = -1;
+      for (int t = pair; t < n_tiles && ok; t += n_pairs) {
+        const Tile d = decode<KIND, BN, GLU>(p, prefix, t, rank);
+        const CUtensorMap *ma = &tmA, *mb = &tmB;
+        if (KIND == DW && p.seg != nullptr) {
+          ma = p.maps + d.e;
+          mb = p.maps + p.E + d.e;
+          if (d.e != last_e && d.slices > 0) {
+            tensormap_acquire(ma);
+            tensormap_acquire(mb);
+            last_e = d.e;
+          }
+        }
+        // first B row (FWD: rows of w, a SwiGLU pair stages gate rows and up rows) or column of this CTA
+        const int nb = GLU ? d.n0 + rank * p.N : d.n0 + rank * (BN / 2);
+        const uint32_t bytes = C::kBBytes + (d.has_rows ? kABytes : 0);
+        const int planes = p.terms > 1 ? 3 : 1;
+        for (int term = 6 - p.terms; term < 6 && ok; ++term) {
+          const int pa = plane_a(term), pb = plane_b(term);
+          for (int kb = 0; kb < d.slices; ++kb, ++it) {
+            const uint32_t s = st, ph = sph;
+            if (++st == (uint32_t)S) { st = 0; sph ^= 1u; }
+            if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abortv, p.status)) { ok = false; break; }
+            const uint32_t a_dst = smem_u32(smem + s * C::kStage), b_dst = a_dst + kABytes;
+            const uint32_t fb = full_lead + 8 * s;
+            const int k = kb * kBK;
+            mbar_expect_tx_cluster(fb, bytes);
+            if (KIND == DW) {
+              const int r = d.row0 + k;
+              if (d.has_rows) {
+                tma_load_3d_pair(a_dst, ma, d.m0, r, pa, fb);
+                tma_load_3d_pair(a_dst + 8192, ma, d.m0 + 64, r, pa, fb);
+              }
+#pragma unroll
+              for (int c = 0; c < BN / 128; ++c) tma_load_3d_pair(b_dst + c * 8192, mb, nb + c * 64, r, pb, fb);
+            } else {
+              if (d.has_rows) tma_load_3d_pair(a_dst, ma, k, d.row0, pa, fb);
+              const int eb = d.e * planes + pb;
+              if (KIND == FWD) {
+                tma_load_3d_pair(b_dst, mb, k, nb, eb, fb);
+              } else {
+#pragma unroll
+                for (int c = 0; c < BN / 128; ++c) tma_load_3d_pair(b_dst + c * 8192, mb, nb + c * 64, k, eb, fb);
+              }
+            }
+          }
+        }
+      }
+      // drain: every stage this thread filled has been consumed (so its data landed)
+      const uint32_t first = it > (uint32_t)S ? it - S : 0u;
+      for (uint32_t i = first; i < it; ++i) mbar_wait(empty0 + 8 * (i % S), (i / S) & 1u, abortv, p.status, false);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer ------
+    if (leader && lane == 0) {
+      constexpr uint32_t idesc = instr_desc<BN>(KIND == DW ? 1u : 0u, KIND == FWD ? 0u : 1u);
+      const uint32_t a0 = smem_u32(smem), b0 = a0 + kABytes;
+      const uint64_t adesc0 = KIND == DW ? smem_desc(a0, 8192, 1024) : smem_desc(a0, 16, 1024);
+      const uint64_t bdesc0 = KIND == FWD ? smem_desc(b0, 16, 1024) : smem_desc(b0, 8192, 1024);
+      constexpr uint64_t a_step = KIND == DW ? (2048 >> 4) : (32 >> 4);
+      constexpr uint64_t b_step = KIND == FWD ? (32 >> 4) : (2048 >> 4);
+      uint32_t st = 0, sph = 0, use = 0;  // operand stage and phase; accumulators used so far
+      bool ok = true;
+      for (int t = pair; t < n_tiles && ok; t += n_pairs) {
+        const Tile d = decode<KIND, BN, GLU>(p, prefix, t, 0);
+        const int total = d.slices * p.terms;
+        for (int k0 = 0; k0 < total && ok; k0 += PROMOTE ? p.pk : total, ++use) {
+          const int k1 = PROMOTE ? min(total, k0 + p.pk) : total;
+          const uint32_t acc = use & 1u;
+          if (!mbar_wait(acce0 + 8 * acc, ((use >> 1) & 1u) ^ 1u, abortv, p.status)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t tmem_d = tmem_base + acc * BN;
+          for (int kb = k0; kb < k1; ++kb) {
+            const uint32_t s = st, ph = sph;
+            if (++st == (uint32_t)S) { st = 0; sph ^= 1u; }
+            if (!mbar_wait(full0 + 8 * s, ph, abortv, p.status)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t soff = (uint64_t)((s * C::kStage) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              mma_bf16(tmem_d, adesc0 + soff + kk * a_step, bdesc0 + soff + kk * b_step, idesc,
+                       kb != k0 || kk != 0 ? 1u : 0u);
+            mma_commit_pair(empty0 + 8 * s);
+          }
+          if (ok) mma_commit_pair(accf0 + 8 * acc);
+        }
+      }
+      mma_commit_pair(drain);
+    }
+    __syncwarp();
+    mbar_wait(drain, 0, abortv, p.status, false);  // all MMAs into this CTA's TMEM are done before it is freed
+  } else {
+    // ---------------------------------------------------------------- epilogue --------
+    constexpr int NC = BN / 64;  // 32-column chunks of a warp (SwiGLU: the second half are up columns)
+    constexpr int NO = GLU ? NC / 2 : NC;
+    static_assert(NO > 0, "a SwiGLU tile needs BN >= 128");
+    const int ew = warp - 2, q = warp & 3, half = ew >> 2;
+    Out out{smem + C::kEpi + ew * kBoxes * kBoxBytes, smem_u32(smem + C::kEpi + ew * kBoxes * kBoxBytes), 0};
+    const int NP = GLU ? 2 * p.N : p.N;
+    // TMEM column of chunk c
+    auto tcol = [&](int c) {
+      return GLU ? (c < NO ? half * (BN / 4) + c * 32 : BN / 2 + half * (BN / 4) + (c - NO) * 32)
+                 : half * (BN / 2) + c * 32;
+    };
+    uint32_t use = 0;
+    bool ok = true;
+    for (int t = pair; t < n_tiles && ok; t += n_pairs) {
+      const Tile d = decode<KIND, BN, GLU>(p, prefix, t, rank);
+      const int row_base = (KIND == DW ? d.m0 : d.row0) + q * 32;
+      const int row_lim = KIND == DW ? p.M : d.row_end;
+      const int nrows = d.has_rows ? min(32, row_lim - row_base) : 0;
+      // without segments the output map ends where the rows end, so TMA clips a partial block
+      const bool whole = nrows == 32 || (nrows > 0 && (KIND == DW || p.seg == nullptr));
+      const bool live = lane < nrows;
+      const int64_t row = row_base + lane;
+      const int n_first = d.n0 + half * (GLU ? BN / 4 : BN / 2);
+      const int total = d.slices * p.terms;
+      const TO* res = KIND == FWD && p.residual != nullptr && live ? static_cast<const TO*>(p.residual) + row * p.N : nullptr;
+      TO* y_row = static_cast<TO*>(p.y) + (KIND == DW ? ((int64_t)d.e * p.M + row) : row) * p.N;
+
+      // one chunk of 32 output columns: v holds the products (and u, for SwiGLU, the up columns')
+      auto finish = [&](int c, float (&v)[32], float (&u)[32]) {
+        const int n = n_first + c * 32;
+        if (nrows <= 0 || n >= p.N) return;  // warp-uniform
+        if (KIND == FWD) {
+          if (p.bias != nullptr) {
+            const TI* b = static_cast<const TI*>(p.bias) + (int64_t)d.e * NP;
+            add_row(v, b, n, p.N);
+            if (GLU) add_row(u, b + p.N, n, p.N);
+          }
+          if (p.z != nullptr) {
+            TI* z_row = static_cast<TI*>(p.z) + row * NP;
+            // (a bf16 z beside an fp32 y has no map of its own)
+            const bool z_whole = whole && sizeof(TI) == sizeof(TO);
+            const bool z_live = live || (whole && row < d.row_end);
+            out.put(v, &tmZ, lane, n, p.N, row_base, 0, z_whole, z_live, z_row);
+            if (GLU) out.put(u, &tmZ, lane, n, p.N, row_base, 1, z_whole, z_live, z_row + p.N);
+          }
+          if (GLU) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = act_value<LRM_ACT_SWIGLU>(v[i]) * u[i];
+          } else {
+            switch (p.act) {
+              case LRM_ACT_RELU: act32<LRM_ACT_RELU>(v); break;
+              case LRM_ACT_GELU: act32<LRM_ACT_GELU>(v); break;
+              case LRM_ACT_SILU: act32<LRM_ACT_SILU>(v); break;
+              default: break;
+            }
+          }
+          if (res != nullptr) add_row(v, res, n, p.N);
+        }
+        out.put(v, &tmY, lane, n, p.N, row_base, KIND == DW ? d.e : 0, whole, live, y_row);
+      };
+
+      if (PROMOTE) {
+        float acc[NC][32];
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[c][i] = 0.f;
+        for (int k0 = 0; k0 < total; k0 += p.pk, ++use) {
+          const uint32_t a = use & 1u;
+          if (!mbar_wait(accf0 + 8 * a, (use >> 1) & 1u, abortv, p.status)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t tbase = tmem_base + a * BN + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            uint32_t r[32];
+            tmem_ld32(tbase + tcol(c), r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[c][i] += __uint_as_float(r[i]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(acce_lead + 8 * a);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < NO; ++c) finish(c, acc[c], acc[GLU ? NO + c : c]);
+      } else {
+        const uint32_t a = use & 1u;
+        if (!mbar_wait(accf0 + 8 * a, (use >> 1) & 1u, abortv, p.status)) { ok = false; break; }
+        ++use;
+        tc_fence_after();
+        const uint32_t tbase = tmem_base + a * BN + ((uint32_t)(q * 32) << 16);
+        for (int c = 0; c < NO; ++c) {
+          uint32_t r[32], w[32];
+          tmem_ld32(tbase + tcol(c), r);
+          if (GLU) tmem_ld32(tbase + tcol(NO + c), w);
+          float v[32], u[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            v[i] = __uint_as_float(r[i]);
+            u[i] = GLU ? __uint_as_float(w[i]) : 0.f;
+          }
+          finish(c, v, u);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acce_lead + 8 * a);
+      }
+    }
+    if (lane == 0) bulk_wait_all();  // stores complete before the CTA exits
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no remote arrive may target a CTA that has exited
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::kTmem);
+  }
+}
+
+// DW with segments: plan[0] = 1 if they are valid, plan[1 ..] the experts by row count, longest first
+// (ties by id), and the operand maps of every expert, the templates with their row extent (dimension
+// 1) cut at the segment's end.
+struct MapPair {
+  CUtensorMap t[2];
+};
+__global__ void __launch_bounds__(1024) linear_plan_kernel(const int32_t* __restrict__ seg, int E, int64_t R,
+                                                           int32_t* __restrict__ plan, CUtensorMap* __restrict__ maps,
+                                                           const __grid_constant__ MapPair tpl,
+                                                           int32_t* __restrict__ status) {
+  chain_wait();
+  __shared__ int s_rows[LRM_MAX_EXPERTS];
+  const bool valid = rows_valid(seg, E, R, status);
+  if (threadIdx.x == 0) plan[0] = valid ? 1 : 0;
+  const int e = threadIdx.x;
+  const int rows = e < E && valid ? seg[e + 1] - seg[e] : 0;
+  if (e < E) s_rows[e] = rows;
+  __syncthreads();
+  if (e < E) {
+    int before = 0;
+    for (int j = 0; j < E; ++j) before += s_rows[j] > rows || (s_rows[j] == rows && j < e);
+    plan[1 + before] = e;
+  }
+  for (int i = threadIdx.x; i < 2 * E; i += blockDim.x) {
+    const int j = i / E, ee = i - j * E;
+    const uint32_t end = valid ? (uint32_t)max(1, seg[ee + 1]) : 1u;
+    uint4* dst = reinterpret_cast<uint4*>(maps + i);
+    const uint4* src = reinterpret_cast<const uint4*>(&tpl.t[j]);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) dst[w] = src[w];
+    asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(
+                     reinterpret_cast<uint64_t>(maps + i)),
+                 "r"(end)
+                 : "memory");
+    asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
+  }
+}
+
+// x (fp32, [groups][n]) as three bf16 planes [groups][3][n] whose sum is x to 24 bits.
+__global__ void __launch_bounds__(256) split_planes_kernel(const float* __restrict__ x, int64_t groups, int64_t n,
+                                                           __nv_bfloat16* __restrict__ out) {
+  chain_wait();
+  const int64_t total = groups * n / 8;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t at = i * 8, g = at / n, c = at - g * n;
+    float a[4], b[4], v[8], p[3][8];
+    unpack(ld_stream16(x + at), a);
+    unpack(ld_stream16(x + at + 4), b);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[q] = a[q];
+      v[4 + q] = b[q];
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      p[0][q] = __bfloat162float(__float2bfloat16_rn(v[q]));
+      const float r1 = v[q] - p[0][q];  // exact
+      p[1][q] = __bfloat162float(__float2bfloat16_rn(r1));
+      p[2][q] = r1 - p[1][q];
+    }
+#pragma unroll
+    for (int j = 0; j < 3; ++j) st16(out + (g * 3 + j) * n + c, pack(p[j]));
+  }
+}
+
+// ---------------------------------------------------------------- host side ----------
+// [d2][d1][d0] of 2- or 4-byte elements, d0 contiguous (a multiple of 16 bytes), with a {b0, b1, 1} box.
+bool make_map(CUtensorMap* m, const void* base, bool f32, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
+              uint64_t stride2, uint32_t b0, uint32_t b1, bool operand) {
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {stride1, stride2};
+  const cuuint32_t box[3] = {b0, b1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode_fn()(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                     const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     operand ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     operand ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// A bf16 operand [planes][rows][cols].
+bool operand_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t planes, uint32_t box_rows) {
+  return make_map(m, base, false, cols, rows, planes, cols * 2, rows * cols * 2, 64, box_rows, true);
+}
+// An output [groups][rows][cols] in 32-row boxes of 64 bytes; halves: [rows][2][cols] seen as two groups.
+bool output_map(CUtensorMap* m, const void* base, bool f32, uint64_t cols, uint64_t rows, uint64_t groups,
+                bool halves = false) {
+  const uint64_t b = f32 ? 4 : 2, line = cols * b * (halves ? 2 : 1);
+  return make_map(m, base, f32, cols, rows, groups, line, halves ? cols * b : rows * line, f32 ? 16 : 32, 32, false);
+}
+
+template <int KIND, int BN, bool GLU, bool PROMOTE, typename TI, typename TO>
+lrm_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& y, const CUtensorMap& z,
+                  const Params& p, int64_t tiles_bound, cudaStream_t s) {
+  constexpr auto kernel = linear_tc_kernel<KIND, BN, GLU, PROMOTE, TI, TO>;
+  const size_t smem = Cfg<BN>::smem();
+  if (ensure_max_smem<kernel>((int)smem) != cudaSuccess) return LRM_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;  // the occupancy query sees the cluster shape only
+  static int resident[kDeviceSlots] = {};  // CTA pairs, per device
+  const int slot = current_device_slot();
+  int pairs = slot >= 0 ? resident[slot] : 0;
+  if (pairs == 0) {
+    cfg.gridDim = dim3(2 * (sm_count() / 2));
+    if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess || pairs <= 0) pairs = sm_count() / 2;
+    if (slot >= 0) resident[slot] = pairs;
+  }
+  cfg.numAttrs = 2;
+  cfg.gridDim = dim3((unsigned)(2 * (tiles_bound < pairs ? tiles_bound : pairs)));
+  if (cudaLaunchKernelEx(&cfg, kernel, a, b, y, z, p) != cudaSuccess) return LRM_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? LRM_OK : LRM_ERR_CUDA;
+}
+
+void split_planes(const void* x, int64_t groups, int64_t n, void* out, cudaStream_t s) {
+  const int64_t blocks = (groups * n / 8 + 255) / 256;
+  launch_chained(split_planes_kernel, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), dim3(256), 0, s, (const float*)x,
+                 groups, n, (__nv_bfloat16*)out);
+}
+
+// K slices per accumulator where the result is fp32: 256 products for split fp32 inputs (5e-7 off at
+// most per sum), 1024 for bf16 inputs (1e-6).
+constexpr int kSlicesF32 = 4, kSlicesBf16 = 16;
+
+int64_t row_tiles(const int32_t* seg, int64_t R, int E) {
+  return (R + 2 * kBM - 1) / (2 * kBM) + (seg != nullptr ? E : 0);
+}
+
+// Tile width: the widest whose tiles give every CTA pair one, else the next narrower (a 256 x 256 tile
+// moves the fewest operand bytes per product; below a tile per pair the idle SMs cost more).
+template <typename F>
+lrm_status with_width(int64_t tiles_m, int N, int least, F&& f) {
+  const int64_t pairs = sm_count() / 2;
+  if (tiles_m * ((N + 255) / 256) >= pairs) return f(IntTag<256>{});
+  if (least > 64 || tiles_m * ((N + 127) / 128) >= pairs) return f(IntTag<128>{});
+  return f(IntTag<64>{});
+}
+
+}  // namespace
+
+size_t linear_planes_bytes(int64_t rows, int64_t cols) { return (size_t)rows * cols * 6; }
+
+lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, void* ws, cudaStream_t s) {
+  if (!device_ok() || encode_fn() == nullptr) return LRM_ERR_UNSUPPORTED;
+  const bool f32 = dt == LRM_F32, glu = a.act == LRM_ACT_SWIGLU;
+  const int NP = glu ? 2 * a.N : a.N;
+  const void *xs = a.x, *wsrc = a.w;
+  if (f32) {
+    char* b = static_cast<char*>(ws);
+    split_planes(a.x, 1, a.R * a.K, b, s);
+    xs = b;
+    b += (linear_planes_bytes(a.R, a.K) + 255) / 256 * 256;
+    split_planes(a.w, a.E, (int64_t)NP * a.K, b, s);
+    wsrc = b;
+  }
+  Params p{};
+  p.E = a.E;
+  p.R = a.R;
+  p.N = a.N;
+  p.red = a.K;
+  p.terms = f32 ? 6 : 1;
+  p.pk = f32 ? kSlicesF32 : kSlicesBf16;
+  p.seg = a.seg_offsets;
+  p.act = a.act;
+  p.bias = a.bias;
+  p.residual = a.residual;
+  p.y = a.y;
+  p.z = a.z;
+  p.status = a.status;
+  const int planes = f32 ? 3 : 1;
+  const bool y32 = out_dt == LRM_F32;
+  CUtensorMap mA, mB, mY, mZ;
+  if (!operand_map(&mA, xs, a.K, a.R, planes, kBM) || !output_map(&mY, a.y, y32, a.N, a.R, 1)) return LRM_ERR_CUDA;
+  mZ = mY;
+  if (a.z != nullptr && y32 == f32 && !output_map(&mZ, a.z, f32, a.N, a.R, glu ? 2 : 1, glu)) return LRM_ERR_CUDA;
+  const int64_t tm = row_tiles(a.seg_offsets, a.R, a.E);
+  auto go = [&](auto bn, auto glu_tag) {
+    constexpr int BN = decltype(bn)::value;
+    constexpr bool GLU = decltype(glu_tag)::value != 0;
+    if constexpr (GLU && BN < 128) {
+      return LRM_ERR_UNSUPPORTED;
+    } else {
+      constexpr int cols = GLU ? BN / 2 : BN;
+      p.tiles_n = (a.N + cols - 1) / cols;
+      if (!operand_map(&mB, wsrc, a.K, NP, (uint64_t)a.E * planes, BN / 2)) return LRM_ERR_CUDA;
+      using B16 = __nv_bfloat16;
+      if (f32) return launch<FWD, BN, GLU, true, float, float>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
+      if (y32) return launch<FWD, BN, GLU, true, B16, float>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
+      return launch<FWD, BN, GLU, false, B16, B16>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
+    }
+  };
+  if (glu) return with_width(tm, NP, 128, [&](auto bn) { return go(bn, IntTag<1>{}); });
+  return with_width(tm, NP, 64, [&](auto bn) { return go(bn, IntTag<0>{}); });
+}
+
+lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void* ws, cudaStream_t s) {
+  if (!device_ok() || encode_fn() == nullptr) return LRM_ERR_UNSUPPORTED;
+  using B16 = __nv_bfloat16;
+  const bool f32 = dt == LRM_F32;
+  const int planes = f32 ? 3 : 1;
+  const void *dzs = a.dz, *xs = a.x, *wsrc = a.w;
+  // scratch: the expert maps of DW (128-byte aligned) and its plan, then the planes
+  char* b = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws) + 127) & ~uintptr_t(127));
+  CUtensorMap* maps = reinterpret_cast<CUtensorMap*>(b);
+  int32_t* plan = reinterpret_cast<int32_t*>(b + 2 * sizeof(CUtensorMap) * (size_t)a.E);
+  b += linear_plan_bytes(a.E);
+  auto split = [&](const void* src, int64_t groups, int64_t n) {
+    split_planes(src, groups, n, b, s);
+    const void* at = b;
+    b += ((size_t)groups * n * 6 + 255) / 256 * 256;
+    return at;
+  };
+  if (f32) {
+    dzs = split(a.dz, 1, a.R * a.N);
+    if (a.dx != nullptr) wsrc = split(a.w, a.E, (int64_t)a.N * a.K);
+    if (a.dw != nullptr) xs = split(a.x, 1, a.R * a.K);
+  }
+  Params p{};
+  p.E = a.E;
+  p.R = a.R;
+  p.N = a.K;
+  p.terms = f32 ? 6 : 1;
+  p.pk = f32 ? kSlicesF32 : kSlicesBf16;
+  p.seg = a.seg_offsets;
+  p.status = a.status;
+  CUtensorMap mA, mB, mY;
+  if (a.dw != nullptr) {
+    p.M = a.N;
+    p.y = a.dw;
+    p.tiles_m = (a.N + 2 * kBM - 1) / (2 * kBM);
+    if (!operand_map(&mA, dzs, a.N, a.R, planes, 64) || !operand_map(&mB, xs, a.K, a.R, planes, 64) ||
+        !output_map(&mY, a.dw, true, a.K, a.N, a.E))
+      return LRM_ERR_CUDA;
+    if (a.seg_offsets != nullptr) {
+      const MapPair tpl{{mA, mB}};
+      launch_chained(linear_plan_kernel, dim3(1), dim3(1024), 0, s, a.seg_offsets, a.E, a.R, plan, maps, tpl, a.status);
+      p.plan = plan;
+      p.maps = maps;
+    }
+    const int64_t tm = (int64_t)a.E * p.tiles_m;
+    const lrm_status st = with_width(tm, a.K, 128, [&](auto bn) {
+      constexpr int BN = decltype(bn)::value;
+      if constexpr (BN < 128) {
+        return LRM_ERR_UNSUPPORTED;
+      } else {
+        p.tiles_n = (a.K + BN - 1) / BN;
+        return launch<DW, BN, false, true, B16, float>(mA, mB, mY, mY, p, tm * p.tiles_n, s);
+      }
+    });
+    if (st) return st;
+  }
+  if (a.dx != nullptr) {
+    p.red = a.N;
+    p.y = a.dx;
+    if (!operand_map(&mA, dzs, a.N, a.R, planes, kBM) ||
+        !operand_map(&mB, wsrc, a.K, a.N, (uint64_t)a.E * planes, 64) || !output_map(&mY, a.dx, f32, a.K, a.R, 1))
+      return LRM_ERR_CUDA;
+    const int64_t tm = row_tiles(a.seg_offsets, a.R, a.E);
+    return with_width(tm, a.K, 128, [&](auto bn) {
+      constexpr int BN = decltype(bn)::value;
+      if constexpr (BN < 128) {
+        return LRM_ERR_UNSUPPORTED;
+      } else {
+        p.tiles_n = (a.K + BN - 1) / BN;
+        if (f32) return launch<DX, BN, false, true, float, float>(mA, mB, mY, mY, p, tm * p.tiles_n, s);
+        return launch<DX, BN, false, false, B16, B16>(mA, mB, mY, mY, p, tm * p.tiles_n, s);
+      }
+    });
+  }
+  return LRM_OK;
+}
+
+size_t linear_plan_bytes(int32_t E) {
+  return (2 * sizeof(CUtensorMap) * (size_t)E + sizeof(int32_t) * ((size_t)E + 1) + 255) / 256 * 256;  // behind `ws` aligned
+}
+
+}  // namespace lrm
