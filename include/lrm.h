@@ -344,13 +344,16 @@ lrm_status lrm_score_norms(const float* alpha, const void* g, const float* phi_s
  *                             May be NULL (then x may be, too): only the three index arrays.
  *   topk_idx [T*k] int32      expert ids; -1: the pair is not routed (padding, a masked token).  Any
  *                             other id outside [0, E) sets LRM_ERR_BAD_INDEX and counts as -1.
- *   ws: scratch of at least lrm_workspace_size bytes.
+ *   ws: scratch of at least lrm_sort_workspace_size bytes (lrm_workspace_size covers it); NULL where that is 0.
  * Deterministic.  Its gradient is lrm_scatter_dx with cap = T*k: dx[t] = sum_j dx_s[row_of_pair[t*k+j]].
  * Errors: LRM_ERR_INVALID_ARG, LRM_ERR_SHAPE, LRM_ERR_DTYPE, LRM_ERR_WORKSPACE, LRM_ERR_CUDA.
  */
 lrm_status lrm_sort_tokens(const int32_t* topk_idx, const void* x, int64_t T, int32_t k, int32_t E, int32_t H,
                            lrm_dtype dt, int32_t* seg_offsets, int32_t* pair_of_row, int32_t* row_of_pair, void* x_s,
                            void* ws, size_t ws_bytes, int32_t* dev_status, cudaStream_t stream);
+
+/* Bytes of scratch of lrm_sort_tokens (0 for few pairs: one launch does everything).  Host-only. */
+lrm_status lrm_sort_workspace_size(int64_t T, int32_t k, int32_t E, size_t* bytes);
 
 /*
  * Back to tokens with the routing weights:  y[t] = residual[t] + sum over j = 0..k-1, in that order,
@@ -400,8 +403,8 @@ lrm_status lrm_linear_workspace_size(int64_t R, int32_t E, int32_t N, int32_t K,
  * dt LRM_BF16 or LRM_F32; out_dt is the type of y: dt, or LRM_F32 from bf16 inputs (a router's logits;
  * no residual then).  Sums, bias, activation and residual are in fp32, each output is rounded once.
  * Rows >= seg_offsets[E] are not written.  N and K are multiples of 8, up to 2^24; R <= INT32_MAX.
- * ws: scratch of at least lrm_linear_workspace_size bytes.  flags: LRM_GEMM_DEFAULT or
- * LRM_GEMM_FORCE_SIMT (products on the CUDA cores).
+ * ws: scratch of at least lrm_linear_workspace_size bytes for fp32 inputs; not used (may be NULL) for bf16.
+ * flags: LRM_GEMM_DEFAULT or LRM_GEMM_FORCE_SIMT (products on the CUDA cores).
  */
 lrm_status lrm_linear(const int32_t* seg_offsets, const void* x, const void* w, const void* bias, const void* residual,
                       int64_t R, int32_t E, int32_t N, int32_t K, lrm_act act, lrm_dtype dt, lrm_dtype out_dt, void* y,

@@ -45,6 +45,7 @@ SIGNATURES = {
                                         _p]),
     "lrm_selftest_wait_timeout": (C.c_int, [_p, _i64, _p]),
     "lrm_sort_tokens": (C.c_int, [_p, _p, _i64, _i32, _i32, _i32, C.c_int, _p, _p, _p, _p, _p, _sz, _p, _p]),
+    "lrm_sort_workspace_size": (C.c_int, [_i64, _i32, _i32, C.POINTER(_sz)]),
     "lrm_combine": (C.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, C.c_int, _i64, _p, _p, _p]),
     "lrm_combine_backward": (C.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, C.c_int, _i64, _p, _p, _p, _p]),
     "lrm_linear_workspace_size": (C.c_int, [_i64, _i32, _i32, _i32, C.c_int, C.c_int, C.POINTER(_sz)]),

@@ -7,6 +7,7 @@ library, a CPU tensor or a failed status raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import torch
 
@@ -49,7 +50,8 @@ def _opt(t, name, dtype=None):
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    # the current device's current stream, without the Stream object (0.2 us instead of 2.9 us a call)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def lrm_workspace_size(T: int, k: int, E: int, H: int, I: int, dtype: torch.dtype) -> int:
@@ -287,6 +289,13 @@ def lrm_scatter_dx(row_of_pair, dx_c, T, k, dx=None, cap=None, dev_status=None):
     return dx
 
 
+@functools.lru_cache(maxsize=4096)
+def _sort_ws(T, k, E):
+    out = C.c_size_t(0)
+    _ok(L.load().lrm_sort_workspace_size(T, k, E, C.byref(out)), "lrm_sort_workspace_size")
+    return int(out.value)
+
+
 def _same(t, shape, name):
     if t is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -312,14 +321,15 @@ def lrm_sort_tokens(topk_idx, x, E, seg_offsets=None, pair_of_row=None, row_of_p
     _same(pair_of_row, (T * k,), "pair_of_row")
     _same(row_of_pair, (T * k,), "row_of_pair")
     _same(x_s, (T * k, H), "x_s")
-    if ws is None:
-        ws = torch.empty(lrm_workspace_size(T, k, E, 8, 8, torch.float32), dtype=torch.uint8, device=dev)
+    if ws is None:  # few pairs need none
+        need = _sort_ws(T, k, E)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _ok(L.load().lrm_sort_tokens(_cuda(topk_idx, "topk_idx", torch.int32), _opt(x, "x"), T, k, E, H,
                                  L.LRM_BF16 if x is None else _dt(x), _cuda(seg_offsets, "seg_offsets", torch.int32),
                                  _cuda(pair_of_row, "pair_of_row", torch.int32),
                                  _cuda(row_of_pair, "row_of_pair", torch.int32),
-                                 _opt(x_s, "x_s", None if x is None else x.dtype), _cuda(ws, "ws"), ws.numel(),
-                                 _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_sort_tokens")
+                                 _opt(x_s, "x_s", None if x is None else x.dtype), _opt(ws, "ws"),
+                                 0 if ws is None else ws.numel(), _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_sort_tokens")
     return seg_offsets, pair_of_row, row_of_pair, x_s
 
 
@@ -389,6 +399,7 @@ def _experts(w, seg_offsets, name):
     return tuple(w.shape)
 
 
+@functools.lru_cache(maxsize=4096)
 def lrm_linear_workspace_size(R: int, E: int, N: int, K: int, act: str, dtype: torch.dtype) -> int:
     """Scratch bytes of lrm_linear, lrm_act_backward and lrm_linear_backward (N: columns of y)."""
     out = C.c_size_t(0)
@@ -420,11 +431,11 @@ def lrm_linear(x, w, bias=None, residual=None, act="none", seg_offsets=None, sav
     _same(y, (R, N), "y")
     _same(z, (R, NP), "z")
     _same(residual, (R, N), "residual")
-    if ws is None:
+    if ws is None and x.dtype == torch.float32:  # bf16 inputs need none
         ws = torch.empty(lrm_linear_workspace_size(R, E, N, K, act, x.dtype), dtype=torch.uint8, device=dev)
     _ok(L.load().lrm_linear(_opt(seg_offsets, "seg_offsets", torch.int32), _cuda(x, "x"), _cuda(w, "w", x.dtype),
                             _opt(bias, "bias", x.dtype), _opt(residual, "residual", y.dtype), R, E, N, K, code, _dt(x),
-                            _dt(y), _cuda(y, "y"), _opt(z, "z", x.dtype), _cuda(ws, "ws"), ws.numel(), int(flags),
+                            _dt(y), _cuda(y, "y"), _opt(z, "z", x.dtype), _opt(ws, "ws"), 0 if ws is None else ws.numel(), int(flags),
                             _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_linear")
     return y, z
 

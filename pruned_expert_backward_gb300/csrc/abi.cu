@@ -41,6 +41,7 @@ struct SortWs {
   size_t counts, loads, total;
 };
 SortWs sort_layout(int64_t T, int32_t k, int32_t E) {
+  if (sort_in_one_launch(T, k, E)) return SortWs{};
   const int64_t ct = sort_chunk_tokens(k), nc = (T + ct - 1) / ct;
   SortWs w{};
   w.loads = up(sizeof(int32_t) * (size_t)(nc > 0 ? nc : 1) * (E + 1));
@@ -50,8 +51,8 @@ SortWs sort_layout(int64_t T, int32_t k, int32_t E) {
 
 // Scratch of the products and of the bias gradient (NP: rows of w, columns of dz).
 size_t linear_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
-  if (dt != LRM_F32) return kAlign;
-  return up(linear_planes_bytes(R, K)) + up(linear_planes_bytes((int64_t)E * NP, K));
+  if (dt != LRM_F32) return 0;
+  return kAlign + up(linear_planes_bytes(R, K)) + up(linear_planes_bytes((int64_t)E * NP, K));
 }
 size_t linear_grad_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
   if (dt != LRM_F32) return kAlign + linear_plan_bytes(E);  // kAlign: the maps start on a 128-byte boundary
@@ -423,11 +424,20 @@ lrm_status lrm_sort_tokens(const int32_t* topk_idx, const void* x, int64_t T, in
   if (T > 0 && (!topk_idx || !pair_of_row || !row_of_pair || (x_s && !x))) return LRM_ERR_INVALID_ARG;
   if (!al16(x) || !al16(x_s)) return LRM_ERR_INVALID_ARG;
   const SortWs w = sort_layout(T, k, E);
-  if (!ws || ws_bytes < w.total) return LRM_ERR_WORKSPACE;
+  if (w.total > 0 && (!ws || ws_bytes < w.total)) return LRM_ERR_WORKSPACE;
   char* b = static_cast<char*>(ws);
   const SortArgs a{topk_idx, x, T, k, E, H, seg_offsets, pair_of_row, row_of_pair, x_s,
                    reinterpret_cast<int32_t*>(b + w.counts), reinterpret_cast<int32_t*>(b + w.loads), dev_status};
   return launch_sort_tokens(a, dt, stream);
+}
+
+lrm_status lrm_sort_workspace_size(int64_t T, int32_t k, int32_t E, size_t* bytes) {
+  LRM_NVTX_RANGE();
+  if (!bytes) return LRM_ERR_INVALID_ARG;
+  const lrm_status st = check_dims(T, k, E, 8, 8);
+  if (st) return st;
+  *bytes = sort_layout(T, k, E).total;
+  return LRM_OK;
 }
 
 lrm_status lrm_combine(const int32_t* row_of_pair, const float* alpha, const void* y_s, const void* residual, int64_t T,
@@ -493,9 +503,14 @@ lrm_status lrm_linear(const int32_t* seg_offsets, const void* x, const void* w, 
   for (const void* p : ptrs)
     if (!al16(p)) return LRM_ERR_INVALID_ARG;
   const int32_t NP = act == LRM_ACT_SWIGLU ? 2 * N : N;
-  if (!ws || ws_bytes < linear_ws_bytes(R, E, NP, K, dt)) return LRM_ERR_WORKSPACE;
+  const size_t need = linear_ws_bytes(R, E, NP, K, dt);
+  if (need > 0 && (!ws || ws_bytes < need)) return LRM_ERR_WORKSPACE;
   if (R == 0) return LRM_OK;
   const LinearArgs a{seg_offsets, x, w, bias, residual, R, E, N, K, act, y, z, dev_status};
+  if (flags == LRM_GEMM_DEFAULT && R <= kFewRows) {
+    launch_linear_rows(a, dt, out_dt, stream);
+    return after_launch();
+  }
   if (flags == LRM_GEMM_DEFAULT) return launch_linear_tc(a, dt, out_dt, ws, stream);
   launch_linear_simt(a, dt, out_dt, stream);
   return after_launch();

@@ -1,7 +1,7 @@
 // lrm_act_backward: dz = dy * act'(z) and the bias gradient db[e] = sum over the segment's rows of dz.
 //
 // One pass over dy and z (HBM bound: dy and z read, dz written once).  A CTA covers kRowBlock rows and
-// 32 lanes of 16-byte columns; its 8 warps take the rows in turn with the loads of kUnroll rows in
+// 32 lanes of 16-byte columns; its 8 warps take the rows in turn with the loads of a few rows in
 // flight, and keep the column sums of the values before rounding in registers.
 // The sums leave as partials part[b + e][column] of (row block b, expert e): along the rows either b or
 // e grows at every step, so b + e names each meeting of a block and a segment once, and no prefix of
@@ -14,18 +14,18 @@ namespace lrm {
 
 namespace {
 
-constexpr int kRowBlock = 128;
+constexpr int kRowBlock = 64;
 constexpr int kWarps = 8;
-constexpr int kUnroll = 4;
 
 template <typename T, int ACT>
-__global__ void __launch_bounds__(32 * kWarps) act_backward_kernel(
+__global__ void __launch_bounds__(32 * kWarps, 3) act_backward_kernel(
     const int32_t* __restrict__ seg, int E, int64_t R, int N, const T* __restrict__ dy, const T* __restrict__ z,
     T* __restrict__ dz, float* __restrict__ part, int32_t* __restrict__ status) {
   chain_wait();
   constexpr int VN = VecTraits<T>::N;
   constexpr bool GLU = ACT == LRM_ACT_SWIGLU;
   constexpr int G = GLU ? 2 : 1;
+  constexpr int kUnroll = GLU ? 2 : 4;  // rows whose loads are in flight (six 16-byte loads a lane)
   const int NP = G * N;
   __shared__ float s_sum[kWarps][32 * VN * G];
   if (!rows_valid(seg, E, R, status)) return;
@@ -60,10 +60,10 @@ __global__ void __launch_bounds__(32 * kWarps) act_backward_kernel(
       for (int i = 0; i < kUnroll; ++i) {
         const int64_t r = r0 + i * kWarps;
         if (r < rb && live) {
-          d4[i] = ld_stream16(dy + r * N + col);
+          d4[i] = ld_stream16_now(dy + r * N + col);
           if (ACT != LRM_ACT_NONE)
 #pragma unroll
-            for (int g = 0; g < G; ++g) z4[i][g] = ld_stream16(z + r * NP + g * N + col);
+            for (int g = 0; g < G; ++g) z4[i][g] = ld_stream16_now(z + r * NP + g * N + col);
         }
       }
 #pragma unroll

@@ -1139,11 +1139,16 @@ int sm_count() {
 }
 
 bool device_ok() {
-  int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  return major == 10 && minor == 3;
+  static signed char known[kDeviceSlots] = {};  // 1: sm_103, -1: not
+  const int slot = current_device_slot();
+  if (slot < 0) return false;
+  if (known[slot] == 0) {
+    int major = 0, minor = 0;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, slot);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, slot);
+    known[slot] = major == 10 && minor == 3 ? 1 : -1;
+  }
+  return known[slot] > 0;
 }
 
 namespace {

@@ -125,6 +125,7 @@ struct SortArgs {
   int32_t* loads;   // scratch [E + 1]
   int32_t* status;
 };
+bool sort_in_one_launch(int64_t T, int32_t k, int32_t E);  // then no scratch is needed
 int sort_chunk_tokens(int32_t k);  // tokens of a chunk of the multi-launch form
 lrm_status launch_sort_tokens(const SortArgs& a, lrm_dtype dt, cudaStream_t s);
 void launch_combine(const int32_t* row_of_pair, const float* alpha, const void* y_s, const void* residual, int64_t T,
@@ -144,6 +145,12 @@ struct LinearArgs {
   int32_t* status;
 };
 void launch_linear_simt(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, cudaStream_t s);
+// Up to this many rows (of all experts together) one pass over the weights by plain loads beats the tensor
+// cores' tiles of 256 rows.  GB300, bf16, weights 1408+1408 x 4096 (SwiGLU), 4096 x 4096, 1536 x 2048:
+// 6.8, 8.7, 3.3 us at 8 rows (tiles: 19.5, 19.3, 11.4), 12.1, 12.7, 6.0 at 32, 20.7, 22.1, 9.2 at 64.
+// 128 experts of 1536 x 2048, top-8: 13.5 against 20.3 us at 8 rows, 27.8 : 29.4 at 32, 43.2 : 40.8 at 64.
+constexpr int64_t kFewRows = 32;
+void launch_linear_rows(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, cudaStream_t s);
 lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, void* ws, cudaStream_t s);
 size_t linear_planes_bytes(int64_t rows, int64_t cols);  // an fp32 operand as three bf16 planes
 size_t linear_plan_bytes(int32_t E);                     // plan and expert maps of the weights' gradient

@@ -5,17 +5,19 @@
 
 namespace lrm {
 
-// sigmoid(z) and the normal distribution's Phi(z), phi(z) in fp32
-__device__ __forceinline__ float sigmoid_f(float z) { return 1.f / (1.f + expf(-z)); }
+// sigmoid(z) and the normal distribution's Phi(z), phi(z) in fp32.  The fast exponential and quotient
+// err by a few units of 2^-23 (2 + 1.2 |z| of them for exp(z), where the result is near 0 or z); the
+// exact ones took the gradient kernel from the memory's rate to a third of it.
+__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 __device__ __forceinline__ float norm_cdf(float z) { return 0.5f * (1.f + erff(z * 0.70710678118654752f)); }
-__device__ __forceinline__ float norm_pdf(float z) { return 0.39894228040143268f * expf(-0.5f * z * z); }
+__device__ __forceinline__ float norm_pdf(float z) { return 0.39894228040143268f * __expf(-0.5f * z * z); }
 
 // act(z) of the one-input activations (SwiGLU takes two: SiLU(gate) * up).
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if (ACT == LRM_ACT_RELU) return fmaxf(z, 0.f);
   if (ACT == LRM_ACT_GELU) return z * norm_cdf(z);
-  if (ACT == LRM_ACT_SILU || ACT == LRM_ACT_SWIGLU) return z / (1.f + expf(-z));
+  if (ACT == LRM_ACT_SILU || ACT == LRM_ACT_SWIGLU) return z * sigmoid_f(z);
   return z;
 }
 // act'(z); ReLU's derivative at 0 is 0.

@@ -51,8 +51,10 @@ enum Kind { FWD = 0, DX = 1, DW = 2 };
 template <int BN>
 struct Cfg {
   static constexpr int kBBytes = BN / 2 * kBK * 2;  // this CTA's half of the columns
-  static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 5 : (BN == 128 ? 6 : 8);
+  static constexpr int kSlice = kABytes + kBBytes;
+  static constexpr int kSub = BN == 256 ? 1 : 2;  // K slices of a stage
+  static constexpr int kStage = kSub * kSlice;
+  static constexpr int kStages = BN == 256 ? 5 : (BN == 128 ? 3 : 4);
   static constexpr uint32_t kEpi = kStages * kStage;
   static constexpr uint32_t kBars = kEpi + kEpiWarps * kBoxes * kBoxBytes;
   static constexpr int kNBars = 2 * kStages + 5;  // full, empty, accumulator full[2] and empty[2], drain
@@ -92,6 +94,12 @@ __host__ __device__ constexpr uint32_t instr_desc(uint32_t a_mn, uint32_t b_mn) 
 
 __device__ __forceinline__ void bulk_wait_read_boxes() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBoxes - 1) : "memory");
+}
+
+// The i-th tile of a CTA pair: round robin, every second round backwards, so that where the tiles get
+// shorter along the order (DW: longest expert first) no pair takes the longer one of every round.
+__device__ __forceinline__ int nth_tile(int i, int pair, int n_pairs) {
+  return i * n_pairs + (i & 1 ? n_pairs - 1 - pair : pair);
 }
 
 struct Tile {
@@ -280,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!valid && threadIdx.x == 0) set_status(p.status, LRM_ERR_BAD_SEGMENTS);
   }
 
+  const int rounds = (n_tiles + n_pairs - 1) / n_pairs;
   volatile int* abortv = abort_flag;
   const uint32_t full_lead = cluster_addr(full0, 0), acce_lead = cluster_addr(acce0, 0);
 
@@ -289,7 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t it = 0, st = 0, sph = 0;
       bool ok = true;
       int last_e = -1;
-      for (int t = pair; t < n_tiles && ok; t += n_pairs) {
+      for (int i = 0, t; i < rounds && ok; ++i) {
+        t = nth_tile(i, pair, n_pairs);
+        if (t >= n_tiles) continue;  // (a last round may leave some pairs without one)
         const Tile d = decode<KIND, BN, GLU>(p, prefix, t, rank);
         const CUtensorMap *ma = &tmA, *mb = &tmB;
         if (KIND == DW && p.seg != nullptr) {
@@ -304,17 +315,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // first B row (FWD: rows of w, a SwiGLU pair stages gate rows and up rows) or column of this CTA
         const int nb = GLU ? d.n0 + rank * p.N : d.n0 + rank * (BN / 2);
         const uint32_t bytes = C::kBBytes + (d.has_rows ? kABytes : 0);
-        const int planes = p.terms > 1 ? 3 : 1;
-        for (int term = 6 - p.terms; term < 6 && ok; ++term) {
-          const int pa = plane_a(term), pb = plane_b(term);
-          for (int kb = 0; kb < d.slices; ++kb, ++it) {
-            const uint32_t s = st, ph = sph;
-            if (++st == (uint32_t)S) { st = 0; sph ^= 1u; }
-            if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abortv, p.status)) { ok = false; break; }
-            const uint32_t a_dst = smem_u32(smem + s * C::kStage), b_dst = a_dst + kABytes;
-            const uint32_t fb = full_lead + 8 * s;
-            const int k = kb * kBK;
-            mbar_expect_tx_cluster(fb, bytes);
+        const int planes = p.terms > 1 ? 3 : 1, total = d.slices * p.terms;
+        int term = 6 - p.terms, kb = 0;
+        for (int k0 = 0; k0 < total; k0 += C::kSub, ++it) {
+          const uint32_t s = st, ph = sph;
+          if (++st == (uint32_t)S) { st = 0; sph ^= 1u; }
+          if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abortv, p.status)) { ok = false; break; }
+          const int n_sub = min(C::kSub, total - k0);
+          const uint32_t fb = full_lead + 8 * s;
+          mbar_expect_tx_cluster(fb, n_sub * bytes);
+          for (int j = 0; j < n_sub; ++j) {
+            const int pa = plane_a(term), pb = plane_b(term), k = kb * kBK;
+            const uint32_t a_dst = smem_u32(smem + s * C::kStage + j * C::kSlice), b_dst = a_dst + kABytes;
             if (KIND == DW) {
               const int r = d.row0 + k;
               if (d.has_rows) {
@@ -333,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < BN / 128; ++c) tma_load_3d_pair(b_dst + c * 8192, mb, nb + c * 64, k, eb, fb);
               }
             }
+            if (++kb == d.slices) { kb = 0; ++term; }
           }
         }
       }
@@ -351,7 +364,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint64_t b_step = KIND == FWD ? (32 >> 4) : (2048 >> 4);
       uint32_t st = 0, sph = 0, use = 0;  // operand stage and phase; accumulators used so far
       bool ok = true;
-      for (int t = pair; t < n_tiles && ok; t += n_pairs) {
+      for (int i = 0, t; i < rounds && ok; ++i) {
+        t = nth_tile(i, pair, n_pairs);
+        if (t >= n_tiles) continue;  // (a last round may leave some pairs without one)
         const Tile d = decode<KIND, BN, GLU>(p, prefix, t, 0);
         const int total = d.slices * p.terms;
         for (int k0 = 0; k0 < total && ok; k0 += PROMOTE ? p.pk : total, ++use) {
@@ -360,16 +375,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!mbar_wait(acce0 + 8 * acc, ((use >> 1) & 1u) ^ 1u, abortv, p.status)) { ok = false; break; }
           tc_fence_after();
           const uint32_t tmem_d = tmem_base + acc * BN;
-          for (int kb = k0; kb < k1; ++kb) {
+          for (int kb = k0; kb < k1; kb += C::kSub) {
             const uint32_t s = st, ph = sph;
             if (++st == (uint32_t)S) { st = 0; sph ^= 1u; }
             if (!mbar_wait(full0 + 8 * s, ph, abortv, p.status)) { ok = false; break; }
             tc_fence_after();
-            const uint64_t soff = (uint64_t)((s * C::kStage) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              mma_bf16(tmem_d, adesc0 + soff + kk * a_step, bdesc0 + soff + kk * b_step, idesc,
-                       kb != k0 || kk != 0 ? 1u : 0u);
+            for (int j = 0; j < C::kSub; ++j) {
+              if (j > 0 && kb + j >= k1) break;
+              const uint64_t soff = (uint64_t)((s * C::kStage + j * C::kSlice) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kBK / 16; ++kk)
+                mma_bf16(tmem_d, adesc0 + soff + kk * a_step, bdesc0 + soff + kk * b_step, idesc,
+                         kb != k0 || j != 0 || kk != 0 ? 1u : 0u);
+            }
             mma_commit_pair(empty0 + 8 * s);
           }
           if (ok) mma_commit_pair(accf0 + 8 * acc);
@@ -394,7 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     uint32_t use = 0;
     bool ok = true;
-    for (int t = pair; t < n_tiles && ok; t += n_pairs) {
+    for (int i = 0, t; i < rounds && ok; ++i) {
+        t = nth_tile(i, pair, n_pairs);
+        if (t >= n_tiles) continue;  // (a last round may leave some pairs without one)
       const Tile d = decode<KIND, BN, GLU>(p, prefix, t, rank);
       const int row_base = (KIND == DW ? d.m0 : d.row0) + q * 32;
       const int row_lim = KIND == DW ? p.M : d.row_end;
@@ -635,18 +656,24 @@ void split_planes(const void* x, int64_t groups, int64_t n, void* out, cudaStrea
 // most per sum), 1024 for bf16 inputs (1e-6).
 constexpr int kSlicesF32 = 4, kSlicesBf16 = 16;
 
+// Most row tiles there can be, and about how many (every segment ends in half a tile).
 int64_t row_tiles(const int32_t* seg, int64_t R, int E) {
   return (R + 2 * kBM - 1) / (2 * kBM) + (seg != nullptr ? E : 0);
 }
+int64_t likely_row_tiles(const int32_t* seg, int64_t R, int E) {
+  return (R + 2 * kBM - 1) / (2 * kBM) + (seg != nullptr ? (R < E ? R : E) / 2 : 0);
+}
 
-// Tile width: the widest whose tiles give every CTA pair one, else the next narrower (a 256 x 256 tile
-// moves the fewest operand bytes per product; below a tile per pair the idle SMs cost more).
+// Tile width by the waves of tiles over the CTA pairs: a K slice of a 256-column tile takes 0.26 us, one of
+// a 128- or 64-column tile 0.21 us (the issue of a stage bounds it, not the product).  On a tie the
+// narrower: more SMs then share the reading of the weights.
 template <typename F>
 lrm_status with_width(int64_t tiles_m, int N, int least, F&& f) {
   const int64_t pairs = sm_count() / 2;
-  if (tiles_m * ((N + 255) / 256) >= pairs) return f(IntTag<256>{});
-  if (least > 64 || tiles_m * ((N + 127) / 128) >= pairs) return f(IntTag<128>{});
-  return f(IntTag<64>{});
+  auto cost = [&](int bn, int slice) { return (tiles_m * ((N + bn - 1) / bn) + pairs - 1) / pairs * slice; };
+  const int64_t c256 = cost(256, 5), c128 = cost(128, 4), c64 = least > 64 ? INT64_MAX : cost(64, 4);
+  if (c64 <= c128 && c64 <= c256) return f(IntTag<64>{});
+  return c128 <= c256 ? f(IntTag<128>{}) : f(IntTag<256>{});
 }
 
 }  // namespace
@@ -659,7 +686,7 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
   const int NP = glu ? 2 * a.N : a.N;
   const void *xs = a.x, *wsrc = a.w;
   if (f32) {
-    char* b = static_cast<char*>(ws);
+    char* b = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws) + 127) & ~uintptr_t(127));
     split_planes(a.x, 1, a.R * a.K, b, s);
     xs = b;
     b += (linear_planes_bytes(a.R, a.K) + 255) / 256 * 256;
@@ -702,8 +729,9 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
       return launch<FWD, BN, GLU, false, B16, B16>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
     }
   };
-  if (glu) return with_width(tm, NP, 128, [&](auto bn) { return go(bn, IntTag<1>{}); });
-  return with_width(tm, NP, 64, [&](auto bn) { return go(bn, IntTag<0>{}); });
+  const int64_t likely = likely_row_tiles(a.seg_offsets, a.R, a.E);
+  if (glu) return with_width(likely, NP, 128, [&](auto bn) { return go(bn, IntTag<1>{}); });
+  return with_width(likely, NP, 64, [&](auto bn) { return go(bn, IntTag<0>{}); });
 }
 
 lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void* ws, cudaStream_t s) {
@@ -769,7 +797,7 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
         !operand_map(&mB, wsrc, a.K, a.N, (uint64_t)a.E * planes, 64) || !output_map(&mY, a.dx, f32, a.K, a.R, 1))
       return LRM_ERR_CUDA;
     const int64_t tm = row_tiles(a.seg_offsets, a.R, a.E);
-    return with_width(tm, a.K, 128, [&](auto bn) {
+    return with_width(likely_row_tiles(a.seg_offsets, a.R, a.E), a.K, 128, [&](auto bn) {
       constexpr int BN = decltype(bn)::value;
       if constexpr (BN < 128) {
         return LRM_ERR_UNSUPPORTED;

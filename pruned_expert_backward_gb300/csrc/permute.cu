@@ -75,7 +75,7 @@ __device__ __forceinline__ void copy_rows(const T* __restrict__ x, T* __restrict
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int i = i0 + q * step;
-      if (i < n) v[q] = ld_stream16(x + t0 * H + (int64_t)i * VN);
+      if (i < n) v[q] = ld_stream16_now(x + t0 * H + (int64_t)i * VN);
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const int32_t* __restrict_
       uint4 vals[L];
 #pragma unroll
       for (int m = 0; m < L; ++m)
-        if (b0 + m < n) vals[m] = ld_stream16(y_s + (int64_t)s_item[b0 + m].y * H + (int64_t)v * VN);
+        if (b0 + m < n) vals[m] = ld_stream16_now(y_s + (int64_t)s_item[b0 + m].y * H + (int64_t)v * VN);
 #pragma unroll
       for (int m = 0; m < L; ++m) {
         if (b0 + m >= n) break;
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const int32_t* __
       if (y_s != nullptr)
 #pragma unroll
         for (int j = 0; j < KB; ++j)
-          if (j0 + j < k && s_row[j0 + j] >= 0) rows[j] = ld_stream16(y_s + s_row[j0 + j] * H + (int64_t)v * VN);
+          if (j0 + j < k && s_row[j0 + j] >= 0) rows[j] = ld_stream16_now(y_s + s_row[j0 + j] * H + (int64_t)v * VN);
       float d[VN];
       unpack(d4, d);
 #pragma unroll
@@ -374,7 +374,7 @@ template <typename T>
 lrm_status sort_all(const SortArgs& a, cudaStream_t s) {
   const int64_t P = a.T * a.k;
   const int B = a.E + 1;
-  if (P <= kSmallPairs && a.E <= kSmallExperts) {
+  if (sort_in_one_launch(a.T, a.k, a.E)) {
     // a warp for every 64 pairs, at least as many threads as a row has 16-byte columns (up to 256)
     int threads = (int)((P + 63) / 64) * 32;
     const int cols = (a.H / VecTraits<T>::N + 31) / 32 * 32;
@@ -428,6 +428,7 @@ void combine_backward_all(const int32_t* row_of_pair, const float* alpha, const 
 
 }  // namespace
 
+bool sort_in_one_launch(int64_t T, int32_t k, int32_t E) { return T * k <= kSmallPairs && E <= kSmallExperts; }
 int sort_chunk_tokens(int32_t k) { return kChunkThreads / k; }
 
 lrm_status launch_sort_tokens(const SortArgs& a, lrm_dtype dt, cudaStream_t s) {

@@ -21,8 +21,9 @@ def test_sort_tokens_host_validation():
     assert f(P, P, 16, 2, 4, 60, 0, P, P, P, P, P, BIG, None, None) == SHAPE
     assert f(P, P, 1 << 40, 2, 4, 64, 0, P, P, P, P, P, BIG, None, None) == SHAPE
     assert f(P, P, 16, 2, 4, 64, 2, P, P, P, P, P, BIG, None, None) == DTYPE
-    assert f(P, P, 16, 2, 4, 64, 0, P, P, P, P, None, 0, None, None) == WS
-    assert f(P, P, 16, 2, 4, 64, 0, P, P, P, P, P, 16, None, None) == WS
+    assert f(P, P, 4096, 2, 4, 64, 0, P, P, P, P, None, 0, None, None) == WS   # many pairs need scratch
+    assert f(P, P, 4096, 2, 4, 64, 0, P, P, P, P, P, 16, None, None) == WS
+    assert f(P, P, 16, 2, 300, 64, 0, P, P, P, P, None, 0, None, None) == WS   # and many experts
 
 
 def test_sort_fits_the_common_workspace():
@@ -31,7 +32,10 @@ def test_sort_fits_the_common_workspace():
     for T, k, E in ((1, 1, 1), (100000, 16, 1024), (5003, 6, 60)):
         assert lib.lrm_workspace_size(T, k, E, 8, 8, 0, C.byref(n)) == OK
         chunks = (T + 256 // k - 1) // (256 // k)
-        assert n.value >= 4 * (chunks + 1) * (E + 1)
+        common = n.value
+        assert lib.lrm_sort_workspace_size(T, k, E, C.byref(n)) == OK
+        assert (n.value == 0) if T == 1 else (common >= n.value >= 4 * (chunks + 1) * (E + 1))
+    assert lib.lrm_sort_workspace_size(1, 1, 1, None) == ARG
 
 
 def test_combine_host_validation():
@@ -79,7 +83,7 @@ def test_linear_host_validation():
     assert call(f, ok, a10=4) == DTYPE and call(f, ok, a11=4) == DTYPE
     assert call(f, ok, a10=1, a11=0) == DTYPE  # fp32 inputs give fp32
     assert call(f, ok, a11=1) == DTYPE         # a residual with an fp32 y of bf16 inputs
-    assert call(f, ok, a14=None) == WS and call(f, ok, a15=0) == WS
+    assert call(f, ok, a10=1, a11=1, a14=None) == WS and call(f, ok, a10=1, a11=1, a15=0) == WS
     assert f(None, None, P, None, None, 0, 1, 64, 64, 0, 0, 0, None, None, P, BIG, 0, None, None) == OK
     f = lib.lrm_act_backward
     ok = (P, P, P, 16, 4, 64, 1, 0, P, P, P, BIG, None, None)

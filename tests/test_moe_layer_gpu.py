@@ -585,7 +585,7 @@ def test_refusals():
     with pytest.raises(lrm.LrmError):  # misaligned start
         lrm.lrm_linear(torch.zeros(4 * 16 + 1, device="cuda", dtype=BF16)[1:].view(4, 16), w)
     with pytest.raises(lrm.LrmError):
-        lrm.lrm_linear(x, w, ws=torch.zeros(0, dtype=torch.uint8, device="cuda"))
+        lrm.lrm_linear(x.float(), w.float(), ws=torch.zeros(0, dtype=torch.uint8, device="cuda"))
     idx = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError):
         lrm.lrm_sort_tokens(idx, x[:3], 4)
