@@ -301,51 +301,61 @@ def _same(t, shape, name):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
+def _out(t, shape, dtype, device, name):
+    """An output and its address: checked if the caller gave it, else made here."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t, _cuda(t, name, dtype)
+
+
+def _scratch(ws, need, device):
+    """(tensor, address, bytes) of a workspace of at least `need` bytes; none is made for 0."""
+    if ws is None:
+        if need == 0:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        return ws, ws.data_ptr(), need
+    return ws, _cuda(ws, "ws"), ws.numel()
+
+
 def lrm_sort_tokens(topk_idx, x, E, seg_offsets=None, pair_of_row=None, row_of_pair=None, x_s=None, ws=None,
                     dev_status=None):
     """Tokens sorted by expert.  topk_idx int32 [T,k] (-1: not routed), x [T,H] or None (indices only).
     Returns seg_offsets [E+1], pair_of_row [T*k], row_of_pair [T*k] (int32) and x_s [T*k,H].
     Its gradient is lrm_scatter_dx(row_of_pair, dx_s, T, k)."""
     T, k = topk_idx.shape
-    dev = topk_idx.device
-    if x is not None and (x.dim() != 2 or x.shape[0] != T):
-        raise ValueError(f"x must be [T,H] with T = {T}, got {list(x.shape)}")
-    H = x.shape[1] if x is not None else 8
-    i32 = dict(dtype=torch.int32, device=dev)
-    seg_offsets = torch.empty(E + 1, **i32) if seg_offsets is None else seg_offsets
-    pair_of_row = torch.empty(T * k, **i32) if pair_of_row is None else pair_of_row
-    row_of_pair = torch.empty(T * k, **i32) if row_of_pair is None else row_of_pair
-    if x is not None and x_s is None:
-        x_s = torch.empty(T * k, H, dtype=x.dtype, device=dev)
-    _same(seg_offsets, (E + 1,), "seg_offsets")
-    _same(pair_of_row, (T * k,), "pair_of_row")
-    _same(row_of_pair, (T * k,), "row_of_pair")
-    _same(x_s, (T * k, H), "x_s")
-    if ws is None:  # few pairs need none
-        need = _sort_ws(T, k, E)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _ok(L.load().lrm_sort_tokens(_cuda(topk_idx, "topk_idx", torch.int32), _opt(x, "x"), T, k, E, H,
-                                 L.LRM_BF16 if x is None else _dt(x), _cuda(seg_offsets, "seg_offsets", torch.int32),
-                                 _cuda(pair_of_row, "pair_of_row", torch.int32),
-                                 _cuda(row_of_pair, "row_of_pair", torch.int32),
-                                 _opt(x_s, "x_s", None if x is None else x.dtype), _opt(ws, "ws"),
-                                 0 if ws is None else ws.numel(), _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_sort_tokens")
+    dev, i32 = topk_idx.device, torch.int32
+    idx_p = _cuda(topk_idx, "topk_idx", i32)
+    seg_offsets, seg_p = _out(seg_offsets, (E + 1,), i32, dev, "seg_offsets")
+    pair_of_row, pair_p = _out(pair_of_row, (T * k,), i32, dev, "pair_of_row")
+    row_of_pair, row_p = _out(row_of_pair, (T * k,), i32, dev, "row_of_pair")
+    if x is None:
+        H, dt, x_p, x_s, xs_p = 8, L.LRM_BF16, None, None, None
+    else:
+        if x.dim() != 2 or x.shape[0] != T:
+            raise ValueError(f"x must be [T,H] with T = {T}, got {list(x.shape)}")
+        H, dt, x_p = x.shape[1], _dt(x), _cuda(x, "x")
+        x_s, xs_p = _out(x_s, (T * k, H), x.dtype, dev, "x_s")
+    ws, ws_p, ws_n = _scratch(ws, _sort_ws(T, k, E) if ws is None else 0, dev)
+    _ok(L.load().lrm_sort_tokens(idx_p, x_p, T, k, E, H, dt, seg_p, pair_p, row_p, xs_p, ws_p, ws_n,
+                                 _opt(dev_status, "dev_status", i32), _stream()), "lrm_sort_tokens")
     return seg_offsets, pair_of_row, row_of_pair, x_s
 
 
 def lrm_combine(row_of_pair, alpha, y_s, residual=None, y=None, dev_status=None):
     """y [T,H] = residual + sum_j alpha[t,j] * y_s[row_of_pair[t,j]]; alpha fp32 [T,k], y_s [rows,H]."""
     T, k = alpha.shape
-    H = y_s.shape[1]
+    rows, H = y_s.shape
     if row_of_pair.numel() != T * k:
         raise ValueError(f"row_of_pair must hold T*k = {T * k} rows, got {row_of_pair.numel()}")
-    y = torch.empty(T, H, dtype=y_s.dtype, device=y_s.device) if y is None else y
-    _same(y, (T, H), "y")
+    y, y_p = _out(y, (T, H), y_s.dtype, y_s.device, "y")
     _same(residual, (T, H), "residual")
     _ok(L.load().lrm_combine(_cuda(row_of_pair, "row_of_pair", torch.int32), _cuda(alpha, "alpha", torch.float32),
-                             _cuda(y_s, "y_s"), _opt(residual, "residual", y_s.dtype), T, k, H, _dt(y_s),
-                             y_s.shape[0], _cuda(y, "y", y_s.dtype), _opt(dev_status, "dev_status", torch.int32),
-                             _stream()), "lrm_combine")
+                             _cuda(y_s, "y_s"), _opt(residual, "residual", y_s.dtype), T, k, H, _dt(y_s), rows, y_p,
+                             _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_combine")
     return y
 
 
@@ -353,26 +363,27 @@ def lrm_combine_backward(row_of_pair, alpha, dy, y_s, dy_s=None, dalpha=None, de
     """Gradient of lrm_combine: dy_s [rows,H] and dalpha fp32 [T,k].  y_s None: dy_s alone (it must then
     be given, it fixes the row count)."""
     T, k = alpha.shape
-    H = dy.shape[1]
+    H, dt, dev = dy.shape[1], dy.dtype, dy.device
     if y_s is None and dy_s is None:
         raise ValueError("dy_s must be given when y_s is not")
     rows = (y_s if y_s is not None else dy_s).shape[0]
     if row_of_pair.numel() != T * k:
         raise ValueError(f"row_of_pair must hold T*k = {T * k} rows, got {row_of_pair.numel()}")
-    dy_s = torch.empty(rows, H, dtype=dy.dtype, device=dy.device) if dy_s is None else dy_s
-    if y_s is not None and dalpha is None:
-        dalpha = torch.empty(T, k, dtype=torch.float32, device=dy.device)
-    elif y_s is None:
+    dy_s, dys_p = _out(dy_s, (rows, H), dt, dev, "dy_s")
+    dalpha_p = None
+    if y_s is None:
         dalpha = None
+    elif dalpha is None:
+        dalpha, dalpha_p = _out(None, (T, k), torch.float32, dev, "dalpha")
+    else:
+        if dalpha.numel() != T * k:
+            raise ValueError(f"dalpha must hold T*k = {T * k} values, got {dalpha.numel()}")
+        dalpha_p = _cuda(dalpha, "dalpha", torch.float32)
     _same(dy, (T, H), "dy")
     _same(y_s, (rows, H), "y_s")
-    _same(dy_s, (rows, H), "dy_s")
-    if dalpha is not None and dalpha.numel() != T * k:
-        raise ValueError(f"dalpha must hold T*k = {T * k} values, got {dalpha.numel()}")
     _ok(L.load().lrm_combine_backward(_cuda(row_of_pair, "row_of_pair", torch.int32),
-                                      _cuda(alpha, "alpha", torch.float32), _cuda(dy, "dy"), _opt(y_s, "y_s", dy.dtype),
-                                      T, k, H, _dt(dy), rows, _cuda(dy_s, "dy_s", dy.dtype),
-                                      _opt(dalpha, "dalpha", torch.float32),
+                                      _cuda(alpha, "alpha", torch.float32), _cuda(dy, "dy"), _opt(y_s, "y_s", dt),
+                                      T, k, H, _dt(dy), rows, dys_p, dalpha_p,
                                       _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_combine_backward")
     return dy_s, dalpha
 
@@ -416,27 +427,29 @@ def lrm_linear(x, w, bias=None, residual=None, act="none", seg_offsets=None, sav
     from bf16 inputs.  Returns (y, z or None)."""
     R, K = x.shape
     E, NP, Kw = _experts(w, seg_offsets, "w")
-    code = _act_code(act)
+    code, dt, dev = _act_code(act), x.dtype, x.device
+    x_p, dt_code = _cuda(x, "x"), _dt(x)
     if Kw != K:
         raise ValueError(f"x has {K} columns, w {Kw}")
     if act == "swiglu" and NP % 2:
         raise ValueError(f"w has {NP} rows: gate and up rows in equal number expected")
     N = NP // 2 if act == "swiglu" else NP
-    dev, out_dtype = x.device, x.dtype if out_dtype is None else out_dtype
     if bias is not None and bias.numel() != E * NP:
         raise ValueError(f"bias must hold {E * NP} values, got {bias.numel()}")
-    y = torch.empty(R, N, dtype=out_dtype, device=dev) if y is None else y
-    if save_z and z is None:
-        z = torch.empty(R, NP, dtype=x.dtype, device=dev)
-    _same(y, (R, N), "y")
-    _same(z, (R, NP), "z")
+    if y is not None and out_dtype is None:
+        out_dtype = y.dtype
+    y, y_p = _out(y, (R, N), dt if out_dtype is None else out_dtype, dev, "y")
+    z_p = None
+    if save_z or z is not None:
+        z, z_p = _out(z, (R, NP), dt, dev, "z")
     _same(residual, (R, N), "residual")
-    if ws is None and x.dtype == torch.float32:  # bf16 inputs need none
-        ws = torch.empty(lrm_linear_workspace_size(R, E, N, K, act, x.dtype), dtype=torch.uint8, device=dev)
-    _ok(L.load().lrm_linear(_opt(seg_offsets, "seg_offsets", torch.int32), _cuda(x, "x"), _cuda(w, "w", x.dtype),
-                            _opt(bias, "bias", x.dtype), _opt(residual, "residual", y.dtype), R, E, N, K, code, _dt(x),
-                            _dt(y), _cuda(y, "y"), _opt(z, "z", x.dtype), _opt(ws, "ws"), 0 if ws is None else ws.numel(), int(flags),
-                            _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_linear")
+    # bf16 inputs need no scratch
+    need = lrm_linear_workspace_size(R, E, N, K, act, dt) if ws is None and dt_code == L.LRM_F32 else 0
+    ws, ws_p, ws_n = _scratch(ws, need, dev)
+    _ok(L.load().lrm_linear(_opt(seg_offsets, "seg_offsets", torch.int32), x_p, _cuda(w, "w", dt),
+                            _opt(bias, "bias", dt), _opt(residual, "residual", y.dtype), R, E, N, K, code, dt_code,
+                            _dt(y), y_p, z_p, ws_p, ws_n, int(flags), _opt(dev_status, "dev_status", torch.int32),
+                            _stream()), "lrm_linear")
     return y, z
 
 
@@ -445,27 +458,29 @@ def lrm_act_backward(dy, z, act="none", seg_offsets=None, bias_grad=True, dz=Non
     """dz = dy * act'(z) [R,N'] and db fp32 [N'] ([E,N'] with seg_offsets), the column sums of dz, unless
     bias_grad is False.  z may be None for act "none"."""
     R, N = dy.shape
-    code = _act_code(act)
+    code, dt, dev = _act_code(act), dy.dtype, dy.device
     NP = 2 * N if act == "swiglu" else N
     E = 1 if seg_offsets is None else seg_offsets.numel() - 1
-    dev = dy.device
-    dz = torch.empty(R, NP, dtype=dy.dtype, device=dev) if dz is None else dz
-    if bias_grad and db is None:
-        db = torch.empty((NP,) if seg_offsets is None else (E, NP), dtype=torch.float32, device=dev)
-    if not bias_grad:
-        db = None
-    if db is not None and db.numel() != E * NP:
-        raise ValueError(f"db must hold {E * NP} values, got {db.numel()}")
+    dy_p, dt_code = _cuda(dy, "dy"), _dt(dy)
     if act != "none" and z is None:
         raise ValueError(f"z is needed for act {act!r}")
     _same(z, (R, NP), "z")
-    _same(dz, (R, NP), "dz")
-    if ws is None and db is not None:
-        ws = torch.empty(lrm_linear_workspace_size(R, E, N, 8, act, dy.dtype), dtype=torch.uint8, device=dev)
-    _ok(L.load().lrm_act_backward(_opt(seg_offsets, "seg_offsets", torch.int32), _cuda(dy, "dy"),
-                                  _opt(z, "z", dy.dtype), R, E, N, code, _dt(dy), _cuda(dz, "dz", dy.dtype),
-                                  _opt(db, "db", torch.float32), _opt(ws, "ws"), 0 if ws is None else ws.numel(),
-                                  _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_act_backward")
+    dz, dz_p = _out(dz, (R, NP), dt, dev, "dz")
+    db_p, need = None, 0
+    if not bias_grad:
+        db = None
+    else:
+        if db is None:
+            db, db_p = _out(None, (NP,) if seg_offsets is None else (E, NP), torch.float32, dev, "db")
+        else:
+            if db.numel() != E * NP:
+                raise ValueError(f"db must hold {E * NP} values, got {db.numel()}")
+            db_p = _cuda(db, "db", torch.float32)
+        need = lrm_linear_workspace_size(R, E, N, 8, act, dt) if ws is None else 0
+    ws, ws_p, ws_n = _scratch(ws, need, dev)
+    _ok(L.load().lrm_act_backward(_opt(seg_offsets, "seg_offsets", torch.int32), dy_p, _opt(z, "z", dt), R, E, N, code,
+                                  dt_code, dz_p, db_p, ws_p, ws_n, _opt(dev_status, "dev_status", torch.int32),
+                                  _stream()), "lrm_act_backward")
     return dz, db
 
 
@@ -475,24 +490,18 @@ def lrm_linear_backward(dz, x, w, seg_offsets=None, need_dx=True, need_dw=True, 
     with seg_offsets).  Returns (dx or None, dw or None)."""
     R, N = dz.shape
     E, Nw, K = _experts(w, seg_offsets, "w")
+    dt, dev = dz.dtype, dz.device
+    dz_p, dt_code = _cuda(dz, "dz"), _dt(dz)
     if Nw != N:
         raise ValueError(f"dz has {N} columns, w {Nw} rows")
-    dev = dz.device
-    if need_dx and dx is None:
-        dx = torch.empty(R, K, dtype=dz.dtype, device=dev)
-    if need_dw and dw is None:
-        dw = torch.empty(w.shape, dtype=torch.float32, device=dev)
-    dx, dw = (dx if need_dx else None), (dw if need_dw else None)
     _same(x, (R, K), "x")
-    _same(dx, (R, K), "dx")
-    _same(dw, w.shape, "dw")
-    if ws is None:
-        ws = torch.empty(lrm_linear_workspace_size(R, E, N, K, "none", dz.dtype), dtype=torch.uint8, device=dev)
-    _ok(L.load().lrm_linear_backward(_opt(seg_offsets, "seg_offsets", torch.int32), _cuda(dz, "dz"),
-                                     _cuda(x, "x", dz.dtype), _cuda(w, "w", dz.dtype), R, E, N, K, _dt(dz),
-                                     _opt(dx, "dx", dz.dtype), _opt(dw, "dw", torch.float32), _cuda(ws, "ws"),
-                                     ws.numel(), int(flags), _opt(dev_status, "dev_status", torch.int32), _stream()),
-        "lrm_linear_backward")
+    dx, dx_p = _out(dx, (R, K), dt, dev, "dx") if need_dx else (None, None)
+    dw, dw_p = _out(dw, tuple(w.shape), torch.float32, dev, "dw") if need_dw else (None, None)
+    need = lrm_linear_workspace_size(R, E, N, K, "none", dt) if ws is None else 0
+    ws, ws_p, ws_n = _scratch(ws, need, dev)
+    _ok(L.load().lrm_linear_backward(_opt(seg_offsets, "seg_offsets", torch.int32), dz_p, _cuda(x, "x", dt),
+                                     _cuda(w, "w", dt), R, E, N, K, dt_code, dx_p, dw_p, ws_p, ws_n, int(flags),
+                                     _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_linear_backward")
     return dx, dw
 
 
