@@ -1,8 +1,8 @@
 // lrm_act_backward: dz = dy * act'(z) and the bias gradient db[e] = sum over the segment's rows of dz.
 //
 // One pass over dy and z (HBM bound: dy and z read, dz written once).  A CTA covers kRowBlock rows and
-// 32 lanes of 16-byte columns; its 8 warps take the rows in turn with the loads of a few rows in
-// flight, and keep the column sums of the values before rounding in registers.
+// 32 lanes of 16-byte columns; its 8 warps take the rows in turn and keep the column sums of the values
+// before rounding in registers.
 // The sums leave as partials part[b + e][column] of (row block b, expert e): along the rows either b or
 // e grows at every step, so b + e names each meeting of a block and a segment once, and no prefix of
 // block counts is needed.  A second launch adds an expert's partials in block order.  No atomics: db
@@ -14,24 +14,33 @@ namespace lrm {
 
 namespace {
 
-constexpr int kRowBlock = 64;
+constexpr int kRowBlock = 128;
 constexpr int kWarps = 8;
+// CTAs an SM holds: many warps with one row's loads each hide the memory better than few with several
+// (65536 x 768 SwiGLU without sums, bf16: 84 us with 4 CTAs and 1 row, 97 us with 3 and 2, 101 us with 2 and
+// 4; GELU of 65536 x 1536: 117 us with 5 CTAs, 123 us with 4, 124 us with 6).
+template <typename T, int ACT>
+constexpr int kCtas = sizeof(T) == 4 ? 6 : (ACT == LRM_ACT_SWIGLU ? 4 : 5);
 
 template <typename T, int ACT>
-__global__ void __launch_bounds__(32 * kWarps, 3) act_backward_kernel(
+__global__ void __launch_bounds__(32 * kWarps, (kCtas<T, ACT>)) act_backward_kernel(
     const int32_t* __restrict__ seg, int E, int64_t R, int N, const T* __restrict__ dy, const T* __restrict__ z,
     T* __restrict__ dz, float* __restrict__ part, int32_t* __restrict__ status) {
   chain_wait();
   constexpr int VN = VecTraits<T>::N;
   constexpr bool GLU = ACT == LRM_ACT_SWIGLU;
   constexpr int G = GLU ? 2 : 1;
-  constexpr int kUnroll = GLU ? 2 : 4;  // rows whose loads are in flight (six 16-byte loads a lane)
   const int NP = G * N;
   __shared__ float s_sum[kWarps][32 * VN * G];
-  if (!rows_valid(seg, E, R, status)) return;
+  __shared__ int s_seg[LRM_MAX_EXPERTS + 1];
+  if (seg != nullptr) {
+    for (int e = threadIdx.x; e <= E; e += blockDim.x) s_seg[e] = seg[e];
+    __syncthreads();
+    if (!rows_valid(s_seg, E, R, status)) return;
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t b = blockIdx.x, b0 = b * kRowBlock;
-  const int64_t end = seg == nullptr ? R : seg[E];
+  const int64_t end = seg == nullptr ? R : s_seg[E];
   const int64_t b1 = b0 + kRowBlock < end ? b0 + kRowBlock : end;
   const int col = (blockIdx.y * 32 + lane) * VN;
   const bool live = col < N;
@@ -40,13 +49,13 @@ __global__ void __launch_bounds__(32 * kWarps, 3) act_backward_kernel(
     int lo = 0, hi = E;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (seg[mid] <= b0) lo = mid; else hi = mid;
+      if (s_seg[mid] <= b0) lo = mid; else hi = mid;
     }
     e = lo;
   }
   // the rows of one expert in the block at a time (all of the block's when no sum is wanted)
   for (int64_t ra = b0; ra < b1; ++e) {
-    const int64_t seg_end = seg != nullptr && part != nullptr ? seg[e + 1] : b1;
+    const int64_t seg_end = seg != nullptr && part != nullptr ? s_seg[e + 1] : b1;
     const int64_t rb = seg_end < b1 ? seg_end : b1;
     if (rb <= ra) continue;  // an expert without rows
     float sum[G][VN];
@@ -54,42 +63,31 @@ __global__ void __launch_bounds__(32 * kWarps, 3) act_backward_kernel(
     for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int q = 0; q < VN; ++q) sum[g][q] = 0.f;
-    for (int64_t r0 = ra + warp; r0 < rb; r0 += kWarps * kUnroll) {
-      uint4 d4[kUnroll], z4[kUnroll][G];
+    for (int64_t r = ra + warp; r < rb && live; r += kWarps) {
+      const uint4 d4 = ld_stream16_now(dy + r * N + col);
+      uint4 z4[G];
+      if (ACT != LRM_ACT_NONE)
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        const int64_t r = r0 + i * kWarps;
-        if (r < rb && live) {
-          d4[i] = ld_stream16_now(dy + r * N + col);
-          if (ACT != LRM_ACT_NONE)
+        for (int g = 0; g < G; ++g) z4[g] = ld_stream16_now(z + r * NP + g * N + col);
+      float d[VN], zf[G][VN], o[G][VN];
+      unpack(d4, d);
+      if (ACT != LRM_ACT_NONE)
 #pragma unroll
-            for (int g = 0; g < G; ++g) z4[i][g] = ld_stream16_now(z + r * NP + g * N + col);
-        }
-      }
+        for (int g = 0; g < G; ++g) unpack(z4[g], zf[g]);
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        const int64_t r = r0 + i * kWarps;
-        if (r >= rb || !live) continue;
-        float d[VN], zf[G][VN], o[G][VN];
-        unpack(d4[i], d);
-        if (ACT != LRM_ACT_NONE)
-#pragma unroll
-          for (int g = 0; g < G; ++g) unpack(z4[i][g], zf[g]);
-#pragma unroll
-        for (int q = 0; q < VN; ++q) {
-          if (GLU) {
-            const float gate = zf[0][q], up = zf[G - 1][q], sg = sigmoid_f(gate);
-            o[0][q] = d[q] * up * sg * (1.f + gate * (1.f - sg));
-            o[G - 1][q] = d[q] * gate * sg;
-          } else {
-            o[0][q] = ACT == LRM_ACT_NONE ? d[q] : d[q] * act_slope<ACT>(zf[0][q]);
-          }
-#pragma unroll
-          for (int g = 0; g < G; ++g) sum[g][q] += o[g][q];
+      for (int q = 0; q < VN; ++q) {
+        if (GLU) {
+          const float gate = zf[0][q], up = zf[G - 1][q], sg = sigmoid_f(gate);
+          o[0][q] = d[q] * up * sg * (1.f + gate * (1.f - sg));
+          o[G - 1][q] = d[q] * gate * sg;
+        } else {
+          o[0][q] = ACT == LRM_ACT_NONE ? d[q] : d[q] * act_slope<ACT>(zf[0][q]);
         }
 #pragma unroll
-        for (int g = 0; g < G; ++g) st16(dz + r * NP + g * N + col, pack(o[g]));
+        for (int g = 0; g < G; ++g) sum[g][q] += o[g][q];
       }
+#pragma unroll
+      for (int g = 0; g < G; ++g) st16(dz + r * NP + g * N + col, pack(o[g]));
     }
     if (part != nullptr) {
 #pragma unroll
@@ -110,28 +108,29 @@ __global__ void __launch_bounds__(32 * kWarps, 3) act_backward_kernel(
   }
 }
 
-// db[e][column] from the partials of the expert's row blocks: 32 columns per CTA, 8 warps taking every
-// eighth block, added in a fixed order.
-__global__ void __launch_bounds__(256) bias_sum_kernel(const int32_t* __restrict__ seg, int E, int64_t R, int NP,
-                                                       const float* __restrict__ part, float* __restrict__ db,
-                                                       int32_t* __restrict__ status) {
+// db[e][column] from the partials of the expert's row blocks: 32 columns per CTA, its warps taking the
+// blocks in turn, added in a fixed order.
+constexpr int kSumWarps = 16;
+__global__ void __launch_bounds__(32 * kSumWarps) bias_sum_kernel(const int32_t* __restrict__ seg, int E, int64_t R,
+                                                                  int NP, const float* __restrict__ part,
+                                                                  float* __restrict__ db,
+                                                                  int32_t* __restrict__ status) {
   chain_wait();
-  __shared__ float s_sum[8][32];
+  __shared__ float s_sum[kSumWarps][32];
   if (!rows_valid(seg, E, R, status)) return;
-  const int e = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   const int64_t r0 = seg_at(seg, e, R), r1 = seg_at(seg, e + 1, R);
   float s = 0.f;
   if (col < NP && r1 > r0) {
     const int64_t last = (r1 - 1) / kRowBlock;
-#pragma unroll 4
-    for (int64_t b = r0 / kRowBlock + warp; b <= last; b += 8) s += part[(b + e) * NP + col];
+#pragma unroll 8
+    for (int64_t b = r0 / kRowBlock + warp; b <= last; b += nw) s += part[(b + e) * NP + col];
   }
   s_sum[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && col < NP) {
-#pragma unroll
-    for (int w = 1; w < 8; ++w) s += s_sum[w][lane];
+    for (int w = 1; w < nw; ++w) s += s_sum[w][lane];
     db[(int64_t)e * NP + col] = s;
   }
 }
@@ -149,8 +148,11 @@ void act_backward_all(const ActGradArgs& a, cudaStream_t s) {
     });
   if (a.db != nullptr) {
     const int NP = a.act == LRM_ACT_SWIGLU ? 2 * a.N : a.N;
-    launch_chained(bias_sum_kernel, dim3((unsigned)((NP + 31) / 32), (unsigned)a.E), dim3(256), 0, s, a.seg_offsets,
-                   a.E, a.R, NP, (const float*)a.part, a.db, a.status);
+    // a warp for every four blocks of a mean segment
+    const int64_t warps = (a.R / kRowBlock / a.E + 3) / 4 + 1;
+    launch_chained(bias_sum_kernel, dim3((unsigned)((NP + 31) / 32), (unsigned)a.E),
+                   dim3(32 * (unsigned)(warps < kSumWarps ? warps : kSumWarps)), 0, s, a.seg_offsets, a.E, a.R, NP,
+                   (const float*)a.part, a.db, a.status);
   }
 }
 
