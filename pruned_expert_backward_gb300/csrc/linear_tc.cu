@@ -44,24 +44,28 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kABytes = kBM * kBK * 2;
 constexpr int kBoxBytes = 2048;  // 32 rows x 64 bytes, 64-byte swizzle: 32 bf16 or 16 fp32 columns
-constexpr int kBoxes = 3;        // boxes of an epilogue warp, used in turn
 
 enum Kind { FWD = 0, DX = 1, DW = 2 };
 
-template <int BN>
+template <int KIND, int BN>
 struct Cfg {
   static constexpr int kBBytes = BN / 2 * kBK * 2;  // this CTA's half of the columns
   static constexpr int kSlice = kABytes + kBBytes;
   static constexpr int kSub = BN == 256 ? 1 : 2;  // K slices of a stage
   static constexpr int kStage = kSub * kSlice;
-  static constexpr int kStages = BN == 256 ? 5 : (BN == 128 ? 3 : 4);
+  static constexpr int kStages = BN == 256 ? 6 : (BN == 128 ? 3 : 4);
+  // Store boxes that an epilogue warp uses in turn.  In the 256-column tile operand stages are worth more:
+  // with 5 stages and 3 boxes 65536 rows over 128 experts took 339 us (SwiGLU, K = 2048) and 334 us (DX)
+  // against 331 and 319 us; 16 epilogue warps and 5 stages 358 and 336 us.
+  static constexpr int kBoxes = BN == 256 ? (KIND == DW ? 2 : 1) : 3;
   static constexpr uint32_t kEpi = kStages * kStage;
   static constexpr uint32_t kBars = kEpi + kEpiWarps * kBoxes * kBoxBytes;
   static constexpr int kNBars = 2 * kStages + 5;  // full, empty, accumulator full[2] and empty[2], drain
   static constexpr int kTmem = BN == 64 ? 128 : 2 * BN;
-  static constexpr size_t smem() { return 1024 + kBars + kNBars * 8 + 16 + 4 * (LRM_MAX_EXPERTS + 2) + 4 * 16; }
+  static constexpr int kPrefix = KIND == DW ? 0 : LRM_MAX_EXPERTS + 2;
+  static constexpr size_t smem() { return 1024 + kBars + kNBars * 8 + 16 + 4 * (kPrefix + kThreads / 32); }
+  static_assert(1024 + kBars + kNBars * 8 + 16 + 4 * (kPrefix + kThreads / 32) <= 232448, "shared memory");
 };
-static_assert(Cfg<256>::smem() <= 232448 && Cfg<128>::smem() <= 232448 && Cfg<64>::smem() <= 232448, "shared memory");
 
 struct Params {
   int E;
@@ -73,6 +77,9 @@ struct Params {
   int tiles_m;    // DW: pair tiles along M
   int terms;      // 1, or 6 for fp32 inputs in three planes
   int pk;         // K slices per accumulator (PROMOTE)
+  // operands that are contiguous along M or N (DX: B, DW: both): both 64-column blocks of a CTA's 128 columns
+  // come in one box, where the columns are a multiple of 64 (else a box would wrap into the next row)
+  bool one_box_a, one_box_b;
   const int32_t* seg;       // NULL: one dense problem
   const int32_t* plan;      // DW with segments: [0] 1 if they are valid, [1 ..] experts, longest first
   const CUtensorMap* maps;  // DW with segments: [2][E] operand maps cut at the segment's end
@@ -92,8 +99,10 @@ __host__ __device__ constexpr uint32_t instr_desc(uint32_t a_mn, uint32_t b_mn) 
          ((uint32_t)((2 * kBM) >> 4) << 24);
 }
 
-__device__ __forceinline__ void bulk_wait_read_boxes() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBoxes - 1) : "memory");
+// At most N of this thread's bulk stores have not read their shared memory yet.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 // The i-th tile of a CTA pair: round robin, every second round backwards, so that where the tiles get
@@ -146,14 +155,27 @@ __device__ __forceinline__ Tile decode(const Params& p, const int* prefix, int t
   return d;
 }
 
+// BLOCKS blocks of 64 columns from column c0 and 64 rows from r of matrix g.
+template <int BLOCKS>
+__device__ __forceinline__ void load_columns(uint32_t dst, const CUtensorMap* map, int c0, int r, int g, bool one_box,
+                                             uint32_t bar) {
+  if (one_box) {
+    tma_load_4d_pair(dst, map, 0, r, c0 / 64, g, bar);
+  } else {
+#pragma unroll
+    for (int c = 0; c < BLOCKS; ++c) tma_load_3d_pair(dst + c * 8192, map, c0 + c * 64, r, g, bar);
+  }
+}
+
 // 32 columns of one row per lane go out: whole 32-row blocks through the warp's next box(es) and TMA
 // (which clips columns past the tensor), others by each live lane.
+template <int BOXES>
 struct Out {
   uint8_t* boxes;
   uint32_t boxes_s;
   int next;
   __device__ __forceinline__ void box(const uint4 (&q)[4], const CUtensorMap* map, int lane, int n, int row, int e) {
-    if (lane == 0) bulk_wait_read_boxes();  // the store that used this box has read it
+    if (lane == 0) bulk_wait_read<BOXES - 1>();  // the store that used this box has read it
     __syncwarp();
     uint8_t* line = boxes + next * kBoxBytes + lane * 64;
     const int swz = (lane >> 1) & 3;  // 64-byte swizzle: piece j of row r sits at j ^ ((r >> 1) & 3)
@@ -162,7 +184,7 @@ struct Out {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) tma_store_3d(map, boxes_s + next * kBoxBytes, n, row, e);
-    next = next + 1 == kBoxes ? 0 : next + 1;
+    next = next + 1 == BOXES ? 0 : next + 1;
   }
   template <typename T>
   __device__ __forceinline__ void put(const float (&v)[32], const CUtensorMap* map, int lane, int n, int cols, int row,
@@ -205,6 +227,18 @@ __device__ __forceinline__ void add_row(float (&v)[32], const T* row, int n, int
     }
 }
 
+template <typename T>
+__device__ __forceinline__ void add_vectors(float (&v)[32], const uint4* r) {
+  constexpr int VN = VecTraits<T>::N;
+#pragma unroll
+  for (int j = 0; j < 32 / VN; ++j) {
+    float f[VN];
+    unpack(r[j], f);
+#pragma unroll
+    for (int i = 0; i < VN; ++i) v[j * VN + i] += f[i];
+  }
+}
+
 template <int ACT>
 __device__ __forceinline__ void act32(float (&v)[32]) {
 #pragma unroll
@@ -215,7 +249,7 @@ template <int KIND, int BN, bool GLU, bool PROMOTE, typename TI, typename TO>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ, const Params p) {
-  using C = Cfg<BN>;
+  using C = Cfg<KIND, BN>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -223,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::kNBars);
   int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
   int* prefix = abort_flag + 3;                   // [E + 1] row tiles before each expert
-  int* scan = prefix + LRM_MAX_EXPERTS + 2;       // [kThreads / 32]
+  int* scan = prefix + C::kPrefix;       // [kThreads / 32]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
@@ -329,20 +363,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t a_dst = smem_u32(smem + s * C::kStage + j * C::kSlice), b_dst = a_dst + kABytes;
             if (KIND == DW) {
               const int r = d.row0 + k;
-              if (d.has_rows) {
-                tma_load_3d_pair(a_dst, ma, d.m0, r, pa, fb);
-                tma_load_3d_pair(a_dst + 8192, ma, d.m0 + 64, r, pa, fb);
-              }
-#pragma unroll
-              for (int c = 0; c < BN / 128; ++c) tma_load_3d_pair(b_dst + c * 8192, mb, nb + c * 64, r, pb, fb);
+              if (d.has_rows) load_columns<2>(a_dst, ma, d.m0, r, pa, p.one_box_a, fb);
+              load_columns<BN / 128>(b_dst, mb, nb, r, pb, p.one_box_b, fb);
             } else {
               if (d.has_rows) tma_load_3d_pair(a_dst, ma, k, d.row0, pa, fb);
               const int eb = d.e * planes + pb;
               if (KIND == FWD) {
                 tma_load_3d_pair(b_dst, mb, k, nb, eb, fb);
               } else {
-#pragma unroll
-                for (int c = 0; c < BN / 128; ++c) tma_load_3d_pair(b_dst + c * 8192, mb, nb + c * 64, k, eb, fb);
+                load_columns<BN / 128>(b_dst, mb, nb, k, eb, p.one_box_b, fb);
               }
             }
             if (++kb == d.slices) { kb = 0; ++term; }
@@ -400,16 +429,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait(drain, 0, abortv, p.status, false);  // all MMAs into this CTA's TMEM are done before it is freed
   } else {
     // ---------------------------------------------------------------- epilogue --------
-    constexpr int NC = BN / 64;  // 32-column chunks of a warp (SwiGLU: the second half are up columns)
+    // a warp reads one 32-row quarter of TMEM and its group's half of the columns
+    constexpr int GROUPS = kEpiWarps / 4;
+    constexpr int NC = BN / GROUPS / 32;  // 32-column chunks of a warp (SwiGLU: the second half are up columns)
     constexpr int NO = GLU ? NC / 2 : NC;
-    static_assert(NO > 0, "a SwiGLU tile needs BN >= 128");
-    const int ew = warp - 2, q = warp & 3, half = ew >> 2;
-    Out out{smem + C::kEpi + ew * kBoxes * kBoxBytes, smem_u32(smem + C::kEpi + ew * kBoxes * kBoxBytes), 0};
+    static_assert(NO > 0, "a warp needs a chunk of output columns");
+    const int ew = warp - 2, q = warp & 3, group = ew >> 2;
+    uint8_t* boxes = smem + C::kEpi + ew * C::kBoxes * kBoxBytes;
+    Out<C::kBoxes> out{boxes, smem_u32(boxes), 0};
+    constexpr int NR = 32 / VecTraits<TO>::N;  // 16-byte pieces of a chunk's row
     const int NP = GLU ? 2 * p.N : p.N;
     // TMEM column of chunk c
     auto tcol = [&](int c) {
-      return GLU ? (c < NO ? half * (BN / 4) + c * 32 : BN / 2 + half * (BN / 4) + (c - NO) * 32)
-                 : half * (BN / 2) + c * 32;
+      return GLU ? (c < NO ? (group * NO + c) * 32 : BN / 2 + (group * NO + c - NO) * 32) : (group * NC + c) * 32;
     };
     uint32_t use = 0;
     bool ok = true;
@@ -424,13 +456,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = nrows == 32 || (nrows > 0 && (KIND == DW || p.seg == nullptr));
       const bool live = lane < nrows;
       const int64_t row = row_base + lane;
-      const int n_first = d.n0 + half * (GLU ? BN / 4 : BN / 2);
+      const int n_first = d.n0 + group * NO * 32;
       const int total = d.slices * p.terms;
       const TO* res = KIND == FWD && p.residual != nullptr && live ? static_cast<const TO*>(p.residual) + row * p.N : nullptr;
       TO* y_row = static_cast<TO*>(p.y) + (KIND == DW ? ((int64_t)d.e * p.M + row) : row) * p.N;
 
+      // the residual of chunk c (zeros past the last column)
+      auto load_residual = [&](int c, uint4* r) {
+        const int n = n_first + c * 32;
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+          r[j] = res != nullptr && n + j * VecTraits<TO>::N < p.N
+                     ? *reinterpret_cast<const uint4*>(res + n + j * VecTraits<TO>::N)
+                     : make_uint4(0, 0, 0, 0);
+      };
       // one chunk of 32 output columns: v holds the products (and u, for SwiGLU, the up columns')
-      auto finish = [&](int c, float (&v)[32], float (&u)[32]) {
+      auto finish = [&](int c, float (&v)[32], float (&u)[32], const uint4* r) {
         const int n = n_first + c * 32;
         if (nrows <= 0 || n >= p.N) return;  // warp-uniform
         if (KIND == FWD) {
@@ -458,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               default: break;
             }
           }
-          if (res != nullptr) add_row(v, res, n, p.N);
+          if (res != nullptr) add_vectors<TO>(v, r);
         }
         out.put(v, &tmY, lane, n, p.N, row_base, KIND == DW ? d.e : 0, whole, live, y_row);
       };
@@ -475,11 +516,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t tbase = tmem_base + a * BN + ((uint32_t)(q * 32) << 16);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            uint32_t r[32];
-            tmem_ld32(tbase + tcol(c), r);
+          for (int c = 0; c < 2 * NC; ++c) {
+            uint32_t r[16];
+            tmem_ld16(tbase + tcol(c / 2) + (c & 1) * 16, r);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[c][i] += __uint_as_float(r[i]);
+            for (int i = 0; i < 16; ++i) acc[c / 2][(c & 1) * 16 + i] += __uint_as_float(r[i]);
           }
           tc_fence_before();
           __syncwarp();
@@ -487,8 +528,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
 #pragma unroll
-        for (int c = 0; c < NO; ++c) finish(c, acc[c], acc[GLU ? NO + c : c]);
+        for (int c = 0; c < NO; ++c) {
+          uint4 r[NR];
+          load_residual(c, r);
+          finish(c, acc[c], acc[GLU ? NO + c : c], r);
+        }
       } else {
+        uint4 res_next[NR];  // loaded a chunk ahead, the first before the products are done
+        load_residual(0, res_next);
         const uint32_t a = use & 1u;
         if (!mbar_wait(accf0 + 8 * a, (use >> 1) & 1u, abortv, p.status)) { ok = false; break; }
         ++use;
@@ -496,6 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tbase = tmem_base + a * BN + ((uint32_t)(q * 32) << 16);
         for (int c = 0; c < NO; ++c) {
           uint32_t r[32], w[32];
+          uint4 res_now[NR];
+#pragma unroll
+          for (int j = 0; j < NR; ++j) res_now[j] = res_next[j];
+          if (c + 1 < NO) load_residual(c + 1, res_next);
           tmem_ld32(tbase + tcol(c), r);
           if (GLU) tmem_ld32(tbase + tcol(NO + c), w);
           float v[32], u[32];
@@ -504,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             v[i] = __uint_as_float(r[i]);
             u[i] = GLU ? __uint_as_float(w[i]) : 0.f;
           }
-          finish(c, v, u);
+          finish(c, v, u, res_now);
         }
         tc_fence_before();
         __syncwarp();
@@ -561,30 +612,39 @@ __global__ void __launch_bounds__(1024) linear_plan_kernel(const int32_t* __rest
   }
 }
 
-// x (fp32, [groups][n]) as three bf16 planes [groups][3][n] whose sum is x to 24 bits.
-__global__ void __launch_bounds__(256) split_planes_kernel(const float* __restrict__ x, int64_t groups, int64_t n,
-                                                           __nv_bfloat16* __restrict__ out) {
+// fp32 tensors [groups][n] as three bf16 planes [groups][3][n] whose sum is the tensor to 24 bits (a value
+// that is not finite stays in the first plane alone, so that no infinity is subtracted from itself).
+struct Split {
+  const float* x;
+  int64_t groups, n;
+  __nv_bfloat16* out;
+};
+struct Splits {
+  Split t[3];
+  int count;
+};
+__global__ void __launch_bounds__(256) split_planes_kernel(const __grid_constant__ Splits a) {
   chain_wait();
-  const int64_t total = groups * n / 8;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t at = i * 8, g = at / n, c = at - g * n;
-    float a[4], b[4], v[8], p[3][8];
-    unpack(ld_stream16(x + at), a);
-    unpack(ld_stream16(x + at + 4), b);
+  for (int k = 0; k < a.count; ++k) {
+    const Split& s = a.t[k];
+    const int64_t total = s.groups * s.n / 8;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+      const int64_t at = i * 8, g = at / s.n, c = at - g * s.n;
+      const uint4 lo = ld_stream16_now(s.x + at), hi = ld_stream16_now(s.x + at + 4);
+      float a4[4], b4[4], p[3][8];
+      unpack(lo, a4);
+      unpack(hi, b4);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      v[q] = a[q];
-      v[4 + q] = b[q];
+      for (int q = 0; q < 8; ++q) {
+        const float v = q < 4 ? a4[q & 3] : b4[q & 3];
+        p[0][q] = __bfloat162float(__float2bfloat16_rn(v));
+        const float r1 = isfinite(p[0][q]) ? v - p[0][q] : 0.f;  // exact
+        p[1][q] = __bfloat162float(__float2bfloat16_rn(r1));
+        p[2][q] = r1 - p[1][q];
+      }
+#pragma unroll
+      for (int j = 0; j < 3; ++j) st16(s.out + (g * 3 + j) * s.n + c, pack(p[j]));
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      p[0][q] = __bfloat162float(__float2bfloat16_rn(v[q]));
-      const float r1 = v[q] - p[0][q];  // exact
-      p[1][q] = __bfloat162float(__float2bfloat16_rn(r1));
-      p[2][q] = r1 - p[1][q];
-    }
-#pragma unroll
-    for (int j = 0; j < 3; ++j) st16(out + (g * 3 + j) * n + c, pack(p[j]));
   }
 }
 
@@ -606,6 +666,20 @@ bool make_map(CUtensorMap* m, const void* base, bool f32, uint64_t d0, uint64_t 
 bool operand_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t planes, uint32_t box_rows) {
   return make_map(m, base, false, cols, rows, planes, cols * 2, rows * cols * 2, 64, box_rows, true);
 }
+// The same seen as [planes][cols / 64][rows][64], `blocks` blocks of 64 columns and 64 rows a box; the plain
+// form with one block where the columns do not divide (*one_box tells).
+bool column_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t planes, uint32_t blocks,
+                bool* one_box) {
+  *one_box = cols % 64 == 0 && cols >= 64 * blocks;
+  if (!*one_box) return operand_map(m, base, cols, rows, planes, 64);
+  const cuuint64_t dims[4] = {64, rows, cols / 64, planes};
+  const cuuint64_t strides[3] = {cols * 2, 128, rows * cols * 2};
+  const cuuint32_t box[4] = {64, 64, blocks, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 // An output [groups][rows][cols] in 32-row boxes of 64 bytes; halves: [rows][2][cols] seen as two groups.
 bool output_map(CUtensorMap* m, const void* base, bool f32, uint64_t cols, uint64_t rows, uint64_t groups,
                 bool halves = false) {
@@ -617,7 +691,8 @@ template <int KIND, int BN, bool GLU, bool PROMOTE, typename TI, typename TO>
 lrm_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& y, const CUtensorMap& z,
                   const Params& p, int64_t tiles_bound, cudaStream_t s) {
   constexpr auto kernel = linear_tc_kernel<KIND, BN, GLU, PROMOTE, TI, TO>;
-  const size_t smem = Cfg<BN>::smem();
+  using C = Cfg<KIND, BN>;
+  const size_t smem = C::smem();
   if (ensure_max_smem<kernel>((int)smem) != cudaSuccess) return LRM_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -646,10 +721,14 @@ lrm_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap&
   return cudaGetLastError() == cudaSuccess ? LRM_OK : LRM_ERR_CUDA;
 }
 
-void split_planes(const void* x, int64_t groups, int64_t n, void* out, cudaStream_t s) {
-  const int64_t blocks = (groups * n / 8 + 255) / 256;
-  launch_chained(split_planes_kernel, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), dim3(256), 0, s, (const float*)x,
-                 groups, n, (__nv_bfloat16*)out);
+void add_split(Splits& a, const void* x, int64_t groups, int64_t n, void* out) {
+  a.t[a.count++] = Split{static_cast<const float*>(x), groups, n, static_cast<__nv_bfloat16*>(out)};
+}
+void launch_splits(const Splits& a, cudaStream_t s) {
+  int64_t most = 1;
+  for (int k = 0; k < a.count; ++k) most = a.t[k].groups * a.t[k].n / 8 > most ? a.t[k].groups * a.t[k].n / 8 : most;
+  const int64_t blocks = (most + 255) / 256;
+  launch_chained(split_planes_kernel, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), dim3(256), 0, s, a);
 }
 
 // K slices per accumulator where the result is fp32: 256 products for split fp32 inputs (5e-7 off at
@@ -687,11 +766,13 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
   const void *xs = a.x, *wsrc = a.w;
   if (f32) {
     char* b = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws) + 127) & ~uintptr_t(127));
-    split_planes(a.x, 1, a.R * a.K, b, s);
+    Splits sp{};
+    add_split(sp, a.x, 1, a.R * a.K, b);
     xs = b;
     b += (linear_planes_bytes(a.R, a.K) + 255) / 256 * 256;
-    split_planes(a.w, a.E, (int64_t)NP * a.K, b, s);
+    add_split(sp, a.w, a.E, (int64_t)NP * a.K, b);
     wsrc = b;
+    launch_splits(sp, s);
   }
   Params p{};
   p.E = a.E;
@@ -745,8 +826,9 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
   CUtensorMap* maps = reinterpret_cast<CUtensorMap*>(b);
   int32_t* plan = reinterpret_cast<int32_t*>(b + 2 * sizeof(CUtensorMap) * (size_t)a.E);
   b += linear_plan_bytes(a.E);
+  Splits sp{};
   auto split = [&](const void* src, int64_t groups, int64_t n) {
-    split_planes(src, groups, n, b, s);
+    add_split(sp, src, groups, n, b);
     const void* at = b;
     b += ((size_t)groups * n * 6 + 255) / 256 * 256;
     return at;
@@ -755,6 +837,7 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
     dzs = split(a.dz, 1, a.R * a.N);
     if (a.dx != nullptr) wsrc = split(a.w, a.E, (int64_t)a.N * a.K);
     if (a.dw != nullptr) xs = split(a.x, 1, a.R * a.K);
+    launch_splits(sp, s);
   }
   Params p{};
   p.E = a.E;
@@ -769,15 +852,8 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
     p.M = a.N;
     p.y = a.dw;
     p.tiles_m = (a.N + 2 * kBM - 1) / (2 * kBM);
-    if (!operand_map(&mA, dzs, a.N, a.R, planes, 64) || !operand_map(&mB, xs, a.K, a.R, planes, 64) ||
-        !output_map(&mY, a.dw, true, a.K, a.N, a.E))
+    if (!column_map(&mA, dzs, a.N, a.R, planes, 2, &p.one_box_a) || !output_map(&mY, a.dw, true, a.K, a.N, a.E))
       return LRM_ERR_CUDA;
-    if (a.seg_offsets != nullptr) {
-      const MapPair tpl{{mA, mB}};
-      launch_chained(linear_plan_kernel, dim3(1), dim3(1024), 0, s, a.seg_offsets, a.E, a.R, plan, maps, tpl, a.status);
-      p.plan = plan;
-      p.maps = maps;
-    }
     const int64_t tm = (int64_t)a.E * p.tiles_m;
     const lrm_status st = with_width(tm, a.K, 128, [&](auto bn) {
       constexpr int BN = decltype(bn)::value;
@@ -785,6 +861,14 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
         return LRM_ERR_UNSUPPORTED;
       } else {
         p.tiles_n = (a.K + BN - 1) / BN;
+        if (!column_map(&mB, xs, a.K, a.R, planes, BN / 128, &p.one_box_b)) return LRM_ERR_CUDA;
+        if (a.seg_offsets != nullptr) {
+          const MapPair tpl{{mA, mB}};
+          launch_chained(linear_plan_kernel, dim3(1), dim3(1024), 0, s, a.seg_offsets, a.E, a.R, plan, maps, tpl,
+                         a.status);
+          p.plan = plan;
+          p.maps = maps;
+        }
         return launch<DW, BN, false, true, B16, float>(mA, mB, mY, mY, p, tm * p.tiles_n, s);
       }
     });
@@ -793,8 +877,7 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
   if (a.dx != nullptr) {
     p.red = a.N;
     p.y = a.dx;
-    if (!operand_map(&mA, dzs, a.N, a.R, planes, kBM) ||
-        !operand_map(&mB, wsrc, a.K, a.N, (uint64_t)a.E * planes, 64) || !output_map(&mY, a.dx, f32, a.K, a.R, 1))
+    if (!operand_map(&mA, dzs, a.N, a.R, planes, kBM) || !output_map(&mY, a.dx, f32, a.K, a.R, 1))
       return LRM_ERR_CUDA;
     const int64_t tm = row_tiles(a.seg_offsets, a.R, a.E);
     return with_width(likely_row_tiles(a.seg_offsets, a.R, a.E), a.K, 128, [&](auto bn) {
@@ -803,6 +886,7 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
         return LRM_ERR_UNSUPPORTED;
       } else {
         p.tiles_n = (a.K + BN - 1) / BN;
+        if (!column_map(&mB, wsrc, a.K, a.N, (uint64_t)a.E * planes, BN / 128, &p.one_box_b)) return LRM_ERR_CUDA;
         if (f32) return launch<DX, BN, false, true, float, float>(mA, mB, mY, mY, p, tm * p.tiles_n, s);
         return launch<DX, BN, false, false, B16, B16>(mA, mB, mY, mY, p, tm * p.tiles_n, s);
       }

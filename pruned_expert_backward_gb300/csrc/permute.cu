@@ -10,9 +10,9 @@
 //
 // sort: up to kSmallPairs pairs one launch does everything: every CTA ranks all pairs for itself
 // (a few hundred nanoseconds in shared memory) and copies the rows of its own tokens.  Beyond that
-// three launches: counts of each chunk of pairs, the scan of every expert's counts down the chunks,
-// and a third that ranks a chunk's pairs and copies its tokens' rows (a token's row is read once and
-// written k times).
+// several launches: counts of each chunk of pairs, the scan of every expert's counts down the chunks,
+// and the ranking of each chunk's pairs.  A token's row is read once and written k times, by a fourth
+// launch with a CTA per token, or beside the ranking where rows are narrow.
 // No atomics on anything that decides an order: all results are deterministic.
 #include "common.cuh"
 #include "kernels.h"
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(1024) sort_small_kernel(const int32_t* __restr
     for (int t = blockIdx.x; t < n_tok; t += gridDim.x) copy_rows(x, x_s, s_row + t * k, t, 1, k, H);
 }
 
-// ---------------------------------------------------------------- three launches -----
+// ---------------------------------------------------------------- several launches ---
 __global__ void __launch_bounds__(kChunkThreads) sort_count_kernel(const int32_t* __restrict__ idx, int64_t P, int E,
                                                                    int chunk, int32_t* __restrict__ counts,
                                                                    int32_t* __restrict__ status) {
@@ -227,6 +227,35 @@ __global__ void __launch_bounds__(kChunkThreads) sort_rows_kernel(
   }
   __syncthreads();
   if (x_s != nullptr) copy_rows(x, x_s, s_row, t0, ntok, k, H);
+}
+
+// One CTA per token copies its row into its pairs' rows; CTA t also zeroes every n_tok-th row behind the
+// last segment, from seg[E] + t on.
+template <typename T>
+__global__ void __launch_bounds__(256) sort_copy_kernel(const int32_t* __restrict__ row_of_pair,
+                                                        const int32_t* __restrict__ seg, const T* __restrict__ x,
+                                                        int64_t n_tok, int k, int E, int H, T* __restrict__ x_s) {
+  chain_wait();
+  constexpr int VN = VecTraits<T>::N;
+  __shared__ int s_row[LRM_MAX_TOPK];
+  const int64_t t = blockIdx.x;
+  if (threadIdx.x < k) s_row[threadIdx.x] = row_of_pair[t * k + threadIdx.x];
+  __syncthreads();
+  const int nv = H / VN;
+  for (int v0 = threadIdx.x; v0 < nv; v0 += 2 * blockDim.x) {
+    const int v1 = v0 + blockDim.x;
+    const uint4 a = ld_stream16_now(x + t * H + (int64_t)v0 * VN);
+    uint4 b = a;
+    if (v1 < nv) b = ld_stream16_now(x + t * H + (int64_t)v1 * VN);
+    for (int j = 0; j < k; ++j) {
+      if (s_row[j] < 0) continue;
+      T* row = x_s + (int64_t)s_row[j] * H;
+      st16(row + (int64_t)v0 * VN, a);
+      if (v1 < nv) st16(row + (int64_t)v1 * VN, b);
+    }
+  }
+  for (int64_t r = seg[E] + t; r < n_tok * k; r += n_tok)
+    for (int v = threadIdx.x; v < nv; v += blockDim.x) st16(x_s + r * H + (int64_t)v * VN, make_uint4(0, 0, 0, 0));
 }
 
 // ---------------------------------------------------------------- the way back -------
@@ -305,6 +334,109 @@ __global__ void __launch_bounds__(256) combine_kernel(const int32_t* __restrict_
   }
 }
 
+// Narrow rows (at most 32 columns of 16 bytes): a warp per token, a lane per column, 8 row loads in flight.
+template <typename T>
+__global__ void __launch_bounds__(256) combine_narrow_kernel(const int32_t* __restrict__ row_of_pair,
+                                                             const float* __restrict__ alpha,
+                                                             const T* __restrict__ y_s, const T* residual,
+                                                             int64_t n_tok, int k, int H, int64_t cap, T* y,
+                                                             int32_t* __restrict__ status) {
+  chain_wait();
+  constexpr int VN = VecTraits<T>::N;
+  constexpr int L = kCombineLoads;
+  const int lane = threadIdx.x & 31, nv = H / VN;
+  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t >= n_tok) return;
+  const bool in = lane < nv;
+  int r = -1;  // lane j holds pair j's row and weight
+  float w = 0.f;
+  if (lane < k) {
+    r = (int)checked_row(row_of_pair[t * k + lane], cap, status);
+    w = alpha[t * k + lane];
+  }
+  float acc[VN];
+#pragma unroll
+  for (int q = 0; q < VN; ++q) acc[q] = 0.f;
+  for (int j0 = 0; j0 < k; j0 += L) {
+    uint4 vals[L];
+#pragma unroll
+    for (int m = 0; m < L; ++m) {
+      const int row = __shfl_sync(0xffffffffu, r, (j0 + m) & 31);
+      if (in && j0 + m < k && row >= 0) vals[m] = ld_stream16_now(y_s + (int64_t)row * H + lane * VN);
+    }
+#pragma unroll
+    for (int m = 0; m < L; ++m) {
+      const int row = __shfl_sync(0xffffffffu, r, (j0 + m) & 31);
+      const float wj = __shfl_sync(0xffffffffu, w, (j0 + m) & 31);
+      if (!in || j0 + m >= k || row < 0) continue;
+      float f[VN];
+      unpack(vals[m], f);
+#pragma unroll
+      for (int q = 0; q < VN; ++q) acc[q] = fmaf(wj, f[q], acc[q]);
+    }
+  }
+  if (!in) return;
+  if (residual != nullptr) {
+    float f[VN];
+    unpack(*reinterpret_cast<const uint4*>(residual + t * H + lane * VN), f);
+#pragma unroll
+    for (int q = 0; q < VN; ++q) acc[q] += f[q];
+  }
+  st16(y + t * H + lane * VN, pack(acc));
+}
+
+// The gradient for narrow rows: a warp per token.
+template <typename T>
+__global__ void __launch_bounds__(256) combine_backward_narrow_kernel(
+    const int32_t* __restrict__ row_of_pair, const float* __restrict__ alpha, const T* __restrict__ dy,
+    const T* __restrict__ y_s, int64_t n_tok, int k, int H, int64_t cap, T* __restrict__ dy_s,
+    float* __restrict__ dalpha, int32_t* __restrict__ status) {
+  chain_wait();
+  constexpr int VN = VecTraits<T>::N;
+  constexpr int L = kCombineLoads;
+  const int lane = threadIdx.x & 31, nv = H / VN;
+  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t >= n_tok) return;
+  const bool in = lane < nv;
+  int r = -1;
+  float w = 0.f, mine = 0.f;  // lane j ends with pair j's dot product
+  if (lane < k) {
+    r = (int)checked_row(row_of_pair[t * k + lane], cap, status);
+    w = alpha[t * k + lane];
+  }
+  float d[VN];
+  unpack(in ? ldg16(dy + t * H + lane * VN) : make_uint4(0, 0, 0, 0), d);
+  for (int j0 = 0; j0 < k; j0 += L) {
+    uint4 vals[L];
+#pragma unroll
+    for (int m = 0; m < L; ++m) {
+      const int row = __shfl_sync(0xffffffffu, r, (j0 + m) & 31);
+      if (y_s != nullptr && in && j0 + m < k && row >= 0)
+        vals[m] = ld_stream16_now(y_s + (int64_t)row * H + lane * VN);
+    }
+#pragma unroll
+    for (int m = 0; m < L; ++m) {
+      const int row = __shfl_sync(0xffffffffu, r, (j0 + m) & 31);
+      const float wj = __shfl_sync(0xffffffffu, w, (j0 + m) & 31);
+      if (j0 + m >= k || row < 0) continue;  // warp-uniform
+      float dot = 0.f, f[VN];
+      if (in) {
+        if (y_s != nullptr) {
+          unpack(vals[m], f);
+#pragma unroll
+          for (int q = 0; q < VN; ++q) dot = fmaf(d[q], f[q], dot);
+        }
+#pragma unroll
+        for (int q = 0; q < VN; ++q) f[q] = wj * d[q];
+        st16(dy_s + (int64_t)row * H + lane * VN, pack(f));
+      }
+      dot = warp_sum(dot);
+      if (lane == j0 + m) mine = dot;
+    }
+  }
+  if (dalpha != nullptr && lane < k) dalpha[t * k + lane] = mine;
+}
+
 // One CTA per token: dy_t is read once; every routed pair's y_s row is read for its dot product with
 // dy_t and its dy_s row written, KB pairs at a time (their loads in flight together).
 template <typename T, int KB>
@@ -370,6 +502,12 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const int32_t* __
   }
 }
 
+// Threads of a row of `nv` 16-byte columns: up to 256, and as few as the same number of passes needs.
+int row_threads(int nv) {
+  const int passes = (nv + 255) / 256;
+  return ((nv + passes - 1) / passes + 31) / 32 * 32;
+}
+
 template <typename T>
 lrm_status sort_all(const SortArgs& a, cudaStream_t s) {
   const int64_t P = a.T * a.k;
@@ -393,9 +531,19 @@ lrm_status sort_all(const SortArgs& a, cudaStream_t s) {
                    chunk_tok * a.k, a.counts, a.status);
     launch_chained(sort_colscan_kernel, dim3(B), dim3(nc > 256 ? 1024 : 256), 0, s, a.counts, nc, B, a.loads);
     const size_t smem = sizeof(int) * ((size_t)B * (1 + kChunkThreads / 32) + kChunkThreads);
+    // Rows of 1 KB and more are copied by a launch of their own, a CTA per token (T = 32768, k = 8, H = 4096:
+    // 370 against 394 us; T = 2048, H = 2048: 16 against 56 us), narrower ones beside the ranking (T = 30000,
+    // H = 72: 16 against 41 us).
+    const bool apart = a.x_s != nullptr && a.H >= 64 * VecTraits<T>::N;
     launch_chained(sort_rows_kernel<T>, dim3((unsigned)nc), dim3(kChunkThreads), smem, s, a.topk_idx, (const T*)a.x,
                    a.T, a.k, a.E, a.H, chunk_tok, (const int32_t*)a.counts, (const int32_t*)a.loads, a.seg_offsets,
-                   a.pair_of_row, a.row_of_pair, (T*)a.x_s);
+                   a.pair_of_row, a.row_of_pair, apart ? (T*)nullptr : (T*)a.x_s);
+    if (apart) {
+      const int cols = row_threads((a.H / VecTraits<T>::N + 1) / 2);
+      launch_chained(sort_copy_kernel<T>, dim3((unsigned)a.T), dim3(cols < 64 ? 64 : cols), 0, s,
+                     (const int32_t*)a.row_of_pair, (const int32_t*)a.seg_offsets, (const T*)a.x, a.T, a.k, a.E, a.H,
+                     (T*)a.x_s);
+    }
   }
   return cudaGetLastError() == cudaSuccess ? LRM_OK : LRM_ERR_CUDA;
 }
@@ -404,15 +552,18 @@ template <typename T>
 void combine_all(const int32_t* row_of_pair, const float* alpha, const void* y_s, const void* residual, int64_t n_tok,
                  int32_t k, int32_t H, int64_t cap, void* y, int32_t* status, cudaStream_t s) {
   const int nv = H / VecTraits<T>::N;
+  if (nv <= 32) {
+    launch_chained(combine_narrow_kernel<T>, dim3((unsigned)((n_tok + 7) / 8)), dim3(256), 0, s, row_of_pair, alpha,
+                   (const T*)y_s, (const T*)residual, n_tok, k, H, cap, (T*)y, status);
+    return;
+  }
   // few tokens: one token and 64 columns per CTA, so that the rows spread over the GPU
   if (n_tok < 2048) {
     launch_chained(combine_kernel<T, 1>, dim3((unsigned)n_tok, (unsigned)((nv + 63) / 64)), dim3(64), 0, s,
                    row_of_pair, alpha, (const T*)y_s, (const T*)residual, n_tok, k, H, cap, (T*)y, status);
     return;
   }
-  int threads = (nv + 31) / 32 * 32;
-  if (threads > 256) threads = 256;
-  launch_chained(combine_kernel<T, 8>, dim3((unsigned)((n_tok + 7) / 8)), dim3(threads), 0, s, row_of_pair, alpha,
+  launch_chained(combine_kernel<T, 8>, dim3((unsigned)((n_tok + 7) / 8)), dim3(row_threads(nv)), 0, s, row_of_pair, alpha,
                  (const T*)y_s, (const T*)residual, n_tok, k, H, cap, (T*)y, status);
 }
 
@@ -420,9 +571,12 @@ template <typename T>
 void combine_backward_all(const int32_t* row_of_pair, const float* alpha, const void* dy, const void* y_s, int64_t n_tok,
                           int32_t k, int32_t H, int64_t cap, void* dy_s, float* dalpha, int32_t* status,
                           cudaStream_t s) {
-  int threads = (H / VecTraits<T>::N + 31) / 32 * 32;
-  if (threads > 256) threads = 256;
-  launch_chained(combine_backward_kernel<T, 8>, dim3((unsigned)n_tok), dim3(threads), 0, s, row_of_pair, alpha,
+  if (H / VecTraits<T>::N <= 32) {
+    launch_chained(combine_backward_narrow_kernel<T>, dim3((unsigned)((n_tok + 7) / 8)), dim3(256), 0, s, row_of_pair,
+                   alpha, (const T*)dy, (const T*)y_s, n_tok, k, H, cap, (T*)dy_s, dalpha, status);
+    return;
+  }
+  launch_chained(combine_backward_kernel<T, 8>, dim3((unsigned)n_tok), dim3(row_threads(H / VecTraits<T>::N)), 0, s, row_of_pair, alpha,
                  (const T*)dy, (const T*)y_s, k, H, cap, (T*)dy_s, dalpha, status);
 }
 
