@@ -8,7 +8,8 @@
 // tcgen05.mma.cta_group::2: each CTA stages its own 128 rows of A and half of the BN columns of B per
 // 64-deep K slice and holds 128 rows of the fp32 accumulator in TMEM, twice, so that one tile's
 // epilogue runs under the next tile's products.  Warp 0 issues the TMA loads, warp 1 of the leader the
-// MMAs, warps 2-9 are the epilogue: two per 32-row TMEM quarter, each taking half of the columns.
+// MMAs (whole warps run the loops and one elected lane issues: under a lane test instead, an MMA took 62-75
+// cycles to issue, not 26, and narrow tiles 0.21 us a K slice, not 0.155), warps 2-9 are the epilogue: two per 32-row TMEM quarter, each taking half of the columns.
 // A SwiGLU tile's columns are BN / 2 gate columns (the leader's half of B) and the BN / 2 up columns
 // that go with them (the other CTA's).
 //
@@ -328,39 +329,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer ----
-    if (lane == 0) {
-      uint32_t it = 0, st = 0, sph = 0;
-      bool ok = true;
-      int last_e = -1;
-      for (int i = 0, t; i < rounds && ok; ++i) {
-        t = nth_tile(i, pair, n_pairs);
-        if (t >= n_tiles) continue;  // (a last round may leave some pairs without one)
-        const Tile d = decode<KIND, BN, GLU>(p, prefix, t, rank);
-        const CUtensorMap *ma = &tmA, *mb = &tmB;
-        if (KIND == DW && p.seg != nullptr) {
-          ma = p.maps + d.e;
-          mb = p.maps + p.E + d.e;
-          if (d.e != last_e && d.slices > 0) {
-            tensormap_acquire(ma);
-            tensormap_acquire(mb);
-            last_e = d.e;
-          }
+    uint32_t it = 0, st = 0, sph = 0;
+    bool ok = true;
+    int last_e = -1;
+    for (int i = 0, t; i < rounds && ok; ++i) {
+      t = nth_tile(i, pair, n_pairs);
+      if (t >= n_tiles) continue;  // (a last round may leave some pairs without one)
+      const Tile d = decode<KIND, BN, GLU>(p, prefix, t, rank);
+      const CUtensorMap *ma = &tmA, *mb = &tmB;
+      if (KIND == DW && p.seg != nullptr) {
+        ma = p.maps + d.e;
+        mb = p.maps + p.E + d.e;
+        if (d.e != last_e && d.slices > 0) {
+          tensormap_acquire(ma);
+          tensormap_acquire(mb);
+          last_e = d.e;
         }
-        // first B row (FWD: rows of w, a SwiGLU pair stages gate rows and up rows) or column of this CTA
-        const int nb = GLU ? d.n0 + rank * p.N : d.n0 + rank * (BN / 2);
-        const uint32_t bytes = C::kBBytes + (d.has_rows ? kABytes : 0);
-        const int planes = p.terms > 1 ? 3 : 1, total = d.slices * p.terms;
-        int term = 6 - p.terms, kb = 0;
-        for (int k0 = 0; k0 < total; k0 += C::kSub, ++it) {
-          const uint32_t s = st, ph = sph;
-          if (++st == (uint32_t)S) { st = 0; sph ^= 1u; }
-          if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abortv, p.status)) { ok = false; break; }
-          const int n_sub = min(C::kSub, total - k0);
-          const uint32_t fb = full_lead + 8 * s;
-          mbar_expect_tx_cluster(fb, n_sub * bytes);
-          for (int j = 0; j < n_sub; ++j) {
-            const int pa = plane_a(term), pb = plane_b(term), k = kb * kBK;
-            const uint32_t a_dst = smem_u32(smem + s * C::kStage + j * C::kSlice), b_dst = a_dst + kABytes;
+      }
+      // first B row (FWD: rows of w, a SwiGLU pair stages gate rows and up rows) or column of this CTA
+      const int nb = GLU ? d.n0 + rank * p.N : d.n0 + rank * (BN / 2);
+      const uint32_t bytes = C::kBBytes + (d.has_rows ? kABytes : 0);
+      const int planes = p.terms > 1 ? 3 : 1, total = d.slices * p.terms;
+      int term = 6 - p.terms, kb = 0;
+      for (int k0 = 0; k0 < total; k0 += C::kSub, ++it) {
+        const uint32_t s = st, ph = sph;
+        if (++st == (uint32_t)S) { st = 0; sph ^= 1u; }
+        if (!mbar_wait_warp(empty0 + 8 * s, ph ^ 1u, abortv, p.status)) { ok = false; break; }
+        const int n_sub = min(C::kSub, total - k0);
+        const uint32_t fb = full_lead + 8 * s;
+        if (elect_one()) mbar_expect_tx_cluster(fb, n_sub * bytes);
+        for (int j = 0; j < n_sub; ++j) {
+          const int pa = plane_a(term), pb = plane_b(term), k = kb * kBK;
+          const uint32_t a_dst = smem_u32(smem + s * C::kStage + j * C::kSlice), b_dst = a_dst + kABytes;
+          if (elect_one()) {
             if (KIND == DW) {
               const int r = d.row0 + k;
               if (d.has_rows) load_columns<2>(a_dst, ma, d.m0, r, pa, p.one_box_a, fb);
@@ -374,17 +375,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load_columns<BN / 128>(b_dst, mb, nb, k, eb, p.one_box_b, fb);
               }
             }
-            if (++kb == d.slices) { kb = 0; ++term; }
           }
+          __syncwarp();
+          if (++kb == d.slices) { kb = 0; ++term; }
         }
       }
-      // drain: every stage this thread filled has been consumed (so its data landed)
-      const uint32_t first = it > (uint32_t)S ? it - S : 0u;
-      for (uint32_t i = first; i < it; ++i) mbar_wait(empty0 + 8 * (i % S), (i / S) & 1u, abortv, p.status, false);
     }
+    // drain: every stage this warp filled has been consumed (so its data landed)
+    const uint32_t first = it > (uint32_t)S ? it - S : 0u;
+    for (uint32_t i = first; i < it; ++i) mbar_wait(empty0 + 8 * (i % S), (i / S) & 1u, abortv, p.status, false);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer ------
-    if (leader && lane == 0) {
+    if (leader) {
       constexpr uint32_t idesc = instr_desc<BN>(KIND == DW ? 1u : 0u, KIND == FWD ? 0u : 1u);
       const uint32_t a0 = smem_u32(smem), b0 = a0 + kABytes;
       const uint64_t adesc0 = KIND == DW ? smem_desc(a0, 8192, 1024) : smem_desc(a0, 16, 1024);
@@ -395,35 +397,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int i = 0, t; i < rounds && ok; ++i) {
         t = nth_tile(i, pair, n_pairs);
-        if (t >= n_tiles) continue;  // (a last round may leave some pairs without one)
+        if (t >= n_tiles) continue;
         const Tile d = decode<KIND, BN, GLU>(p, prefix, t, 0);
         const int total = d.slices * p.terms;
         for (int k0 = 0; k0 < total && ok; k0 += PROMOTE ? p.pk : total, ++use) {
           const int k1 = PROMOTE ? min(total, k0 + p.pk) : total;
           const uint32_t acc = use & 1u;
-          if (!mbar_wait(acce0 + 8 * acc, ((use >> 1) & 1u) ^ 1u, abortv, p.status)) { ok = false; break; }
+          if (!mbar_wait_warp(acce0 + 8 * acc, ((use >> 1) & 1u) ^ 1u, abortv, p.status)) { ok = false; break; }
           tc_fence_after();
           const uint32_t tmem_d = tmem_base + acc * BN;
           for (int kb = k0; kb < k1; kb += C::kSub) {
             const uint32_t s = st, ph = sph;
             if (++st == (uint32_t)S) { st = 0; sph ^= 1u; }
-            if (!mbar_wait(full0 + 8 * s, ph, abortv, p.status)) { ok = false; break; }
+            if (!mbar_wait_warp(full0 + 8 * s, ph, abortv, p.status)) { ok = false; break; }
             tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < C::kSub; ++j) {
-              if (j > 0 && kb + j >= k1) break;
-              const uint64_t soff = (uint64_t)((s * C::kStage + j * C::kSlice) >> 4);
+              for (int j = 0; j < C::kSub; ++j) {
+                if (j > 0 && kb + j >= k1) break;
+                const uint64_t soff = (uint64_t)((s * C::kStage + j * C::kSlice) >> 4);
 #pragma unroll
-              for (int kk = 0; kk < kBK / 16; ++kk)
-                mma_bf16(tmem_d, adesc0 + soff + kk * a_step, bdesc0 + soff + kk * b_step, idesc,
-                         kb != k0 || j != 0 || kk != 0 ? 1u : 0u);
+                for (int kk = 0; kk < kBK / 16; ++kk)
+                  mma_bf16(tmem_d, adesc0 + soff + kk * a_step, bdesc0 + soff + kk * b_step, idesc,
+                           kb != k0 || j != 0 || kk != 0 ? 1u : 0u);
+              }
+              mma_commit_pair(empty0 + 8 * s);
             }
-            mma_commit_pair(empty0 + 8 * s);
+            __syncwarp();
           }
-          if (ok) mma_commit_pair(accf0 + 8 * acc);
+          if (ok && elect_one()) mma_commit_pair(accf0 + 8 * acc);
+          __syncwarp();
         }
       }
-      mma_commit_pair(drain);
+      if (elect_one()) mma_commit_pair(drain);
     }
     __syncwarp();
     mbar_wait(drain, 0, abortv, p.status, false);  // all MMAs into this CTA's TMEM are done before it is freed
@@ -743,14 +749,14 @@ int64_t likely_row_tiles(const int32_t* seg, int64_t R, int E) {
   return (R + 2 * kBM - 1) / (2 * kBM) + (seg != nullptr ? (R < E ? R : E) / 2 : 0);
 }
 
-// Tile width by the waves of tiles over the CTA pairs: a K slice of a 256-column tile takes 0.26 us, one of
-// a 128- or 64-column tile 0.21 us (the issue of a stage bounds it, not the product).  On a tie the
-// narrower: more SMs then share the reading of the weights.
+// Tile width by the waves of tiles over the CTA pairs: a K slice of a 256-column tile takes 0.26 us (its
+// products), one of a 128- or 64-column tile 0.155 us (the operands' way in).  On a tie the narrower: more
+// SMs then share the reading of the weights.
 template <typename F>
 lrm_status with_width(int64_t tiles_m, int N, int least, F&& f) {
   const int64_t pairs = sm_count() / 2;
   auto cost = [&](int bn, int slice) { return (tiles_m * ((N + bn - 1) / bn) + pairs - 1) / pairs * slice; };
-  const int64_t c256 = cost(256, 5), c128 = cost(128, 4), c64 = least > 64 ? INT64_MAX : cost(64, 4);
+  const int64_t c256 = cost(256, 5), c128 = cost(128, 3), c64 = least > 64 ? INT64_MAX : cost(64, 3);
   if (c64 <= c128 && c64 <= c256) return f(IntTag<64>{});
   return c128 <= c256 ? f(IntTag<128>{}) : f(IntTag<256>{});
 }

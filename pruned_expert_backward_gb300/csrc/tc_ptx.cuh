@@ -71,6 +71,21 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   if (mbar_try(bar, parity)) return true;
   return mbar_wait_slow(bar, parity, abort_flag, status, honour_abort);
 }
+// The wait of a whole warp: every lane waits, and all of them get the same answer.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                               int32_t* status) {
+  bool r = mbar_try(bar, parity);
+  if (__all_sync(0xffffffffu, r)) return true;
+  if (!r) r = mbar_wait_slow(bar, parity, abort_flag, status, true);
+  return __all_sync(0xffffffffu, r);
+}
+// One lane of a converged warp.  Roles that issue tcgen05 or TMA instructions run their loops with the
+// whole warp and issue under this predicate: addresses and descriptors then stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
 // The same with cluster-scope acquire: the waiter then sees what the other CTA of the pair wrote
 // before its release-arrive (shared-memory operands copied by threads, not by TMA).
 __device__ __forceinline__ bool mbar_wait_cl(uint32_t bar, uint32_t parity, volatile int* abort_flag,
