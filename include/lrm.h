@@ -331,7 +331,7 @@ lrm_status lrm_score_norms(const float* alpha, const void* g, const float* phi_s
  * through the library: lrm_route, lrm_sort_tokens, lrm_linear (SwiGLU), lrm_linear, lrm_combine,
  * and back: lrm_combine_backward, lrm_linear_backward, lrm_act_backward, lrm_linear_backward,
  * lrm_scatter_dx (the gradient of lrm_sort_tokens).  The pages name these steps ("forward completo")
- * but give no form for them.
+ * but give no form for them.  Outputs do not overlap inputs unless an entry says so.
  * ------------------------------------------------------------------------------------------- */
 
 /*
@@ -401,7 +401,8 @@ lrm_status lrm_linear_workspace_size(int64_t R, int32_t E, int32_t N, int32_t K,
  *   x [R,K] dt, w [E,N',K] dt, bias [E,N'] dt or NULL, residual [R,N] (type of y) or NULL
  *   -> y [R,N], z [R,N'] dt or NULL (the pre-activation, for lrm_act_backward); N' = 2N for SwiGLU, else N.
  * dt LRM_BF16 or LRM_F32; out_dt is the type of y: dt, or LRM_F32 from bf16 inputs (a router's logits;
- * no residual then).  Sums, bias, activation and residual are in fp32, each output is rounded once.
+ * no residual then).  Sums, bias, activation and residual are in fp32, each output is rounded once.  An
+ * infinity or NaN in x spoils the outputs of its own row only (as NaN where fp32 inputs are split).
  * Rows >= seg_offsets[E] are not written.  N and K are multiples of 8, up to 2^24; R <= INT32_MAX.
  * ws: scratch of at least lrm_linear_workspace_size bytes for fp32 inputs; not used (may be NULL) for bf16.
  * flags: LRM_GEMM_DEFAULT or LRM_GEMM_FORCE_SIMT (products on the CUDA cores).

@@ -17,6 +17,7 @@ namespace {
 constexpr size_t kAlign = 256;
 size_t up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 lrm_status check_dims(int64_t T, int32_t k, int32_t E, int32_t H, int32_t I) {
   if (T < 0 || k < 1 || E < 1 || H < 1 || I < 1) return LRM_ERR_INVALID_ARG;
@@ -55,9 +56,12 @@ size_t linear_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt
   return kAlign + up(linear_planes_bytes(R, K)) + up(linear_planes_bytes((int64_t)E * NP, K));
 }
 size_t linear_grad_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
-  if (dt != LRM_F32) return kAlign + linear_plan_bytes(E);  // kAlign: the maps start on a 128-byte boundary
-  return kAlign + linear_plan_bytes(E) + up(linear_planes_bytes(R, NP)) + up(linear_planes_bytes(R, K)) +
-         up(linear_planes_bytes((int64_t)E * NP, K));
+  size_t n = kAlign + linear_plan_bytes(E);  // kAlign: the maps start on a 128-byte boundary
+  const int parts = E == 1 ? linear_grad_parts(R, NP, K) : 1;
+  if (parts > 1) n += up(sizeof(float) * (size_t)parts * NP * K);
+  if (dt == LRM_F32)
+    n += up(linear_planes_bytes(R, NP)) + up(linear_planes_bytes(R, K)) + up(linear_planes_bytes((int64_t)E * NP, K));
+  return n;
 }
 size_t act_grad_ws_bytes(int64_t R, int32_t E, int32_t NP) {
   return up(sizeof(float) * act_backward_part_rows(R, E) * NP);
@@ -422,7 +426,8 @@ lrm_status lrm_sort_tokens(const int32_t* topk_idx, const void* x, int64_t T, in
   if ((st = check_dt(dt))) return st;
   if (!seg_offsets) return LRM_ERR_INVALID_ARG;
   if (T > 0 && (!topk_idx || !pair_of_row || !row_of_pair || (x_s && !x))) return LRM_ERR_INVALID_ARG;
-  if (!al16(x) || !al16(x_s)) return LRM_ERR_INVALID_ARG;
+  if (!al16(x) || !al16(x_s) || !al16(ws)) return LRM_ERR_INVALID_ARG;
+  if (!al4(topk_idx) || !al4(seg_offsets) || !al4(pair_of_row) || !al4(row_of_pair)) return LRM_ERR_INVALID_ARG;
   const SortWs w = sort_layout(T, k, E);
   if (w.total > 0 && (!ws || ws_bytes < w.total)) return LRM_ERR_WORKSPACE;
   char* b = static_cast<char*>(ws);
@@ -449,7 +454,7 @@ lrm_status lrm_combine(const int32_t* row_of_pair, const float* alpha, const voi
   if ((st = check_dt(dt))) return st;
   if (cap < 0 || cap > INT32_MAX) return LRM_ERR_INVALID_ARG;
   if (T > 0 && (!row_of_pair || !alpha || !y || (cap > 0 && !y_s))) return LRM_ERR_INVALID_ARG;
-  if (!al16(y_s) || !al16(residual) || !al16(y)) return LRM_ERR_INVALID_ARG;
+  if (!al16(y_s) || !al16(residual) || !al16(y) || !al4(row_of_pair) || !al4(alpha)) return LRM_ERR_INVALID_ARG;
   if (T == 0) return LRM_OK;
   launch_combine(row_of_pair, alpha, y_s, residual, T, k, H, dt, cap, y, dev_status, stream);
   return after_launch();
@@ -466,6 +471,7 @@ lrm_status lrm_combine_backward(const int32_t* row_of_pair, const float* alpha, 
   if (T > 0 && (!row_of_pair || !alpha || !dy)) return LRM_ERR_INVALID_ARG;
   if (T > 0 && cap > 0 && (!dy_s || (dalpha && !y_s))) return LRM_ERR_INVALID_ARG;
   if (!al16(dy) || !al16(y_s) || !al16(dy_s)) return LRM_ERR_INVALID_ARG;
+  if (!al4(row_of_pair) || !al4(alpha) || !al4(dalpha)) return LRM_ERR_INVALID_ARG;
   if (T == 0) return LRM_OK;
   launch_combine_backward(row_of_pair, alpha, dy, dalpha ? y_s : nullptr, T, k, H, dt, cap, dy_s, dalpha, dev_status,
                           stream);
@@ -499,9 +505,10 @@ lrm_status lrm_linear(const int32_t* seg_offsets, const void* x, const void* w, 
   if (flags != LRM_GEMM_DEFAULT && flags != LRM_GEMM_FORCE_SIMT) return LRM_ERR_INVALID_ARG;
   if (!w || (!seg_offsets && E != 1)) return LRM_ERR_INVALID_ARG;
   if (R > 0 && (!x || !y)) return LRM_ERR_INVALID_ARG;
-  const void* ptrs[] = {x, w, bias, residual, y, z};
+  const void* ptrs[] = {x, w, bias, residual, y, z, ws};
   for (const void* p : ptrs)
     if (!al16(p)) return LRM_ERR_INVALID_ARG;
+  if (!al4(seg_offsets)) return LRM_ERR_INVALID_ARG;
   const int32_t NP = act == LRM_ACT_SWIGLU ? 2 * N : N;
   const size_t need = linear_ws_bytes(R, E, NP, K, dt);
   if (need > 0 && (!ws || ws_bytes < need)) return LRM_ERR_WORKSPACE;
@@ -524,9 +531,10 @@ lrm_status lrm_act_backward(const int32_t* seg_offsets, const void* dy, const vo
   if (st) return st;
   if (!seg_offsets && E != 1) return LRM_ERR_INVALID_ARG;
   if (R > 0 && (!dy || !dz || (act != LRM_ACT_NONE && !z))) return LRM_ERR_INVALID_ARG;
-  const void* ptrs[] = {dy, z, dz, db};
+  const void* ptrs[] = {dy, z, dz, db, ws};
   for (const void* p : ptrs)
     if (!al16(p)) return LRM_ERR_INVALID_ARG;
+  if (!al4(seg_offsets)) return LRM_ERR_INVALID_ARG;
   const int32_t NP = act == LRM_ACT_SWIGLU ? 2 * N : N;
   if (db && (!ws || ws_bytes < act_grad_ws_bytes(R, E, NP))) return LRM_ERR_WORKSPACE;
   if (R == 0 && !db) return LRM_OK;
@@ -544,9 +552,10 @@ lrm_status lrm_linear_backward(const int32_t* seg_offsets, const void* dz, const
   if (flags != LRM_GEMM_DEFAULT && flags != LRM_GEMM_FORCE_SIMT) return LRM_ERR_INVALID_ARG;
   if ((!seg_offsets && E != 1) || (!dx && !dw)) return LRM_ERR_INVALID_ARG;
   if (R > 0 && (!dz || (dx && !w) || (dw && !x))) return LRM_ERR_INVALID_ARG;
-  const void* ptrs[] = {dz, x, w, dx, dw};
+  const void* ptrs[] = {dz, x, w, dx, dw, ws};
   for (const void* p : ptrs)
     if (!al16(p)) return LRM_ERR_INVALID_ARG;
+  if (!al4(seg_offsets)) return LRM_ERR_INVALID_ARG;
   if (!ws || ws_bytes < linear_grad_ws_bytes(R, E, N, K, dt)) return LRM_ERR_WORKSPACE;
   if (R == 0) {  // no rows anywhere: every dW is zero
     if (dw && cudaMemsetAsync(dw, 0, sizeof(float) * (size_t)E * N * K, stream) != cudaSuccess) return LRM_ERR_CUDA;

@@ -32,7 +32,7 @@ __device__ __forceinline__ float norm_cdf(float z, float* exp_out) {
 // act(z) of the one-input activations (SwiGLU takes two: SiLU(gate) * up).
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
-  if (ACT == LRM_ACT_RELU) return fmaxf(z, 0.f);
+  if (ACT == LRM_ACT_RELU) return z < 0.f ? 0.f : z;  // a NaN stays
   if (ACT == LRM_ACT_GELU) {
     float e;
     return z * norm_cdf(z, &e);

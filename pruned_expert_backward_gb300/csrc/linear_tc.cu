@@ -76,6 +76,7 @@ struct Params {
   int red;        // FWD, DX: length of the reduction
   int tiles_n;
   int tiles_m;    // DW: pair tiles along M
+  int part_rows;  // DW without segments: rows of each part of the reduction (E parts, each with its own output)
   int terms;      // 1, or 6 for fp32 inputs in three planes
   int pk;         // K slices per accumulator (PROMOTE)
   // operands that are contiguous along M or N (DX: B, DW: both): both 64-column blocks of a CTA's 128 columns
@@ -127,10 +128,10 @@ __device__ __forceinline__ Tile decode(const Params& p, const int* prefix, int t
   d.n0 = nt * (GLU ? BN / 2 : BN);
   if (KIND == DW) {
     const int ei = mg / p.tiles_m;
-    d.e = p.seg != nullptr ? __ldg(p.plan + 1 + ei) : 0;
+    d.e = p.seg != nullptr ? __ldg(p.plan + 1 + ei) : ei;
     d.m0 = (2 * (mg - ei * p.tiles_m) + rank) * kBM;
-    d.row0 = p.seg != nullptr ? __ldg(p.seg + d.e) : 0;
-    d.row_end = p.seg != nullptr ? __ldg(p.seg + d.e + 1) : (int)p.R;
+    d.row0 = p.seg != nullptr ? __ldg(p.seg + d.e) : d.e * p.part_rows;
+    d.row_end = p.seg != nullptr ? __ldg(p.seg + d.e + 1) : (int)min(p.R, (int64_t)d.row0 + p.part_rows);
     d.slices = (d.row_end - d.row0 + kBK - 1) / kBK;
     d.has_rows = d.m0 < p.M;
     return d;
@@ -618,8 +619,9 @@ __global__ void __launch_bounds__(1024) linear_plan_kernel(const int32_t* __rest
   }
 }
 
-// fp32 tensors [groups][n] as three bf16 planes [groups][3][n] whose sum is the tensor to 24 bits (a value
-// that is not finite stays in the first plane alone, so that no infinity is subtracted from itself).
+// fp32 tensors [groups][n] as three bf16 planes [groups][3][n] whose sum is the tensor to 24 bits.  A value
+// that is not finite stays in the first plane alone, so that no infinity is subtracted from itself; one
+// that bf16 would round to infinity is cut instead.
 struct Split {
   const float* x;
   int64_t groups, n;
@@ -644,13 +646,30 @@ __global__ void __launch_bounds__(256) split_planes_kernel(const __grid_constant
       for (int q = 0; q < 8; ++q) {
         const float v = q < 4 ? a4[q & 3] : b4[q & 3];
         p[0][q] = __bfloat162float(__float2bfloat16_rn(v));
-        const float r1 = isfinite(p[0][q]) ? v - p[0][q] : 0.f;  // exact
+        if (isinf(p[0][q])) p[0][q] = __bfloat162float(__float2bfloat16_rz(v));
+        const float r1 = isfinite(v) ? v - p[0][q] : 0.f;  // exact
         p[1][q] = __bfloat162float(__float2bfloat16_rn(r1));
         p[2][q] = r1 - p[1][q];
       }
 #pragma unroll
       for (int j = 0; j < 3; ++j) st16(s.out + (g * 3 + j) * s.n + c, pack(p[j]));
     }
+  }
+}
+
+// out = the sum of `parts` arrays of n floats (a multiple of 4), in order.
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict__ part, int parts, int64_t n,
+                                                        float* __restrict__ out) {
+  chain_wait();
+  for (int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * blockDim.x * 4) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < parts; ++s) {
+      float f[4];
+      unpack(ld_stream16(part + s * n + i), f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[q] += f[q];
+    }
+    st16(out + i, pack(acc));
   }
 }
 
@@ -737,9 +756,9 @@ void launch_splits(const Splits& a, cudaStream_t s) {
   launch_chained(split_planes_kernel, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), dim3(256), 0, s, a);
 }
 
-// K slices per accumulator where the result is fp32: 256 products for split fp32 inputs (5e-7 off at
-// most per sum), 1024 for bf16 inputs (1e-6).
-constexpr int kSlicesF32 = 4, kSlicesBf16 = 16;
+// K slices per accumulator where the result is fp32: 256 products for split fp32 inputs (2.4e-7 off against
+// 64 bits, as fp32 arithmetic itself), 512 for bf16 inputs (4.7e-7; 1024 products: 9.9e-7).
+constexpr int kSlicesF32 = 4, kSlicesBf16 = 8;
 
 // Most row tiles there can be, and about how many (every segment ends in half a tile).
 int64_t row_tiles(const int32_t* seg, int64_t R, int E) {
@@ -856,11 +875,17 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
   CUtensorMap mA, mB, mY;
   if (a.dw != nullptr) {
     p.M = a.N;
-    p.y = a.dw;
     p.tiles_m = (a.N + 2 * kBM - 1) / (2 * kBM);
-    if (!column_map(&mA, dzs, a.N, a.R, planes, 2, &p.one_box_a) || !output_map(&mY, a.dw, true, a.K, a.N, a.E))
+    const int parts = a.seg_offsets == nullptr ? linear_grad_parts(a.R, a.N, a.K) : 1;
+    float* sums = parts > 1 ? reinterpret_cast<float*>(b) : a.dw;
+    p.y = sums;
+    if (a.seg_offsets == nullptr) {
+      p.E = parts;
+      p.part_rows = (int)((a.R + (int64_t)parts * kBK - 1) / ((int64_t)parts * kBK) * kBK);
+    }
+    if (!column_map(&mA, dzs, a.N, a.R, planes, 2, &p.one_box_a) || !output_map(&mY, sums, true, a.K, a.N, p.E))
       return LRM_ERR_CUDA;
-    const int64_t tm = (int64_t)a.E * p.tiles_m;
+    const int64_t tm = (int64_t)p.E * p.tiles_m;
     const lrm_status st = with_width(tm, a.K, 128, [&](auto bn) {
       constexpr int BN = decltype(bn)::value;
       if constexpr (BN < 128) {
@@ -879,8 +904,14 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
       }
     });
     if (st) return st;
+    if (parts > 1) {
+      const int64_t n = (int64_t)a.N * a.K, blocks = (n / 4 + 255) / 256;
+      launch_chained(sum_parts_kernel, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), dim3(256), 0, s,
+                     (const float*)sums, parts, n, a.dw);
+    }
   }
   if (a.dx != nullptr) {
+    p.E = a.E;
     p.red = a.N;
     p.y = a.dx;
     if (!operand_map(&mA, dzs, a.N, a.R, planes, kBM) || !output_map(&mY, a.dx, f32, a.K, a.R, 1))
@@ -899,6 +930,15 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
     });
   }
   return LRM_OK;
+}
+
+// Parts of the rows that the dense weight gradient sums apart where its tiles alone would leave most of the
+// 76 CTA pairs idle; at least 1024 rows each.
+int linear_grad_parts(int64_t R, int32_t N, int32_t K) {
+  const int64_t tiles = (int64_t)((N + 255) / 256) * ((K + 127) / 128);
+  int64_t parts = 76 / tiles;
+  if (parts > R / 1024) parts = R / 1024;
+  return parts < 1 ? 1 : (int)parts;
 }
 
 size_t linear_plan_bytes(int32_t E) {

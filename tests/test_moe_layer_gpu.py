@@ -286,6 +286,8 @@ LINEARS = [  # dtype, R, N, K, act, bias, residual, save_z, out_f32
     (BF16, 255, 512, 1000, "silu", False, True, False, False), (BF16, 257, 776, 1032, "swiglu", True, True, True, False),
     (BF16, 513, 64, 320, "none", True, False, True, True), (BF16, 1537, 776, 1032, "gelu", True, True, True, False),
     (BF16, 3001, 1416, 520, "swiglu", True, False, True, False), (BF16, 4000, 128, 2048, "none", True, False, False, True),
+    (BF16, 70, 8, 8, "gelu", True, True, True, False), (BF16, 33, 16, 24, "swiglu", True, True, True, False),
+    (BF16, 300, 8, 2048, "relu", True, False, False, True), (F32, 70, 8, 8, "silu", True, True, True, False),
     (F32, 3, 40, 72, "gelu", True, True, True, False), (F32, 70, 136, 264, "swiglu", True, True, True, False),
     (F32, 257, 264, 1032, "silu", True, True, True, False), (F32, 700, 520, 136, "none", False, False, False, False),
     (F32, 1300, 72, 2056, "relu", True, True, False, False), (F32, 40, 520, 2048, "swiglu", False, True, False, False),
@@ -376,6 +378,24 @@ def test_linear_infinities_and_nan_stay_in_their_rows(status):
             check_linear(x[1:R - 1].contiguous(), w, b, res[1:R - 1].contiguous(), "none", None, y[1:R - 1], None)
 
 
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("R", [3, 200])
+def test_linear_of_the_lowest_values_and_nan(R, dt, status):
+    """The type's lowest value times one weight is itself; ReLU keeps a NaN; -0 and the lowest give 0."""
+    import pruned_expert_backward_gb300 as lrm
+    low = torch.finfo(dt).min
+    x = torch.zeros(R, 16, dtype=dt, device="cuda")
+    x[0, 0], x[1, 0], x[2, 0] = low, float("nan"), -low
+    w = torch.eye(16, dtype=dt, device="cuda")
+    y, _ = lrm.lrm_linear(x, w, dev_status=status)
+    # (fp32 values are held to 24 bits as three bf16 parts)
+    assert abs(y[0, 0].item() / low - 1) <= 2.0 ** -23 and abs(y[2, 0].item() / low + 1) <= 2.0 ** -23
+    assert bool((y[0, 1:] == 0).all()) and bool((y[2, 1:] == 0).all())
+    r, _ = lrm.lrm_linear(x, w, act="relu", dev_status=status)
+    assert r[0, 0].item() == 0 and bool(torch.isnan(r[1, 0])) and r[2, 0].item() == y[2, 0].item()
+    assert torch.count_nonzero(r[3:]) == 0
+
+
 @pytest.mark.parametrize("act", ACTS)
 def test_linear_large_pre_activations(act, status):
     """Saturated activations: |z| up to 500 gives 0, z or the product, never NaN."""
@@ -439,7 +459,8 @@ def test_act_backward(case, act, status):
 LINEAR_GRADS = [  # dtype, R, N, K, E, segments
     (BF16, 1, 8, 8, None, None), (F32, 1, 8, 16, None, None), (BF16, 63, 72, 136, None, None),
     (BF16, 65, 264, 64, None, None), (BF16, 300, 128, 520, None, None), (BF16, 1537, 776, 264, None, None),
-    (BF16, 5000, 256, 256, None, None), (BF16, 20000, 40, 72, None, None), (F32, 70, 72, 40, None, None),
+    (BF16, 5000, 256, 256, None, None), (BF16, 40, 8, 8, None, None), (F32, 3100, 40, 24, None, None),
+    (BF16, 4133, 520, 136, None, None), (BF16, 20000, 40, 72, None, None), (F32, 70, 72, 40, None, None),
     (F32, 1500, 136, 264, None, None), (BF16, 8, 72, 64, 12, "ragged"), (BF16, 700, 264, 136, 5, "short"),
     (BF16, 3000, 520, 72, 64, "ragged"), (BF16, 6000, 136, 392, 3, "one"), (BF16, 9000, 72, 328, 2, "ragged"),
     (F32, 900, 72, 136, 9, "short"), (F32, 4000, 40, 264, 4, "ragged"),
