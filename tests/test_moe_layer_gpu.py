@@ -625,3 +625,20 @@ def test_refusals():
         lrm.lrm_act_backward(x, None, act="gelu")
     with pytest.raises(ValueError):
         lrm.lrm_linear_backward(x, x, w)
+
+
+def test_the_example_runs_and_pruning_nothing_changes_nothing():
+    """examples/moe_layer.py: with every pair kept the pruned backward gives the full gradients (bf16 rounding
+    of a few intermediates apart); a token alone gives its row of the batch."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_layer.py")
+    spec = importlib.util.spec_from_file_location("moe_layer_example", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    r = example.run(tokens=600, hidden=256, inter=128, experts=16, topk=4, keep=(1, 1))
+    assert r["kept"] == 1.0
+    assert max(r["dx"], r["dw_gate_up"], r["dw_down"]) <= 1e-2
+    assert r["token_vs_batch"] <= 2.0 ** -7
+    r = example.run(tokens=600, hidden=256, inter=128, experts=16, topk=4, keep=(8, 10))
+    assert 0.8 <= r["kept"] <= 0.83 and 0 < r["dw_down"] < 0.5
