@@ -619,12 +619,13 @@ __global__ void __launch_bounds__(1024) linear_plan_kernel(const int32_t* __rest
   }
 }
 
-// fp32 tensors [groups][n] as three bf16 planes [groups][3][n] whose sum is the tensor to 24 bits.  A value
-// that is not finite stays in the first plane alone, so that no infinity is subtracted from itself; one
-// that bf16 would round to infinity is cut instead.
+// fp32 tensors [groups][rows][cols] as three bf16 planes [groups][3][rows][pitch] whose sum is the tensor to
+// 24 bits.  A value that is not finite stays in the first plane alone, so that no infinity is subtracted
+// from itself; one that bf16 would round to infinity is cut instead.  The pitch is a multiple of 64: rows
+// that do not start on a 128-byte line cost TMA two lines for one.
 struct Split {
   const float* x;
-  int64_t groups, n;
+  int64_t groups, rows, cols, pitch;
   __nv_bfloat16* out;
 };
 struct Splits {
@@ -635,10 +636,10 @@ __global__ void __launch_bounds__(256) split_planes_kernel(const __grid_constant
   chain_wait();
   for (int k = 0; k < a.count; ++k) {
     const Split& s = a.t[k];
-    const int64_t total = s.groups * s.n / 8;
+    const int64_t nv = s.cols / 8, total = s.groups * s.rows * nv;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-      const int64_t at = i * 8, g = at / s.n, c = at - g * s.n;
-      const uint4 lo = ld_stream16_now(s.x + at), hi = ld_stream16_now(s.x + at + 4);
+      const int64_t row = i / nv, g = row / s.rows;
+      const uint4 lo = ld_stream16_now(s.x + i * 8), hi = ld_stream16_now(s.x + i * 8 + 4);
       float a4[4], b4[4], p[3][8];
       unpack(lo, a4);
       unpack(hi, b4);
@@ -652,7 +653,8 @@ __global__ void __launch_bounds__(256) split_planes_kernel(const __grid_constant
         p[2][q] = r1 - p[1][q];
       }
 #pragma unroll
-      for (int j = 0; j < 3; ++j) st16(s.out + (g * 3 + j) * s.n + c, pack(p[j]));
+      for (int j = 0; j < 3; ++j)
+        st16(s.out + ((g * 2 + j) * s.rows + row) * s.pitch + (i - row * nv) * 8, pack(p[j]));
     }
   }
 }
@@ -687,18 +689,19 @@ bool make_map(CUtensorMap* m, const void* base, bool f32, uint64_t d0, uint64_t 
                      operand ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// A bf16 operand [planes][rows][cols].
-bool operand_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t planes, uint32_t box_rows) {
-  return make_map(m, base, false, cols, rows, planes, cols * 2, rows * cols * 2, 64, box_rows, true);
+// A bf16 operand [planes][rows][cols], its rows `pitch` apart.
+bool operand_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t pitch, uint64_t rows, uint64_t planes,
+                 uint32_t box_rows) {
+  return make_map(m, base, false, cols, rows, planes, pitch * 2, rows * pitch * 2, 64, box_rows, true);
 }
-// The same seen as [planes][cols / 64][rows][64], `blocks` blocks of 64 columns and 64 rows a box; the plain
-// form with one block where the columns do not divide (*one_box tells).
-bool column_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t planes, uint32_t blocks,
-                bool* one_box) {
-  *one_box = cols % 64 == 0 && cols >= 64 * blocks;
-  if (!*one_box) return operand_map(m, base, cols, rows, planes, 64);
-  const cuuint64_t dims[4] = {64, rows, cols / 64, planes};
-  const cuuint64_t strides[3] = {cols * 2, 128, rows * cols * 2};
+// The same seen as [planes][pitch / 64][rows][64], `blocks` blocks of 64 columns and 64 rows a box; the plain
+// form with one block where the pitch does not divide (*one_box tells).
+bool column_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t pitch, uint64_t rows, uint64_t planes,
+                uint32_t blocks, bool* one_box) {
+  *one_box = pitch % 64 == 0 && pitch >= 64 * blocks;
+  if (!*one_box) return operand_map(m, base, cols, pitch, rows, planes, 64);
+  const cuuint64_t dims[4] = {64, rows, pitch / 64, planes};
+  const cuuint64_t strides[3] = {pitch * 2, 128, rows * pitch * 2};
   const cuuint32_t box[4] = {64, 64, blocks, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
@@ -746,13 +749,18 @@ lrm_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap&
   return cudaGetLastError() == cudaSuccess ? LRM_OK : LRM_ERR_CUDA;
 }
 
-void add_split(Splits& a, const void* x, int64_t groups, int64_t n, void* out) {
-  a.t[a.count++] = Split{static_cast<const float*>(x), groups, n, static_cast<__nv_bfloat16*>(out)};
+uint64_t plane_pitch(uint64_t cols) { return (cols + 63) / 64 * 64; }
+
+void add_split(Splits& a, const void* x, int64_t groups, int64_t rows, int64_t cols, void* out) {
+  a.t[a.count++] = Split{static_cast<const float*>(x), groups, rows, cols, (int64_t)plane_pitch((uint64_t)cols),
+                         static_cast<__nv_bfloat16*>(out)};
 }
 void launch_splits(const Splits& a, cudaStream_t s) {
-  int64_t most = 1;
-  for (int k = 0; k < a.count; ++k) most = a.t[k].groups * a.t[k].n / 8 > most ? a.t[k].groups * a.t[k].n / 8 : most;
-  const int64_t blocks = (most + 255) / 256;
+  int64_t blocks = 1;
+  for (int k = 0; k < a.count; ++k) {
+    const int64_t n = (a.t[k].groups * a.t[k].rows * a.t[k].cols / 8 + 255) / 256;
+    blocks = n > blocks ? n : blocks;
+  }
   launch_chained(split_planes_kernel, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), dim3(256), 0, s, a);
 }
 
@@ -782,7 +790,7 @@ lrm_status with_width(int64_t tiles_m, int N, int least, F&& f) {
 
 }  // namespace
 
-size_t linear_planes_bytes(int64_t rows, int64_t cols) { return (size_t)rows * cols * 6; }
+size_t linear_planes_bytes(int64_t rows, int64_t cols) { return (size_t)rows * plane_pitch((uint64_t)cols) * 6; }
 
 lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, void* ws, cudaStream_t s) {
   if (!device_ok() || encode_fn() == nullptr) return LRM_ERR_UNSUPPORTED;
@@ -792,10 +800,10 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
   if (f32) {
     char* b = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws) + 127) & ~uintptr_t(127));
     Splits sp{};
-    add_split(sp, a.x, 1, a.R * a.K, b);
+    add_split(sp, a.x, 1, a.R, a.K, b);
     xs = b;
     b += (linear_planes_bytes(a.R, a.K) + 255) / 256 * 256;
-    add_split(sp, a.w, a.E, (int64_t)NP * a.K, b);
+    add_split(sp, a.w, a.E, NP, a.K, b);
     wsrc = b;
     launch_splits(sp, s);
   }
@@ -814,9 +822,10 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
   p.z = a.z;
   p.status = a.status;
   const int planes = f32 ? 3 : 1;
+  const uint64_t pitch = f32 ? plane_pitch(a.K) : a.K;
   const bool y32 = out_dt == LRM_F32;
   CUtensorMap mA, mB, mY, mZ;
-  if (!operand_map(&mA, xs, a.K, a.R, planes, kBM) || !output_map(&mY, a.y, y32, a.N, a.R, 1)) return LRM_ERR_CUDA;
+  if (!operand_map(&mA, xs, a.K, pitch, a.R, planes, kBM) || !output_map(&mY, a.y, y32, a.N, a.R, 1)) return LRM_ERR_CUDA;
   mZ = mY;
   if (a.z != nullptr && y32 == f32 && !output_map(&mZ, a.z, f32, a.N, a.R, glu ? 2 : 1, glu)) return LRM_ERR_CUDA;
   const int64_t tm = row_tiles(a.seg_offsets, a.R, a.E);
@@ -828,7 +837,7 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
     } else {
       constexpr int cols = GLU ? BN / 2 : BN;
       p.tiles_n = (a.N + cols - 1) / cols;
-      if (!operand_map(&mB, wsrc, a.K, NP, (uint64_t)a.E * planes, BN / 2)) return LRM_ERR_CUDA;
+      if (!operand_map(&mB, wsrc, a.K, pitch, NP, (uint64_t)a.E * planes, BN / 2)) return LRM_ERR_CUDA;
       using B16 = __nv_bfloat16;
       if (f32) return launch<FWD, BN, GLU, true, float, float>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
       if (y32) return launch<FWD, BN, GLU, true, B16, float>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
@@ -852,18 +861,19 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
   int32_t* plan = reinterpret_cast<int32_t*>(b + 2 * sizeof(CUtensorMap) * (size_t)a.E);
   b += linear_plan_bytes(a.E);
   Splits sp{};
-  auto split = [&](const void* src, int64_t groups, int64_t n) {
-    add_split(sp, src, groups, n, b);
+  auto split = [&](const void* src, int64_t groups, int64_t rows, int64_t cols) {
+    add_split(sp, src, groups, rows, cols, b);
     const void* at = b;
-    b += ((size_t)groups * n * 6 + 255) / 256 * 256;
+    b += (linear_planes_bytes(groups * rows, cols) + 255) / 256 * 256;
     return at;
   };
   if (f32) {
-    dzs = split(a.dz, 1, a.R * a.N);
-    if (a.dx != nullptr) wsrc = split(a.w, a.E, (int64_t)a.N * a.K);
-    if (a.dw != nullptr) xs = split(a.x, 1, a.R * a.K);
+    dzs = split(a.dz, 1, a.R, a.N);
+    if (a.dx != nullptr) wsrc = split(a.w, a.E, a.N, a.K);
+    if (a.dw != nullptr) xs = split(a.x, 1, a.R, a.K);
     launch_splits(sp, s);
   }
+  const uint64_t pitch_n = f32 ? plane_pitch(a.N) : a.N, pitch_k = f32 ? plane_pitch(a.K) : a.K;
   Params p{};
   p.E = a.E;
   p.R = a.R;
@@ -883,7 +893,7 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
       p.E = parts;
       p.part_rows = (int)((a.R + (int64_t)parts * kBK - 1) / ((int64_t)parts * kBK) * kBK);
     }
-    if (!column_map(&mA, dzs, a.N, a.R, planes, 2, &p.one_box_a) || !output_map(&mY, sums, true, a.K, a.N, p.E))
+    if (!column_map(&mA, dzs, a.N, pitch_n, a.R, planes, 2, &p.one_box_a) || !output_map(&mY, sums, true, a.K, a.N, p.E))
       return LRM_ERR_CUDA;
     const int64_t tm = (int64_t)p.E * p.tiles_m;
     const lrm_status st = with_width(tm, a.K, 128, [&](auto bn) {
@@ -892,7 +902,7 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
         return LRM_ERR_UNSUPPORTED;
       } else {
         p.tiles_n = (a.K + BN - 1) / BN;
-        if (!column_map(&mB, xs, a.K, a.R, planes, BN / 128, &p.one_box_b)) return LRM_ERR_CUDA;
+        if (!column_map(&mB, xs, a.K, pitch_k, a.R, planes, BN / 128, &p.one_box_b)) return LRM_ERR_CUDA;
         if (a.seg_offsets != nullptr) {
           const MapPair tpl{{mA, mB}};
           launch_chained(linear_plan_kernel, dim3(1), dim3(1024), 0, s, a.seg_offsets, a.E, a.R, plan, maps, tpl,
@@ -914,7 +924,7 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
     p.E = a.E;
     p.red = a.N;
     p.y = a.dx;
-    if (!operand_map(&mA, dzs, a.N, a.R, planes, kBM) || !output_map(&mY, a.dx, f32, a.K, a.R, 1))
+    if (!operand_map(&mA, dzs, a.N, pitch_n, a.R, planes, kBM) || !output_map(&mY, a.dx, f32, a.K, a.R, 1))
       return LRM_ERR_CUDA;
     const int64_t tm = row_tiles(a.seg_offsets, a.R, a.E);
     return with_width(likely_row_tiles(a.seg_offsets, a.R, a.E), a.K, 128, [&](auto bn) {
@@ -923,7 +933,7 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
         return LRM_ERR_UNSUPPORTED;
       } else {
         p.tiles_n = (a.K + BN - 1) / BN;
-        if (!column_map(&mB, wsrc, a.K, a.N, (uint64_t)a.E * planes, BN / 128, &p.one_box_b)) return LRM_ERR_CUDA;
+        if (!column_map(&mB, wsrc, a.K, pitch_k, a.N, (uint64_t)a.E * planes, BN / 128, &p.one_box_b)) return LRM_ERR_CUDA;
         if (f32) return launch<DX, BN, false, true, float, float>(mA, mB, mY, mY, p, tm * p.tiles_n, s);
         return launch<DX, BN, false, false, B16, B16>(mA, mB, mY, mY, p, tm * p.tiles_n, s);
       }
