@@ -108,30 +108,38 @@ __global__ void __launch_bounds__(32 * kWarps, (kCtas<T, ACT>)) act_backward_ker
   }
 }
 
-// db[e][column] from the partials of the expert's row blocks: 32 columns per CTA, its warps taking the
-// blocks in turn, added in a fixed order.
-constexpr int kSumWarps = 16;
+// db[e][column] from the partials of the expert's row blocks: 128 columns per CTA (a lane has four), its
+// warps taking the blocks in turn, added in a fixed order.
+constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(32 * kSumWarps) bias_sum_kernel(const int32_t* __restrict__ seg, int E, int64_t R,
                                                                   int NP, const float* __restrict__ part,
                                                                   float* __restrict__ db,
                                                                   int32_t* __restrict__ status) {
   chain_wait();
-  __shared__ float s_sum[kSumWarps][32];
+  extern __shared__ float s_part[];  // [warps][128]
   if (!rows_valid(seg, E, R, status)) return;
   const int e = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  const int col = blockIdx.x * 32 + lane;
+  const int col = blockIdx.x * 128 + lane * 4;  // NP is a multiple of 8
   const int64_t r0 = seg_at(seg, e, R), r1 = seg_at(seg, e + 1, R);
-  float s = 0.f;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
   if (col < NP && r1 > r0) {
     const int64_t last = (r1 - 1) / kRowBlock;
 #pragma unroll 8
-    for (int64_t b = r0 / kRowBlock + warp; b <= last; b += nw) s += part[(b + e) * NP + col];
+    for (int64_t b = r0 / kRowBlock + warp; b <= last; b += nw) {
+      float f[4];
+      unpack(ldg16(part + (b + e) * NP + col), f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s[q] += f[q];
+    }
   }
-  s_sum[warp][lane] = s;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) s_part[warp * 128 + lane * 4 + q] = s[q];
   __syncthreads();
   if (warp == 0 && col < NP) {
-    for (int w = 1; w < nw; ++w) s += s_sum[w][lane];
-    db[(int64_t)e * NP + col] = s;
+    for (int w = 1; w < nw; ++w)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s[q] += s_part[w * 128 + lane * 4 + q];
+    st16(db + (int64_t)e * NP + col, pack(s));
   }
 }
 
@@ -149,10 +157,10 @@ void act_backward_all(const ActGradArgs& a, cudaStream_t s) {
   if (a.db != nullptr) {
     const int NP = a.act == LRM_ACT_SWIGLU ? 2 * a.N : a.N;
     // a warp for every four blocks of a mean segment
-    const int64_t warps = (a.R / kRowBlock / a.E + 3) / 4 + 1;
-    launch_chained(bias_sum_kernel, dim3((unsigned)((NP + 31) / 32), (unsigned)a.E),
-                   dim3(32 * (unsigned)(warps < kSumWarps ? warps : kSumWarps)), 0, s, a.seg_offsets, a.E, a.R, NP,
-                   (const float*)a.part, a.db, a.status);
+    const int64_t want = (a.R / kRowBlock / a.E + 3) / 4 + 1;
+    const unsigned warps = (unsigned)(want < kSumWarps ? want : kSumWarps);
+    launch_chained(bias_sum_kernel, dim3((unsigned)((NP + 127) / 128), (unsigned)a.E), dim3(32 * warps),
+                   warps * 128 * sizeof(float), s, a.seg_offsets, a.E, a.R, NP, (const float*)a.part, a.db, a.status);
   }
 }
 

@@ -12,6 +12,7 @@
 // x is read by every CTA through L2, R / 16 of W's bytes, which bounds the rows this form is used for.
 #include "kernels.h"
 #include "linear.cuh"
+#include "tc_host.h"
 
 namespace lrm {
 
@@ -78,7 +79,7 @@ template <int NT>
 __device__ __forceinline__ void warp_products(const float* w0, const float* w1, const float* x, int rows, int K,
                                               int warp, int lane, float (*out)[8 * NT + 1]) {
   static_assert(NT == 1, "fp32 takes 8 rows at a time");
-  constexpr int U = 4;
+  constexpr int U = 2, XR = 4;  // steps of W, and rows of x, whose loads are in flight
   const int g = lane >> 2, t = lane & 3;
   float c[2][8];
 #pragma unroll
@@ -96,25 +97,36 @@ __device__ __forceinline__ void warp_products(const float* w0, const float* w1, 
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * kWarps * kStep;
+    for (int r0 = 0; r0 < 8; r0 += XR) {
+      if (r0 >= rows) break;
+      uint4 v[XR][U][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float fa[4], fb[4];
-        unpack(a[u][h], fa);
-        unpack(b[u][h], fb);
+      for (int r = 0; r < XR; ++r)
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          if (k >= K || r >= rows) continue;
-          float f[4];
-          unpack(ldg16(x + (int64_t)r * K + k + 4 * h), f);
+        for (int u = 0; u < U; ++u) {
+          const int k = k0 + u * kWarps * kStep;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            c[0][r] = fmaf(fa[q], f[q], c[0][r]);
-            c[1][r] = fmaf(fb[q], f[q], c[1][r]);
+          for (int h = 0; h < 2; ++h)
+            v[r][u][h] = k < K && r0 + r < rows ? ldg16_now(x + (int64_t)(r0 + r) * K + k + 4 * h) : zero;
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float fa[4], fb[4];
+          unpack(a[u][h], fa);
+          unpack(b[u][h], fb);
+#pragma unroll
+          for (int r = 0; r < XR; ++r) {
+            float f[4];
+            unpack(v[r][u][h], f);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              c[0][r0 + r] = fmaf(fa[q], f[q], c[0][r0 + r]);
+              c[1][r0 + r] = fmaf(fb[q], f[q], c[1][r0 + r]);
+            }
           }
         }
-      }
     }
   }
 #pragma unroll
@@ -127,12 +139,16 @@ __device__ __forceinline__ void warp_products(const float* w0, const float* w1, 
     }
 }
 
-// The nth expert that has rows, or -1 (fewer have, or the segments are not valid); by the whole block.
-__device__ __forceinline__ int nth_expert(const int32_t* seg, int E, int64_t R, int nth, int* s_e, int32_t* status) {
+// The experts that have rows (at most kFewRows of them), listed in shared memory by the whole block;
+// returns their number, 0 when the segments are not valid.
+struct Rows {
+  int e, begin, end;
+};
+__device__ __forceinline__ int list_experts(const int32_t* seg, int E, int64_t R, Rows* list, int32_t* status) {
   __shared__ int s_count[kWarps];
+  __shared__ int s_total;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (E + 32 * kWarps - 1) / (32 * kWarps), e0 = threadIdx.x * per, e1 = min(E, e0 + per);
-  if (threadIdx.x == 0) *s_e = -1;
   int ok = 1, count = 0;
   for (int e = e0; e < e1; ++e) {
     const int a = seg[e], b = seg[e + 1];
@@ -149,15 +165,17 @@ __device__ __forceinline__ int nth_expert(const int32_t* seg, int E, int64_t R, 
   if (lane == 31) s_count[warp] = incl;
   if (!__syncthreads_and(ok)) {
     if (threadIdx.x == 0) set_status(status, LRM_ERR_BAD_SEGMENTS);
-    return -1;
+    return 0;
   }
-  int before = incl - count;
-  for (int w = 0; w < warp; ++w) before += s_count[w];
-  if (before <= nth && nth < before + count)
-    for (int e = e0; e < e1; ++e)
-      if (seg[e] < seg[e + 1] && before++ == nth) *s_e = e;
+  int at = incl - count;
+  for (int w = 0; w < warp; ++w) at += s_count[w];
+  for (int e = e0; e < e1 && count > 0; ++e) {
+    const int a = seg[e], b = seg[e + 1];
+    if (a < b) list[at++] = Rows{e, a, b};
+  }
+  if (threadIdx.x == blockDim.x - 1) s_total = at;
   __syncthreads();
-  return *s_e;
+  return s_total;
 }
 
 template <typename TI, typename TO, bool GLU, int NT>
@@ -169,69 +187,68 @@ __global__ void __launch_bounds__(32 * kWarps, 2) rows_kernel(const int32_t* __r
   constexpr int CN = GLU ? 8 : 16;  // output columns
   constexpr int RT = 8 * NT;        // rows of x at a time
   __shared__ float s_sum[kWarps][16][RT + 1];
+  __shared__ Rows s_list[kFewRows];
   chain_wait();
-  __shared__ int s_e;
-  int e = 0, r_begin = 0, r_end = (int)R;
-  if (seg != nullptr) {
-    // blockIdx.y counts the experts that have rows: at most R of E, so that few CTAs find nothing to do
-    e = nth_expert(seg, E, R, blockIdx.y, &s_e, status);
-    if (e < 0) return;
-    r_begin = seg[e];
-    r_end = seg[e + 1];
-  }
-  const int n0 = blockIdx.x * CN, NP = GLU ? 2 * N : N;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
-  const TI* we = w + (int64_t)e * NP * K;
-  // rows g and g + 8 of this CTA's 16 (N is a multiple of 8: the second half may not exist; it repeats the first)
-  const int second = GLU ? N + n0 : (n0 + 8 < N ? n0 + 8 : n0);
-  const TI* w0 = we + (int64_t)(n0 + g) * K;
-  const TI* w1 = we + (int64_t)(second + g) * K;
-  for (int r0 = r_begin; r0 < r_end; r0 += RT) {
-    const int rows = min(RT, r_end - r0);
-    warp_products<NT>(w0, w1, x + (int64_t)r0 * K, rows, K, warp, lane, s_sum[warp]);
-    __syncthreads();
-    for (int i = threadIdx.x; i < CN * RT; i += blockDim.x) {
-      const int c = i % CN, r = i / CN, n = n0 + c;
-      if (r >= rows || n >= N) continue;
-      float v = 0.f, u = 0.f;
+  const int blocks = (N + CN - 1) / CN, NP = GLU ? 2 * N : N;
+  const int experts = seg != nullptr ? list_experts(seg, E, R, s_list, status) : 1;
+  // a task is one block of output columns of one expert
+  for (int task = blockIdx.x; task < experts * blocks; task += gridDim.x) {
+    const int i_e = task / blocks, n0 = (task - i_e * blocks) * CN;
+    const Rows seg_e = seg != nullptr ? s_list[i_e] : Rows{0, 0, (int)R};
+    const int e = seg_e.e, r_begin = seg_e.begin, r_end = seg_e.end;
+    const TI* we = w + (int64_t)e * NP * K;
+    // rows g and g + 8 of this CTA's 16 (N is a multiple of 8: the second half may not exist; it repeats the first)
+    const int second = GLU ? N + n0 : (n0 + 8 < N ? n0 + 8 : n0);
+    const TI* w0 = we + (int64_t)(n0 + g) * K;
+    const TI* w1 = we + (int64_t)(second + g) * K;
+    for (int r0 = r_begin; r0 < r_end; r0 += RT) {
+      const int rows = min(RT, r_end - r0);
+      warp_products<NT>(w0, w1, x + (int64_t)r0 * K, rows, K, warp, lane, s_sum[warp]);
+      __syncthreads();
+      for (int i = threadIdx.x; i < CN * RT; i += blockDim.x) {
+        const int c = i % CN, r = i / CN, n = n0 + c;
+        if (r >= rows || n >= N) continue;
+        float v = 0.f, u = 0.f;
 #pragma unroll
-      for (int q = 0; q < kWarps; ++q) {
-        v += s_sum[q][c][r];
-        if (GLU) u += s_sum[q][c + 8][r];
-      }
-      const int64_t row = r0 + r, at = row * N + n;
-      if (bias != nullptr) {
-        v += to_f(bias[(int64_t)e * NP + n]);
-        if (GLU) u += to_f(bias[(int64_t)e * NP + N + n]);
-      }
-      if (z != nullptr) {
-        z[row * NP + n] = from_f<TI>(v);
-        if (GLU) z[row * NP + N + n] = from_f<TI>(u);
-      }
-      if (GLU) {
-        v = act_value<LRM_ACT_SWIGLU>(v) * u;
-      } else {
-        switch (act) {
-          case LRM_ACT_RELU: v = act_value<LRM_ACT_RELU>(v); break;
-          case LRM_ACT_GELU: v = act_value<LRM_ACT_GELU>(v); break;
-          case LRM_ACT_SILU: v = act_value<LRM_ACT_SILU>(v); break;
-          default: break;
+        for (int q = 0; q < kWarps; ++q) {
+          v += s_sum[q][c][r];
+          if (GLU) u += s_sum[q][c + 8][r];
         }
+        const int64_t row = r0 + r, at = row * N + n;
+        if (bias != nullptr) {
+          v += to_f(bias[(int64_t)e * NP + n]);
+          if (GLU) u += to_f(bias[(int64_t)e * NP + N + n]);
+        }
+        if (z != nullptr) {
+          z[row * NP + n] = from_f<TI>(v);
+          if (GLU) z[row * NP + N + n] = from_f<TI>(u);
+        }
+        if (GLU) {
+          v = act_value<LRM_ACT_SWIGLU>(v) * u;
+        } else {
+          switch (act) {
+            case LRM_ACT_RELU: v = act_value<LRM_ACT_RELU>(v); break;
+            case LRM_ACT_GELU: v = act_value<LRM_ACT_GELU>(v); break;
+            case LRM_ACT_SILU: v = act_value<LRM_ACT_SILU>(v); break;
+            default: break;
+          }
+        }
+        if (residual != nullptr) v += to_f(residual[at]);
+        y[at] = from_f<TO>(v);
       }
-      if (residual != nullptr) v += to_f(residual[at]);
-      y[at] = from_f<TO>(v);
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
 template <typename TI, typename TO, bool GLU, int NT>
 void launch(const LinearArgs& a, cudaStream_t s) {
   constexpr int CN = GLU ? 8 : 16;
-  const int64_t experts = a.R < a.E ? a.R : a.E;  // that can have a row
-  launch_chained(rows_kernel<TI, TO, GLU, NT>, dim3((unsigned)((a.N + CN - 1) / CN), (unsigned)experts), dim3(32 * kWarps),
-                 0, s, a.seg_offsets, a.E, a.R, (const TI*)a.x, (const TI*)a.w, (const TI*)a.bias,
-                 (const TO*)a.residual, a.N, a.K, (int)a.act, (TO*)a.y, (TI*)a.z, a.status);
+  const int64_t tasks = (a.R < a.E ? a.R : a.E) * ((a.N + CN - 1) / CN), room = 2 * (int64_t)sm_count();
+  launch_chained(rows_kernel<TI, TO, GLU, NT>, dim3((unsigned)(tasks < room ? tasks : room)), dim3(32 * kWarps), 0, s,
+                 a.seg_offsets, a.E, a.R, (const TI*)a.x, (const TI*)a.w, (const TI*)a.bias, (const TO*)a.residual, a.N,
+                 a.K, (int)a.act, (TO*)a.y, (TI*)a.z, a.status);
 }
 
 template <typename TO, bool GLU>
