@@ -146,9 +146,10 @@ struct LinearArgs {
 };
 void launch_linear_simt(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, cudaStream_t s);
 // Up to this many rows (of all experts together) one pass over the weights by plain loads beats the tensor
-// cores' tiles of 256 rows.  GB300, bf16, weights 1408+1408 x 4096 (SwiGLU), 4096 x 4096, 1536 x 2048:
-// 6.8, 8.7, 3.3 us at 8 rows (tiles: 19.5, 19.3, 11.4), 12.1, 12.7, 6.0 at 32, 20.7, 22.1, 9.2 at 64.
-// 128 experts of 1536 x 2048, top-8: 13.5 against 20.3 us at 8 rows, 27.8 : 29.4 at 32, 43.2 : 40.8 at 64.
+// cores' tiles of 256 rows.  GB300, bf16, weights 1408+1408 x 4096 (SwiGLU), 4096 x 4096, 768+768 x 2048:
+// 7.5, 8.7, 3.8 us at 8 rows, 12.4, 12.8, 6.5 at 32 (tiles: 17.4, 15.6, 10.3 at any of these), 20.7, 22.1, 9.2
+// at 64.  128 experts of 768+768 x 2048, top-8: 13 against 20 us at 8 rows, 25 : 29 at 32, 43 : 40 at 64.
+// fp32 4096 x 4096: 69 us at 32 rows, 99 us through the tiles.
 constexpr int64_t kFewRows = 32;
 void launch_linear_rows(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, cudaStream_t s);
 lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, void* ws, cudaStream_t s);

@@ -1,5 +1,5 @@
-// lrm_linear and lrm_linear_backward on the CUDA cores (fp32 products and sums): fp32 inputs, and
-// bf16 on request.
+// lrm_linear and lrm_linear_backward on the CUDA cores (fp32 products and sums), on request
+// (LRM_GEMM_FORCE_SIMT): the plain form the tensor-core kernels are checked beside.
 //
 //   forward   z = x W[e]^T + b[e], y = act(z) + residual
 //   gradient  dx = dz W[e];  dW[e] = dz^T x over the segment's rows
@@ -206,8 +206,8 @@ void backward_all(const LinearGradArgs& a, cudaStream_t s) {
                    (const T*)nullptr, (T*)a.dx, (T*)nullptr, a.status);
   if (a.dw != nullptr)
     launch_chained(weights_kernel<T>,
-                   dim3((unsigned)((a.K + BN - 1) / BN), (unsigned)((a.N + BM - 1) / BM), (unsigned)a.E), dim3(NT), 0, s,
-                   a.seg_offsets, a.E, a.R, (const T*)a.dz, (const T*)a.x, a.N, a.K, a.dw, a.status);
+                   dim3((unsigned)((a.K + BN - 1) / BN), (unsigned)((a.N + BM - 1) / BM), (unsigned)a.E), dim3(NT), 0,
+                   s, a.seg_offsets, a.E, a.R, (const T*)a.dz, (const T*)a.x, a.N, a.K, a.dw, a.status);
 }
 
 }  // namespace

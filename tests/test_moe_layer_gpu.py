@@ -283,9 +283,11 @@ LINEARS = [  # dtype, R, N, K, act, bias, residual, save_z, out_f32
     (BF16, 63, 520, 512, "silu", True, True, False, False), (BF16, 64, 264, 128, "swiglu", True, True, True, False),
     (BF16, 65, 40, 136, "relu", True, True, True, False), (BF16, 127, 128, 192, "none", False, False, False, True),
     (BF16, 128, 256, 64, "swiglu", True, True, True, False), (BF16, 129, 136, 72, "gelu", True, True, True, False),
-    (BF16, 255, 512, 1000, "silu", False, True, False, False), (BF16, 257, 776, 1032, "swiglu", True, True, True, False),
+    (BF16, 255, 512, 1000, "silu", False, True, False, False),
+    (BF16, 257, 776, 1032, "swiglu", True, True, True, False),
     (BF16, 513, 64, 320, "none", True, False, True, True), (BF16, 1537, 776, 1032, "gelu", True, True, True, False),
-    (BF16, 3001, 1416, 520, "swiglu", True, False, True, False), (BF16, 4000, 128, 2048, "none", True, False, False, True),
+    (BF16, 3001, 1416, 520, "swiglu", True, False, True, False),
+    (BF16, 4000, 128, 2048, "none", True, False, False, True),
     (BF16, 70, 8, 8, "gelu", True, True, True, False), (BF16, 33, 16, 24, "swiglu", True, True, True, False),
     (BF16, 300, 8, 2048, "relu", True, False, False, True), (F32, 70, 8, 8, "silu", True, True, True, False),
     (F32, 3, 40, 72, "gelu", True, True, True, False), (F32, 70, 136, 264, "swiglu", True, True, True, False),
@@ -337,12 +339,18 @@ def test_linear(case, simt, status):
 
 
 GROUPED = [  # dtype, R, E, segments, N, K, act, bias, residual, save_z
-    (BF16, 1, 4, "one", 64, 72, "swiglu", True, True, True), (BF16, 8, 128, "ragged", 768, 256, "swiglu", False, False, False),
-    (BF16, 100, 5, "short", 136, 264, "gelu", True, True, True), (BF16, 512, 128, "ragged", 264, 520, "swiglu", True, False, True),
-    (BF16, 512, 16, "one", 72, 136, "none", True, True, False), (BF16, 1000, 3, "even", 520, 72, "silu", True, True, True),
-    (BF16, 2000, 7, "short", 264, 328, "swiglu", True, True, True), (BF16, 5000, 40, "ragged", 392, 200, "relu", True, False, False),
-    (BF16, 3000, 1, "even", 136, 64, "swiglu", False, True, True), (BF16, 6000, 1024, "ragged", 72, 64, "none", True, False, False),
-    (F32, 60, 6, "ragged", 40, 72, "swiglu", True, True, True), (F32, 900, 9, "short", 136, 264, "gelu", True, True, True),
+    (BF16, 1, 4, "one", 64, 72, "swiglu", True, True, True),
+    (BF16, 8, 128, "ragged", 768, 256, "swiglu", False, False, False),
+    (BF16, 100, 5, "short", 136, 264, "gelu", True, True, True),
+    (BF16, 512, 128, "ragged", 264, 520, "swiglu", True, False, True),
+    (BF16, 512, 16, "one", 72, 136, "none", True, True, False),
+    (BF16, 1000, 3, "even", 520, 72, "silu", True, True, True),
+    (BF16, 2000, 7, "short", 264, 328, "swiglu", True, True, True),
+    (BF16, 5000, 40, "ragged", 392, 200, "relu", True, False, False),
+    (BF16, 3000, 1, "even", 136, 64, "swiglu", False, True, True),
+    (BF16, 6000, 1024, "ragged", 72, 64, "none", True, False, False),
+    (F32, 60, 6, "ragged", 40, 72, "swiglu", True, True, True),
+    (F32, 900, 9, "short", 136, 264, "gelu", True, True, True),
     (F32, 2500, 4, "ragged", 72, 1032, "silu", False, True, False),
 ]
 
@@ -582,7 +590,8 @@ def test_bad_segments_compute_nothing():
             y, dx = torch.full((R, 72), 7.0, dtype=dt, device="cuda"), torch.full((R, 64), 7.0, dtype=dt, device="cuda")
             dw = torch.full((3, 72, 64), 7.0, device="cuda")
             for call in (lambda: lrm.lrm_linear(x, w, seg_offsets=s, y=y, flags=simt, dev_status=st),
-                         lambda: lrm.lrm_linear_backward(y, x, w, seg_offsets=s, dx=dx, dw=dw, flags=simt, dev_status=st),
+                         lambda: lrm.lrm_linear_backward(y, x, w, seg_offsets=s, dx=dx, dw=dw, flags=simt,
+                                                         dev_status=st),
                          lambda: lrm.lrm_act_backward(y, y, act="silu", seg_offsets=s, dz=y, dev_status=st)):
                 st.zero_()
                 call()
