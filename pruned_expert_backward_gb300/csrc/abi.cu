@@ -42,7 +42,7 @@ struct SortWs {
   size_t counts, loads, total;
 };
 SortWs sort_layout(int64_t T, int32_t k, int32_t E) {
-  if (sort_in_one_launch(T, k, E)) return SortWs{};
+  if (!sort_needs_scratch(T, k, E)) return SortWs{};
   const int64_t ct = sort_chunk_tokens(k), nc = (T + ct - 1) / ct;
   SortWs w{};
   w.loads = up(sizeof(int32_t) * (size_t)(nc > 0 ? nc : 1) * (E + 1));

@@ -125,7 +125,9 @@ struct SortArgs {
   int32_t* loads;   // scratch [E + 1]
   int32_t* status;
 };
-bool sort_in_one_launch(int64_t T, int32_t k, int32_t E);  // then no scratch is needed
+bool sort_in_one_launch(int64_t T, int32_t k, int32_t E);
+bool sort_self_counted(int64_t T, int32_t k);  // up to so many pairs the ranking counts them itself
+bool sort_needs_scratch(int64_t T, int32_t k, int32_t E);
 int sort_chunk_tokens(int32_t k);  // tokens of a chunk of the multi-launch form
 lrm_status launch_sort_tokens(const SortArgs& a, lrm_dtype dt, cudaStream_t s);
 void launch_combine(const int32_t* row_of_pair, const float* alpha, const void* y_s, const void* residual, int64_t T,

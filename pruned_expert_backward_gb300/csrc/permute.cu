@@ -12,9 +12,9 @@
 //
 // sort: up to kSmallPairs pairs one launch does everything: every CTA ranks all pairs for itself
 // (a few hundred nanoseconds in shared memory) and copies the rows of its own tokens.  Beyond that
-// several launches: counts of each chunk of pairs, the scan of every expert's counts down the chunks,
-// and the ranking of each chunk's pairs.  A token's row is read once and written k times, by a fourth
-// launch with a CTA per token, or beside the ranking where rows are narrow.
+// several launches: counts of each chunk of pairs, the scan of every expert's counts down the chunks
+// (neither up to kSelfPairs pairs), and the ranking of each chunk's pairs.  A token's row is read once and
+// written k times, by a launch of its own with a CTA per token, or beside the ranking where rows are narrow.
 // No atomics on anything that decides an order: all results are deterministic.
 #include "common.cuh"
 #include "kernels.h"
@@ -27,6 +27,10 @@ namespace {
 // 64 tokens take 4.2 us, the several launches 9 us at the least.
 constexpr int kSmallPairs = 2048;
 constexpr int kSmallExperts = 256;
+// Up to this many pairs every chunk's ranking counts all pairs itself, which saves two launches and the
+// scratch (128 experts, H = 512: 4096 pairs 6.3 us on the device against 7.3, 8192 pairs 8.3 and 8.3, 16384
+// pairs 12.8 and 10.0; a call through the binding 21 against 26 us).
+constexpr int kSelfPairs = 8192;
 constexpr int kChunkThreads = 256;  // multi-launch form: pairs of a chunk (whole tokens), at most one per thread
 
 // Bucket of a pair: its expert, or E when it is not routed (-1) or its id is out of range (recorded).
@@ -188,11 +192,14 @@ __global__ void __launch_bounds__(1024) sort_colscan_kernel(int32_t* __restrict_
   if (threadIdx.x == 0) loads[e] = run;
 }
 
-template <typename T>
+// SELF: every CTA counts all pairs itself, those before its chunk and the others, instead of reading the
+// scanned counts of two launches before it.
+template <typename T, bool SELF>
 __global__ void __launch_bounds__(kChunkThreads) sort_rows_kernel(
     const int32_t* __restrict__ idx, const T* __restrict__ x, int64_t n_tok, int k, int E, int H, int chunk_tok,
     const int32_t* __restrict__ counts, const int32_t* __restrict__ loads, int32_t* __restrict__ seg,
-    int32_t* __restrict__ pair_of_row, int32_t* __restrict__ row_of_pair, T* __restrict__ x_s) {
+    int32_t* __restrict__ pair_of_row, int32_t* __restrict__ row_of_pair, T* __restrict__ x_s,
+    int32_t* __restrict__ status) {
   chain_wait();
   constexpr int kWarps = kChunkThreads / 32;
   extern __shared__ int sh[];
@@ -205,14 +212,36 @@ __global__ void __launch_bounds__(kChunkThreads) sort_rows_kernel(
   const int ntok = (int)min((int64_t)chunk_tok, n_tok - t0), np = ntok * k;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < kWarps * B; i += blockDim.x) s_cnt[i] = 0;
+  int* s_before = s_cnt;  // SELF: pairs of each bucket before the chunk, and the others
+  int* s_after = s_cnt + B;
+  if (SELF) {
+    __syncthreads();
+    const int P = (int)(n_tok * k), first = (int)(t0 * k);
+    for (int u0 = threadIdx.x; u0 < P; u0 += 4 * kChunkThreads) {
+      int id[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) id[q] = u0 + q * kChunkThreads < P ? idx[u0 + q * kChunkThreads] : 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int u = u0 + q * kChunkThreads;
+        if (u < P) atomicAdd((u < first ? s_before : s_after) + bucket_of(id[q], E, c == 0 ? status : nullptr), 1);
+      }
+    }
+    __syncthreads();
+  }
   for (int b0 = 0, run = 0; b0 < B; b0 += blockDim.x) {
     const int e = b0 + threadIdx.x;
-    const int ex = block_prefix(e < B ? loads[e] : 0, s_scan);
+    const int load = e >= B ? 0 : (SELF ? s_before[e] + s_after[e] : loads[e]);
+    const int ex = block_prefix(load, s_scan);
     if (e < B) {
-      s_start[e] = run + ex + counts[c * B + e];
+      s_start[e] = run + ex + (SELF ? s_before[e] : counts[c * B + e]);
       if (c == 0) seg[e] = run + ex;
     }
     run += s_scan[32];
+    __syncthreads();
+  }
+  if (SELF) {  // their place becomes the warps' counts
+    for (int i = threadIdx.x; i < 2 * B; i += blockDim.x) s_cnt[i] = 0;
     __syncthreads();
   }
   const bool in = threadIdx.x < np;
@@ -530,17 +559,24 @@ lrm_status sort_all(const SortArgs& a, cudaStream_t s) {
   } else {
     const int chunk_tok = sort_chunk_tokens(a.k);
     const int64_t nc = a.T > 0 ? (a.T + chunk_tok - 1) / chunk_tok : 1;
-    launch_chained(sort_count_kernel, dim3((unsigned)nc), dim3(kChunkThreads), sizeof(int) * B, s, a.topk_idx, P, a.E,
-                   chunk_tok * a.k, a.counts, a.status);
-    launch_chained(sort_colscan_kernel, dim3(B), dim3(nc > 256 ? 1024 : 256), 0, s, a.counts, nc, B, a.loads);
-    const size_t smem = sizeof(int) * ((size_t)B * (1 + kChunkThreads / 32) + kChunkThreads);
     // Rows of 1 KB and more are copied by a launch of their own, a CTA per token (T = 32768, k = 8, H = 4096:
     // 370 against 394 us; T = 2048, H = 2048: 16 against 56 us), narrower ones beside the ranking (T = 30000,
     // H = 72: 16 against 41 us).
     const bool apart = a.x_s != nullptr && a.H >= 64 * VecTraits<T>::N;
-    launch_chained(sort_rows_kernel<T>, dim3((unsigned)nc), dim3(kChunkThreads), smem, s, a.topk_idx, (const T*)a.x,
-                   a.T, a.k, a.E, a.H, chunk_tok, (const int32_t*)a.counts, (const int32_t*)a.loads, a.seg_offsets,
-                   a.pair_of_row, a.row_of_pair, apart ? (T*)nullptr : (T*)a.x_s);
+    T* beside = apart ? nullptr : (T*)a.x_s;
+    const size_t smem = sizeof(int) * ((size_t)B * (1 + kChunkThreads / 32) + kChunkThreads);
+    if (sort_self_counted(a.T, a.k)) {
+      launch_chained(sort_rows_kernel<T, true>, dim3((unsigned)nc), dim3(kChunkThreads), smem, s, a.topk_idx,
+                     (const T*)a.x, a.T, a.k, a.E, a.H, chunk_tok, (const int32_t*)nullptr, (const int32_t*)nullptr,
+                     a.seg_offsets, a.pair_of_row, a.row_of_pair, beside, a.status);
+    } else {
+      launch_chained(sort_count_kernel, dim3((unsigned)nc), dim3(kChunkThreads), sizeof(int) * B, s, a.topk_idx, P,
+                     a.E, chunk_tok * a.k, a.counts, a.status);
+      launch_chained(sort_colscan_kernel, dim3(B), dim3(nc > 256 ? 1024 : 256), 0, s, a.counts, nc, B, a.loads);
+      launch_chained(sort_rows_kernel<T, false>, dim3((unsigned)nc), dim3(kChunkThreads), smem, s, a.topk_idx,
+                     (const T*)a.x, a.T, a.k, a.E, a.H, chunk_tok, (const int32_t*)a.counts, (const int32_t*)a.loads,
+                     a.seg_offsets, a.pair_of_row, a.row_of_pair, beside, a.status);
+    }
     if (apart) {
       const int cols = row_threads((a.H / VecTraits<T>::N + 1) / 2);
       launch_chained(sort_copy_kernel<T>, dim3((unsigned)a.T), dim3(cols < 64 ? 64 : cols), 0, s,
@@ -597,6 +633,10 @@ void combine_backward_all(const int32_t* row_of_pair, const float* alpha, const 
 }  // namespace
 
 bool sort_in_one_launch(int64_t T, int32_t k, int32_t E) { return T * k <= kSmallPairs && E <= kSmallExperts; }
+bool sort_self_counted(int64_t T, int32_t k) { return T * k <= kSelfPairs; }
+bool sort_needs_scratch(int64_t T, int32_t k, int32_t E) {
+  return !sort_in_one_launch(T, k, E) && !sort_self_counted(T, k);
+}
 int sort_chunk_tokens(int32_t k) { return kChunkThreads / k; }
 
 lrm_status launch_sort_tokens(const SortArgs& a, lrm_dtype dt, cudaStream_t s) {

@@ -21,20 +21,19 @@ def test_sort_tokens_host_validation():
     assert f(P, P, 16, 2, 4, 60, 0, P, P, P, P, P, BIG, None, None) == SHAPE
     assert f(P, P, 1 << 40, 2, 4, 64, 0, P, P, P, P, P, BIG, None, None) == SHAPE
     assert f(P, P, 16, 2, 4, 64, 2, P, P, P, P, P, BIG, None, None) == DTYPE
-    assert f(P, P, 4096, 2, 4, 64, 0, P, P, P, P, None, 0, None, None) == WS   # many pairs need scratch
-    assert f(P, P, 4096, 2, 4, 64, 0, P, P, P, P, P, 16, None, None) == WS
-    assert f(P, P, 16, 2, 300, 64, 0, P, P, P, P, None, 0, None, None) == WS   # and many experts
+    assert f(P, P, 1 << 20, 2, 4, 64, 0, P, P, P, P, None, 0, None, None) == WS   # many pairs need scratch
+    assert f(P, P, 1 << 20, 2, 4, 64, 0, P, P, P, P, P, 16, None, None) == WS
 
 
 def test_sort_fits_the_common_workspace():
     lib = ensure_built()
     n = C.c_size_t(0)
-    for T, k, E in ((1, 1, 1), (100000, 16, 1024), (5003, 6, 60)):
+    for T, k, E in ((1, 1, 1), (100000, 16, 1024), (50003, 6, 60)):
         assert lib.lrm_workspace_size(T, k, E, 8, 8, 0, C.byref(n)) == OK
         chunks = (T + 256 // k - 1) // (256 // k)
         common = n.value
         assert lib.lrm_sort_workspace_size(T, k, E, C.byref(n)) == OK
-        assert (n.value == 0) if T == 1 else (common >= n.value >= 4 * (chunks + 1) * (E + 1))
+        assert (n.value == 0) if T * k < 10000 else (common >= n.value >= 4 * (chunks + 1) * (E + 1))
     assert lib.lrm_sort_workspace_size(1, 1, 1, None) == ARG
 
 
