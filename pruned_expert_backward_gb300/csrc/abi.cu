@@ -53,12 +53,14 @@ SortWs sort_layout(int64_t T, int32_t k, int32_t E) {
 // Scratch of the products and of the bias gradient (NP: rows of w, columns of dz).
 size_t linear_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
   if (dt != LRM_F32) return 0;
-  return kAlign + up(linear_planes_bytes(R, K)) + up(linear_planes_bytes((int64_t)E * NP, K));
+  return kAlign + up(linear_planes_bytes(R, K)) + up(linear_planes_bytes((int64_t)E * NP, K)) +
+         up(linear_parts_bytes(R, E, NP, K, dt));
 }
 size_t linear_grad_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
   size_t n = kAlign + linear_plan_bytes(E);  // kAlign: the maps start on a 128-byte boundary
   const int parts = E == 1 ? linear_grad_parts(R, NP, K) : 1;
   if (parts > 1) n += up(sizeof(float) * (size_t)parts * NP * K);
+  n += up(linear_grad_parts_bytes(R, E, NP, K, dt));
   if (dt == LRM_F32)
     n += up(linear_planes_bytes(R, NP)) + up(linear_planes_bytes(R, K)) + up(linear_planes_bytes((int64_t)E * NP, K));
   return n;

@@ -157,6 +157,9 @@ void launch_linear_rows(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, cud
 lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, void* ws, cudaStream_t s);
 size_t linear_planes_bytes(int64_t rows, int64_t cols);  // an fp32 operand as three bf16 planes
 size_t linear_plan_bytes(int32_t E);                     // plan and expert maps of the weights' gradient
+// parts of a long reduction, added up by a launch of their own: bytes for the forward's, and for dx's
+size_t linear_parts_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt);
+size_t linear_grad_parts_bytes(int64_t R, int32_t E, int32_t N, int32_t K, lrm_dtype dt);
 int linear_grad_parts(int64_t R, int32_t N, int32_t K);  // parts of the dense weights' gradient, summed apart
 struct LinearGradArgs {
   const int32_t* seg_offsets;

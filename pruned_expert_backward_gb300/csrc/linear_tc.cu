@@ -42,6 +42,8 @@
 #include "tc_host.h"
 #include "tc_ptx.cuh"
 
+#include <type_traits>
+
 namespace lrm {
 
 namespace {
@@ -51,6 +53,7 @@ constexpr int kBK = 64;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kABytes = kBM * kBK * 2;
+constexpr int kPairs = 76;  // CTA pairs of the GPU, for the choices that fix the scratch
 constexpr int kBoxBytes = 2048;  // 32 rows x 64 bytes, 64-byte swizzle: 32 bf16 or 16 fp32 columns
 
 enum Kind { FWD = 0, DX = 1, DW = 2 };
@@ -86,6 +89,8 @@ struct Params {
   int part_rows;  // DW without segments: rows of each part of the reduction (E parts, each with its own output)
   int terms;      // 1, or 6 for fp32 inputs in three planes
   int pk;         // K slices per accumulator (PROMOTE)
+  int parts;      // FWD, DX: parts of the reduction, each a tile of its own with its own output [R][N]
+  int part_len;   // K slices of a part (of all terms together)
   // operands that are contiguous along M or N (DX: B, DW: both): both 64-column blocks of a CTA's 128 columns
   // come in one box, where the columns are a multiple of 64 (else a box would wrap into the next row)
   bool one_box_a, one_box_b;
@@ -125,12 +130,18 @@ struct Tile {
   int row0, row_end;  // FWD, DX: this CTA's output rows; DW: the rows summed over
   int m0, n0;         // DW: this CTA's first output row; n0: first output column
   int slices;         // K slices of one term
+  int part, lo, hi;   // part of the reduction, and its K slices, counted over all terms
   bool has_rows;
 };
 
 template <int KIND, int BN, bool GLU>
 __device__ __forceinline__ Tile decode(const Params& p, const int* prefix, int t, int rank) {
   Tile d;
+  d.part = 0;
+  if (KIND != DW && p.parts > 1) {
+    d.part = t % p.parts;
+    t /= p.parts;
+  }
   const int mg = t / p.tiles_n, nt = t - mg * p.tiles_n;
   d.n0 = nt * (GLU ? BN / 2 : BN);
   if (KIND == DW) {
@@ -140,6 +151,8 @@ __device__ __forceinline__ Tile decode(const Params& p, const int* prefix, int t
     d.row0 = p.seg != nullptr ? __ldg(p.seg + d.e) : d.e * p.part_rows;
     d.row_end = p.seg != nullptr ? __ldg(p.seg + d.e + 1) : (int)min(p.R, (int64_t)d.row0 + p.part_rows);
     d.slices = (d.row_end - d.row0 + kBK - 1) / kBK;
+    d.lo = 0;
+    d.hi = d.slices * p.terms;
     d.has_rows = d.m0 < p.M;
     return d;
   }
@@ -160,6 +173,8 @@ __device__ __forceinline__ Tile decode(const Params& p, const int* prefix, int t
   }
   d.row_end = min(end, d.row0 + kBM);
   d.slices = (p.red + kBK - 1) / kBK;
+  d.lo = d.part * p.part_len;
+  d.hi = min(d.slices * p.terms, d.lo + p.part_len);
   d.has_rows = d.row0 < end;
   return d;
 }
@@ -300,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (KIND == DW) {
     n_tiles = p.seg == nullptr || __ldg(p.plan) == 1 ? p.E * p.tiles_m * p.tiles_n : 0;
   } else if (p.seg == nullptr) {
-    n_tiles = (int)((p.R + 2 * kBM - 1) / (2 * kBM)) * p.tiles_n;
+    n_tiles = (int)((p.R + 2 * kBM - 1) / (2 * kBM)) * p.tiles_n * p.parts;
   } else {
     // each thread sums a run of experts; a scan over the threads gives the prefix
     const int per = (p.E + kThreads - 1) / kThreads, e0 = threadIdx.x * per, e1 = min(p.E, e0 + per);
@@ -327,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (e0 < p.E && e1 == p.E) prefix[p.E] = run;
     __syncthreads();
-    n_tiles = valid ? prefix[p.E] * p.tiles_n : 0;
+    n_tiles = valid ? prefix[p.E] * p.tiles_n * p.parts : 0;
     if (!valid && threadIdx.x == 0) set_status(p.status, LRM_ERR_BAD_SEGMENTS);
   }
 
@@ -357,13 +372,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // first B row (FWD: rows of w, a SwiGLU pair stages gate rows and up rows) or column of this CTA
       const int nb = GLU ? d.n0 + rank * p.N : d.n0 + rank * (BN / 2);
       const uint32_t bytes = C::kBBytes + (d.has_rows ? kABytes : 0);
-      const int planes = p.terms > 1 ? 3 : 1, total = d.slices * p.terms;
-      int term = 6 - p.terms, kb = 0;
-      for (int k0 = 0; k0 < total; k0 += C::kSub, ++it) {
+      const int planes = p.terms > 1 ? 3 : 1;
+      int term = 6 - p.terms, kb = d.lo;
+      if (d.lo > 0) {
+        term += d.lo / d.slices;
+        kb = d.lo % d.slices;
+      }
+      for (int k0 = d.lo; k0 < d.hi; k0 += C::kSub, ++it) {
         const uint32_t s = st, ph = sph;
         if (++st == (uint32_t)S) { st = 0; sph ^= 1u; }
         if (!mbar_wait_warp(empty0 + 8 * s, ph ^ 1u, abortv, p.status)) { ok = false; break; }
-        const int n_sub = min(C::kSub, total - k0);
+        const int n_sub = min(C::kSub, d.hi - k0);
         const uint32_t fb = full_lead + 8 * s;
         if (elect_one()) mbar_expect_tx_cluster(fb, n_sub * bytes);
         for (int j = 0; j < n_sub; ++j) {
@@ -407,9 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         t = nth_tile(i, pair, n_pairs);
         if (t >= n_tiles) continue;
         const Tile d = decode<KIND, BN, GLU>(p, prefix, t, 0);
-        const int total = d.slices * p.terms;
-        for (int k0 = 0; k0 < total && ok; k0 += PROMOTE ? p.pk : total, ++use) {
-          const int k1 = PROMOTE ? min(total, k0 + p.pk) : total;
+        for (int k0 = d.lo; k0 < d.hi && ok; k0 += PROMOTE ? p.pk : d.hi, ++use) {
+          const int k1 = PROMOTE ? min(d.hi, k0 + p.pk) : d.hi;
           const uint32_t acc = use & 1u;
           if (!mbar_wait_warp(acce0 + 8 * acc, ((use >> 1) & 1u) ^ 1u, abortv, p.status)) { ok = false; break; }
           tc_fence_after();
@@ -471,10 +489,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = lane < nrows;
       const int64_t row = row_base + lane;
       const int n_first = d.n0 + group * NO * 32;
-      const int total = d.slices * p.terms;
       const TO* res =
           KIND == FWD && p.residual != nullptr && live ? static_cast<const TO*>(p.residual) + row * p.N : nullptr;
-      TO* y_row = static_cast<TO*>(p.y) + (KIND == DW ? ((int64_t)d.e * p.M + row) : row) * p.N;
+      const int group = KIND == DW ? d.e : d.part;  // of the output
+      TO* y_row = static_cast<TO*>(p.y) + (group * (KIND == DW ? (int64_t)p.M : p.R) + row) * p.N;
 
       // the residual of chunk c (zeros past the last column)
       auto load_residual = [&](int c, uint4* r) {
@@ -516,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (res != nullptr) add_vectors<TO>(v, r);
         }
-        out.put(v, &tmY, lane, n, p.N, row_base, KIND == DW ? d.e : 0, whole, live, y_row);
+        out.put(v, &tmY, lane, n, p.N, row_base, group, whole, live, y_row);
       };
 
       if (PROMOTE) {
@@ -525,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < NC; ++c)
 #pragma unroll
           for (int i = 0; i < 32; ++i) acc[c][i] = 0.f;
-        for (int k0 = 0; k0 < total; k0 += p.pk, ++use) {
+        for (int k0 = d.lo; k0 < d.hi; k0 += p.pk, ++use) {
           const uint32_t a = use & 1u;
           if (!mbar_wait(accf0 + 8 * a, (use >> 1) & 1u, abortv, p.status)) { ok = false; break; }
           tc_fence_after();
@@ -684,6 +702,72 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict_
   }
 }
 
+// The products' parts [parts][R][NP] added in order, with the epilogue of lrm_linear (DX: none): a CTA per row,
+// 8 columns a thread.
+template <typename TI, typename TO>
+__global__ void __launch_bounds__(128) finish_parts_kernel(const int32_t* __restrict__ seg, int E, int64_t R, int N,
+                                                           const float* __restrict__ part, int parts, int act,
+                                                           const TI* __restrict__ bias, const TO* __restrict__ residual,
+                                                           TO* __restrict__ y, TI* __restrict__ z) {
+  chain_wait();
+  const bool glu = act == LRM_ACT_SWIGLU;
+  const int NP = glu ? 2 * N : N;
+  const int64_t row = blockIdx.x;
+  int e = 0;
+  if (seg != nullptr) {
+    if (!rows_valid(seg, E, R, nullptr) || row >= seg[E]) return;  // (recorded by the products)
+    int lo = 0, hi = E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (seg[mid] <= row) lo = mid; else hi = mid;
+    }
+    e = lo;
+  }
+  auto sum8 = [&](int col, float (&v)[8]) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) {
+      const float* at = part + ((int64_t)s * R + row) * NP + col;
+      float a[4], b[4];
+      unpack(ldg16(at), a);
+      unpack(ldg16(at + 4), b);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[q] += a[q];
+        v[4 + q] += b[q];
+      }
+    }
+    if (bias != nullptr)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] += to_f(bias[(int64_t)e * NP + col + q]);
+    if (z != nullptr)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) z[row * NP + col + q] = from_f<TI>(v[q]);
+  };
+  for (int c = threadIdx.x * 8; c < N; c += blockDim.x * 8) {
+    float v[8], u[8];
+    sum8(c, v);
+    if (glu) sum8(N + c, u);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (glu) {
+        v[q] = act_value<LRM_ACT_SWIGLU>(v[q]) * u[q];
+      } else {
+        switch (act) {
+          case LRM_ACT_RELU: v[q] = act_value<LRM_ACT_RELU>(v[q]); break;
+          case LRM_ACT_GELU: v[q] = act_value<LRM_ACT_GELU>(v[q]); break;
+          case LRM_ACT_SILU: v[q] = act_value<LRM_ACT_SILU>(v[q]); break;
+          default: break;
+        }
+      }
+      if (residual != nullptr) v[q] += to_f(residual[row * N + c + q]);
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) y[row * N + c + q] = from_f<TO>(v[q]);
+  }
+}
+
 // ---------------------------------------------------------------- host side ----------
 // [d2][d1][d0] of 2- or 4-byte elements, d0 contiguous (a multiple of 16 bytes), with a {b0, b1, 1} box.
 bool make_map(CUtensorMap* m, const void* base, bool f32, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
@@ -785,6 +869,35 @@ int64_t likely_row_tiles(const int32_t* seg, int64_t R, int E) {
   return (R + 2 * kBM - 1) / (2 * kBM) + (seg != nullptr ? (R < E ? R : E) / 2 : 0);
 }
 
+// How a product is cut where its tiles are few and its reduction long (fp32 inputs, whose six terms make it
+// six times as long, and dx): tile width and parts of the reduction by the least time, in units of 0.05 us.  A
+// slice takes 3 units (5 in the 256-column tile), adding the parts up costs a launch and a pass, 80 units.
+struct Cut {
+  int bn, parts, len;
+};
+Cut cut_product(int64_t R, int32_t E, int64_t cols, int total, int least) {
+  const int64_t tm = (R + 2 * kBM - 1) / (2 * kBM) + (E > 1 ? (R < E ? R : E) / 2 : 0);
+  Cut best{0, 1, total};
+  int64_t best_time = INT64_MAX;
+  for (int bn = least; bn <= 256; bn *= 2) {
+    const int64_t base = tm * ((cols + bn - 1) / bn);
+    int64_t parts = kPairs / base;
+    if (parts > total / 16) parts = total / 16;
+    for (int64_t n : {(int64_t)1, parts}) {
+      if (n < 1) continue;
+      const int64_t len = ((total + n - 1) / n + 7) / 8 * 8, used = (total + len - 1) / len;
+      const int64_t waves = (base * used + kPairs - 1) / kPairs;
+      const int64_t time = waves * (n == 1 ? total : len) * (bn == 256 ? 5 : 3) + (used > 1 ? 80 : 0);
+      if (time < best_time) {
+        best_time = time;
+        best = Cut{bn, (int)used, used > 1 ? (int)len : total};
+      }
+    }
+  }
+  return best;
+}
+int slices_of(int64_t red, lrm_dtype dt) { return (int)((red + kBK - 1) / kBK) * (dt == LRM_F32 ? 6 : 1); }
+
 // Tile width by the waves of tiles over the CTA pairs: a K slice of a 256-column tile takes 0.26 us (its
 // products), one of a 128- or 64-column tile 0.155 us (the operands' way in).  On a tie the narrower: more
 // SMs then share the reading of the weights.
@@ -806,6 +919,7 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
   const bool f32 = dt == LRM_F32, glu = a.act == LRM_ACT_SWIGLU;
   const int NP = glu ? 2 * a.N : a.N;
   const void *xs = a.x, *wsrc = a.w;
+  void* planes_end = nullptr;
   if (f32) {
     char* b = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws) + 127) & ~uintptr_t(127));
     Splits sp{};
@@ -814,6 +928,7 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
     b += (linear_planes_bytes(a.R, a.K) + 255) / 256 * 256;
     add_split(sp, a.w, a.E, NP, a.K, b);
     wsrc = b;
+    planes_end = b + (linear_planes_bytes((int64_t)a.E * NP, a.K) + 255) / 256 * 256;
     launch_splits(sp, s);
   }
   Params p{};
@@ -854,6 +969,35 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
       return launch<FWD, BN, GLU, false, B16, B16>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
     }
   };
+  p.parts = 1;
+  p.part_len = slices_of(a.K, dt);
+  if (f32) {
+    const Cut cut = cut_product(a.R, a.E, NP, p.part_len, 64);
+    if (cut.parts > 1) {
+      float* part = reinterpret_cast<float*>(static_cast<char*>(planes_end));
+      Params raw = p;  // the products alone, over all columns of w
+      raw.N = NP;
+      raw.act = LRM_ACT_NONE;
+      raw.bias = raw.residual = raw.z = nullptr;
+      raw.y = part;
+      raw.parts = cut.parts;
+      raw.part_len = cut.len;
+      raw.tiles_n = (NP + cut.bn - 1) / cut.bn;
+      if (!operand_map(&mB, wsrc, a.K, pitch, NP, (uint64_t)a.E * planes, cut.bn / 2) ||
+          !output_map(&mY, part, true, NP, a.R, cut.parts))
+        return LRM_ERR_CUDA;
+      const int64_t tiles = tm * raw.tiles_n * cut.parts;
+      const lrm_status st =
+          cut.bn == 256   ? launch<FWD, 256, false, true, float, float>(mA, mB, mY, mY, raw, tiles, s)
+          : cut.bn == 128 ? launch<FWD, 128, false, true, float, float>(mA, mB, mY, mY, raw, tiles, s)
+                          : launch<FWD, 64, false, true, float, float>(mA, mB, mY, mY, raw, tiles, s);
+      if (st) return st;
+      launch_chained(finish_parts_kernel<float, float>, dim3((unsigned)a.R), dim3(128), 0, s, a.seg_offsets, a.E, a.R,
+                     a.N, (const float*)part, cut.parts, (int)a.act, (const float*)a.bias, (const float*)a.residual,
+                     (float*)a.y, (float*)a.z);
+      return cudaGetLastError() == cudaSuccess ? LRM_OK : LRM_ERR_CUDA;
+    }
+  }
   const int64_t likely = likely_row_tiles(a.seg_offsets, a.R, a.E);
   if (glu) return with_width(likely, NP, 128, [&](auto bn) { return go(bn, IntTag<1>{}); });
   return with_width(likely, NP, 64, [&](auto bn) { return go(bn, IntTag<0>{}); });
@@ -895,6 +1039,7 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
   CUtensorMap mA, mB, mY;
   if (a.dw != nullptr) {
     p.M = a.N;
+    p.parts = 1;
     p.tiles_m = (a.N + 2 * kBM - 1) / (2 * kBM);
     const int parts = a.seg_offsets == nullptr ? linear_grad_parts(a.R, a.N, a.K) : 1;
     float* sums = parts > 1 ? reinterpret_cast<float*>(b) : a.dw;
@@ -926,6 +1071,7 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
     });
     if (st) return st;
     if (parts > 1) {
+      b += (sizeof(float) * (size_t)parts * a.N * a.K + 255) / 256 * 256;
       const int64_t n = (int64_t)a.N * a.K, blocks = (n / 4 + 255) / 256;
       launch_chained(sum_parts_kernel, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), dim3(256), 0, s,
                      (const float*)sums, parts, n, a.dw);
@@ -934,10 +1080,37 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
   if (a.dx != nullptr) {
     p.E = a.E;
     p.red = a.N;
-    p.y = a.dx;
-    if (!operand_map(&mA, dzs, a.N, pitch_n, a.R, planes, kBM) || !output_map(&mY, a.dx, f32, a.K, a.R, 1))
+    const Cut cut = cut_product(a.R, a.E, a.K, slices_of(a.N, dt), 128);
+    p.parts = cut.parts;
+    p.part_len = cut.len;
+    float* part = reinterpret_cast<float*>(b);
+    p.y = cut.parts > 1 ? part : a.dx;
+    if (!operand_map(&mA, dzs, a.N, pitch_n, a.R, planes, kBM) ||
+        !output_map(&mY, p.y, f32 || cut.parts > 1, a.K, a.R, cut.parts))
       return LRM_ERR_CUDA;
     const int64_t tm = row_tiles(a.seg_offsets, a.R, a.E);
+    if (cut.parts > 1) {
+      p.tiles_n = (a.K + cut.bn - 1) / cut.bn;
+      if (!column_map(&mB, wsrc, a.K, pitch_k, a.N, (uint64_t)a.E * planes, cut.bn / 128, &p.one_box_b))
+        return LRM_ERR_CUDA;
+      const int64_t tiles = tm * p.tiles_n * cut.parts;
+      const lrm_status st =
+          f32 ? (cut.bn == 256 ? launch<DX, 256, false, true, float, float>(mA, mB, mY, mY, p, tiles, s)
+                               : launch<DX, 128, false, true, float, float>(mA, mB, mY, mY, p, tiles, s))
+              : (cut.bn == 256 ? launch<DX, 256, false, true, B16, float>(mA, mB, mY, mY, p, tiles, s)
+                               : launch<DX, 128, false, true, B16, float>(mA, mB, mY, mY, p, tiles, s));
+      if (st) return st;
+      auto finish = [&](auto kernel, auto* out) {
+        using T = std::remove_pointer_t<decltype(out)>;
+        launch_chained(kernel, dim3((unsigned)a.R), dim3(128), 0, s, a.seg_offsets, a.E, a.R, a.K, (const float*)part,
+                       cut.parts, (int)LRM_ACT_NONE, (const T*)nullptr, (const T*)nullptr, out, (T*)nullptr);
+      };
+      if (f32)
+        finish(finish_parts_kernel<float, float>, static_cast<float*>(a.dx));
+      else
+        finish(finish_parts_kernel<B16, B16>, static_cast<B16*>(a.dx));
+      return cudaGetLastError() == cudaSuccess ? LRM_OK : LRM_ERR_CUDA;
+    }
     return with_width(likely_row_tiles(a.seg_offsets, a.R, a.E), a.K, 128, [&](auto bn) {
       constexpr int BN = decltype(bn)::value;
       if constexpr (BN < 128) {
@@ -961,6 +1134,15 @@ int linear_grad_parts(int64_t R, int32_t N, int32_t K) {
   int64_t parts = 76 / tiles;
   if (parts > R / 1024) parts = R / 1024;
   return parts < 1 ? 1 : (int)parts;
+}
+
+size_t linear_parts_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
+  const int parts = dt == LRM_F32 ? cut_product(R, E, NP, slices_of(K, dt), 64).parts : 1;
+  return parts > 1 ? sizeof(float) * (size_t)parts * R * NP : 0;
+}
+size_t linear_grad_parts_bytes(int64_t R, int32_t E, int32_t N, int32_t K, lrm_dtype dt) {
+  const int parts = cut_product(R, E, K, slices_of(N, dt), 128).parts;
+  return parts > 1 ? sizeof(float) * (size_t)parts * R * K : 0;
 }
 
 size_t linear_plan_bytes(int32_t E) {

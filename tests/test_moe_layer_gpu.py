@@ -290,6 +290,9 @@ LINEARS = [  # dtype, R, N, K, act, bias, residual, save_z, out_f32
     (BF16, 4000, 128, 2048, "none", True, False, False, True),
     (BF16, 70, 8, 8, "gelu", True, True, True, False), (BF16, 33, 16, 24, "swiglu", True, True, True, False),
     (BF16, 300, 8, 2048, "relu", True, False, False, True), (F32, 70, 8, 8, "silu", True, True, True, False),
+    # fp32 products with few tiles and a long reduction: summed in parts
+    (F32, 327, 128, 1016, "relu", True, False, True, False), (F32, 53, 72, 3000, "swiglu", True, True, True, False),
+    (F32, 600, 264, 2048, "gelu", True, True, False, False), (F32, 33, 8, 4096, "silu", True, True, True, False),
     (F32, 3, 40, 72, "gelu", True, True, True, False), (F32, 70, 136, 264, "swiglu", True, True, True, False),
     (F32, 257, 264, 1032, "silu", True, True, True, False), (F32, 700, 520, 136, "none", False, False, False, False),
     (F32, 1300, 72, 2056, "relu", True, True, False, False), (F32, 40, 520, 2048, "swiglu", False, True, False, False),
@@ -352,6 +355,8 @@ GROUPED = [  # dtype, R, E, segments, N, K, act, bias, residual, save_z
     (F32, 60, 6, "ragged", 40, 72, "swiglu", True, True, True),
     (F32, 900, 9, "short", 136, 264, "gelu", True, True, True),
     (F32, 2500, 4, "ragged", 72, 1032, "silu", False, True, False),
+    (F32, 200, 5, "short", 72, 2048, "swiglu", True, True, True),
+    (F32, 700, 3, "one", 136, 1480, "gelu", True, False, True),
 ]
 
 
@@ -472,6 +477,9 @@ LINEAR_GRADS = [  # dtype, R, N, K, E, segments
     (F32, 1500, 136, 264, None, None), (BF16, 8, 72, 64, 12, "ragged"), (BF16, 700, 264, 136, 5, "short"),
     (BF16, 3000, 520, 72, 64, "ragged"), (BF16, 6000, 136, 392, 3, "one"), (BF16, 9000, 72, 328, 2, "ragged"),
     (F32, 900, 72, 136, 9, "short"), (F32, 4000, 40, 264, 4, "ragged"),
+    # dx with few tiles and a long reduction: summed in parts
+    (F32, 48, 1232, 288, None, None), (BF16, 300, 4104, 72, None, None), (BF16, 200, 4104, 136, 4, "short"),
+    (F32, 130, 2000, 40, 3, "ragged"), (BF16, 33, 8192, 264, None, None),
 ]
 
 
@@ -597,6 +605,17 @@ def test_bad_segments_compute_nothing():
                 call()
                 assert int(st.item()) == 11
             assert bool((y == 7.0).all()) and bool((dx == 7.0).all()) and bool((dw == 7.0).all())
+    # long reductions, summed in parts: the second launch must not write either
+    for dt, N, K in ((F32, 72, 2048), (F32, 2048, 72), (BF16, 4096, 72)):
+        x, w, _, _ = linear_inputs(gen(N), dt, 200, N, N, K, False, False, 3)
+        y, dx = torch.full((200, N), 7.0, dtype=dt, device="cuda"), torch.full((200, K), 7.0, dtype=dt, device="cuda")
+        s = torch.tensor([0, 90, 80, 200], dtype=torch.int32, device="cuda")
+        for call in (lambda: lrm.lrm_linear(x, w, seg_offsets=s, y=y, dev_status=st),
+                     lambda: lrm.lrm_linear_backward(y, x, w, seg_offsets=s, dx=dx, need_dw=False, dev_status=st)):
+            st.zero_()
+            call()
+            assert int(st.item()) == 11
+        assert bool((y == 7.0).all()) and bool((dx == 7.0).all())
 
 
 def test_refusals():
