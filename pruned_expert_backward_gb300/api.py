@@ -443,8 +443,9 @@ def lrm_linear(x, w, bias=None, residual=None, act="none", seg_offsets=None, sav
     if save_z or z is not None:
         z, z_p = _out(z, (R, NP), dt, dev, "z")
     _same(residual, (R, N), "residual")
-    # bf16 inputs need no scratch
-    need = lrm_linear_workspace_size(R, E, N, K, act, dt) if ws is None and dt_code == L.LRM_F32 else 0
+    # bf16 inputs need scratch only where a long reduction over few rows may be summed in parts
+    want = dt_code == L.LRM_F32 or (32 < R <= 1024 and K >= 2560)
+    need = lrm_linear_workspace_size(R, E, N, K, act, dt) if ws is None and want else 0
     ws, ws_p, ws_n = _scratch(ws, need, dev)
     _ok(L.load().lrm_linear(_opt(seg_offsets, "seg_offsets", torch.int32), x_p, _cuda(w, "w", dt),
                             _opt(bias, "bias", dt), _opt(residual, "residual", y.dtype), R, E, N, K, code, dt_code,

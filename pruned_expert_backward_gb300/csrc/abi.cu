@@ -487,7 +487,7 @@ lrm_status lrm_linear_workspace_size(int64_t R, int32_t E, int32_t N, int32_t K,
   lrm_status st = check_linear(R, E, N, K, act, dt);
   if (st) return st;
   const int32_t NP = act == LRM_ACT_SWIGLU ? 2 * N : N;
-  const size_t need[] = {linear_ws_bytes(R, E, NP, K, dt), act_grad_ws_bytes(R, E, NP),
+  const size_t need[] = {linear_ws_bytes(R, E, NP, K, dt), up(linear_parts_bytes(R, E, NP, K, dt)), act_grad_ws_bytes(R, E, NP),
                          linear_grad_ws_bytes(R, E, NP, K, dt)};
   size_t most = 0;
   for (const size_t n : need) most = n > most ? n : most;
@@ -516,11 +516,15 @@ lrm_status lrm_linear(const int32_t* seg_offsets, const void* x, const void* w, 
   if (need > 0 && (!ws || ws_bytes < need)) return LRM_ERR_WORKSPACE;
   if (R == 0) return LRM_OK;
   const LinearArgs a{seg_offsets, x, w, bias, residual, R, E, N, K, act, y, z, dev_status};
-  if (flags == LRM_GEMM_DEFAULT && R <= kFewRows) {
+  if (flags == LRM_GEMM_DEFAULT && linear_few_rows(R, E, seg_offsets != nullptr, dt)) {
     launch_linear_rows(a, dt, out_dt, stream);
     return after_launch();
   }
-  if (flags == LRM_GEMM_DEFAULT) return launch_linear_tc(a, dt, out_dt, ws, stream);
+  if (flags == LRM_GEMM_DEFAULT) {
+    // bf16 inputs: the workspace is optional, for a long reduction in parts
+    const bool room = dt == LRM_F32 || (ws && ws_bytes >= linear_parts_bytes(R, E, NP, K, dt));
+    return launch_linear_tc(a, dt, out_dt, room ? ws : nullptr, stream);
+  }
   launch_linear_simt(a, dt, out_dt, stream);
   return after_launch();
 }

@@ -147,13 +147,21 @@ struct LinearArgs {
   int32_t* status;
 };
 void launch_linear_simt(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, cudaStream_t s);
-// Up to this many rows (of all experts together) one pass over the weights by plain loads beats the tensor
-// cores' tiles of 256 rows.  GB300, bf16, weights 1408+1408 x 4096 (SwiGLU), 4096 x 4096, 768+768 x 2048:
-// 7.5, 8.7, 3.8 us at 8 rows, 12.4, 12.8, 6.5 at 32 (tiles: 17.4, 15.6, 10.3 at any of these), 20.7, 22.1, 9.2
-// at 64.  128 experts of 768+768 x 2048, top-8: 13 against 20 us at 8 rows, 25 : 29 at 32, 43 : 40 at 64.
-// fp32 4096 x 4096: 69 us at 32 rows, 99 us through the tiles.
-constexpr int64_t kFewRows = 32;
+// Whether one pass over the weights by plain loads takes a product of so few rows, not the tensor cores' tiles
+// of 256 rows.  GB300, us, rows kernel : tiles.
+// Dense, up to 32 rows (fp32 24).  bf16, weights 1408+1408 x 4096 (SwiGLU), 4096 x 4096, 768+768 x 2048: 12.4 : 17.4,
+// 12.8 : 15.6, 6.5 : 10.3 at 32 rows, 20.7 : 17.4, 22.1 : 15.6, 9.2 : 10.3 at 64; fp32 the same at 24 rows 52 : 50,
+// 53 : 70, 21 : 23.
+// Per expert, bf16, up to 64 rows in all: 128 experts of 768+768 x 2048, popularity even and zipf 1, 65 : 66 and
+// 36 : 42 at 64 rows, 101 : 92 and 51 : 46 at 128; 42 experts of 232 x 1472 8.8 : 11 and 9.2 : 10.4 at 84.
+// Per expert, fp32, up to 8 rows a mean expert (the tiles split every expert's weights first): 128 experts
+// 502 : 1599 and 532 : 1238 at 1024 rows, 42 experts 32 : 69 and 58 : 68 at 336, 46 : 71 and 99 : 70 at 672.
+inline bool linear_few_rows(int64_t R, int32_t E, bool grouped, lrm_dtype dt) {
+  if (!grouped) return R <= (dt == LRM_F32 ? 24 : 32);
+  return R <= 32 || (dt == LRM_F32 ? R <= 8 * (int64_t)E : R <= 64);
+}
 void launch_linear_rows(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, cudaStream_t s);
+// ws: for bf16 inputs NULL, or room for linear_parts_bytes.
 lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, void* ws, cudaStream_t s);
 size_t linear_planes_bytes(int64_t rows, int64_t cols);  // an fp32 operand as three bf16 planes
 size_t linear_plan_bytes(int32_t E);                     // plan and expert maps of the weights' gradient

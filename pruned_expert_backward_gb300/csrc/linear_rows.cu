@@ -145,7 +145,7 @@ __device__ __forceinline__ void warp_products(const float* w0, const float* w1, 
     }
 }
 
-// The experts that have rows (at most kFewRows of them), listed in shared memory by the whole block;
+// The experts that have rows, listed in shared memory by the whole block;
 // returns their number, 0 when the segments are not valid.
 struct Rows {
   int e, begin, end;
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) rows_kernel(const int32_t* __r
   constexpr int CN = GLU ? 8 : 16;  // output columns
   constexpr int RT = 8 * NT;        // rows of x at a time
   __shared__ float s_sum[kWarps][16][RT + 1];
-  __shared__ Rows s_list[kFewRows];
+  __shared__ Rows s_list[LRM_MAX_EXPERTS];
   chain_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
   const int blocks = (N + CN - 1) / CN, NP = GLU ? 2 * N : N;

@@ -869,9 +869,11 @@ int64_t likely_row_tiles(const int32_t* seg, int64_t R, int E) {
   return (R + 2 * kBM - 1) / (2 * kBM) + (seg != nullptr ? (R < E ? R : E) / 2 : 0);
 }
 
-// How a product is cut where its tiles are few and its reduction long (fp32 inputs, whose six terms make it
-// six times as long, and dx): tile width and parts of the reduction by the least time, in units of 0.05 us.  A
-// slice takes 3 units (5 in the 256-column tile), adding the parts up costs a launch and a pass, 80 units.
+// How a product is cut where its tiles are few and its reduction long (with fp32 inputs six terms make it six
+// times as long): tile width and parts of the reduction by the least time, in units of 0.05 us.  A
+// slice takes 3 units (5 in the 256-column tile); adding the parts up, by a launch and a pass, is worth 130
+// (fp32 128 x 128 x 2048 12.8 us in parts, 37 us without; bf16 64 x 4096 x 4096 22.9 us in parts, 15.9 us
+// without, and left whole by this).
 struct Cut {
   int bn, parts, len;
 };
@@ -887,7 +889,7 @@ Cut cut_product(int64_t R, int32_t E, int64_t cols, int total, int least) {
       if (n < 1) continue;
       const int64_t len = ((total + n - 1) / n + 7) / 8 * 8, used = (total + len - 1) / len;
       const int64_t waves = (base * used + kPairs - 1) / kPairs;
-      const int64_t time = waves * (n == 1 ? total : len) * (bn == 256 ? 5 : 3) + (used > 1 ? 80 : 0);
+      const int64_t time = waves * (n == 1 ? total : len) * (bn == 256 ? 5 : 3) + (used > 1 ? 130 : 0);
       if (time < best_time) {
         best_time = time;
         best = Cut{bn, (int)used, used > 1 ? (int)len : total};
@@ -916,10 +918,11 @@ size_t linear_planes_bytes(int64_t rows, int64_t cols) { return (size_t)rows * p
 
 lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, void* ws, cudaStream_t s) {
   if (!device_ok() || encode_fn() == nullptr) return LRM_ERR_UNSUPPORTED;
+  using B16 = __nv_bfloat16;
   const bool f32 = dt == LRM_F32, glu = a.act == LRM_ACT_SWIGLU;
   const int NP = glu ? 2 * a.N : a.N;
   const void *xs = a.x, *wsrc = a.w;
-  void* planes_end = nullptr;
+  void* parts_ws = ws;
   if (f32) {
     char* b = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws) + 127) & ~uintptr_t(127));
     Splits sp{};
@@ -928,7 +931,7 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
     b += (linear_planes_bytes(a.R, a.K) + 255) / 256 * 256;
     add_split(sp, a.w, a.E, NP, a.K, b);
     wsrc = b;
-    planes_end = b + (linear_planes_bytes((int64_t)a.E * NP, a.K) + 255) / 256 * 256;
+    parts_ws = b + (linear_planes_bytes((int64_t)a.E * NP, a.K) + 255) / 256 * 256;
     launch_splits(sp, s);
   }
   Params p{};
@@ -963,7 +966,6 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
       constexpr int cols = GLU ? BN / 2 : BN;
       p.tiles_n = (a.N + cols - 1) / cols;
       if (!operand_map(&mB, wsrc, a.K, pitch, NP, (uint64_t)a.E * planes, BN / 2)) return LRM_ERR_CUDA;
-      using B16 = __nv_bfloat16;
       if (f32) return launch<FWD, BN, GLU, true, float, float>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
       if (y32) return launch<FWD, BN, GLU, true, B16, float>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
       return launch<FWD, BN, GLU, false, B16, B16>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
@@ -971,32 +973,43 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
   };
   p.parts = 1;
   p.part_len = slices_of(a.K, dt);
-  if (f32) {
-    const Cut cut = cut_product(a.R, a.E, NP, p.part_len, 64);
-    if (cut.parts > 1) {
-      float* part = reinterpret_cast<float*>(static_cast<char*>(planes_end));
-      Params raw = p;  // the products alone, over all columns of w
-      raw.N = NP;
-      raw.act = LRM_ACT_NONE;
-      raw.bias = raw.residual = raw.z = nullptr;
-      raw.y = part;
-      raw.parts = cut.parts;
-      raw.part_len = cut.len;
-      raw.tiles_n = (NP + cut.bn - 1) / cut.bn;
-      if (!operand_map(&mB, wsrc, a.K, pitch, NP, (uint64_t)a.E * planes, cut.bn / 2) ||
-          !output_map(&mY, part, true, NP, a.R, cut.parts))
-        return LRM_ERR_CUDA;
-      const int64_t tiles = tm * raw.tiles_n * cut.parts;
-      const lrm_status st =
-          cut.bn == 256   ? launch<FWD, 256, false, true, float, float>(mA, mB, mY, mY, raw, tiles, s)
-          : cut.bn == 128 ? launch<FWD, 128, false, true, float, float>(mA, mB, mY, mY, raw, tiles, s)
-                          : launch<FWD, 64, false, true, float, float>(mA, mB, mY, mY, raw, tiles, s);
-      if (st) return st;
-      launch_chained(finish_parts_kernel<float, float>, dim3((unsigned)a.R), dim3(128), 0, s, a.seg_offsets, a.E, a.R,
-                     a.N, (const float*)part, cut.parts, (int)a.act, (const float*)a.bias, (const float*)a.residual,
-                     (float*)a.y, (float*)a.z);
-      return cudaGetLastError() == cudaSuccess ? LRM_OK : LRM_ERR_CUDA;
-    }
+  const Cut cut = parts_ws != nullptr ? cut_product(a.R, a.E, NP, p.part_len, 64) : Cut{0, 1, p.part_len};
+  if (cut.parts > 1) {
+    float* part = static_cast<float*>(parts_ws);
+    Params raw = p;  // the products alone, over all columns of w
+    raw.N = NP;
+    raw.act = LRM_ACT_NONE;
+    raw.bias = raw.residual = raw.z = nullptr;
+    raw.y = part;
+    raw.parts = cut.parts;
+    raw.part_len = cut.len;
+    raw.tiles_n = (NP + cut.bn - 1) / cut.bn;
+    if (!operand_map(&mB, wsrc, a.K, pitch, NP, (uint64_t)a.E * planes, cut.bn / 2) ||
+        !output_map(&mY, part, true, NP, a.R, cut.parts))
+      return LRM_ERR_CUDA;
+    const int64_t tiles = tm * raw.tiles_n * cut.parts;
+    auto products = [&](auto bn) {
+      constexpr int BN = decltype(bn)::value;
+      return f32 ? launch<FWD, BN, false, true, float, float>(mA, mB, mY, mY, raw, tiles, s)
+                 : launch<FWD, BN, false, true, B16, float>(mA, mB, mY, mY, raw, tiles, s);
+    };
+    const lrm_status st = cut.bn == 256   ? products(IntTag<256>{})
+                          : cut.bn == 128 ? products(IntTag<128>{})
+                                          : products(IntTag<64>{});
+    if (st) return st;
+    auto finish = [&](auto kernel, auto* y, auto* z) {
+      using TO = std::remove_pointer_t<decltype(y)>;
+      using TI = std::remove_pointer_t<decltype(z)>;
+      launch_chained(kernel, dim3((unsigned)a.R), dim3(128), 0, s, a.seg_offsets, a.E, a.R, a.N, (const float*)part,
+                     cut.parts, (int)a.act, (const TI*)a.bias, (const TO*)a.residual, y, z);
+    };
+    if (f32)
+      finish(finish_parts_kernel<float, float>, static_cast<float*>(a.y), static_cast<float*>(a.z));
+    else if (y32)
+      finish(finish_parts_kernel<B16, float>, static_cast<float*>(a.y), static_cast<B16*>(a.z));
+    else
+      finish(finish_parts_kernel<B16, B16>, static_cast<B16*>(a.y), static_cast<B16*>(a.z));
+    return cudaGetLastError() == cudaSuccess ? LRM_OK : LRM_ERR_CUDA;
   }
   const int64_t likely = likely_row_tiles(a.seg_offsets, a.R, a.E);
   if (glu) return with_width(likely, NP, 128, [&](auto bn) { return go(bn, IntTag<1>{}); });
@@ -1137,7 +1150,7 @@ int linear_grad_parts(int64_t R, int32_t N, int32_t K) {
 }
 
 size_t linear_parts_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
-  const int parts = dt == LRM_F32 ? cut_product(R, E, NP, slices_of(K, dt), 64).parts : 1;
+  const int parts = cut_product(R, E, NP, slices_of(K, dt), 64).parts;
   return parts > 1 ? sizeof(float) * (size_t)parts * R * NP : 0;
 }
 size_t linear_grad_parts_bytes(int64_t R, int32_t E, int32_t N, int32_t K, lrm_dtype dt) {

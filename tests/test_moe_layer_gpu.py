@@ -290,7 +290,9 @@ LINEARS = [  # dtype, R, N, K, act, bias, residual, save_z, out_f32
     (BF16, 4000, 128, 2048, "none", True, False, False, True),
     (BF16, 70, 8, 8, "gelu", True, True, True, False), (BF16, 33, 16, 24, "swiglu", True, True, True, False),
     (BF16, 300, 8, 2048, "relu", True, False, False, True), (F32, 70, 8, 8, "silu", True, True, True, False),
-    # fp32 products with few tiles and a long reduction: summed in parts
+    # products with few tiles and a long reduction: summed in parts
+    (BF16, 64, 1408, 4096, "swiglu", True, True, True, False), (BF16, 100, 264, 6000, "gelu", True, True, True, False),
+    (BF16, 300, 128, 4096, "none", True, False, True, True),
     (F32, 327, 128, 1016, "relu", True, False, True, False), (F32, 53, 72, 3000, "swiglu", True, True, True, False),
     (F32, 600, 264, 2048, "gelu", True, True, False, False), (F32, 33, 8, 4096, "silu", True, True, True, False),
     (F32, 3, 40, 72, "gelu", True, True, True, False), (F32, 70, 136, 264, "swiglu", True, True, True, False),
