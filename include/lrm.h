@@ -404,9 +404,9 @@ lrm_status lrm_linear_workspace_size(int64_t R, int32_t E, int32_t N, int32_t K,
  * no residual then).  Sums, bias, activation and residual are in fp32, each output is rounded once.  An
  * infinity or NaN in x spoils the outputs of its own row only (as NaN where fp32 inputs are split).
  * Rows >= seg_offsets[E] are not written.  N and K are multiples of 8, up to 2^24; R <= INT32_MAX.
- * ws: scratch of at least lrm_linear_workspace_size bytes for fp32 inputs; for bf16 inputs it may be NULL: with
- * it, a product of few tiles and a long reduction is summed in parts on the whole GPU (the same sums in
- * another order).
+ * ws: scratch of at least lrm_linear_workspace_size bytes for fp32 inputs; for bf16 inputs it may be NULL, and
+ * speeds two kinds of product up: few tiles and a long reduction (summed in parts on the whole GPU, the
+ * same sums in another order), and many rows with K an odd multiple of 8 (w copied to aligned rows first).
  * flags: LRM_GEMM_DEFAULT or LRM_GEMM_FORCE_SIMT (products on the CUDA cores).
  */
 lrm_status lrm_linear(const int32_t* seg_offsets, const void* x, const void* w, const void* bias, const void* residual,

@@ -443,8 +443,8 @@ def lrm_linear(x, w, bias=None, residual=None, act="none", seg_offsets=None, sav
     if save_z or z is not None:
         z, z_p = _out(z, (R, NP), dt, dev, "z")
     _same(residual, (R, N), "residual")
-    # bf16 inputs need scratch only where a long reduction over few rows may be summed in parts
-    want = dt_code == L.LRM_F32 or (32 < R <= 1024 and K >= 2560)
+    # bf16 inputs: scratch is taken where it helps (a long reduction over few rows, rows of w off the sectors)
+    want = dt_code == L.LRM_F32 or (32 < R <= 1024 and K >= 2560) or (K % 16 and R >= 4096 * E)
     need = lrm_linear_workspace_size(R, E, N, K, act, dt) if ws is None and want else 0
     ws, ws_p, ws_n = _scratch(ws, need, dev)
     _ok(L.load().lrm_linear(_opt(seg_offsets, "seg_offsets", torch.int32), x_p, _cuda(w, "w", dt),

@@ -54,7 +54,7 @@ SortWs sort_layout(int64_t T, int32_t k, int32_t E) {
 size_t linear_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
   if (dt != LRM_F32) return 0;
   return kAlign + up(linear_planes_bytes(R, K)) + up(linear_planes_bytes((int64_t)E * NP, K)) +
-         up(linear_parts_bytes(R, E, NP, K, dt));
+         up(linear_extra_bytes(R, E, NP, K, dt));
 }
 size_t linear_grad_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
   size_t n = kAlign + linear_plan_bytes(E);  // kAlign: the maps start on a 128-byte boundary
@@ -487,7 +487,7 @@ lrm_status lrm_linear_workspace_size(int64_t R, int32_t E, int32_t N, int32_t K,
   lrm_status st = check_linear(R, E, N, K, act, dt);
   if (st) return st;
   const int32_t NP = act == LRM_ACT_SWIGLU ? 2 * N : N;
-  const size_t need[] = {linear_ws_bytes(R, E, NP, K, dt), up(linear_parts_bytes(R, E, NP, K, dt)), act_grad_ws_bytes(R, E, NP),
+  const size_t need[] = {linear_ws_bytes(R, E, NP, K, dt), up(linear_extra_bytes(R, E, NP, K, dt)), act_grad_ws_bytes(R, E, NP),
                          linear_grad_ws_bytes(R, E, NP, K, dt)};
   size_t most = 0;
   for (const size_t n : need) most = n > most ? n : most;
@@ -521,8 +521,8 @@ lrm_status lrm_linear(const int32_t* seg_offsets, const void* x, const void* w, 
     return after_launch();
   }
   if (flags == LRM_GEMM_DEFAULT) {
-    // bf16 inputs: the workspace is optional, for a long reduction in parts
-    const bool room = dt == LRM_F32 || (ws && ws_bytes >= linear_parts_bytes(R, E, NP, K, dt));
+    // bf16 inputs: the workspace is optional, for a long reduction in parts or weights on aligned rows
+    const bool room = dt == LRM_F32 || (ws && ws_bytes >= linear_extra_bytes(R, E, NP, K, dt));
     return launch_linear_tc(a, dt, out_dt, room ? ws : nullptr, stream);
   }
   launch_linear_simt(a, dt, out_dt, stream);

@@ -161,12 +161,12 @@ inline bool linear_few_rows(int64_t R, int32_t E, bool grouped, lrm_dtype dt) {
   return R <= 32 || (dt == LRM_F32 ? R <= 8 * (int64_t)E : R <= 64);
 }
 void launch_linear_rows(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, cudaStream_t s);
-// ws: for bf16 inputs NULL, or room for linear_parts_bytes.
+// ws: for bf16 inputs NULL, or room for linear_extra_bytes.
 lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt, void* ws, cudaStream_t s);
 size_t linear_planes_bytes(int64_t rows, int64_t cols);  // an fp32 operand as three bf16 planes
 size_t linear_plan_bytes(int32_t E);                     // plan and expert maps of the weights' gradient
-// parts of a long reduction, added up by a launch of their own: bytes for the forward's, and for dx's
-size_t linear_parts_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt);
+// scratch beside the planes: parts of a long reduction, or weights copied to aligned rows (forward); parts (dx)
+size_t linear_extra_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt);
 size_t linear_grad_parts_bytes(int64_t R, int32_t E, int32_t N, int32_t K, lrm_dtype dt);
 int linear_grad_parts(int64_t R, int32_t N, int32_t K);  // parts of the dense weights' gradient, summed apart
 struct LinearGradArgs {

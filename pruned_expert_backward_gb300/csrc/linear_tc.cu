@@ -685,6 +685,17 @@ __global__ void __launch_bounds__(256) split_planes_kernel(const __grid_constant
   }
 }
 
+// bf16 rows [rows][cols] copied to rows `pitch` apart.
+__global__ void __launch_bounds__(256) repitch_kernel(const __nv_bfloat16* __restrict__ in, int64_t rows, int64_t cols,
+                                                      int64_t pitch, __nv_bfloat16* __restrict__ out) {
+  chain_wait();
+  const int64_t nv = cols / 8, total = rows * nv;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t r = i / nv;
+    st16(out + r * pitch + (i - r * nv) * 8, ld_stream16(in + i * 8));
+  }
+}
+
 // out = the sum of `parts` arrays of n floats (a multiple of 4), in order.
 __global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict__ part, int parts, int64_t n,
                                                         float* __restrict__ out) {
@@ -898,6 +909,13 @@ Cut cut_product(int64_t R, int32_t E, int64_t cols, int total, int least) {
   }
   return best;
 }
+// bf16 weights whose rows start off the 32-byte sectors (K an odd multiple of 8) are copied to 128-byte rows
+// first where they serve many rows: with x off the sectors too, TMA reads five sectors for four of both
+// operands.  32768 x 4096 x 4072: 615 us with the copy, 780 us without; 8192 x 2048 x 2040: 49 and 58 us.
+// (x copied as well: 686 and 57 us.)
+bool repitch_weights(int64_t R, int32_t E, int32_t K, lrm_dtype dt) {
+  return dt == LRM_BF16 && K % 16 != 0 && R >= 4096 * (int64_t)E;
+}
 int slices_of(int64_t red, lrm_dtype dt) { return (int)((red + kBK - 1) / kBK) * (dt == LRM_F32 ? 6 : 1); }
 
 // Tile width by the waves of tiles over the CTA pairs: a K slice of a 256-column tile takes 0.26 us (its
@@ -949,7 +967,7 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
   p.z = a.z;
   p.status = a.status;
   const int planes = f32 ? 3 : 1;
-  const uint64_t pitch = f32 ? plane_pitch(a.K) : a.K;
+  uint64_t pitch = f32 ? plane_pitch(a.K) : a.K, pitch_w = pitch;
   const bool y32 = out_dt == LRM_F32;
   CUtensorMap mA, mB, mY, mZ;
   if (!operand_map(&mA, xs, a.K, pitch, a.R, planes, kBM) || !output_map(&mY, a.y, y32, a.N, a.R, 1))
@@ -965,7 +983,7 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
     } else {
       constexpr int cols = GLU ? BN / 2 : BN;
       p.tiles_n = (a.N + cols - 1) / cols;
-      if (!operand_map(&mB, wsrc, a.K, pitch, NP, (uint64_t)a.E * planes, BN / 2)) return LRM_ERR_CUDA;
+      if (!operand_map(&mB, wsrc, a.K, pitch_w, NP, (uint64_t)a.E * planes, BN / 2)) return LRM_ERR_CUDA;
       if (f32) return launch<FWD, BN, GLU, true, float, float>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
       if (y32) return launch<FWD, BN, GLU, true, B16, float>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
       return launch<FWD, BN, GLU, false, B16, B16>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
@@ -984,7 +1002,7 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
     raw.parts = cut.parts;
     raw.part_len = cut.len;
     raw.tiles_n = (NP + cut.bn - 1) / cut.bn;
-    if (!operand_map(&mB, wsrc, a.K, pitch, NP, (uint64_t)a.E * planes, cut.bn / 2) ||
+    if (!operand_map(&mB, wsrc, a.K, pitch_w, NP, (uint64_t)a.E * planes, cut.bn / 2) ||
         !output_map(&mY, part, true, NP, a.R, cut.parts))
       return LRM_ERR_CUDA;
     const int64_t tiles = tm * raw.tiles_n * cut.parts;
@@ -1010,6 +1028,14 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
     else
       finish(finish_parts_kernel<B16, B16>, static_cast<B16*>(a.y), static_cast<B16*>(a.z));
     return cudaGetLastError() == cudaSuccess ? LRM_OK : LRM_ERR_CUDA;
+  }
+  if (parts_ws != nullptr && repitch_weights(a.R, a.E, a.K, dt)) {
+    B16* wp = static_cast<B16*>(parts_ws);
+    pitch_w = plane_pitch(a.K);
+    const int64_t rows = (int64_t)a.E * NP, blocks = (rows * (a.K / 8) + 255) / 256;
+    launch_chained(repitch_kernel, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), dim3(256), 0, s,
+                   static_cast<const B16*>(a.w), rows, (int64_t)a.K, (int64_t)pitch_w, wp);
+    wsrc = wp;
   }
   const int64_t likely = likely_row_tiles(a.seg_offsets, a.R, a.E);
   if (glu) return with_width(likely, NP, 128, [&](auto bn) { return go(bn, IntTag<1>{}); });
@@ -1149,9 +1175,10 @@ int linear_grad_parts(int64_t R, int32_t N, int32_t K) {
   return parts < 1 ? 1 : (int)parts;
 }
 
-size_t linear_parts_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
+size_t linear_extra_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
   const int parts = cut_product(R, E, NP, slices_of(K, dt), 64).parts;
-  return parts > 1 ? sizeof(float) * (size_t)parts * R * NP : 0;
+  if (parts > 1) return sizeof(float) * (size_t)parts * R * NP;
+  return repitch_weights(R, E, K, dt) ? 2 * (size_t)E * NP * plane_pitch((uint64_t)K) : 0;
 }
 size_t linear_grad_parts_bytes(int64_t R, int32_t E, int32_t N, int32_t K, lrm_dtype dt) {
   const int parts = cut_product(R, E, K, slices_of(N, dt), 128).parts;

@@ -290,6 +290,8 @@ LINEARS = [  # dtype, R, N, K, act, bias, residual, save_z, out_f32
     (BF16, 4000, 128, 2048, "none", True, False, False, True),
     (BF16, 70, 8, 8, "gelu", True, True, True, False), (BF16, 33, 16, 24, "swiglu", True, True, True, False),
     (BF16, 300, 8, 2048, "relu", True, False, False, True), (F32, 70, 8, 8, "silu", True, True, True, False),
+    # many rows and K an odd multiple of 8: weights copied to aligned rows
+    (BF16, 4096, 136, 72, "silu", True, True, True, False), (BF16, 5000, 264, 328, "swiglu", True, True, True, False),
     # products with few tiles and a long reduction: summed in parts
     (BF16, 64, 1408, 4096, "swiglu", True, True, True, False), (BF16, 100, 264, 6000, "gelu", True, True, True, False),
     (BF16, 300, 128, 4096, "none", True, False, True, True),
@@ -357,6 +359,7 @@ GROUPED = [  # dtype, R, E, segments, N, K, act, bias, residual, save_z
     (F32, 60, 6, "ragged", 40, 72, "swiglu", True, True, True),
     (F32, 900, 9, "short", 136, 264, "gelu", True, True, True),
     (F32, 2500, 4, "ragged", 72, 1032, "silu", False, True, False),
+    (BF16, 9000, 2, "ragged", 136, 72, "gelu", True, True, True),
     (F32, 200, 5, "short", 72, 2048, "swiglu", True, True, True),
     (F32, 700, 3, "one", 136, 1480, "gelu", True, False, True),
 ]
