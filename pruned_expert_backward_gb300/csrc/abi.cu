@@ -57,10 +57,10 @@ size_t linear_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt
          up(linear_extra_bytes(R, E, NP, K, dt));
 }
 size_t linear_grad_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
-  size_t n = kAlign + linear_plan_bytes(E);  // kAlign: the maps start on a 128-byte boundary
+  size_t n = kAlign + linear_plan_bytes(linear_grad_segments(R, E, NP, K, dt));  // kAlign: the maps' 128-byte boundary
   const int parts = E == 1 ? linear_grad_parts(R, NP, K) : 1;
   if (parts > 1) n += up(sizeof(float) * (size_t)parts * NP * K);
-  n += up(linear_grad_parts_bytes(R, E, NP, K, dt));
+  n += up(linear_grad_parts_bytes(R, E, NP, K, dt)) + up(linear_grad_runs_bytes(R, E, NP, K, dt));
   if (dt == LRM_F32)
     n += up(linear_planes_bytes(R, NP)) + up(linear_planes_bytes(R, K)) + up(linear_planes_bytes((int64_t)E * NP, K));
   return n;
@@ -487,8 +487,8 @@ lrm_status lrm_linear_workspace_size(int64_t R, int32_t E, int32_t N, int32_t K,
   lrm_status st = check_linear(R, E, N, K, act, dt);
   if (st) return st;
   const int32_t NP = act == LRM_ACT_SWIGLU ? 2 * N : N;
-  const size_t need[] = {linear_ws_bytes(R, E, NP, K, dt), up(linear_extra_bytes(R, E, NP, K, dt)), act_grad_ws_bytes(R, E, NP),
-                         linear_grad_ws_bytes(R, E, NP, K, dt)};
+  const size_t need[] = {linear_ws_bytes(R, E, NP, K, dt), up(linear_extra_bytes(R, E, NP, K, dt)),
+                         act_grad_ws_bytes(R, E, NP), linear_grad_ws_bytes(R, E, NP, K, dt)};
   size_t most = 0;
   for (const size_t n : need) most = n > most ? n : most;
   *bytes = most;

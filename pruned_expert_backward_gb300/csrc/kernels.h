@@ -168,6 +168,9 @@ size_t linear_plan_bytes(int32_t E);                     // plan and expert maps
 // scratch beside the planes: parts of a long reduction, or weights copied to aligned rows (forward); parts (dx)
 size_t linear_extra_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt);
 size_t linear_grad_parts_bytes(int64_t R, int32_t E, int32_t N, int32_t K, lrm_dtype dt);
+// weight gradients per expert cut into runs of rows: segments in the plan, and bytes of the runs
+int linear_grad_segments(int64_t R, int32_t E, int32_t N, int32_t K, lrm_dtype dt);
+size_t linear_grad_runs_bytes(int64_t R, int32_t E, int32_t N, int32_t K, lrm_dtype dt);
 int linear_grad_parts(int64_t R, int32_t N, int32_t K);  // parts of the dense weights' gradient, summed apart
 struct LinearGradArgs {
   const int32_t* seg_offsets;

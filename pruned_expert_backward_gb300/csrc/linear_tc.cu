@@ -645,6 +645,66 @@ __global__ void __launch_bounds__(1024) linear_plan_kernel(const int32_t* __rest
   }
 }
 
+// The segments cut into runs of at most `chunk` rows: vseg [EV + 1], a segmentation of the same rows whose first
+// runs are those of expert 0 and so on (first_run [E + 1]); runs that are not needed are empty, at the end.  Segments
+// that are not valid give none that is (vseg[0] = 1), so that the product computes nothing.
+__global__ void __launch_bounds__(1024) cut_segments_kernel(const int32_t* __restrict__ seg, int E, int64_t R,
+                                                            int chunk, int EV, int32_t* __restrict__ vseg,
+                                                            int32_t* __restrict__ first_run,
+                                                            int32_t* __restrict__ status) {
+  chain_wait();
+  __shared__ int s_seg[LRM_MAX_EXPERTS + 1];
+  __shared__ int s_first[LRM_MAX_EXPERTS + 1];
+  const bool valid = rows_valid(seg, E, R, status);
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) s_seg[e] = seg[e];
+  __syncthreads();
+  if (threadIdx.x == 0) {  // (this form is for products of few tiles, so of few experts)
+    int run = 0;
+    for (int e = 0; e < E; ++e) {
+      s_first[e] = run;
+      if (valid) run += (s_seg[e + 1] - s_seg[e] + chunk - 1) / chunk;
+    }
+    s_first[E] = run;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) first_run[e] = s_first[e];
+  const int runs = s_first[E], end = s_seg[E];
+  for (int v = threadIdx.x; v <= EV; v += blockDim.x) {
+    int at = end;
+    if (v < runs) {
+      int lo = 0, hi = E;  // the expert of run v: the last e with first[e] <= v
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_first[mid] <= v) lo = mid; else hi = mid;
+      }
+      at = s_seg[lo] + (v - s_first[lo]) * chunk;
+    }
+    vseg[v] = valid ? at : 1;
+  }
+}
+
+// dw[e] = the sum of the expert's runs' weight gradients, in order (0 without a run).
+__global__ void __launch_bounds__(256) sum_runs_kernel(const int32_t* __restrict__ vseg,
+                                                       const int32_t* __restrict__ first_run,
+                                                       const float* __restrict__ part, int64_t n,
+                                                       float* __restrict__ out) {
+  chain_wait();
+  if (vseg[0] != 0) return;  // (recorded by cut_segments_kernel)
+  const int e = blockIdx.y, r0 = first_run[e], r1 = first_run[e + 1];
+  const int64_t step = (int64_t)gridDim.x * blockDim.x * 4;
+  for (int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4; i < n; i += step) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int r = r0; r < r1; ++r) {
+      float f[4];
+      unpack(ld_stream16(part + r * n + i), f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[q] += f[q];
+    }
+    st16(out + e * n + i, pack(acc));
+  }
+}
+
 // fp32 tensors [groups][rows][cols] as three bf16 planes [groups][3][rows][pitch] whose sum is the tensor to
 // 24 bits.  A value that is not finite stays in the first plane alone, so that no infinity is subtracted
 // from itself; one that bf16 would round to infinity is cut instead.  The pitch is a multiple of 64: rows
@@ -918,6 +978,25 @@ bool repitch_weights(int64_t R, int32_t E, int32_t K, lrm_dtype dt) {
 }
 int slices_of(int64_t red, lrm_dtype dt) { return (int)((red + kBK - 1) / kBK) * (dt == LRM_F32 ? 6 : 1); }
 
+// Runs of rows for the weight gradient per expert where a popular expert's tiles would run long after the others
+// (taken to have three times its share of the rows): run length and the most runs there can be, 0 for none.
+// Times in us: a slice 0.155, the rows' products over all CTA pairs; 12 for two launches and the adding up.
+struct Runs {
+  int chunk, count;
+};
+Runs cut_rows(int64_t R, int32_t E, int64_t N, int64_t K, lrm_dtype dt) {
+  const double slice = 0.155 * (dt == LRM_F32 ? 6 : 1) / kBK;  // per row
+  const double tiles = (double)((N + 255) / 256) * (double)((K + 127) / 128);
+  const double longest = slice * (double)(3 * R / E < R ? 3 * R / E : R), even = slice * (double)R * tiles / kPairs;
+  double want = (even > 8 ? even / 2 : 4) / slice;  // rows of a run
+  if (want < 256) want = 256;
+  const int chunk = (int)(((int64_t)want + kBK - 1) / kBK * kBK);
+  const int64_t count = (R + chunk - 1) / chunk + E;
+  const double adding = 12 + 8.0 * (double)count * (double)N * (double)K / 6.8e6;
+  if (count > LRM_MAX_EXPERTS || longest < even + adding) return Runs{0, 0};
+  return Runs{chunk, (int)count};
+}
+
 // Tile width by the waves of tiles over the CTA pairs: a K slice of a 256-column tile takes 0.26 us (its
 // products), one of a 128- or 64-column tile 0.155 us (the operands' way in).  On a tie the narrower: more
 // SMs then share the reading of the weights.
@@ -1050,9 +1129,10 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
   const void *dzs = a.dz, *xs = a.x, *wsrc = a.w;
   // scratch: the expert maps of DW (128-byte aligned) and its plan, then the planes
   char* b = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws) + 127) & ~uintptr_t(127));
+  const int segments = linear_grad_segments(a.R, a.E, a.N, a.K, dt);
   CUtensorMap* maps = reinterpret_cast<CUtensorMap*>(b);
-  int32_t* plan = reinterpret_cast<int32_t*>(b + 2 * sizeof(CUtensorMap) * (size_t)a.E);
-  b += linear_plan_bytes(a.E);
+  int32_t* plan = reinterpret_cast<int32_t*>(b + 2 * sizeof(CUtensorMap) * (size_t)segments);
+  b += linear_plan_bytes(segments);
   Splits sp{};
   auto split = [&](const void* src, int64_t groups, int64_t rows, int64_t cols) {
     add_split(sp, src, groups, rows, cols, b);
@@ -1081,7 +1161,20 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
     p.parts = 1;
     p.tiles_m = (a.N + 2 * kBM - 1) / (2 * kBM);
     const int parts = a.seg_offsets == nullptr ? linear_grad_parts(a.R, a.N, a.K) : 1;
-    float* sums = parts > 1 ? reinterpret_cast<float*>(b) : a.dw;
+    const Runs runs = a.seg_offsets == nullptr ? Runs{0, 0} : cut_rows(a.R, a.E, a.N, a.K, dt);
+    const int32_t* seg = a.seg_offsets;
+    int32_t *vseg = nullptr, *first_run = nullptr;
+    if (runs.count > 0) {
+      vseg = reinterpret_cast<int32_t*>(b);
+      first_run = vseg + runs.count + 1;
+      b += (sizeof(int32_t) * ((size_t)runs.count + a.E + 2) + 255) / 256 * 256;
+      launch_chained(cut_segments_kernel, dim3(1), dim3(1024), 0, s, a.seg_offsets, a.E, a.R, runs.chunk, runs.count,
+                     vseg, first_run, a.status);
+      seg = vseg;
+      p.seg = vseg;
+      p.E = runs.count;
+    }
+    float* sums = parts > 1 || runs.count > 0 ? reinterpret_cast<float*>(b) : a.dw;
     p.y = sums;
     if (a.seg_offsets == nullptr) {
       p.E = parts;
@@ -1100,8 +1193,7 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
         if (!column_map(&mB, xs, a.K, pitch_k, a.R, planes, BN / 128, &p.one_box_b)) return LRM_ERR_CUDA;
         if (a.seg_offsets != nullptr) {
           const MapPair tpl{{mA, mB}};
-          launch_chained(linear_plan_kernel, dim3(1), dim3(1024), 0, s, a.seg_offsets, a.E, a.R, plan, maps, tpl,
-                         a.status);
+          launch_chained(linear_plan_kernel, dim3(1), dim3(1024), 0, s, seg, p.E, a.R, plan, maps, tpl, a.status);
           p.plan = plan;
           p.maps = maps;
         }
@@ -1109,6 +1201,12 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
       }
     });
     if (st) return st;
+    if (runs.count > 0) {
+      b += (sizeof(float) * (size_t)runs.count * a.N * a.K + 255) / 256 * 256;
+      const int64_t n = (int64_t)a.N * a.K, blocks = (n / 4 + 255) / 256;
+      launch_chained(sum_runs_kernel, dim3((unsigned)(blocks < 304 ? blocks : 304), (unsigned)a.E), dim3(256), 0, s,
+                     (const int32_t*)vseg, (const int32_t*)first_run, (const float*)sums, n, a.dw);
+    }
     if (parts > 1) {
       b += (sizeof(float) * (size_t)parts * a.N * a.K + 255) / 256 * 256;
       const int64_t n = (int64_t)a.N * a.K, blocks = (n / 4 + 255) / 256;
@@ -1118,6 +1216,7 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
   }
   if (a.dx != nullptr) {
     p.E = a.E;
+    p.seg = a.seg_offsets;
     p.red = a.N;
     const Cut cut = cut_product(a.R, a.E, a.K, slices_of(a.N, dt), 128);
     p.parts = cut.parts;
@@ -1183,6 +1282,15 @@ size_t linear_extra_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype
 size_t linear_grad_parts_bytes(int64_t R, int32_t E, int32_t N, int32_t K, lrm_dtype dt) {
   const int parts = cut_product(R, E, K, slices_of(N, dt), 128).parts;
   return parts > 1 ? sizeof(float) * (size_t)parts * R * K : 0;
+}
+
+int linear_grad_segments(int64_t R, int32_t E, int32_t N, int32_t K, lrm_dtype dt) {
+  const int runs = cut_rows(R, E, N, K, dt).count;
+  return runs > E ? runs : E;
+}
+size_t linear_grad_runs_bytes(int64_t R, int32_t E, int32_t N, int32_t K, lrm_dtype dt) {
+  const int runs = cut_rows(R, E, N, K, dt).count;
+  return runs > 0 ? 512 + sizeof(int32_t) * ((size_t)runs + E + 2) + sizeof(float) * (size_t)runs * N * K : 0;
 }
 
 size_t linear_plan_bytes(int32_t E) {

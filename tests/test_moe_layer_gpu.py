@@ -482,6 +482,9 @@ LINEAR_GRADS = [  # dtype, R, N, K, E, segments
     (F32, 1500, 136, 264, None, None), (BF16, 8, 72, 64, 12, "ragged"), (BF16, 700, 264, 136, 5, "short"),
     (BF16, 3000, 520, 72, 64, "ragged"), (BF16, 6000, 136, 392, 3, "one"), (BF16, 9000, 72, 328, 2, "ragged"),
     (F32, 900, 72, 136, 9, "short"), (F32, 4000, 40, 264, 4, "ragged"),
+    # a popular expert's rows in several runs
+    (F32, 9000, 72, 136, 4, "ragged"), (F32, 12000, 136, 264, 10, "short"), (BF16, 40000, 136, 264, 3, "ragged"),
+    (F32, 8000, 40, 72, 6, "one"), (BF16, 30000, 72, 40, 2, "short"),
     # dx with few tiles and a long reduction: summed in parts
     (F32, 48, 1232, 288, None, None), (BF16, 300, 4104, 72, None, None), (BF16, 200, 4104, 136, 4, "short"),
     (F32, 130, 2000, 40, 3, "ragged"), (BF16, 33, 8192, 264, None, None),
@@ -611,6 +614,12 @@ def test_bad_segments_compute_nothing():
                 assert int(st.item()) == 11
             assert bool((y == 7.0).all()) and bool((dx == 7.0).all()) and bool((dw == 7.0).all())
     # long reductions, summed in parts: the second launch must not write either
+    big = torch.full((9000, 72), 7.0, device="cuda")
+    wide = torch.full((3, 72, 72), 7.0, device="cuda")
+    st.zero_()
+    s = torch.tensor([0, 9000, 4, 9000], dtype=torch.int32, device="cuda")
+    lrm.lrm_linear_backward(big, big, wide, seg_offsets=s, need_dx=False, dw=wide, dev_status=st)  # (w is not read)
+    assert int(st.item()) == 11 and bool((wide == 7.0).all())
     for dt, N, K in ((F32, 72, 2048), (F32, 2048, 72), (BF16, 4096, 72)):
         x, w, _, _ = linear_inputs(gen(N), dt, 200, N, N, K, False, False, 3)
         y, dx = torch.full((200, N), 7.0, dtype=dt, device="cuda"), torch.full((200, K), 7.0, dtype=dt, device="cuda")
