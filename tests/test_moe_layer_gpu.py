@@ -436,6 +436,7 @@ ACT_GRADS = [  # dtype, R, N, E, segments
     (BF16, 129, 768, None, None), (F32, 1000, 136, None, None), (BF16, 5000, 520, None, None),
     (BF16, 1000, 264, 7, "ragged"), (BF16, 700, 768, 128, "ragged"), (F32, 300, 40, 16, "one"),
     (BF16, 2000, 136, 5, "short"), (BF16, 4096, 72, 32, "even"), (F32, 900, 24, 300, "ragged"),
+    (BF16, 20000, 72, 64, "ragged"), (F32, 17001, 24, 100, "one"), (F32, 2049, 16, 2, "short"),
 ]
 
 
