@@ -950,7 +950,8 @@ struct Cut {
 };
 Cut cut_product(int64_t R, int32_t E, int64_t cols, int total, int least) {
   const int64_t tm = (R + 2 * kBM - 1) / (2 * kBM) + (E > 1 ? (R < E ? R : E) / 2 : 0);
-  Cut best{0, 1, total};
+  Cut best{least, 1, total};
+  if (R <= 0) return best;  // no tiles at all (the size functions ask)
   int64_t best_time = INT64_MAX;
   for (int bn = least; bn <= 256; bn *= 2) {
     const int64_t base = tm * ((cols + bn - 1) / bn);
