@@ -387,9 +387,21 @@ typedef enum lrm_act {
   LRM_ACT_SWIGLU = 4  /* SiLU(z_gate) * z_up: w and bias hold N gate rows, then N up rows */
 } lrm_act;
 
-/* Bytes of scratch `ws` that lrm_linear, lrm_act_backward and lrm_linear_backward need for a product of
- * R rows (one buffer serves all three).  N: columns of y; for lrm_linear_backward alone, those of dz with
- * LRM_ACT_NONE.  Host-only.  Errors: LRM_ERR_INVALID_ARG, LRM_ERR_SHAPE, LRM_ERR_DTYPE. */
+/* The calls that a scratch buffer is sized for, or-ed together (DX and DW together: one call for both). */
+typedef enum lrm_linear_use {
+  LRM_LINEAR_USE_FORWARD = 1,       /* lrm_linear */
+  LRM_LINEAR_USE_ACT_BACKWARD = 2,  /* lrm_act_backward with db */
+  LRM_LINEAR_USE_DX = 4,            /* lrm_linear_backward with dx */
+  LRM_LINEAR_USE_DW = 8,            /* lrm_linear_backward with dw */
+  LRM_LINEAR_USE_ALL = 15
+} lrm_linear_use;
+
+/* Bytes of scratch `ws` for the calls in `uses` on a product of R rows: one buffer serves them in turn, with
+ * segments or (E = 1) without.  N: columns of y; for lrm_linear_backward alone, those of dz with LRM_ACT_NONE.
+ * Host-only.  Errors: LRM_ERR_INVALID_ARG, LRM_ERR_SHAPE, LRM_ERR_DTYPE. */
+lrm_status lrm_linear_workspace_size_for(int32_t uses, int64_t R, int32_t E, int32_t N, int32_t K, lrm_act act,
+                                         lrm_dtype dt, size_t* bytes);
+/* The same for LRM_LINEAR_USE_ALL. */
 lrm_status lrm_linear_workspace_size(int64_t R, int32_t E, int32_t N, int32_t K, lrm_act act, lrm_dtype dt,
                                      size_t* bytes);
 
@@ -404,7 +416,8 @@ lrm_status lrm_linear_workspace_size(int64_t R, int32_t E, int32_t N, int32_t K,
  * no residual then).  Sums, bias, activation and residual are in fp32, each output is rounded once.  An
  * infinity or NaN in x spoils the outputs of its own row only (as NaN where fp32 inputs are split).
  * Rows >= seg_offsets[E] are not written.  N and K are multiples of 8, up to 2^24; R <= INT32_MAX.
- * ws: scratch of at least lrm_linear_workspace_size bytes for fp32 inputs; for bf16 inputs it may be NULL, and
+ * ws: scratch of at least lrm_linear_workspace_size_for(LRM_LINEAR_USE_FORWARD, ...) bytes for fp32 inputs (256
+ * bytes where few rows, or LRM_GEMM_FORCE_SIMT, take no planes of them); for bf16 inputs it may be NULL, and
  * speeds two kinds of product up: few tiles and a long reduction (summed in parts on the whole GPU, the
  * same sums in another order), and many rows with K an odd multiple of 8 (w copied to aligned rows first).
  * flags: LRM_GEMM_DEFAULT or LRM_GEMM_FORCE_SIMT (products on the CUDA cores).
@@ -428,7 +441,8 @@ lrm_status lrm_act_backward(const int32_t* seg_offsets, const void* dy, const vo
  * Gradients of lrm_linear's product from dz [R,N] (lrm_act_backward's; N counts all columns of dz):
  *   dx = dz W[e]   [R,K] dt (NULL skips it),   dw[e] = dz^T x over the segment's rows   [E,N,K] fp32
  *   (NULL skips it); an expert without rows gets dw = 0.
- * The residual's gradient is dy itself.  Segments, ws, flags and limits as for lrm_linear.
+ * The residual's gradient is dy itself.  Segments, flags and limits as for lrm_linear.  ws: for either type, scratch
+ * of at least lrm_linear_workspace_size_for bytes of the gradients asked for.
  */
 lrm_status lrm_linear_backward(const int32_t* seg_offsets, const void* dz, const void* x, const void* w, int64_t R,
                                int32_t E, int32_t N, int32_t K, lrm_dtype dt, void* dx, float* dw, void* ws,

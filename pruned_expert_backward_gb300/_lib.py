@@ -20,6 +20,8 @@ LRM_QUOTA_RATIO, LRM_QUOTA_CAP, LRM_QUOTA_EXPLICIT = 0, 1, 2
 LRM_GEMM_DEFAULT, LRM_GEMM_FORCE_SIMT = 0, 1
 LRM_SCORE_LRM, LRM_SCORE_GRAD_SQ, LRM_SCORE_GRAD_ABS = 0, 1, 2
 LRM_ACT_NONE, LRM_ACT_RELU, LRM_ACT_GELU, LRM_ACT_SILU, LRM_ACT_SWIGLU = 0, 1, 2, 3, 4
+LRM_LINEAR_USE_FORWARD, LRM_LINEAR_USE_ACT_BACKWARD, LRM_LINEAR_USE_DX, LRM_LINEAR_USE_DW = 1, 2, 4, 8
+LRM_LINEAR_USE_ALL = 15
 LRM_MAX_EXPERTS, LRM_MAX_TOPK = 1024, 16
 
 _p, _i32, _i64, _sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
@@ -49,6 +51,7 @@ SIGNATURES = {
     "lrm_combine": (C.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, C.c_int, _i64, _p, _p, _p]),
     "lrm_combine_backward": (C.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, C.c_int, _i64, _p, _p, _p, _p]),
     "lrm_linear_workspace_size": (C.c_int, [_i64, _i32, _i32, _i32, C.c_int, C.c_int, C.POINTER(_sz)]),
+    "lrm_linear_workspace_size_for": (C.c_int, [_i32, _i64, _i32, _i32, _i32, C.c_int, C.c_int, C.POINTER(_sz)]),
     "lrm_linear": (C.c_int, [_p, _p, _p, _p, _p, _i64, _i32, _i32, _i32, C.c_int, C.c_int, C.c_int, _p, _p, _p, _sz,
                              _i32, _p, _p]),
     "lrm_act_backward": (C.c_int, [_p, _p, _p, _i64, _i32, _i32, C.c_int, C.c_int, _p, _p, _p, _sz, _p, _p]),

@@ -411,11 +411,14 @@ def _experts(w, seg_offsets, name):
 
 
 @functools.lru_cache(maxsize=4096)
-def lrm_linear_workspace_size(R: int, E: int, N: int, K: int, act: str, dtype: torch.dtype) -> int:
-    """Scratch bytes of lrm_linear, lrm_act_backward and lrm_linear_backward (N: columns of y)."""
+def lrm_linear_workspace_size(R: int, E: int, N: int, K: int, act: str, dtype: torch.dtype,
+                              uses: int = L.LRM_LINEAR_USE_ALL) -> int:
+    """Scratch bytes of lrm_linear, lrm_act_backward and lrm_linear_backward (N: columns of y), or of those
+    in `uses` (LRM_LINEAR_USE_* or-ed)."""
     out = C.c_size_t(0)
     dt = L.LRM_BF16 if dtype == torch.bfloat16 else L.LRM_F32
-    _ok(L.load().lrm_linear_workspace_size(R, E, N, K, _act_code(act), dt, C.byref(out)), "lrm_linear_workspace_size")
+    _ok(L.load().lrm_linear_workspace_size_for(uses, R, E, N, K, _act_code(act), dt, C.byref(out)),
+        "lrm_linear_workspace_size")
     return int(out.value)
 
 
@@ -445,7 +448,10 @@ def lrm_linear(x, w, bias=None, residual=None, act="none", seg_offsets=None, sav
     _same(residual, (R, N), "residual")
     # bf16 inputs: scratch is taken where it helps (a long reduction over few rows, rows of w off the sectors)
     want = dt_code == L.LRM_F32 or (32 < R <= 1024 and K >= 2560) or (K % 16 and R >= 4096 * E)
-    need = lrm_linear_workspace_size(R, E, N, K, act, dt) if ws is None and want else 0
+    need = 0
+    if ws is None and want:
+        simt = flags == L.LRM_GEMM_FORCE_SIMT
+        need = 256 if simt else lrm_linear_workspace_size(R, E, N, K, act, dt, L.LRM_LINEAR_USE_FORWARD)
     ws, ws_p, ws_n = _scratch(ws, need, dev)
     _ok(L.load().lrm_linear(_opt(seg_offsets, "seg_offsets", torch.int32), x_p, _cuda(w, "w", dt),
                             _opt(bias, "bias", dt), _opt(residual, "residual", y.dtype), R, E, N, K, code, dt_code,
@@ -477,7 +483,8 @@ def lrm_act_backward(dy, z, act="none", seg_offsets=None, bias_grad=True, dz=Non
             if db.numel() != E * NP:
                 raise ValueError(f"db must hold {E * NP} values, got {db.numel()}")
             db_p = _cuda(db, "db", torch.float32)
-        need = lrm_linear_workspace_size(R, E, N, 8, act, dt) if ws is None else 0
+        if ws is None:
+            need = lrm_linear_workspace_size(R, E, N, 8, act, dt, L.LRM_LINEAR_USE_ACT_BACKWARD)
     ws, ws_p, ws_n = _scratch(ws, need, dev)
     _ok(L.load().lrm_act_backward(_opt(seg_offsets, "seg_offsets", torch.int32), dy_p, _opt(z, "z", dt), R, E, N, code,
                                   dt_code, dz_p, db_p, ws_p, ws_n, _opt(dev_status, "dev_status", torch.int32),
@@ -498,7 +505,8 @@ def lrm_linear_backward(dz, x, w, seg_offsets=None, need_dx=True, need_dw=True, 
     _same(x, (R, K), "x")
     dx, dx_p = _out(dx, (R, K), dt, dev, "dx") if need_dx else (None, None)
     dw, dw_p = _out(dw, tuple(w.shape), torch.float32, dev, "dw") if need_dw else (None, None)
-    need = lrm_linear_workspace_size(R, E, N, K, "none", dt) if ws is None else 0
+    uses = (L.LRM_LINEAR_USE_DX if need_dx else 0) | (L.LRM_LINEAR_USE_DW if need_dw else 0)
+    need = lrm_linear_workspace_size(R, E, N, K, "none", dt, uses) if ws is None and uses else 0
     ws, ws_p, ws_n = _scratch(ws, need, dev)
     _ok(L.load().lrm_linear_backward(_opt(seg_offsets, "seg_offsets", torch.int32), dz_p, _cuda(x, "x", dt),
                                      _cuda(w, "w", dt), R, E, N, K, dt_code, dx_p, dw_p, ws_p, ws_n, int(flags),
@@ -630,9 +638,11 @@ class MoeLayer:
         self.x_s, self.phi_s = torch.empty(P, H, **new), torch.empty(P, I, **new)
         self.y_s, self.y = torch.empty(P, H, **new), torch.empty(T, H, **new)
         self.dev_status = torch.zeros(1, **i32)
-        ws = max(lrm_workspace_size(T, k, E, 8, 8, torch.float32),
-                 lrm_linear_workspace_size(P, E, I, H, "swiglu", dtype),
-                 lrm_linear_workspace_size(P, E, H, I, "none", dtype))
+        uses = L.LRM_LINEAR_USE_FORWARD
+        if train:
+            uses |= L.LRM_LINEAR_USE_DX | L.LRM_LINEAR_USE_DW
+        ws = max(_sort_ws(T, k, E), lrm_linear_workspace_size(P, E, I, H, "swiglu", dtype, uses),
+                 lrm_linear_workspace_size(P, E, H, I, "none", dtype, uses))
         if train:
             self.h_s, self.dh_s = torch.empty(P, 2 * I, **new), torch.empty(P, 2 * I, **new)
             self.dy_s, self.dphi_s = torch.empty(P, H, **new), torch.empty(P, I, **new)
@@ -640,7 +650,6 @@ class MoeLayer:
             self.dalpha = torch.empty(T, k, dtype=torch.float32, device=dev)
             self.dw_gate_up = torch.empty(E, 2 * I, H, dtype=torch.float32, device=dev)
             self.dw_down = torch.empty(E, H, I, dtype=torch.float32, device=dev)
-            ws = max(ws, lrm_linear_workspace_size(P, E, 2 * I, H, "none", dtype))
         self.ws = torch.empty(ws, dtype=torch.uint8, device=dev)
 
     def forward(self, x, topk_idx, alpha, w_gate_up, w_down, residual=None):

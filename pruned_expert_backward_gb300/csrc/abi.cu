@@ -50,19 +50,25 @@ SortWs sort_layout(int64_t T, int32_t k, int32_t E) {
   return w;
 }
 
-// Scratch of the products and of the bias gradient (NP: rows of w, columns of dz).
-size_t linear_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
+// Scratch of the products and of the bias gradient (NP: rows of w, columns of dz), as each call uses it.
+// The forward's is needed for fp32 inputs (never 0 then, one rule for every size) and optional for bf16 ones;
+// `plain`: the product runs without planes and parts (few rows, or on the CUDA cores).
+size_t linear_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt, bool plain) {
   if (dt != LRM_F32) return 0;
+  if (plain) return kAlign;
   return kAlign + up(linear_planes_bytes(R, K)) + up(linear_planes_bytes((int64_t)E * NP, K)) +
          up(linear_extra_bytes(R, E, NP, K, dt));
 }
-size_t linear_grad_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt) {
-  size_t n = kAlign + linear_plan_bytes(linear_grad_segments(R, E, NP, K, dt));  // kAlign: the maps' 128-byte boundary
-  const int parts = E == 1 ? linear_grad_parts(R, NP, K) : 1;
+size_t linear_grad_ws_bytes(int64_t R, int32_t E, int32_t NP, int32_t K, lrm_dtype dt, bool grouped, bool dx, bool dw) {
+  // kAlign: the maps' 128-byte boundary
+  size_t n = kAlign + linear_plan_bytes(grouped && dw ? linear_grad_segments(R, E, NP, K, dt) : 0);
+  const int parts = dw && !grouped ? linear_grad_parts(R, NP, K) : 1;
   if (parts > 1) n += up(sizeof(float) * (size_t)parts * NP * K);
-  n += up(linear_grad_parts_bytes(R, E, NP, K, dt)) + up(linear_grad_runs_bytes(R, E, NP, K, dt));
+  if (dw && grouped) n += up(linear_grad_runs_bytes(R, E, NP, K, dt));
+  if (dx) n += up(linear_grad_parts_bytes(R, E, NP, K, dt));
   if (dt == LRM_F32)
-    n += up(linear_planes_bytes(R, NP)) + up(linear_planes_bytes(R, K)) + up(linear_planes_bytes((int64_t)E * NP, K));
+    n += up(linear_planes_bytes(R, NP)) + (dw ? up(linear_planes_bytes(R, K)) : 0) +
+         (dx ? up(linear_planes_bytes((int64_t)E * NP, K)) : 0);
   return n;
 }
 size_t act_grad_ws_bytes(int64_t R, int32_t E, int32_t NP) {
@@ -480,19 +486,33 @@ lrm_status lrm_combine_backward(const int32_t* row_of_pair, const float* alpha, 
   return after_launch();
 }
 
-lrm_status lrm_linear_workspace_size(int64_t R, int32_t E, int32_t N, int32_t K, lrm_act act, lrm_dtype dt,
-                                     size_t* bytes) {
+lrm_status lrm_linear_workspace_size_for(int32_t uses, int64_t R, int32_t E, int32_t N, int32_t K, lrm_act act,
+                                         lrm_dtype dt, size_t* bytes) {
   LRM_NVTX_RANGE();
-  if (!bytes) return LRM_ERR_INVALID_ARG;
-  lrm_status st = check_linear(R, E, N, K, act, dt);
+  if (!bytes || uses < 1 || uses > LRM_LINEAR_USE_ALL) return LRM_ERR_INVALID_ARG;
+  const lrm_status st = check_linear(R, E, N, K, act, dt);
   if (st) return st;
   const int32_t NP = act == LRM_ACT_SWIGLU ? 2 * N : N;
-  const size_t need[] = {linear_ws_bytes(R, E, NP, K, dt), up(linear_extra_bytes(R, E, NP, K, dt)),
-                         act_grad_ws_bytes(R, E, NP), linear_grad_ws_bytes(R, E, NP, K, dt)};
+  const bool dx = (uses & LRM_LINEAR_USE_DX) != 0, dw = (uses & LRM_LINEAR_USE_DW) != 0;
   size_t most = 0;
-  for (const size_t n : need) most = n > most ? n : most;
+  auto at_least = [&](size_t n) { most = n > most ? n : most; };
+  for (const bool grouped : {false, true}) {  // one weight may come with segments or without
+    if (!grouped && E > 1) continue;
+    if (uses & LRM_LINEAR_USE_FORWARD) {
+      const bool few = linear_few_rows(R, E, grouped, dt);
+      at_least(linear_ws_bytes(R, E, NP, K, dt, few));
+      if (dt == LRM_BF16 && !few) at_least(up(linear_extra_bytes(R, E, NP, K, dt)));
+    }
+    if (dx || dw) at_least(linear_grad_ws_bytes(R, E, NP, K, dt, grouped, dx, dw));
+  }
+  if (uses & LRM_LINEAR_USE_ACT_BACKWARD) at_least(act_grad_ws_bytes(R, E, NP));
   *bytes = most;
   return LRM_OK;
+}
+
+lrm_status lrm_linear_workspace_size(int64_t R, int32_t E, int32_t N, int32_t K, lrm_act act, lrm_dtype dt,
+                                     size_t* bytes) {
+  return lrm_linear_workspace_size_for(LRM_LINEAR_USE_ALL, R, E, N, K, act, dt, bytes);
 }
 
 lrm_status lrm_linear(const int32_t* seg_offsets, const void* x, const void* w, const void* bias, const void* residual,
@@ -512,11 +532,12 @@ lrm_status lrm_linear(const int32_t* seg_offsets, const void* x, const void* w, 
     if (!al16(p)) return LRM_ERR_INVALID_ARG;
   if (!al4(seg_offsets)) return LRM_ERR_INVALID_ARG;
   const int32_t NP = act == LRM_ACT_SWIGLU ? 2 * N : N;
-  const size_t need = linear_ws_bytes(R, E, NP, K, dt);
+  const bool few = linear_few_rows(R, E, seg_offsets != nullptr, dt);
+  const size_t need = linear_ws_bytes(R, E, NP, K, dt, few || flags == LRM_GEMM_FORCE_SIMT);
   if (need > 0 && (!ws || ws_bytes < need)) return LRM_ERR_WORKSPACE;
   if (R == 0) return LRM_OK;
   const LinearArgs a{seg_offsets, x, w, bias, residual, R, E, N, K, act, y, z, dev_status};
-  if (flags == LRM_GEMM_DEFAULT && linear_few_rows(R, E, seg_offsets != nullptr, dt)) {
+  if (flags == LRM_GEMM_DEFAULT && few) {
     launch_linear_rows(a, dt, out_dt, stream);
     return after_launch();
   }
@@ -562,7 +583,10 @@ lrm_status lrm_linear_backward(const int32_t* seg_offsets, const void* dz, const
   for (const void* p : ptrs)
     if (!al16(p)) return LRM_ERR_INVALID_ARG;
   if (!al4(seg_offsets)) return LRM_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < linear_grad_ws_bytes(R, E, N, K, dt)) return LRM_ERR_WORKSPACE;
+  const size_t need = flags == LRM_GEMM_FORCE_SIMT
+                          ? kAlign
+                          : linear_grad_ws_bytes(R, E, N, K, dt, seg_offsets != nullptr, dx != nullptr, dw != nullptr);
+  if (!ws || ws_bytes < need) return LRM_ERR_WORKSPACE;
   if (R == 0) {  // no rows anywhere: every dW is zero
     if (dw && cudaMemsetAsync(dw, 0, sizeof(float) * (size_t)E * N * K, stream) != cudaSuccess) return LRM_ERR_CUDA;
     return LRM_OK;

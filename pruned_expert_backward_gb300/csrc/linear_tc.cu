@@ -1130,7 +1130,8 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
   const void *dzs = a.dz, *xs = a.x, *wsrc = a.w;
   // scratch: the expert maps of DW (128-byte aligned) and its plan, then the planes
   char* b = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws) + 127) & ~uintptr_t(127));
-  const int segments = linear_grad_segments(a.R, a.E, a.N, a.K, dt);
+  const bool by_segment = a.dw != nullptr && a.seg_offsets != nullptr;
+  const int segments = by_segment ? linear_grad_segments(a.R, a.E, a.N, a.K, dt) : 0;
   CUtensorMap* maps = reinterpret_cast<CUtensorMap*>(b);
   int32_t* plan = reinterpret_cast<int32_t*>(b + 2 * sizeof(CUtensorMap) * (size_t)segments);
   b += linear_plan_bytes(segments);

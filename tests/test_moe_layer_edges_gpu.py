@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from helpers import ensure_built
-from test_moe_layer_gpu import BF16, F32, gen, randn
+from test_moe_layer_gpu import BF16, F32, check_linear, gen, linear_inputs, randn, segments
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +52,44 @@ def test_layer_without_tokens():
         assert dx.shape == (0, 64) and dalpha.shape == (0, 2)
         assert torch.count_nonzero(dwg) == 0 and torch.count_nonzero(dwd) == 0
         assert int(layer.dev_status.item()) == 0
+
+
+def test_few_fp32_rows_take_no_planes(status):
+    """fp32 products of few rows, and any on the CUDA cores, run with 256 bytes of scratch, dense and per expert."""
+    import pruned_expert_backward_gb300 as lrm
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    for R, E, simt in ((8, None, 0), (24, None, 0), (8, 16, 0), (100, 16, 0), (200, None, 1), (200, 3, 1)):
+        g = gen(R)
+        seg = segments("ragged", R, E, g) if E else None
+        x, w, b, res = linear_inputs(g, F32, R, 80, 40, 136, True, True, E)
+        y, z = lrm.lrm_linear(x, w, bias=b, residual=res, act="swiglu", seg_offsets=seg, save_z=True, ws=small, flags=simt,
+                              dev_status=status)
+        check_linear(x, w, b, res, "swiglu", seg, y, z)
+    x, w = randn(gen(1), 200, 136, dt=F32), randn(gen(2), 80, 136, dt=F32)
+    with pytest.raises(lrm.LrmError):  # the tiles need the planes
+        lrm.lrm_linear(x, w, ws=small)
+
+
+def test_calls_allocate_what_they_use():
+    """Scratch made by the binding: none that belongs to another call of the layer."""
+    import pruned_expert_backward_gb300 as lrm
+
+    def peak(call):
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        out = call()
+        torch.cuda.synchronize()
+        made = sum(t.numel() * t.element_size() for t in out if t is not None)
+        return torch.cuda.max_memory_allocated() - before - made
+
+    mb = 1 << 20
+    dy, z = torch.zeros(16384, 512, device="cuda"), torch.zeros(16384, 512, device="cuda")
+    assert peak(lambda: lrm.lrm_act_backward(dy, z, act="silu")) <= 2 * mb
+    seg = torch.zeros(65, dtype=torch.int32, device="cuda")
+    x, w = torch.zeros(8, 512, device="cuda"), torch.zeros(64, 256, 512, device="cuda")
+    assert peak(lambda: lrm.lrm_linear(x, w, seg_offsets=seg)) <= 2 * mb
+    x, w = torch.zeros(4096, 512, device="cuda"), torch.zeros(512, 512, device="cuda")
+    assert peak(lambda: lrm.lrm_linear_backward(x, x, w, need_dw=False)) <= 6 * (4096 + 512) * 512 + 8 * mb
+    served = lrm.MoeLayer(1, 8, 128, 2048, 768, dtype=F32, train=False)
+    assert served.ws.numel() <= mb
