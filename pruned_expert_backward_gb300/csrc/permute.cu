@@ -562,7 +562,7 @@ lrm_status sort_all(const SortArgs& a, cudaStream_t s) {
     // Rows of 1 KB and more are copied by a launch of their own, a CTA per token (T = 32768, k = 8, H = 4096:
     // 370 against 394 us; T = 2048, H = 2048: 16 against 56 us), narrower ones beside the ranking (T = 30000,
     // H = 72: 16 against 41 us).
-    const bool apart = a.x_s != nullptr && a.H >= 64 * VecTraits<T>::N;
+    const bool apart = a.x_s != nullptr && a.T > 0 && a.H >= 64 * VecTraits<T>::N;
     T* beside = apart ? nullptr : (T*)a.x_s;
     const size_t smem = sizeof(int) * ((size_t)B * (1 + kChunkThreads / 32) + kChunkThreads);
     if (sort_self_counted(a.T, a.k)) {

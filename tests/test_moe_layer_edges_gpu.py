@@ -93,3 +93,18 @@ def test_calls_allocate_what_they_use():
     assert peak(lambda: lrm.lrm_linear_backward(x, x, w, need_dw=False)) <= 6 * (4096 + 512) * 512 + 8 * mb
     served = lrm.MoeLayer(1, 8, 128, 2048, 768, dtype=F32, train=False)
     assert served.ws.numel() <= mb
+
+
+def test_sort_of_no_tokens_with_rows_given(status):
+    """T = 0 through the C ABI with buffers at hand: the segments come out empty, in every form and width."""
+    lib = ensure_built()
+    buf = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    p = buf.data_ptr()
+    stream = torch.cuda.current_stream().cuda_stream
+    for E in (4, 300, 1024):
+        for H in (8, 512, 4096):
+            for dt in (0, 1):
+                seg = torch.full((E + 1,), 7, dtype=torch.int32, device="cuda")
+                st = lib.lrm_sort_tokens(p, p, 0, 2, E, H, dt, seg.data_ptr(), p, p, p, p, buf.numel(), status.data_ptr(),
+                                         stream)
+                assert st == 0 and torch.count_nonzero(seg) == 0
