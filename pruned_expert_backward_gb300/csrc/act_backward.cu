@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(32 * kWarps, (kCtas<T, ACT>)) act_backward_ker
   const int64_t b = blockIdx.x, b0 = b * kRowBlock;
   const int64_t end = seg == nullptr ? R : s_seg[E];
   const int64_t b1 = b0 + kRowBlock < end ? b0 + kRowBlock : end;
-  const int col = (blockIdx.y * 32 + lane) * VN;
+  const int slab = wide_y(), col = (slab * 32 + lane) * VN;
   const bool live = col < N;
   int e = 0;
   if (seg != nullptr && part != nullptr) {  // the expert of row b0: the last e with seg[e] <= b0
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(32 * kWarps, (kCtas<T, ACT>)) act_backward_ker
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) s += s_sum[w][i];
-        const int g = i / (32 * VN), c = blockIdx.y * 32 * VN + i % (32 * VN);
+        const int g = i / (32 * VN), c = slab * 32 * VN + i % (32 * VN);
         if (c < N) part[(b + e) * NP + g * N + c] = s;
       }
       __syncthreads();
@@ -150,7 +150,7 @@ void act_backward_all(const ActGradArgs& a, cudaStream_t s) {
   if (a.R > 0)
     with_act(a.act, [&](auto tag) {
       launch_chained(act_backward_kernel<T, decltype(tag)::value>,
-                     dim3((unsigned)((a.R + kRowBlock - 1) / kRowBlock), (unsigned)slabs), dim3(32 * kWarps), 0, s,
+                     grid_wide((a.R + kRowBlock - 1) / kRowBlock, slabs), dim3(32 * kWarps), 0, s,
                      a.seg_offsets, a.E, a.R, a.N, (const T*)a.dy, (const T*)a.z, (T*)a.dz,
                      a.db != nullptr ? a.part : (float*)nullptr, a.status);
     });

@@ -130,6 +130,14 @@ __device__ __forceinline__ void chain_wait() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A grid of x by y blocks where y may pass the 65535 of a grid's second dimension: it is dealt over the second and
+// third, the last blocks of which may lie past y.
+inline dim3 grid_wide(int64_t x, int64_t y) {
+  const int64_t z = (y + 65534) / 65535;
+  return dim3((unsigned)x, (unsigned)((y + z - 1) / z), (unsigned)z);
+}
+__device__ __forceinline__ int wide_y() { return (int)(blockIdx.z * gridDim.y + blockIdx.y); }
+
 // One-time set-up that belongs to a device (kernel attributes, occupancy, SM counts) is kept
 // per device: a process may drive several GPUs.
 constexpr int kDeviceSlots = 64;

@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(NT) rows_kernel(const int32_t* __restrict__ se
   int e, r0, r1;
   if (!find_rows(seg, E, R, blockIdx.x, s_prefix, &e, &r0, &r1)) return;
   const int NP = GLU ? 2 * N : N;
-  const int n0 = blockIdx.y * CN;
+  const int n0 = wide_y() * CN;
   const T* Be = B + (int64_t)e * NP * K;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   // product column held at tile column c, and whether its output column exists
@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(NT) weights_kernel(const int32_t* __restrict__
   __shared__ float Bs[BK][BN + 4];
   chain_wait();
   if (!rows_valid(seg, E, R, status)) return;
-  const int e = blockIdx.z, m0 = blockIdx.y * BM, n0 = blockIdx.x * BN;
+  const int blocks_n = (N + BN - 1) / BN;  // (blocks of rows and columns in one grid dimension: both may be many)
+  const int e = blockIdx.y, m0 = blockIdx.x / blocks_n * BM, n0 = blockIdx.x % blocks_n * BN;
   const int r0 = seg_at(seg, e, R), r1 = seg_at(seg, e + 1, R);
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   float acc[4][4] = {};
@@ -191,7 +192,7 @@ void forward_all(const LinearArgs& a, cudaStream_t s) {
     constexpr int ACT = decltype(tag)::value;
     constexpr int CN = ACT == LRM_ACT_SWIGLU ? BN / 2 : BN;
     launch_chained(rows_kernel<T, TO, FWD, ACT>,
-                   dim3((unsigned)row_tiles(a.seg_offsets, a.R, a.E), (unsigned)((a.N + CN - 1) / CN)), dim3(NT), 0, s,
+                   grid_wide(row_tiles(a.seg_offsets, a.R, a.E), (a.N + CN - 1) / CN), dim3(NT), 0, s,
                    a.seg_offsets, a.E, a.R, (const T*)a.x, (const T*)a.w, a.N, a.K, (const T*)a.bias,
                    (const TO*)a.residual, (TO*)a.y, (T*)a.z, a.status);
   });
@@ -201,12 +202,12 @@ template <typename T>
 void backward_all(const LinearGradArgs& a, cudaStream_t s) {
   if (a.dx != nullptr && a.R > 0)
     launch_chained(rows_kernel<T, T, DX, LRM_ACT_NONE>,
-                   dim3((unsigned)row_tiles(a.seg_offsets, a.R, a.E), (unsigned)((a.K + BN - 1) / BN)), dim3(NT), 0, s,
+                   grid_wide(row_tiles(a.seg_offsets, a.R, a.E), (a.K + BN - 1) / BN), dim3(NT), 0, s,
                    a.seg_offsets, a.E, a.R, (const T*)a.dz, (const T*)a.w, a.K, a.N, (const T*)nullptr,
                    (const T*)nullptr, (T*)a.dx, (T*)nullptr, a.status);
   if (a.dw != nullptr)
     launch_chained(weights_kernel<T>,
-                   dim3((unsigned)((a.K + BN - 1) / BN), (unsigned)((a.N + BM - 1) / BM), (unsigned)a.E), dim3(NT), 0,
+                   dim3((unsigned)((int64_t)((a.K + BN - 1) / BN) * ((a.N + BM - 1) / BM)), (unsigned)a.E), dim3(NT), 0,
                    s, a.seg_offsets, a.E, a.R, (const T*)a.dz, (const T*)a.x, a.N, a.K, a.dw, a.status);
 }
 

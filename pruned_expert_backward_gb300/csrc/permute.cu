@@ -598,8 +598,9 @@ void combine_all(const int32_t* row_of_pair, const float* alpha, const void* y_s
   }
   // few tokens: one token and 64 columns per CTA, so that the rows spread over the GPU
   if (n_tok < 2048) {
-    launch_chained(combine_kernel<T, 1>, dim3((unsigned)n_tok, (unsigned)((nv + 63) / 64)), dim3(64), 0, s,
-                   row_of_pair, alpha, (const T*)y_s, (const T*)residual, n_tok, k, H, cap, (T*)y, status);
+    const int blocks = (nv + 63) / 64;
+    launch_chained(combine_kernel<T, 1>, dim3((unsigned)n_tok, (unsigned)(blocks < 65535 ? blocks : 65535)), dim3(64), 0,
+                   s, row_of_pair, alpha, (const T*)y_s, (const T*)residual, n_tok, k, H, cap, (T*)y, status);
     return;
   }
   // tokens of a CTA: about 32 rows to walk (T = 8192, H = 2048, bf16: k = 8 50 us with 4 tokens, 55 us with 8;

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from helpers import ensure_built
-from test_moe_layer_gpu import BF16, F32, check_linear, gen, linear_inputs, randn, segments
+from test_moe_layer_gpu import BF16, EPS, F32, check, check_linear, gen, linear_inputs, randn, segments
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +108,39 @@ def test_sort_of_no_tokens_with_rows_given(status):
                 st = lib.lrm_sort_tokens(p, p, 0, 2, E, H, dt, seg.data_ptr(), p, p, p, p, buf.numel(), status.data_ptr(),
                                          stream)
                 assert st == 0 and torch.count_nonzero(seg) == 0
+
+
+@pytest.mark.parametrize("dt,N", [(F32, 8388616), (BF16, 16777216)], ids=["f32", "bf16"])
+def test_act_backward_of_many_columns(dt, N, status):
+    """Up to 2^24 columns: more blocks of columns than a launch grid's second dimension holds."""
+    import pruned_expert_backward_gb300 as lrm
+    dy, z = randn(gen(1), 2, N, dt=dt), randn(gen(2), 2, N, dt=dt)
+    dz, db = lrm.lrm_act_backward(dy, z, act="relu", dev_status=status)
+    want = torch.where(z > 0, dy, torch.zeros_like(dy))
+    assert torch.equal(dz, want) and torch.equal(db, want[0].float() + want[1].float())
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+def test_products_of_many_columns_on_the_cuda_cores(dt, status):
+    import pruned_expert_backward_gb300 as lrm
+    N = 4194320
+    x, w = randn(gen(1), 3, 8, dt=dt), randn(gen(2), N, 8, dt=dt)
+    y, _ = lrm.lrm_linear(x, w, flags=1, dev_status=status)
+    check_linear(x, w, None, None, "none", None, y, None)
+    y, _ = lrm.lrm_linear(x, w, act="swiglu", flags=1, dev_status=status)
+    check_linear(x, w, None, None, "swiglu", None, y, None)
+    dz = randn(gen(3), 3, N, dt=dt)
+    _, dw = lrm.lrm_linear_backward(dz, x, w, need_dx=False, flags=1, dev_status=status)
+    check(dw, dz.double().t() @ x.double(), 4 * EPS * (dz.double().abs().t() @ x.double().abs()))
+    wt, d8 = w.t().contiguous(), randn(gen(4), 3, 8, dt=dt)
+    dx, _ = lrm.lrm_linear_backward(d8, dz, wt, need_dw=False, flags=1, dev_status=status)
+    check(dx, d8.double() @ wt.double(), 9 * EPS * (d8.double().abs() @ wt.double().abs()))
+
+
+@pytest.mark.parametrize("dt,H", [(BF16, 33554432), (F32, 16777216)], ids=["bf16", "f32"])
+def test_combine_of_wide_rows(dt, H, status):
+    import pruned_expert_backward_gb300 as lrm
+    row, alpha = torch.tensor([[1], [0]], dtype=torch.int32, device="cuda"), torch.tensor([[0.5], [2.0]], device="cuda")
+    y_s = randn(gen(1), 2, H, dt=dt)
+    y = lrm.lrm_combine(row, alpha, y_s, dev_status=status)  # (exact: powers of two)
+    assert torch.equal(y[0], y_s[1] * 0.5) and torch.equal(y[1], y_s[0] * 2)
