@@ -415,7 +415,7 @@ lrm_status lrm_linear_workspace_size(int64_t R, int32_t E, int32_t N, int32_t K,
  * dt LRM_BF16 or LRM_F32; out_dt is the type of y: dt, or LRM_F32 from bf16 inputs (a router's logits;
  * no residual then).  Sums, bias, activation and residual are in fp32, each output is rounded once.  An
  * infinity or NaN in x spoils the outputs of its own row only (as NaN where fp32 inputs are split).
- * Rows >= seg_offsets[E] are not written.  N and K are multiples of 8, up to 2^24; R <= INT32_MAX.
+ * Rows >= seg_offsets[E] are not written.  N and K are multiples of 8, up to 2^24; R <= INT32_MAX - 1023.
  * ws: scratch of at least lrm_linear_workspace_size_for(LRM_LINEAR_USE_FORWARD, ...) bytes for fp32 inputs (256
  * bytes where few rows, or LRM_GEMM_FORCE_SIMT, take no planes of them); for bf16 inputs it may be NULL, and
  * speeds two kinds of product up: few tiles and a long reduction (summed in parts on the whole GPU, the

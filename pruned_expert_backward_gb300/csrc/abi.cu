@@ -28,11 +28,13 @@ lrm_status check_dims(int64_t T, int32_t k, int32_t E, int32_t H, int32_t I) {
 }
 lrm_status check_dt(lrm_dtype dt) { return (dt == LRM_BF16 || dt == LRM_F32) ? LRM_OK : LRM_ERR_DTYPE; }
 
-// Sizes of lrm_linear and its gradients: R rows, E weights of N (2N for SwiGLU) x K.
+// Sizes of lrm_linear and its gradients: R rows, E weights of N (2N for SwiGLU) x K.  The kernels number rows in
+// 32 bits up to the end of the last tile, which may lie past the last row by less than 1024.
+constexpr int64_t kMaxRows = (int64_t)INT32_MAX - 1023;
 lrm_status check_linear(int64_t R, int32_t E, int32_t N, int32_t K, lrm_act act, lrm_dtype dt) {
   if (R < 0 || E < 1 || N < 1 || K < 1) return LRM_ERR_INVALID_ARG;
   if (act < LRM_ACT_NONE || act > LRM_ACT_SWIGLU) return LRM_ERR_INVALID_ARG;
-  if (R > INT32_MAX || E > LRM_MAX_EXPERTS || N > (1 << 24) || K > (1 << 24)) return LRM_ERR_SHAPE;
+  if (R > kMaxRows || E > LRM_MAX_EXPERTS || N > (1 << 24) || K > (1 << 24)) return LRM_ERR_SHAPE;
   if (N % 8 != 0 || K % 8 != 0) return LRM_ERR_SHAPE;
   return check_dt(dt);
 }

@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(1024) cut_segments_kernel(const int32_t* __res
     int run = 0;
     for (int e = 0; e < E; ++e) {
       s_first[e] = run;
-      if (valid) run += (s_seg[e + 1] - s_seg[e] + chunk - 1) / chunk;
+      if (valid) run += (int)(((int64_t)s_seg[e + 1] - s_seg[e] + chunk - 1) / chunk);
     }
     s_first[E] = run;
   }

@@ -73,3 +73,16 @@ def test_scratch_size_refusals():
     assert f(0, 100, 4, 64, 64, 0, 0, C.byref(n)) == ARG and f(16, 100, 4, 64, 64, 0, 0, C.byref(n)) == ARG
     assert f(1, 100, 4, 64, 64, 0, 0, None) == ARG and f(1, 100, 4, 64, 64, 5, 0, C.byref(n)) == ARG
     assert f(1, 100, 4, 60, 64, 0, 0, C.byref(n)) == SHAPE and f(1, 100, 4, 64, 64, 0, 2, C.byref(n)) == DTYPE
+
+
+def test_most_rows():
+    """Row numbers of a tile past the last row stay in 32 bits: 1023 rows below INT32_MAX are the most."""
+    lib, n = ensure_built(), C.c_size_t(0)
+    most = (1 << 31) - 1024
+    for E in (1, 4):
+        assert size(most, E, 8, 8) > 0
+        for R in (most + 1, (1 << 31) - 1):
+            assert lib.lrm_linear_workspace_size(R, E, 8, 8, NONE, BF16, C.byref(n)) == SHAPE
+            assert lib.lrm_linear(P, P, P, None, None, R, E, 8, 8, NONE, 0, 0, P, None, P, BIG, 0, None, None) == SHAPE
+            assert lib.lrm_linear_backward(P, P, P, P, R, E, 8, 8, 0, P, P, P, BIG, 0, None, None) == SHAPE
+            assert lib.lrm_act_backward(P, P, P, R, E, 8, NONE, 0, P, P, P, BIG, None, None) == SHAPE
