@@ -64,13 +64,25 @@ __device__ __forceinline__ void warp_products(const __nv_bfloat16* w0, const __n
         const int k = k0 + u * kWarps * kStep;
         v[i][u] = k < K && i * 8 + g < rows ? ldg16_now(x + (int64_t)(i * 8 + g) * K + k) : zero;
       }
+    // This round's products apart: the tensor core truncates as it adds, the sum of the rounds is to nearest (65536
+    // products of one sign were 2.9e-5 off in one accumulator, and take as long; 4096 x 4096 with 16 rows 9.0 us, 8.6
+    // us in one).
+    float s[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s[i][q] = 0.f;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        mma_16x8(c[i], a[u].x, b[u].x, a[u].y, b[u].y, v[i][u].x, v[i][u].y);
-        mma_16x8(c[i], a[u].z, b[u].z, a[u].w, b[u].w, v[i][u].z, v[i][u].w);
+        mma_16x8(s[i], a[u].x, b[u].x, a[u].y, b[u].y, v[i][u].x, v[i][u].y);
+        mma_16x8(s[i], a[u].z, b[u].z, a[u].w, b[u].w, v[i][u].z, v[i][u].w);
       }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) c[i][q] += s[i][q];
   }
 #pragma unroll
   for (int i = 0; i < NT; ++i) {

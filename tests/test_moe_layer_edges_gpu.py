@@ -144,3 +144,28 @@ def test_combine_of_wide_rows(dt, H, status):
     y_s = randn(gen(1), 2, H, dt=dt)
     y = lrm.lrm_combine(row, alpha, y_s, dev_status=status)  # (exact: powers of two)
     assert torch.equal(y[0], y_s[1] * 0.5) and torch.equal(y[1], y_s[0] * 2)
+
+
+def one_sign(g, rows, K):
+    """Values of one sign, the rows scaled apart over a factor of two, so that sums round to bf16 evenly."""
+    scale = 2.0 ** (torch.arange(rows, device="cuda", dtype=F32)[:, None] / rows)
+    return ((torch.rand(rows, K, generator=g, device="cuda") + 0.5) * scale).to(BF16)
+
+
+def bias_of(got, want):
+    return ((got.double() - want) / want).mean().abs().item()
+
+
+@pytest.mark.parametrize("E", [None, 3], ids=["dense", "experts"])
+@pytest.mark.parametrize("R", [3, 13, 27])
+def test_fp32_sums_of_few_rows(R, E, status):
+    """fp32 outputs of bf16 inputs, long sums of one sign: at most 256 products in a row are added with truncation
+    (16 steps of at most 2^-23 each), the rest to nearest."""
+    import pruned_expert_backward_gb300 as lrm
+    K, N = 65536, 64
+    g = gen(R)
+    x, w = one_sign(g, R, K), one_sign(g, N * (E or 1), K).view(*((E,) if E else ()), N, K)
+    seg = torch.tensor([0, 0, R, R], dtype=torch.int32, device="cuda") if E else None
+    y, _ = lrm.lrm_linear(x, w, seg_offsets=seg, out_dtype=F32, dev_status=status)
+    want = x.double() @ (w[1] if E else w).double().t()
+    assert bias_of(y, want) <= 16 * EPS
