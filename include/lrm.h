@@ -413,7 +413,9 @@ lrm_status lrm_linear_workspace_size(int64_t R, int32_t E, int32_t N, int32_t K,
  *   x [R,K] dt, w [E,N',K] dt, bias [E,N'] dt or NULL, residual [R,N] (type of y) or NULL
  *   -> y [R,N], z [R,N'] dt or NULL (the pre-activation, for lrm_act_backward); N' = 2N for SwiGLU, else N.
  * dt LRM_BF16 or LRM_F32; out_dt is the type of y: dt, or LRM_F32 from bf16 inputs (a router's logits;
- * no residual then).  Sums, bias, activation and residual are in fp32, each output is rounded once.  An
+ * no residual then).  Sums, bias, activation and residual are in fp32, each output is rounded once.  The tensor
+ * core truncates as it adds: sums for fp32 results err by about 5e-7 of the sum of |products|, those for bf16
+ * results, before their rounding, by at most 4e-4 (65536 products of one sign; 6e-6 for 2048).  An
  * infinity or NaN in x spoils the outputs of its own row only (as NaN where fp32 inputs are split).
  * Rows >= seg_offsets[E] are not written.  N and K are multiples of 8, up to 2^24; R <= INT32_MAX - 1023.
  * ws: scratch of at least lrm_linear_workspace_size_for(LRM_LINEAR_USE_FORWARD, ...) bytes for fp32 inputs (256

@@ -29,9 +29,9 @@
 //
 // fp32 accumulation.  The tensor core adds into its fp32 accumulator by truncation: against 64 bits a
 // sum of 2048 products is 2e-6 off (5.6e-6 when all have one sign), one of 32768 3.8e-5 (1.8e-4).
-// That is far below one bf16 rounding, so bf16 results are taken as they are.  For fp32 results
-// (PROMOTE) the accumulator is moved out of TMEM every `pk` K slices and added up in registers,
-// rounding to nearest.
+// That is far below one bf16 rounding, so bf16 results of up to 65536 products are taken as they are.  For fp32
+// results and longer sums (PROMOTE) the accumulator is moved out of TMEM every `pk` K slices and added up in
+// registers, rounding to nearest.
 //
 // fp32 inputs are split into three bf16 planes, x = x0 + x1 + x2 (24 bits), and the six products of
 // weight 2^-16 and more are summed, the smallest first: x2 w0, x0 w2, x1 w1, x1 w0, x0 w1, x0 w0.  Only
@@ -931,6 +931,9 @@ void launch_splits(const Splits& a, cudaStream_t s) {
 // K slices per accumulator where the result is fp32: 256 products for split fp32 inputs (2.4e-7 off against
 // 64 bits, as fp32 arithmetic itself), 512 for bf16 inputs (4.7e-7; 1024 products: 9.9e-7).
 constexpr int kSlicesF32 = 4, kSlicesBf16 = 8;
+// bf16 results of longer sums leave TMEM like fp32 ones: sums of one sign are 4e-4 off after 65536 products and 1.6e-3
+// after 262144, near half a bf16 unit (8192 x 4096 x 65600: 2291 us, 2220 us in one accumulator).
+constexpr int kLongSum = 65536;
 
 // Most row tiles there can be, and about how many (every segment ends in half a tile).
 int64_t row_tiles(const int32_t* seg, int64_t R, int E) {
@@ -1066,6 +1069,7 @@ lrm_status launch_linear_tc(const LinearArgs& a, lrm_dtype dt, lrm_dtype out_dt,
       if (!operand_map(&mB, wsrc, a.K, pitch_w, NP, (uint64_t)a.E * planes, BN / 2)) return LRM_ERR_CUDA;
       if (f32) return launch<FWD, BN, GLU, true, float, float>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
       if (y32) return launch<FWD, BN, GLU, true, B16, float>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
+      if (a.K > kLongSum) return launch<FWD, BN, GLU, true, B16, B16>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
       return launch<FWD, BN, GLU, false, B16, B16>(mA, mB, mY, mZ, p, tm * p.tiles_n, s);
     }
   };
@@ -1260,6 +1264,7 @@ lrm_status launch_linear_backward_tc(const LinearGradArgs& a, lrm_dtype dt, void
         if (!column_map(&mB, wsrc, a.K, pitch_k, a.N, (uint64_t)a.E * planes, BN / 128, &p.one_box_b))
           return LRM_ERR_CUDA;
         if (f32) return launch<DX, BN, false, true, float, float>(mA, mB, mY, mY, p, tm * p.tiles_n, s);
+        if (a.N > kLongSum) return launch<DX, BN, false, true, B16, B16>(mA, mB, mY, mY, p, tm * p.tiles_n, s);
         return launch<DX, BN, false, false, B16, B16>(mA, mB, mY, mY, p, tm * p.tiles_n, s);
       }
     });

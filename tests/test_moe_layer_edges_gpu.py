@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from helpers import ensure_built
-from test_moe_layer_gpu import BF16, EPS, F32, check, check_linear, gen, linear_inputs, randn, segments
+from test_moe_layer_gpu import BF16, EPS, F32, act64, check, check_linear, gen, linear_inputs, randn, segments
 
 pytestmark = pytest.mark.gpu
 
@@ -169,3 +169,32 @@ def test_fp32_sums_of_few_rows(R, E, status):
     y, _ = lrm.lrm_linear(x, w, seg_offsets=seg, out_dtype=F32, dev_status=status)
     want = x.double() @ (w[1] if E else w).double().t()
     assert bias_of(y, want) <= 16 * EPS
+
+
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_long_bf16_sums(act, status):
+    """bf16 outputs of sums of 262144 products of one sign: the mean error is that of 5120 (SwiGLU: 2560) roundings to
+    2^-9, 6 deviations of 2^-9 / sqrt 3 allowed; a truncating accumulator is 1.4e-3 off."""
+    import pruned_expert_backward_gb300 as lrm
+    R, N, K = 40, 128, 262144
+    g = gen(7)
+    x, w = one_sign(g, R, K) * 0.125, one_sign(g, N, K) * 0.125
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")  # (with scratch the sum would be cut into parts)
+    y, _ = lrm.lrm_linear(x, w, act=act, ws=none, dev_status=status)
+    want = x.double() @ w.double().t()
+    if act == "swiglu":
+        want = act64(want, act)
+    assert bias_of(y, want) <= 6 * 2.0 ** -9 / 3 ** 0.5 / want.numel() ** 0.5 + 32 * EPS
+
+
+def test_long_bf16_sums_of_the_gradient(status):
+    import pruned_expert_backward_gb300 as lrm
+    R, N, K = 40, 262144, 9984  # (wide enough not to be cut into parts)
+    g = gen(8)
+    dz, w = one_sign(g, R, N), torch.empty(N, K, dtype=BF16, device="cuda")
+    want = torch.zeros(R, K, dtype=torch.float64, device="cuda")
+    for i in range(0, N, 16384):
+        w[i:i + 16384] = one_sign(g, K, 16384).t()
+        want += dz[:, i:i + 16384].double() @ w[i:i + 16384].double()
+    dx, _ = lrm.lrm_linear_backward(dz, dz[:, :K].contiguous(), w, need_dw=False, dev_status=status)
+    assert bias_of(dx, want) <= 6 * 2.0 ** -9 / 3 ** 0.5 / want.numel() ** 0.5 + 32 * EPS
