@@ -35,9 +35,10 @@
  *  - Index arrays handed from one call to the next (row_of_pair, seg_offsets) are checked
  *    where they are used: an index outside its range is never followed; the pair (or the
  *    whole grouped backward) is skipped and the status word records why.  A build with
- *    -DLRM_DEBUG (liblrm_debug.so) adds the same kind of check to every index the kernels
- *    form themselves (bucket slots, compacted rows of a tile, gathered pair rows); a failed
- *    check records LRM_ERR_BAD_INDEX and skips the access, it never traps.
+ *    -DLRM_DEBUG (liblrm_debug.so) adds the same kind of check to the indices that the kernels
+ *    form themselves and write by (bucket slots, rows of the selection and of the sort, rows of a
+ *    product's tile, partial sums); TMA copies are clipped by their tensor maps.  A failed check
+ *    records LRM_ERR_BAD_INDEX and skips the access, it never traps.
  *  - Each entry point opens an NVTX range of its own name around its host work when the
  *    environment variable LRM_NVTX is 1 at the library's first call (off otherwise).
  *  - The kernels of lrm_score, lrm_select, lrm_select_static, lrm_compact,

@@ -2,8 +2,8 @@
 
 Each .cu under csrc/ compiles to an object in parallel; the objects link into
 pruned_expert_backward_gb300/liblrm.so (static CUDA runtime, no other dependency).
-The same sources compiled with -DLRM_DEBUG link into liblrm_debug.so: every index the
-kernels form themselves is checked as well (a failed check records LRM_ERR_BAD_INDEX in the
+The same sources compiled with -DLRM_DEBUG link into liblrm_debug.so: the indices that the
+kernels form themselves and write by are checked as well (a failed check records LRM_ERR_BAD_INDEX in the
 status word and skips the access).  Both builds run side by side by default.
 Run: python -m pruned_expert_backward_gb300.build [--release-only] [-v]
 (or __graft_entry__.build()).

@@ -100,7 +100,8 @@ __global__ void __launch_bounds__(32 * kWarps, (kCtas<T, ACT>)) act_backward_ker
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) s += s_sum[w][i];
         const int g = i / (32 * VN), c = slab * 32 * VN + i % (32 * VN);
-        if (c < N) part[(b + e) * NP + g * N + c] = s;
+        if (c < N && LRM_DCHECK(b + e < (int64_t)gridDim.x + E, status, LRM_ERR_BAD_INDEX))
+          part[(b + e) * NP + g * N + c] = s;
       }
       __syncthreads();
     }
@@ -126,6 +127,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) bias_sum_kernel(const int32_t*
     const int64_t last = (r1 - 1) / kRowBlock;
 #pragma unroll 8
     for (int64_t b = r0 / kRowBlock + warp; b <= last; b += nw) {
+      if (!LRM_DCHECK(b + e < (R + kRowBlock - 1) / kRowBlock + E, status, LRM_ERR_BAD_INDEX)) break;
       float f[4];
       unpack(ldg16(part + (b + e) * NP + col), f);
 #pragma unroll

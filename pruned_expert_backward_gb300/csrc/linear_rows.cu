@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) rows_kernel(const int32_t* __r
       __syncthreads();
       for (int i = threadIdx.x; i < CN * RT; i += blockDim.x) {
         const int c = i % CN, r = i / CN, n = n0 + c;
-        if (r >= rows || n >= N) continue;
+        if (r >= rows || n >= N || !LRM_DCHECK(r0 >= 0 && r0 + r < R, status, LRM_ERR_BAD_INDEX)) continue;
         float v = 0.f, u = 0.f;
 #pragma unroll
         for (int q = 0; q < kWarps; ++q) {

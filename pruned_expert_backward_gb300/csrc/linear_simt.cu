@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(NT) rows_kernel(const int32_t* __restrict__ se
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t r = r0 + ty * 4 + i;
-    if (r >= r1) continue;
+    if (r >= r1 || !LRM_DCHECK(r >= 0 && r < R, status, LRM_ERR_BAD_INDEX)) continue;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int c = tx * 4 + j;

@@ -483,7 +483,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile d = decode<KIND, BN, GLU>(p, prefix, t, rank);
       const int row_base = (KIND == DW ? d.m0 : d.row0) + q * 32;
       const int row_lim = KIND == DW ? p.M : d.row_end;
-      const int nrows = d.has_rows ? min(32, row_lim - row_base) : 0;
+      // (the check, where it is on, covers what this warp's stores address: the expert, and its first and last row)
+      const int nrows =
+          d.has_rows && LRM_DCHECK(d.e >= 0 && d.e < p.E && row_base >= 0 && row_lim <= (KIND == DW ? p.M : p.R),
+                                   p.status, LRM_ERR_BAD_INDEX)
+              ? min(32, row_lim - row_base)
+              : 0;
       // without segments the output map ends where the rows end, so TMA clips a partial block
       const bool whole = nrows == 32 || (nrows > 0 && (KIND == DW || p.seg == nullptr));
       const bool live = lane < nrows;
@@ -628,7 +633,7 @@ __global__ void __launch_bounds__(1024) linear_plan_kernel(const int32_t* __rest
   if (e < E) {
     int before = 0;
     for (int j = 0; j < E; ++j) before += s_rows[j] > rows || (s_rows[j] == rows && j < e);
-    plan[1 + before] = e;
+    if (LRM_DCHECK(before < E, status, LRM_ERR_BAD_INDEX)) plan[1 + before] = e;
   }
   for (int i = threadIdx.x; i < 2 * E; i += blockDim.x) {
     const int j = i / E, ee = i - j * E;
@@ -679,6 +684,7 @@ __global__ void __launch_bounds__(1024) cut_segments_kernel(const int32_t* __res
       }
       at = s_seg[lo] + (v - s_first[lo]) * chunk;
     }
+    if (!LRM_DCHECK(runs <= EV && at >= 0 && at <= end, status, LRM_ERR_BAD_INDEX)) at = end;
     vseg[v] = valid ? at : 1;
   }
 }

@@ -70,10 +70,11 @@ __device__ __forceinline__ int block_prefix(int v, int* sm) {
 
 // Copies x rows of `ntok` tokens from t0 into their pairs' rows: s_dst[i * k + j] >= 0 is the row of
 // pair (t0 + i, j); a negative entry -1 - r zeroes row r (an unrouted pair's place).  (token, 16-byte
-// column) items are dealt to the threads, four tokens' loads in flight.
+// column) items are dealt to the threads, four tokens' loads in flight.  x_s has n_rows rows.
 template <typename T>
 __device__ __forceinline__ void copy_rows(const T* __restrict__ x, T* __restrict__ x_s, const int* s_dst, int64_t t0,
-                                          int ntok, int k, int H) {
+                                          int ntok, int k, int H, [[maybe_unused]] int64_t n_rows,
+                                          [[maybe_unused]] int32_t* status) {
   constexpr int VN = VecTraits<T>::N;
   const int nv = H / VN;
   const int n = ntok * nv, step = blockDim.x;
@@ -91,6 +92,7 @@ __device__ __forceinline__ void copy_rows(const T* __restrict__ x, T* __restrict
       const int tok = i / nv, col = (i - tok * nv) * VN;
       for (int j = 0; j < k; ++j) {
         const int r = s_dst[tok * k + j];
+        if (!LRM_DCHECK(r < n_rows && -1 - r < n_rows, status, LRM_ERR_BAD_INDEX)) continue;
         st16(x_s + (int64_t)(r >= 0 ? r : -1 - r) * H + col, r >= 0 ? v[q] : make_uint4(0, 0, 0, 0));
       }
     }
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(1024) sort_small_kernel(const int32_t* __restr
   for (int u = threadIdx.x; u < P; u += blockDim.x) {
     const int e = s_row[u] >> 16, r = s_start[e] + s_cnt[(u / ppw) * B + e] + (s_row[u] & 0xffff);
     s_row[u] = e < E ? r : -1 - r;
-    if (blockIdx.x == 0) {
+    if (blockIdx.x == 0 && LRM_DCHECK(r >= 0 && r < P, status, LRM_ERR_BAD_INDEX)) {
       row_of_pair[u] = e < E ? r : -1;
       pair_of_row[r] = e < E ? u : -1;
     }
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(1024) sort_small_kernel(const int32_t* __restr
     for (int e = threadIdx.x; e < B; e += blockDim.x) seg[e] = s_start[e];
   __syncthreads();
   if (x_s != nullptr)
-    for (int t = blockIdx.x; t < n_tok; t += gridDim.x) copy_rows(x, x_s, s_row + t * k, t, 1, k, H);
+    for (int t = blockIdx.x; t < n_tok; t += gridDim.x) copy_rows(x, x_s, s_row + t * k, t, 1, k, H, P, status);
 }
 
 // ---------------------------------------------------------------- several launches ---
@@ -254,11 +256,13 @@ __global__ void __launch_bounds__(kChunkThreads) sort_rows_kernel(
     int r = s_start[e] + __popc(same & ((1u << lane) - 1u));
     for (int w = 0; w < warp; ++w) r += s_cnt[w * B + e];
     s_row[threadIdx.x] = e < E ? r : -1 - r;
-    row_of_pair[u] = e < E ? r : -1;
-    pair_of_row[r] = e < E ? (int32_t)u : -1;
+    if (LRM_DCHECK(r >= 0 && r < n_tok * k, status, LRM_ERR_BAD_INDEX)) {
+      row_of_pair[u] = e < E ? r : -1;
+      pair_of_row[r] = e < E ? (int32_t)u : -1;
+    }
   }
   __syncthreads();
-  if (x_s != nullptr) copy_rows(x, x_s, s_row, t0, ntok, k, H);
+  if (x_s != nullptr) copy_rows(x, x_s, s_row, t0, ntok, k, H, n_tok * k, status);
 }
 
 // One CTA per token copies its row into its pairs' rows; CTA t also zeroes every n_tok-th row behind the
@@ -266,12 +270,16 @@ __global__ void __launch_bounds__(kChunkThreads) sort_rows_kernel(
 template <typename T>
 __global__ void __launch_bounds__(256) sort_copy_kernel(const int32_t* __restrict__ row_of_pair,
                                                         const int32_t* __restrict__ seg, const T* __restrict__ x,
-                                                        int64_t n_tok, int k, int E, int H, T* __restrict__ x_s) {
+                                                        int64_t n_tok, int k, int E, int H, T* __restrict__ x_s,
+                                                        [[maybe_unused]] int32_t* status) {
   chain_wait();
   constexpr int VN = VecTraits<T>::N;
   __shared__ int s_row[LRM_MAX_TOPK];
   const int64_t t = blockIdx.x;
-  if (threadIdx.x < k) s_row[threadIdx.x] = row_of_pair[t * k + threadIdx.x];
+  if (threadIdx.x < k) {
+    const int r = row_of_pair[t * k + threadIdx.x];
+    s_row[threadIdx.x] = LRM_DCHECK(r >= -1 && r < n_tok * k, status, LRM_ERR_BAD_INDEX) ? r : -1;
+  }
   __syncthreads();
   const int nv = H / VN;
   for (int v0 = threadIdx.x; v0 < nv; v0 += 2 * blockDim.x) {
@@ -581,7 +589,7 @@ lrm_status sort_all(const SortArgs& a, cudaStream_t s) {
       const int cols = row_threads((a.H / VecTraits<T>::N + 1) / 2);
       launch_chained(sort_copy_kernel<T>, dim3((unsigned)a.T), dim3(cols < 64 ? 64 : cols), 0, s,
                      (const int32_t*)a.row_of_pair, (const int32_t*)a.seg_offsets, (const T*)a.x, a.T, a.k, a.E, a.H,
-                     (T*)a.x_s);
+                     (T*)a.x_s, a.status);
     }
   }
   return cudaGetLastError() == cudaSuccess ? LRM_OK : LRM_ERR_CUDA;
@@ -599,8 +607,9 @@ void combine_all(const int32_t* row_of_pair, const float* alpha, const void* y_s
   // few tokens: one token and 64 columns per CTA, so that the rows spread over the GPU
   if (n_tok < 2048) {
     const int blocks = (nv + 63) / 64;
-    launch_chained(combine_kernel<T, 1>, dim3((unsigned)n_tok, (unsigned)(blocks < 65535 ? blocks : 65535)), dim3(64), 0,
-                   s, row_of_pair, alpha, (const T*)y_s, (const T*)residual, n_tok, k, H, cap, (T*)y, status);
+    const dim3 grid((unsigned)n_tok, (unsigned)(blocks < 65535 ? blocks : 65535));
+    launch_chained(combine_kernel<T, 1>, grid, dim3(64), 0, s, row_of_pair, alpha, (const T*)y_s,
+                   (const T*)residual, n_tok, k, H, cap, (T*)y, status);
     return;
   }
   // tokens of a CTA: about 32 rows to walk (T = 8192, H = 2048, bf16: k = 8 50 us with 4 tokens, 55 us with 8;

@@ -152,3 +152,56 @@ def test_gradients(case, status):
             continue
         check(got, want, (b - a + 1) * EPS * (de.abs().t() @ xe.abs()))
         assert (got.double() - want).norm() <= 5e-6 * want.norm()
+
+
+# ------------------------------------------------------------------------------- debug build ----
+_EVERY_CALL = r"""
+import os, sys, torch
+sys.path.insert(0, sys.argv[1]); sys.path.insert(0, sys.argv[1] + "/tests")
+from pruned_expert_backward_gb300 import _lib
+assert _lib.library_path().endswith(sys.argv[3])
+import pruned_expert_backward_gb300 as lrm
+from test_moe_layer_gpu import BF16, F32, gen, linear_inputs, randn, routing, segments
+st, out = torch.zeros(1, dtype=torch.int32, device="cuda"), []
+for T, k, E, H, dt in ((3, 8, 16, 520, BF16), (40, 4, 300, 72, F32), (700, 8, 60, 512, BF16), (3000, 6, 60, 136, F32),
+                       (2000, 1, 7, 1032, BF16)):
+    g = gen(T)
+    idx, alpha = routing(g, T, k, E, 1.0, 0.2)
+    seg, pair, row, x_s = lrm.lrm_sort_tokens(idx, randn(g, T, H, dt=dt), E, dev_status=st)
+    out += [seg, pair, row, x_s, lrm.lrm_combine(row, alpha, x_s, dev_status=st)]
+    out += lrm.lrm_combine_backward(row, alpha, randn(g, T, H, dt=dt), x_s, dy_s=torch.zeros_like(x_s), dev_status=st)
+sizes = [(3, None, 72, 136), (8, 16, 72, 136), (300, None, 136, 264), (900, 7, 136, 264), (4096, None, 1024, 72),
+         (12000, 3, 128, 264), (200, 3, 72, 4096), (50, None, 72, 4096), (150, 2, 4104, 72)]
+for R, E, N, K in sizes:
+    for dt in (BF16, F32):
+        for simt in (0, 1):
+            g = gen(R)
+            seg = segments("short", R, E, g) if E else None
+            x, w, b, res = linear_inputs(g, dt, R, 2 * N, N, K, True, True, E)
+            y, z, dz = torch.zeros_like(res), randn(g, R, 2 * N, dt=dt), torch.zeros(R, 2 * N, dtype=dt, device="cuda")
+            lrm.lrm_linear(x, w, bias=b, residual=res, act="swiglu", seg_offsets=seg, y=y, flags=simt, dev_status=st)
+            _, db = lrm.lrm_act_backward(res, z, act="swiglu", seg_offsets=seg, dz=dz, dev_status=st)
+            dx = torch.zeros_like(x)
+            _, dw = lrm.lrm_linear_backward(dz, x, w, seg_offsets=seg, dx=dx, flags=simt, dev_status=st)
+            out += [y, dz, db, dx, dw]
+assert int(st.item()) == 0, int(st.item())
+torch.save([t.cpu() for t in out], sys.argv[2])
+"""
+
+
+def test_debug_build_checks_the_layer_and_matches_release(tmp_path):
+    """liblrm_debug.so runs every call of the layer with no index check failing, and gives the same bits."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    results = []
+    for debug, name in (("1", "liblrm_debug.so"), ("0", "liblrm.so")):
+        path = str(tmp_path / name) + ".pt"
+        r = subprocess.run([sys.executable, "-c", _EVERY_CALL, root, path, "/" + name],
+                           env=dict(os.environ, LRM_DEBUG=debug), capture_output=True, text=True, timeout=600)
+        assert r.returncode == 0, r.stdout + r.stderr
+        results.append(torch.load(path))
+    assert len(results[0]) == len(results[1]) > 100
+    for a, b in zip(*results):
+        assert torch.equal(a, b)

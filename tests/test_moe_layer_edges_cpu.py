@@ -86,3 +86,12 @@ def test_most_rows():
             assert lib.lrm_linear(P, P, P, None, None, R, E, 8, 8, NONE, 0, 0, P, None, P, BIG, 0, None, None) == SHAPE
             assert lib.lrm_linear_backward(P, P, P, P, R, E, 8, 8, 0, P, P, P, BIG, 0, None, None) == SHAPE
             assert lib.lrm_act_backward(P, P, P, R, E, 8, NONE, 0, P, P, P, BIG, None, None) == SHAPE
+
+
+def test_kernels_check_their_own_indices():
+    """Every source file of the layer's kernels that writes by an index of its own has checks for the debug build."""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    csrc = os.path.join(root, "pruned_expert_backward_gb300", "csrc")
+    for name in ("permute.cu", "act_backward.cu", "linear_rows.cu", "linear_simt.cu", "linear_tc.cu"):
+        assert "LRM_DCHECK(" in open(os.path.join(csrc, name)).read(), name

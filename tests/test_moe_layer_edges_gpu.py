@@ -62,8 +62,8 @@ def test_few_fp32_rows_take_no_planes(status):
         g = gen(R)
         seg = segments("ragged", R, E, g) if E else None
         x, w, b, res = linear_inputs(g, F32, R, 80, 40, 136, True, True, E)
-        y, z = lrm.lrm_linear(x, w, bias=b, residual=res, act="swiglu", seg_offsets=seg, save_z=True, ws=small, flags=simt,
-                              dev_status=status)
+        y, z = lrm.lrm_linear(x, w, bias=b, residual=res, act="swiglu", seg_offsets=seg, save_z=True, ws=small,
+                              flags=simt, dev_status=status)
         check_linear(x, w, b, res, "swiglu", seg, y, z)
     x, w = randn(gen(1), 200, 136, dt=F32), randn(gen(2), 80, 136, dt=F32)
     with pytest.raises(lrm.LrmError):  # the tiles need the planes
@@ -105,8 +105,8 @@ def test_sort_of_no_tokens_with_rows_given(status):
         for H in (8, 512, 4096):
             for dt in (0, 1):
                 seg = torch.full((E + 1,), 7, dtype=torch.int32, device="cuda")
-                st = lib.lrm_sort_tokens(p, p, 0, 2, E, H, dt, seg.data_ptr(), p, p, p, p, buf.numel(), status.data_ptr(),
-                                         stream)
+                st = lib.lrm_sort_tokens(p, p, 0, 2, E, H, dt, seg.data_ptr(), p, p, p, p, buf.numel(),
+                                         status.data_ptr(), stream)
                 assert st == 0 and torch.count_nonzero(seg) == 0
 
 
