@@ -95,3 +95,14 @@ def test_kernels_check_their_own_indices():
     csrc = os.path.join(root, "pruned_expert_backward_gb300", "csrc")
     for name in ("permute.cu", "act_backward.cu", "linear_rows.cu", "linear_simt.cu", "linear_tc.cu"):
         assert "LRM_DCHECK(" in open(os.path.join(csrc, name)).read(), name
+
+
+def test_scratch_size_of_a_type_that_is_not_supported():
+    """The binding refuses other types; it answered for fp32."""
+    import torch
+
+    import pruned_expert_backward_gb300 as lrm
+    assert lrm.lrm_linear_workspace_size(100, 4, 64, 64, "swiglu", torch.bfloat16) > 0
+    for dtype in (torch.float16, torch.float64, torch.int32):
+        with pytest.raises(TypeError):
+            lrm.lrm_linear_workspace_size(100, 4, 64, 64, "swiglu", dtype)
