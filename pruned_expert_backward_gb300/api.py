@@ -365,7 +365,8 @@ def lrm_combine(row_of_pair, alpha, y_s, residual=None, y=None, dev_status=None)
 
 def lrm_combine_backward(row_of_pair, alpha, dy, y_s, dy_s=None, dalpha=None, dev_status=None):
     """Gradient of lrm_combine: dy_s [rows,H] and dalpha fp32 [T,k].  y_s None: dy_s alone (it must then
-    be given, it fixes the row count)."""
+    be given, it fixes the row count).  Rows that no pair names are not written: uninitialised memory in a
+    dy_s made here."""
     T, k = alpha.shape
     H, dt, dev = dy.shape[1], dy.dtype, dy.device
     if y_s is None and dy_s is None:
@@ -430,7 +431,8 @@ def lrm_linear(x, w, bias=None, residual=None, act="none", seg_offsets=None, sav
     """y = act(x w^T + bias) + residual; act "none", "relu", "gelu", "silu" or "swiglu" (w: gate rows, then
     up rows).  x [R,K]; w [N',K] and bias [N'], or, with seg_offsets (rows sorted by expert), w [E,N',K] and
     bias [E,N'].  save_z also returns the pre-activation z [R,N'].  out_dtype torch.float32 gives an fp32 y
-    from bf16 inputs.  Returns (y, z or None)."""
+    from bf16 inputs.  Rows of no segment are not written: uninitialised memory in a y or z made here.
+    Returns (y, z or None)."""
     R, K = x.shape
     E, NP, Kw = _experts(w, seg_offsets, "w")
     code, dt, dev = _act_code(act), x.dtype, x.device
@@ -466,7 +468,8 @@ def lrm_linear(x, w, bias=None, residual=None, act="none", seg_offsets=None, sav
 def lrm_act_backward(dy, z, act="none", seg_offsets=None, bias_grad=True, dz=None, db=None, ws=None,
                      dev_status=None):
     """dz = dy * act'(z) [R,N'] and db fp32 [N'] ([E,N'] with seg_offsets), the column sums of dz, unless
-    bias_grad is False.  z may be None for act "none"."""
+    bias_grad is False.  z may be None for act "none".  Rows of no segment are not written: uninitialised
+    memory in a dz made here."""
     R, N = dy.shape
     code, dt, dev = _act_code(act), dy.dtype, dy.device
     NP = 2 * N if act == "swiglu" else N
@@ -498,7 +501,8 @@ def lrm_act_backward(dy, z, act="none", seg_offsets=None, bias_grad=True, dz=Non
 def lrm_linear_backward(dz, x, w, seg_offsets=None, need_dx=True, need_dw=True, dx=None, dw=None, ws=None,
                         flags=L.LRM_GEMM_DEFAULT, dev_status=None):
     """Gradients of lrm_linear's product from dz [R,N]: dx [R,K] = dz w and dw fp32 [N,K] = dz^T x ([E,N,K]
-    with seg_offsets).  Returns (dx or None, dw or None)."""
+    with seg_offsets).  Rows of no segment are not written: uninitialised memory in a dx made here.  Returns
+    (dx or None, dw or None)."""
     R, N = dz.shape
     E, Nw, K = _experts(w, seg_offsets, "w")
     dt, dev = dz.dtype, dz.device
