@@ -478,8 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t use = 0;
     bool ok = true;
     for (int i = 0, t; i < rounds && ok; ++i) {
-        t = nth_tile(i, pair, n_pairs);
-        if (t >= n_tiles) continue;  // (a last round may leave some pairs without one)
+      t = nth_tile(i, pair, n_pairs);
+      if (t >= n_tiles) continue;  // (a last round may leave some pairs without one)
       const Tile d = decode<KIND, BN, GLU>(p, prefix, t, rank);
       const int row_base = (KIND == DW ? d.m0 : d.row0) + q * 32;
       const int row_lim = KIND == DW ? p.M : d.row_end;
@@ -496,8 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_first = d.n0 + group * NO * 32;
       const TO* res =
           KIND == FWD && p.residual != nullptr && live ? static_cast<const TO*>(p.residual) + row * p.N : nullptr;
-      const int group = KIND == DW ? d.e : d.part;  // of the output
-      TO* y_row = static_cast<TO*>(p.y) + (group * (KIND == DW ? (int64_t)p.M : p.R) + row) * p.N;
+      const int out_group = KIND == DW ? d.e : d.part;
+      TO* y_row = static_cast<TO*>(p.y) + (out_group * (KIND == DW ? (int64_t)p.M : p.R) + row) * p.N;
 
       // the residual of chunk c (zeros past the last column)
       auto load_residual = [&](int c, uint4* r) {
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (res != nullptr) add_vectors<TO>(v, r);
         }
-        out.put(v, &tmY, lane, n, p.N, row_base, group, whole, live, y_row);
+        out.put(v, &tmY, lane, n, p.N, row_base, out_group, whole, live, y_row);
       };
 
       if (PROMOTE) {
