@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from helpers import ensure_built
-from test_moe_layer_gpu import BF16, EPS, F32, act64, check, check_linear, gen, linear_inputs, randn, segments
+from test_moe_layer_gpu import BF16, EPS, F32, act64, check, check_linear, gen, linear_inputs, randn, routing, segments
 
 pytestmark = pytest.mark.gpu
 
@@ -198,3 +198,31 @@ def test_long_bf16_sums_of_the_gradient(status):
         want += dz[:, i:i + 16384].double() @ w[i:i + 16384].double()
     dx, _ = lrm.lrm_linear_backward(dz, dz[:, :K].contiguous(), w, need_dw=False, dev_status=status)
     assert bias_of(dx, want) <= 6 * 2.0 ** -9 / 3 ** 0.5 / want.numel() ** 0.5 + 32 * EPS
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+def test_the_layer_allocates_nothing_after_the_first_call(dt):
+    """MoeLayer's calls make no tensor and the library takes no device memory, trained or served; tokens enough for
+    the sort to need its scratch.  Both give the same y."""
+    import pruned_expert_backward_gb300 as lrm
+    T, k, E, H, I = 2000, 8, 12, 136, 72
+    g = gen(5)
+    idx, alpha = routing(g, T, k, E, 1.0, 0.1)
+    x, dy = randn(g, T, H, dt=dt), randn(g, T, H, dt=dt)
+    wg, wd = randn(g, E, 2 * I, H, dt=dt, std=H ** -0.5), randn(g, E, H, I, dt=dt, std=I ** -0.5)
+    layer, served = lrm.MoeLayer(T, k, E, H, I, dtype=dt), lrm.MoeLayer(T, k, E, H, I, dtype=dt, train=False)
+
+    def step():
+        y = layer.forward(x, idx, alpha, wg, wd, residual=x)
+        layer.backward(dy, alpha, wg, wd)
+        return y, served.forward(x, idx, alpha, wg, wd, residual=x)
+
+    step()
+    torch.cuda.synchronize()
+    made, free = torch.cuda.memory_stats()["allocation.all.allocated"], torch.cuda.mem_get_info()[0]
+    y, y_served = step()
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == made
+    assert torch.cuda.mem_get_info()[0] >= free
+    assert torch.equal(y, y_served)
+    assert int(layer.dev_status.item()) == 0 and int(served.dev_status.item()) == 0
