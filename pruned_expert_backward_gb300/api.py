@@ -27,16 +27,12 @@ def _ok(code: int, where: str):
         raise LrmError(code, where)
 
 
-def _code(dtype: torch.dtype) -> int:
-    if dtype == torch.bfloat16:
-        return L.LRM_BF16
-    if dtype == torch.float32:
-        return L.LRM_F32
-    raise TypeError(f"unsupported dtype {dtype}: bf16 or fp32")
-
-
 def _dt(t: torch.Tensor) -> int:
-    return _code(t.dtype)
+    if t.dtype == torch.bfloat16:
+        return L.LRM_BF16
+    if t.dtype == torch.float32:
+        return L.LRM_F32
+    raise TypeError(f"unsupported dtype {t.dtype}: bf16 or fp32")
 
 
 def _cuda(t: torch.Tensor, name: str, dtype=None) -> int:
@@ -420,8 +416,11 @@ def lrm_linear_workspace_size(R: int, E: int, N: int, K: int, act: str, dtype: t
                               uses: int = L.LRM_LINEAR_USE_ALL) -> int:
     """Scratch bytes of lrm_linear, lrm_act_backward and lrm_linear_backward (N: columns of y), or of those
     in `uses` (LRM_LINEAR_USE_* or-ed)."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {dtype}: bf16 or fp32")
     out = C.c_size_t(0)
-    _ok(L.load().lrm_linear_workspace_size_for(uses, R, E, N, K, _act_code(act), _code(dtype), C.byref(out)),
+    dt = L.LRM_BF16 if dtype == torch.bfloat16 else L.LRM_F32
+    _ok(L.load().lrm_linear_workspace_size_for(uses, R, E, N, K, _act_code(act), dt, C.byref(out)),
         "lrm_linear_workspace_size")
     return int(out.value)
 
