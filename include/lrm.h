@@ -416,7 +416,8 @@ lrm_status lrm_linear_workspace_size(int64_t R, int32_t E, int32_t N, int32_t K,
  * dt LRM_BF16 or LRM_F32; out_dt is the type of y: dt, or LRM_F32 from bf16 inputs (a router's logits;
  * no residual then).  Sums, bias, activation and residual are in fp32, each output is rounded once.  The tensor
  * core truncates as it adds: sums for fp32 results err by about 5e-7 of the sum of |products|, those for bf16
- * results, before their rounding, by at most 4e-4 (65536 products of one sign; 6e-6 for 2048).  An
+ * results, before their rounding, by at most 4e-4 (65536 products of one sign; 6e-6 for 2048).  Exponentials
+ * of activations and their gradients err by 2 + 1.2 |z| units of 2^-23 of their value, in either type.  An
  * infinity or NaN in x spoils the outputs of its own row only (as NaN where fp32 inputs are split).
  * Rows >= seg_offsets[E] are not written.  N and K are multiples of 8, up to 2^24; R <= INT32_MAX - 1023.
  * ws: scratch of at least lrm_linear_workspace_size_for(LRM_LINEAR_USE_FORWARD, ...) bytes for fp32 inputs (256

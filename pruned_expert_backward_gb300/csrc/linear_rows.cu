@@ -13,9 +13,10 @@
 // their use, 4 rows x (1408+1408) x 4096 took 12.9 us, not 6.7).  x is read by every CTA through L2, R / 16
 // of W's bytes, which bounds the rows this form is used for.
 // With segments a CTA first lists the experts that have rows (at most R), then takes their column blocks in
-// turn, two CTAs per SM: one CTA for every block of every expert spent 29 us on 8 rows over 128 experts,
-// mostly starting CTAs with nothing to do, where this takes 13 us.
-// GB300, bf16 8 rows: 4096 x 4096 8.7 us, (768+768) x 2048 3.8 us; fp32 8 rows x 4096 x 4096 22 us.
+// turn, two CTAs per SM: one CTA for every block of every expert spent 29 us on a token's 8 rows over 8 of 128
+// experts of (768+768) x 2048, mostly starting CTAs with nothing to do, where this takes 13 us (50 MB of weights: 7.4
+// us at the copy rate).
+// GB300, bf16 8 rows: 4096 x 4096 8.4 us, (768+768) x 2048 3.8 us; fp32 8 rows x 4096 x 4096 23 us, 24 rows 57 us.
 #include "kernels.h"
 #include "linear.cuh"
 #include "tc_host.h"
