@@ -1,7 +1,7 @@
 """Cases of the layer's operators in 8 bits and of its optimiser, for timing and comparison.
 
 Four calls, with the values in e4m3 (torch.float8_e4m3fn) and fp32 scales:
-  rows     lrm_fp8_quantize: rows in 8 bits with a scale for each row's 128 columns, gathered by expert or not
+  rows     lrm_fp8_quantize: rows in 8 bits with a scale for each 128 columns of a row, sorted by expert or not
   weights  lrm_fp8_quantize_weight: a scale for each block of 128 x 128
   product  lrm_fp8_linear: the product of the two with bias, activation and residual, dense or per expert
   dx       lrm_fp8_linear_backward: the gradient of its rows from the same 8-bit weights
@@ -179,13 +179,16 @@ def prepare(case, seed):
     types = {"bf16": torch.bfloat16, "f32": torch.float32}
     if op == "rows":
         T, k, E, K = c["T"], c["k"], c["E"], c["K"]
-        s["x"], s["pair"] = randn(T, K, dtype=types[c["dtype"]]), None
+        s["x"], s["row"], s["q"], s["scale"] = randn(T, K, dtype=types[c["dtype"]]), None, None, None
         if k:
             e = _route(gen, T, k, E, 1.0)
             drop = torch.rand(T * k, generator=gen, device="cuda") < c["masked"]
             order = torch.sort(torch.where(drop, torch.full_like(e, E), e), stable=True).indices
-            routed = torch.arange(T * k, device="cuda") < (~drop).sum()
-            s["pair"] = torch.where(routed, order, torch.full_like(order, -1)).to(torch.int32)
+            row = torch.empty_like(order).scatter_(0, order, torch.arange(T * k, device="cuda"))
+            s["row"] = torch.where(drop, torch.full_like(row, -1), row).to(torch.int32)
+            # the layer's buffers: rows of no pair stay as they are
+            s["q"] = torch.zeros(T * k, K, device="cuda").to(FP8)
+            s["scale"] = torch.ones(T * k, -(-K // BLOCK), device="cuda")
     elif op == "weights":
         rows = c["N"] * (2 if c["glu"] else 1)
         s["w"] = randn(c["E"], rows, c["K"], std=c["K"] ** -0.5, dtype=types[c["dtype"]])
@@ -329,11 +332,12 @@ def _plain_adamw(s):
 def _plain(s):
     c, op = s["case"], s["case"]["op"]
     if op == "rows":
-        x = s["x"]
-        if s["pair"] is not None:
-            p = s["pair"].long()
-            x = torch.where((p >= 0)[:, None], x[p.clamp_min(0) // c["k"]], torch.zeros((), dtype=x.dtype, device="cuda"))
-        q, scale = _quantize(x, 1)
+        q, scale = _quantize(s["x"], 1)
+        if s["row"] is not None:
+            pair = torch.nonzero(s["row"] >= 0).flatten()
+            row, token = s["row"][pair].long(), pair // c["k"]
+            s["q"].view(torch.uint8)[row], s["scale"][row] = q.view(torch.uint8)[token], scale[token]
+            q, scale = s["q"], s["scale"]
         return {"q": q, "scale": scale}
     if op == "weights":
         q, scale = _quantize(_halves(s["w"], c["glu"]), BLOCK)
@@ -367,7 +371,8 @@ def _own(s):
     import pruned_expert_backward_gb300 as lrm
     c, op, st = s["case"], s["case"]["op"], s["status"]
     if op == "rows":
-        q, scale = lrm.lrm_fp8_quantize(s["x"], pair_of_row=s["pair"], k=c["k"] or 1, dev_status=st)
+        q, scale = lrm.lrm_fp8_quantize(s["x"], row_of_pair=s["row"], k=c["k"] or 1, q=s["q"], scale=s["scale"],
+                                        dev_status=st)
         return {"q": q, "scale": scale}
     if op == "weights":
         q, scale = lrm.lrm_fp8_quantize_weight(s["w"], glu=c["glu"])
@@ -413,7 +418,9 @@ def work(case):
     if op == "rows":
         T, K = c["T"], c["K"]
         R = T * max(c["k"], 1)
-        return {"bytes": T * K * size[c["dtype"]] + (4 * R if c["k"] else 0) + R * (K + 4 * -(-K // BLOCK)), "flops": R * K}
+        rows = R * (1 - c["masked"])  # that a pair names
+        read = T * K * size[c["dtype"]] + (4 * R if c["k"] else 0)
+        return {"bytes": read + rows * (K + 4 * -(-K // BLOCK)), "flops": T * K}
     if op == "weights":
         n = c["E"] * c["N"] * (2 if c["glu"] else 1) * c["K"]
         return {"bytes": n * (size[c["dtype"]] + 1) + n // 4096, "flops": n}
@@ -471,14 +478,15 @@ def exact(case, seed):
     s = prepare(case, seed)
     c, op = case, case["op"]
     if op == "rows":
-        x = s["x"]
-        if s["pair"] is not None:
-            rows = torch.zeros(c["T"] * c["k"], c["K"], dtype=x.dtype, device="cuda")
-            live = torch.nonzero(s["pair"] >= 0).flatten()
-            rows[live] = x[s["pair"][live].long().div(c["k"], rounding_mode="floor")]
-            x = rows
-        q, scale = _f64_blocks(x, 1)
-        return {"q": q, "scale": scale}
+        q, scale = _f64_blocks(s["x"], 1)
+        if s["row"] is None:
+            return {"q": q, "scale": scale}
+        row = s["row"].view(c["T"], c["k"]).long()
+        q_s, scale_s = s["q"].double(), s["scale"].double()
+        for j in range(c["k"]):
+            t = torch.nonzero(row[:, j] >= 0).flatten()
+            q_s[row[t, j]], scale_s[row[t, j]] = q[t], scale[t]
+        return {"q": q_s, "scale": scale_s}
     if op == "weights":
         parts = [_f64_blocks(half, BLOCK) for w in s["w"] for half in (w.chunk(2) if c["glu"] else (w,))]
         q = torch.stack([p[0] for p in parts]).view(s["w"].shape)
