@@ -452,6 +452,63 @@ lrm_status lrm_linear_backward(const int32_t* seg_offsets, const void* dz, const
                                int32_t E, int32_t N, int32_t K, lrm_dtype dt, void* dx, float* dw, void* ws,
                                size_t ws_bytes, int32_t flags, int32_t* dev_status, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The layer in 8 bits: e4m3 values with an fp32 scale for each block of 128, dense or per expert.
+ * The pages do not go below 16 bits; these calls stand beside lrm_linear and lrm_linear_backward for
+ * weights that are kept, served or trained in 8 bits.  K, and N where it is a row's length, are multiples
+ * of 16 (rows start on 16 bytes).  Blocks: nk = ceil(K / 128) of a row, nn = ceil(N / 128) rows of them in a
+ * weight; the last of each may be shorter.  A SwiGLU weight holds N gate rows, then N up rows: its halves are
+ * two matrices of N rows, and each has blocks of its own.
+ *   top = max(largest magnitude of the block, 2^-100),  scale = top / 448,  q = e4m3(x * (448 / top))
+ * in fp32, each step rounded to nearest (ties to even); the value is q * scale.  An infinity or a NaN makes its
+ * whole block NaN.
+ * ------------------------------------------------------------------------------------------- */
+
+/*
+ * Rows in 8 bits, in place (row_of_pair NULL, k = 1: row t to row t), or each token's row to the rows of its pairs in
+ * the sorted batch (lrm_sort_tokens without x, then this, in place of the rows it would copy).
+ *   x [T,K] dt, row_of_pair [T*k] int32 or NULL  ->  q [cap,K] e4m3, scale [cap,nk] fp32
+ * A row outside [-1, cap) is not followed and sets LRM_ERR_BAD_INDEX.  Rows that no pair names are not written.
+ * Without row_of_pair cap >= T.  For a gradient of SwiGLU's columns [R,2N] call it on 2R rows of N columns.
+ * Errors: LRM_ERR_INVALID_ARG, LRM_ERR_SHAPE, LRM_ERR_DTYPE, LRM_ERR_CUDA.
+ */
+lrm_status lrm_fp8_quantize(const void* x, const int32_t* row_of_pair, int64_t T, int32_t k, int32_t K, lrm_dtype dt,
+                            int64_t cap, void* q, float* scale, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Weights in 8 bits, G matrices of N rows (E, or 2E for SwiGLU weights, whose halves are two matrices each):
+ *   w [G,N,K] dt  ->  q [G,N,K] e4m3, scale [G,nn,nk] fp32, one for each block of 128 x 128.
+ * Errors as for lrm_fp8_quantize; LRM_ERR_SHAPE also beyond INT32_MAX blocks.
+ */
+lrm_status lrm_fp8_quantize_weight(const void* w, int32_t G, int32_t N, int32_t K, lrm_dtype dt, void* q, float* scale,
+                                   cudaStream_t stream);
+
+/*
+ * lrm_linear from 8-bit operands, bf16 out:
+ *   z = sum over blocks b of x_scale[r,b] w_scale[n/128,b] (sum over the block's k of x[r,k] w[n,k]) + bias
+ *   y = act(z) + residual
+ *   x [R,K] e4m3, x_scale [R,nk], w [E,N',K] e4m3, w_scale [E,N'/N * nn,nk] (halves one after the other),
+ *   bias [E,N'] bf16 or NULL, residual [R,N] bf16 or NULL  ->  y [R,N] bf16, z [R,N'] bf16 or NULL
+ * N' = 2N for SwiGLU, else N; N a multiple of 8.  Segments, activations, limits and rows that are not written as
+ * for lrm_linear.  The 128 products of a block are summed by the tensor core, the blocks in fp32; bias,
+ * activation and residual are in fp32 and each output is rounded once.  Needs no scratch.
+ * A NaN in x spoils its own row's outputs, one in w its own column's.
+ */
+lrm_status lrm_fp8_linear(const int32_t* seg_offsets, const void* x, const float* x_scale, const void* w,
+                          const float* w_scale, const void* bias, const void* residual, int64_t R, int32_t E, int32_t N,
+                          int32_t K, lrm_act act, void* y, void* z, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Gradient of lrm_fp8_linear's rows from dz in 8 bits and the same weights, bf16 out:
+ *   dx[r,k] = sum over blocks b of dz_scale[r,b] w_scale[b,k/128] (sum over the block's n of dz[r,n] w[n,k])
+ *   dz [R,N'] e4m3, dz_scale [R,N'/N * nn] (SwiGLU: lrm_fp8_quantize on 2R rows of N columns), w and w_scale as in
+ *   lrm_fp8_linear  ->  dx [R,K] bf16.  glu: 1 for SwiGLU weights (N' = 2N), else 0.  N a multiple of 16.
+ * The weights' gradient is lrm_linear_backward's, from the bf16 rows.  Rows >= seg_offsets[E] are not written.
+ */
+lrm_status lrm_fp8_linear_backward(const int32_t* seg_offsets, const void* dz, const float* dz_scale, const void* w,
+                                   const float* w_scale, int64_t R, int32_t E, int32_t N, int32_t K, int32_t glu,
+                                   void* dx, int32_t* dev_status, cudaStream_t stream);
+
 /*
  * Self-test of failure detection (no counterpart in the pages; part of this library's fault
  * handling).  The tensor-core kernels bound every wait on an mbarrier (about one second of

@@ -56,6 +56,10 @@ SIGNATURES = {
                              _i32, _p, _p]),
     "lrm_act_backward": (C.c_int, [_p, _p, _p, _i64, _i32, _i32, C.c_int, C.c_int, _p, _p, _p, _sz, _p, _p]),
     "lrm_linear_backward": (C.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, _i32, C.c_int, _p, _p, _p, _sz, _i32, _p, _p]),
+    "lrm_fp8_quantize": (C.c_int, [_p, _p, _i64, _i32, _i32, C.c_int, _i64, _p, _p, _p, _p]),
+    "lrm_fp8_quantize_weight": (C.c_int, [_p, _i32, _i32, _i32, C.c_int, _p, _p, _p]),
+    "lrm_fp8_linear": (C.c_int, [_p, _p, _p, _p, _p, _p, _p, _i64, _i32, _i32, _i32, C.c_int, _p, _p, _p, _p]),
+    "lrm_fp8_linear_backward": (C.c_int, [_p, _p, _p, _p, _p, _i64, _i32, _i32, _i32, _i32, _p, _p, _p]),
     "lrm_score_mode": (C.c_int, [_p, _p, _p, _i64, _i32, _i32, _i32, C.c_int, C.c_int, _p, _p, _p]),
 }
 

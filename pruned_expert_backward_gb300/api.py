@@ -520,6 +520,113 @@ def lrm_linear_backward(dz, x, w, seg_offsets=None, need_dx=True, need_dw=True, 
     return dx, dw
 
 
+FP8 = torch.float8_e4m3fn
+_QBLOCK = 128  # columns of a row, or rows and columns of a weight, that share a scale
+
+
+def _qblocks(n: int) -> int:
+    return -(-n // _QBLOCK)
+
+
+def lrm_fp8_quantize(x, row_of_pair=None, k=1, glu=False, q=None, scale=None, dev_status=None):
+    """Rows in 8 bits: q e4m3 and scale fp32, one for each 128 columns of a row.  x [T,K] bf16 or fp32.
+    With row_of_pair int32 [T*k] (lrm_sort_tokens without x) each token's row goes to the rows of its k pairs: q
+    [rows,K] (default T*k rows).  Rows that no pair names are not written: uninitialised memory in a q or scale made
+    here.  glu: x holds SwiGLU's gate columns, then the up columns, and each half has blocks of its own.
+    Returns (q [rows,K], scale [rows, blocks])."""
+    T, K = x.shape
+    x_p, dt, dev = _cuda(x, "x"), _dt(x), x.device
+    cols, per = K, 1
+    if glu:
+        if row_of_pair is not None or K % 2:
+            raise ValueError("glu is for a gradient [R,2N] in place")
+        cols, per = K // 2, 2
+    if row_of_pair is not None and row_of_pair.numel() != T * k:
+        raise ValueError(f"row_of_pair must hold T*k = {T * k} rows, got {row_of_pair.numel()}")
+    if row_of_pair is None and k != 1:
+        raise ValueError(f"k = {k} needs row_of_pair")
+    rows = q.shape[0] if q is not None else scale.shape[0] if scale is not None else T * k
+    if row_of_pair is None and rows != T:
+        raise ValueError(f"q and scale must have x's {T} rows")
+    q, q_p = _out(q, (rows, K), FP8, dev, "q")
+    scale, s_p = _out(scale, (rows, per * _qblocks(cols)), torch.float32, dev, "scale")
+    _ok(L.load().lrm_fp8_quantize(x_p, _opt(row_of_pair, "row_of_pair", torch.int32), T * per, k, cols, dt, rows * per,
+                                  q_p, s_p, _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_fp8_quantize")
+    return q, scale
+
+
+def lrm_fp8_quantize_weight(w, glu=False, q=None, scale=None):
+    """Weights in 8 bits with a scale for each block of 128 x 128: w [N',K] or [E,N',K], bf16 or fp32.  glu: N'
+    holds the gate rows, then the up rows, and each half has blocks of its own.  Returns (q like w, scale
+    [blocks of rows, blocks of columns], or [E, ...])."""
+    if w.dim() not in (2, 3):
+        raise ValueError(f"w must be [N,K] or [E,N,K], got {list(w.shape)}")
+    E, N, K = w.shape if w.dim() == 3 else (1, *w.shape)
+    w_p, dt, per = _cuda(w, "w"), _dt(w), 2 if glu else 1
+    if N % per:
+        raise ValueError(f"w has {N} rows: gate and up rows in equal number expected")
+    q, q_p = _out(q, tuple(w.shape), FP8, w.device, "q")
+    scale, s_p = _out(scale, (*w.shape[:-2], per * _qblocks(N // per), _qblocks(K)), torch.float32, w.device, "scale")
+    _ok(L.load().lrm_fp8_quantize_weight(w_p, E * per, N // per, K, dt, q_p, s_p, _stream()), "lrm_fp8_quantize_weight")
+    return q, scale
+
+
+def _fp8_weight(w, w_scale, per, seg_offsets):
+    """(E, rows, columns) of an 8-bit weight whose scales have been checked."""
+    E, NP, K = _experts(w, seg_offsets, "w")
+    if NP % per:
+        raise ValueError(f"w has {NP} rows: gate and up rows in equal number expected")
+    _same(w_scale, (*w.shape[:-2], per * _qblocks(NP // per), _qblocks(K)), "w_scale")
+    return E, NP, K
+
+
+def lrm_fp8_linear(x, x_scale, w, w_scale, bias=None, residual=None, act="none", seg_offsets=None, save_z=False, y=None,
+                   z=None, dev_status=None):
+    """lrm_linear from 8-bit rows (lrm_fp8_quantize) and weights (lrm_fp8_quantize_weight): y = act(x w^T + bias) +
+    residual in bf16.  x [R,K], x_scale [R,blocks]; w [N',K] and bias bf16 [N'], or, with seg_offsets (rows sorted by
+    expert), w [E,N',K] and bias [E,N'].  save_z also returns the pre-activation z [R,N'].  Rows of no segment are
+    not written: uninitialised memory in a y or z made here.  Returns (y, z or None)."""
+    R, K = x.shape
+    code, dev, b16 = _act_code(act), x.device, torch.bfloat16
+    per = 2 if act == "swiglu" else 1
+    x_p = _cuda(x, "x", FP8)
+    E, NP, Kw = _fp8_weight(w, w_scale, per, seg_offsets)
+    N = NP // per
+    if Kw != K:
+        raise ValueError(f"x has {K} columns, w {Kw}")
+    _same(x_scale, (R, _qblocks(K)), "x_scale")
+    if bias is not None and bias.numel() != E * NP:
+        raise ValueError(f"bias must hold {E * NP} values, got {bias.numel()}")
+    y, y_p = _out(y, (R, N), b16, dev, "y")
+    z_p = None
+    if save_z or z is not None:
+        z, z_p = _out(z, (R, NP), b16, dev, "z")
+    _same(residual, (R, N), "residual")
+    _ok(L.load().lrm_fp8_linear(_opt(seg_offsets, "seg_offsets", torch.int32), x_p, _cuda(x_scale, "x_scale", torch.float32),
+                                _cuda(w, "w", FP8), _cuda(w_scale, "w_scale", torch.float32), _opt(bias, "bias", b16),
+                                _opt(residual, "residual", b16), R, E, N, K, code, y_p, z_p,
+                                _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_fp8_linear")
+    return y, z
+
+
+def lrm_fp8_linear_backward(dz, dz_scale, w, w_scale, glu=False, seg_offsets=None, dx=None, dev_status=None):
+    """Gradient of lrm_fp8_linear's rows, dx [R,K] bf16 = dz w, from dz in 8 bits (lrm_fp8_quantize; glu=True for
+    SwiGLU's columns) and the forward's weights.  The weights' gradient is lrm_linear_backward's, from the bf16
+    rows.  Rows of no segment are not written: uninitialised memory in a dx made here."""
+    R, NP = dz.shape
+    per = 2 if glu else 1
+    E, Nw, K = _fp8_weight(w, w_scale, per, seg_offsets)
+    if Nw != NP:
+        raise ValueError(f"dz has {NP} columns, w {Nw} rows")
+    _same(dz_scale, (R, per * _qblocks(NP // per)), "dz_scale")
+    dx, dx_p = _out(dx, (R, K), torch.bfloat16, dz.device, "dx")
+    _ok(L.load().lrm_fp8_linear_backward(
+        _opt(seg_offsets, "seg_offsets", torch.int32), _cuda(dz, "dz", FP8), _cuda(dz_scale, "dz_scale", torch.float32),
+        _cuda(w, "w", FP8), _cuda(w_scale, "w_scale", torch.float32), R, E, NP // per, K, per - 1, dx_p,
+        _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_fp8_linear_backward")
+    return dx
+
+
 class PrunedBackward:
     """The whole pruned expert backward for one fixed problem size, with every buffer
     allocated once (device memory from torch).  `run` queues score -> select -> compact ->

@@ -39,6 +39,12 @@ lrm_status check_linear(int64_t R, int32_t E, int32_t N, int32_t K, lrm_act act,
   return check_dt(dt);
 }
 
+// The length of a row of 8-bit values.
+lrm_status check_fp8_width(int32_t K) {
+  if (K < 1) return LRM_ERR_INVALID_ARG;
+  return K % 16 != 0 || K > (1 << 24) ? LRM_ERR_SHAPE : LRM_OK;
+}
+
 // Scratch of lrm_sort_tokens: the counts of each chunk of pairs and the buckets' sizes.
 struct SortWs {
   size_t counts, loads, total;
@@ -597,6 +603,71 @@ lrm_status lrm_linear_backward(const int32_t* seg_offsets, const void* dz, const
   if (flags == LRM_GEMM_DEFAULT) return launch_linear_backward_tc(a, dt, ws, stream);
   launch_linear_backward_simt(a, dt, stream);
   return after_launch();
+}
+
+lrm_status lrm_fp8_quantize(const void* x, const int32_t* row_of_pair, int64_t T, int32_t k, int32_t K, lrm_dtype dt,
+                            int64_t cap, void* q, float* scale, int32_t* dev_status, cudaStream_t stream) {
+  LRM_NVTX_RANGE();
+  lrm_status st = check_dims(T, k, 1, 8, 8);
+  if (st) return st;
+  if ((st = check_fp8_width(K))) return st;
+  if ((st = check_dt(dt))) return st;
+  if (cap < 0 || cap > INT32_MAX || (!row_of_pair && (k != 1 || cap < T))) return LRM_ERR_INVALID_ARG;
+  if (T > 0 && (!x || (cap > 0 && (!q || !scale)))) return LRM_ERR_INVALID_ARG;
+  if (!al16(x) || !al16(q) || !al4(scale) || !al4(row_of_pair)) return LRM_ERR_INVALID_ARG;
+  if (T == 0 || (cap == 0 && !row_of_pair)) return LRM_OK;
+  launch_fp8_quantize(x, row_of_pair, T, k, K, dt, cap, q, scale, dev_status, stream);
+  return after_launch();
+}
+
+lrm_status lrm_fp8_quantize_weight(const void* w, int32_t G, int32_t N, int32_t K, lrm_dtype dt, void* q, float* scale,
+                                   cudaStream_t stream) {
+  LRM_NVTX_RANGE();
+  lrm_status st;
+  if (G < 1 || N < 1) return LRM_ERR_INVALID_ARG;
+  if ((st = check_fp8_width(K))) return st;
+  if ((st = check_dt(dt))) return st;
+  if (G > 2 * LRM_MAX_EXPERTS || N > (1 << 24)) return LRM_ERR_SHAPE;
+  if ((int64_t)G * ((N + 127) / 128) > INT32_MAX / ((K + 127) / 128)) return LRM_ERR_SHAPE;
+  if (!w || !q || !scale || !al16(w) || !al16(q) || !al4(scale)) return LRM_ERR_INVALID_ARG;
+  launch_fp8_quantize_weight(w, G, N, K, dt, q, scale, stream);
+  return after_launch();
+}
+
+lrm_status lrm_fp8_linear(const int32_t* seg_offsets, const void* x, const float* x_scale, const void* w,
+                          const float* w_scale, const void* bias, const void* residual, int64_t R, int32_t E, int32_t N,
+                          int32_t K, lrm_act act, void* y, void* z, int32_t* dev_status, cudaStream_t stream) {
+  LRM_NVTX_RANGE();
+  lrm_status st = check_linear(R, E, N, K, act, LRM_BF16);
+  if (st) return st;
+  if ((st = check_fp8_width(K))) return st;
+  if (!w || !w_scale || (!seg_offsets && E != 1)) return LRM_ERR_INVALID_ARG;
+  if (R > 0 && (!x || !x_scale || !y)) return LRM_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, w, bias, residual, y, z};
+  for (const void* p : ptrs)
+    if (!al16(p)) return LRM_ERR_INVALID_ARG;
+  if (!al4(seg_offsets) || !al4(x_scale) || !al4(w_scale)) return LRM_ERR_INVALID_ARG;
+  if (R == 0) return LRM_OK;
+  const Fp8Args a{seg_offsets, x, x_scale, w, w_scale, bias, residual, R, E, N, K, act, y, z, dev_status};
+  if (!fp8_few_rows(R, E, seg_offsets != nullptr)) return launch_fp8_tc(a, stream);
+  launch_fp8_rows(a, stream);
+  return after_launch();
+}
+
+lrm_status lrm_fp8_linear_backward(const int32_t* seg_offsets, const void* dz, const float* dz_scale, const void* w,
+                                   const float* w_scale, int64_t R, int32_t E, int32_t N, int32_t K, int32_t glu,
+                                   void* dx, int32_t* dev_status, cudaStream_t stream) {
+  LRM_NVTX_RANGE();
+  lrm_status st = check_linear(R, E, N, K, LRM_ACT_NONE, LRM_BF16);
+  if (st) return st;
+  if ((st = check_fp8_width(K)) || (st = check_fp8_width(N))) return st;
+  if (glu != 0 && glu != 1) return LRM_ERR_INVALID_ARG;
+  if (!w || !w_scale || (!seg_offsets && E != 1)) return LRM_ERR_INVALID_ARG;
+  if (R > 0 && (!dz || !dz_scale || !dx)) return LRM_ERR_INVALID_ARG;
+  if (!al16(dz) || !al16(w) || !al16(dx)) return LRM_ERR_INVALID_ARG;
+  if (!al4(seg_offsets) || !al4(dz_scale) || !al4(w_scale)) return LRM_ERR_INVALID_ARG;
+  if (R == 0) return LRM_OK;
+  return launch_fp8_dx(Fp8GradArgs{seg_offsets, dz, dz_scale, w, w_scale, R, E, N, K, glu != 0, dx, dev_status}, stream);
 }
 
 lrm_status lrm_selftest_wait_timeout(int32_t* dev_status, int64_t limit_ns, cudaStream_t stream) {

@@ -197,4 +197,43 @@ struct ActGradArgs {
 size_t act_backward_part_rows(int64_t R, int32_t E);
 void launch_act_backward(const ActGradArgs& a, lrm_dtype dt, cudaStream_t s);
 
+// The operators in 8 bits: e4m3 values with a scale for each block of 128.
+void launch_fp8_quantize(const void* x, const int32_t* row_of_pair, int64_t T, int32_t k, int32_t K, lrm_dtype dt,
+                         int64_t cap, void* q, float* scale, int32_t* status, cudaStream_t s);
+void launch_fp8_quantize_weight(const void* w, int32_t G, int32_t N, int32_t K, lrm_dtype dt, void* q, float* scale,
+                                cudaStream_t s);
+struct Fp8Args {
+  const int32_t* seg_offsets;  // NULL for one dense product (E = 1)
+  const void* x;
+  const float* x_scale;
+  const void* w;
+  const float* w_scale;
+  const void *bias, *residual;  // optional
+  int64_t R;
+  int32_t E, N, K;  // N: columns of y (w has 2N rows per expert for SwiGLU)
+  lrm_act act;
+  void *y, *z;  // z optional: the pre-activation
+  int32_t* status;
+};
+// Whether one pass over the weights by plain loads takes a product of so few rows, not the tensor cores' tiles.
+inline bool fp8_few_rows(int64_t R, int32_t E, bool grouped) {
+  (void)E;
+  return R <= (grouped ? 64 : 32);
+}
+void launch_fp8_rows(const Fp8Args& a, cudaStream_t s);
+lrm_status launch_fp8_tc(const Fp8Args& a, cudaStream_t s);
+struct Fp8GradArgs {
+  const int32_t* seg_offsets;
+  const void* dz;
+  const float* dz_scale;
+  const void* w;
+  const float* w_scale;
+  int64_t R;
+  int32_t E, N, K;  // N: columns of one half of dz with SwiGLU weights, else of dz
+  bool glu;
+  void* dx;
+  int32_t* status;
+};
+lrm_status launch_fp8_dx(const Fp8GradArgs& a, cudaStream_t s);
+
 }  // namespace lrm

@@ -19,13 +19,13 @@
 // GB300, bf16 8 rows: 4096 x 4096 8.4 us, (768+768) x 2048 3.8 us; fp32 8 rows x 4096 x 4096 23 us, 24 rows 57 us.
 #include "kernels.h"
 #include "linear.cuh"
+#include "rows_list.cuh"
 #include "tc_host.h"
 
 namespace lrm {
 
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kStep = 32;  // K of a warp's step
 
 __device__ __forceinline__ void mma_16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -156,45 +156,6 @@ __device__ __forceinline__ void warp_products(const float* w0, const float* w1, 
       c[h][r] += __shfl_xor_sync(0xffffffffu, c[h][r], 2);
       if (t == 0) out[g + 8 * h][r] = c[h][r];
     }
-}
-
-// The experts that have rows, listed in shared memory by the whole block;
-// returns their number, 0 when the segments are not valid.
-struct Rows {
-  int e, begin, end;
-};
-__device__ __forceinline__ int list_experts(const int32_t* seg, int E, int64_t R, Rows* list, int32_t* status) {
-  __shared__ int s_count[kWarps];
-  __shared__ int s_total;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (E + 32 * kWarps - 1) / (32 * kWarps), e0 = threadIdx.x * per, e1 = min(E, e0 + per);
-  int ok = 1, count = 0;
-  for (int e = e0; e < e1; ++e) {
-    const int a = seg[e], b = seg[e + 1];
-    ok &= a <= b ? 1 : 0;
-    count += a < b ? 1 : 0;
-  }
-  if (threadIdx.x == 0) ok &= seg[0] == 0 && (int64_t)seg[E] <= R ? 1 : 0;
-  int incl = count;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) s_count[warp] = incl;
-  if (!__syncthreads_and(ok)) {
-    if (threadIdx.x == 0) set_status(status, LRM_ERR_BAD_SEGMENTS);
-    return 0;
-  }
-  int at = incl - count;
-  for (int w = 0; w < warp; ++w) at += s_count[w];
-  for (int e = e0; e < e1 && count > 0; ++e) {
-    const int a = seg[e], b = seg[e + 1];
-    if (a < b) list[at++] = Rows{e, a, b};
-  }
-  if (threadIdx.x == blockDim.x - 1) s_total = at;
-  __syncthreads();
-  return s_total;
 }
 
 template <typename TI, typename TO, bool GLU, int NT>
