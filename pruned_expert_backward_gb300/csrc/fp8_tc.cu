@@ -6,12 +6,12 @@
 // The scales change with every 128 steps of the reduction, so the products of a block are a sum of their own: each K
 // slice of 128 (one stage of operands, four MMAs of K = 32) goes to the next of the accumulators that TMEM holds, and
 // the epilogue warps take it out, scale it by row and block and add it up in fp32 registers while the tensor core is
-// at the next.  A slice's products are exact to fp32's last bits, so the result errs like a sum of K / 128 fp32 numbers.
+// at the next.
 //
-// CTA pairs, roles and tiles are those of linear_tc.cu: 256 x BN tiles over a persistent grid, warp 0 the TMA
-// producer, warp 1 of the leader the MMA issuer.  BN / 16 epilogue warps each hold a 32-row quarter of TMEM by 64
-// columns (64 registers of sums); SwiGLU: 32 gate columns and the 32 up columns that go with them.  They lie within
-// one block of 128 columns, so that a warp has one weight scale a slice (two for SwiGLU).
+// CTA pairs and tiles are those of linear_tc.cu: 256 x BN tiles over a persistent grid.  Warp 0 issues the TMA loads,
+// warp 1 of the leader the MMAs, warps 2 and 3 bring the scales to shared memory, the rest are the epilogue: each has a
+// 32-row quarter of TMEM by 64 columns (SwiGLU: 32 gate columns and the 32 up columns that go with them), which lie in
+// one block of 128 columns of W.
 //
 // W stays as it was quantised: FWD reads its rows K-major, DX the same bytes with the columns contiguous (MN-major).
 #include "fp8.cuh"
@@ -20,6 +20,8 @@
 #include "tc_host.h"
 #include "tc_ptx.cuh"
 #include "tc_tile.cuh"
+
+#include <stddef.h>
 
 namespace lrm {
 
@@ -32,18 +34,28 @@ constexpr int kBK = 128;  // bytes, and elements, of a K slice
 
 enum Kind { FWD = 0, DX = 1 };
 
-template <int BN>
+// The scales of a tile's rows and columns for the next kRun K slices, two of them in turn.
+constexpr int kRun = 8;
+struct Scales {
+  float x[kRun][kBM + 4];  // (the pad keeps the writing lanes' eight slices of four rows off each other's banks)
+  float w[kRun][4];        // of the tile's two blocks of columns; SwiGLU: of the gate columns', then of the up columns'
+};
+
+template <int KIND, int BN, bool RES>
 struct Cfg {
   static constexpr int kABytes = kBM * kBK;
   static constexpr int kBBytes = BN / 2 * kBK;  // this CTA's half of the columns
   static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 5 : 7;
+  static constexpr int kBoxes = BN == 256 && !RES ? 1 : 2;  // of an epilogue warp; the residual comes into both
+  static constexpr int kStages = BN == 256 ? (RES ? 4 : 5) : 6;
   static constexpr int kEpiWarps = BN / 16;
-  static constexpr int kThreads = 64 + 32 * kEpiWarps;
-  static constexpr int kAccs = 512 / BN;  // accumulators: all of TMEM
+  static constexpr int kThreads = 128 + 32 * kEpiWarps;
+  static constexpr int kAccs = 512 / BN;  // all of TMEM
   static constexpr uint32_t kEpi = kStages * kStage;
-  static constexpr uint32_t kBars = kEpi + kEpiWarps * kBoxBytes;
-  static constexpr int kNBars = 2 * kStages + 2 * kAccs + 1;  // full, empty; accumulator full, empty; drain
+  static constexpr uint32_t kScales = kEpi + kEpiWarps * kBoxes * kBoxBytes;
+  static constexpr uint32_t kBars = kScales + 2 * sizeof(Scales);
+  // full, empty; accumulator full, empty; scales full[2], empty[2]; drain; residual of each epilogue warp
+  static constexpr int kNBars = 2 * kStages + 2 * kAccs + 5 + kEpiWarps;
   static constexpr int kPrefix = LRM_MAX_EXPERTS + 2;
   static constexpr size_t smem() { return 1024 + kBars + kNBars * 8 + 16 + 4 * (kPrefix + kThreads / 32); }
   static_assert(1024 + kBars + kNBars * 8 + 16 + 4 * (kPrefix + kThreads / 32) <= 232448, "shared memory");
@@ -61,7 +73,7 @@ struct Params {
   const float *x_scale, *w_scale;
   const int32_t* seg;  // NULL: one dense problem
   int act;
-  const void *bias, *residual;
+  const void* bias;
   void *y, *z;
   int32_t* status;
 };
@@ -81,32 +93,127 @@ __device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t adesc, uint64
       : "memory");
 }
 
-// 16 columns of TMEM on their way: the values are there after tmem_wait16 of the same registers.
-__device__ __forceinline__ void tmem_start16(uint32_t taddr, uint32_t (&v)[16]) {
+// 16 columns of this warp's quarter of TMEM.
+__device__ __forceinline__ void tmem_take16(uint32_t taddr, float (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      "%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait16(uint32_t (&v)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-               :
-               : "memory");
-}
-// acc[16 i ..] += s * v, two at a time
-__device__ __forceinline__ void add_scaled16(float (&acc)[32], int at, const uint32_t (&v)[16], float s) {
+// acc += s * v, two sums at a time
+__device__ __forceinline__ void add_scaled(float* acc, const float (&v)[16], float s) {
   const float2 s2 = make_float2(s, s);
 #pragma unroll
   for (int i = 0; i < 16; i += 2) {
-    const float2 r = __ffma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), s2,
-                                make_float2(acc[at + i], acc[at + i + 1]));
-    acc[at + i] = r.x;
-    acc[at + i + 1] = r.y;
+    const float2 r = __ffma2_rn(make_float2(v[i], v[i + 1]), s2, make_float2(acc[i], acc[i + 1]));
+    acc[i] = r.x;
+    acc[i + 1] = r.y;
   }
+}
+__device__ __forceinline__ float lds(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// One arrival, in either CTA of the pair, for the converged warp.
+__device__ __forceinline__ void mbar_arrive_one(uint32_t cbar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+      "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cbar)
+      : "memory");
+}
+// mbar_wait without a call: what the epilogue holds in registers stays there.  (With a poll at once after the first,
+// plain 32768 x 4096 x 4096 463 us, with the pause 447 us: the polls take issue slots from the warps at work.)
+__device__ __forceinline__ bool mbar_wait_here(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                               int32_t* status) {
+  if (mbar_try(bar, parity)) return true;
+  __nanosleep(20);
+  uint64_t t0 = 0;
+  for (uint32_t it = 0; it < (1u << 30); ++it) {
+    if (mbar_try(bar, parity)) return true;
+    if ((it & 255u) == 255u) {
+      if (*abort_flag) return false;
+      const uint64_t now = globaltimer();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitNs) break;
+    }
+  }
+  *abort_flag = 1;
+  set_status(status, LRM_ERR_TIMEOUT);
+  return false;
+}
+
+// The waits of warps that are ahead of the others: they sleep between polls.  `last`: the wait for everything this
+// CTA has under way, which may take as long as the kernel does and outlives an abort; its limit counts from one.
+__device__ __noinline__ bool mbar_wait_ahead(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status,
+                                             bool last) {
+  uint64_t t0 = globaltimer();
+  for (uint32_t it = 1; it < (1u << 30); ++it) {
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    __nanosleep(20);
+    if ((it & 63u) == 0) {
+      const bool stop = __any_sync(0xffffffffu, *abort_flag != 0);
+      if (stop && !last) return false;
+      if (last && !stop) t0 = globaltimer();
+      if (__any_sync(0xffffffffu, globaltimer() - t0 > kWaitNs)) break;
+    }
+  }
+  *abort_flag = 1;
+  set_status(status, LRM_ERR_TIMEOUT);
+  return false;
+}
+
+// v += 8 bf16 values
+__device__ __forceinline__ void add8(float* v, uint4 r) {
+  float f[8];
+  unpack(r, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] += f[i];
+}
+
+// 32 columns of one row per lane go out in bf16: whole 32-row blocks through a swizzled box of the warp and TMA (which
+// clips columns past the tensor), others by each live lane.
+struct Box {
+  uint8_t* box;
+  int lane;
+  __device__ __forceinline__ uint4* piece(int j) const {  // 64-byte swizzle: piece j of row r sits at j ^ ((r >> 1) & 3)
+    return reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
+  }
+  __device__ __forceinline__ void put(const float (&v)[32], const CUtensorMap* map, int n, int cols, int row, int half,
+                                      bool whole, bool live, B16* at) const {
+    if (whole) {  // warp-uniform
+      if (lane == 0) bulk_wait_read<0>();  // the last store has read the box
+      __syncwarp();
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = v[8 * j + i];
+      const uint4 q = pack(f);
+      if (whole)
+        *piece(j) = q;
+      else if (live && n + 8 * j < cols)
+        st16(at + 8 * j, q);
+    }
+    if (whole) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tma_store_3d(map, smem_u32(box), n, row, half);
+    }
+  }
+};
+
+template <int ACT>
+__device__ __forceinline__ void act_all(float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = act_value<ACT>(v[i]);
 }
 
 struct Tile {
@@ -135,13 +242,13 @@ __device__ __forceinline__ Tile decode(const Params& p, const int* prefix, int t
   return d;
 }
 
-template <int KIND, int BN, bool GLU>
-__global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
+template <int KIND, int BN, bool GLU, bool RES>
+__global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
     fp8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                  const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ, const Params p) {
-  using C = Cfg<BN>;
+                  const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ,
+                  const __grid_constant__ CUtensorMap tmR, const Params p) {
+  using C = Cfg<KIND, BN, RES>;
   constexpr int S = C::kStages, ACCS = C::kAccs;
-  static_assert(KIND == FWD || BN == 256, "DX stages 128 columns a CTA, one row of the 128-byte swizzle");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
@@ -155,7 +262,9 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S;
-  const uint32_t accf0 = empty0 + 8 * S, acce0 = accf0 + 8 * ACCS, drain = acce0 + 8 * ACCS;
+  const uint32_t accf0 = empty0 + 8 * S, acce0 = accf0 + 8 * ACCS;
+  const uint32_t sf0 = acce0 + 8 * ACCS, se0 = sf0 + 16, drain = se0 + 16, res0 = drain + 8;
+  Scales* scales = reinterpret_cast<Scales*>(smem + C::kScales);
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full0 + 8 * s, 2);   // leader's: both producers arrive with their byte counts
@@ -165,7 +274,12 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
       mbar_init(accf0 + 8 * i, 1);
       mbar_init(acce0 + 8 * i, 2 * C::kEpiWarps);  // leader's: the epilogue warps of both CTAs
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sf0 + 8 * i, 2);             // both scale warps
+      mbar_init(se0 + 8 * i, C::kEpiWarps);  // the epilogue warps
+    }
     mbar_init(drain, 1);
+    for (int i = 0; i < C::kEpiWarps; ++i) mbar_init(res0 + 8 * i, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -198,14 +312,14 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
       for (int kb = 0; kb < p.slices; ++kb, ++it) {
         const uint32_t s = st, ph = sph;
         if (++st == (uint32_t)S) { st = 0; sph ^= 1u; }
-        if (!mbar_wait_warp(empty0 + 8 * s, ph ^ 1u, abortv, p.status)) { ok = false; break; }
+        if (!mbar_wait_ahead(empty0 + 8 * s, ph ^ 1u, abortv, p.status, false)) { ok = false; break; }
         const uint32_t fb = full_lead + 8 * s, a_dst = smem_u32(smem + s * C::kStage), b_dst = a_dst + C::kABytes;
         const int half = KIND == DX && kb >= p.half_slices ? 1 : 0, k = (kb - half * p.half_slices) * kBK;
         if (elect_one()) {
           mbar_expect_tx_cluster(fb, bytes);
           if (d.has_rows) tma_load_3d_pair(a_dst, &tmA, k, half, d.row0, fb);
           if (KIND == DX)
-            tma_load_3d_pair(b_dst, &tmB, d.n0 + rank * 128, k, d.e * p.halves + half, fb);
+            tma_load_3d_pair(b_dst, &tmB, d.n0 + rank * (BN / 2), k, d.e * p.halves + half, fb);
           else if (GLU)  // the leader stages the gate rows, the other CTA the up rows
             tma_load_3d_pair(b_dst, &tmB, k, d.n0, d.e * 2 + rank, fb);
           else
@@ -222,10 +336,9 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
     if (leader) {
       constexpr uint32_t idesc = instr_desc<BN>(KIND == DX ? 1u : 0u);
       const uint32_t a0 = smem_u32(smem), b0 = a0 + C::kABytes;
-      // a row of the swizzle is 128 bytes: of K (rows of x and W), or of columns (DX: 128 rows of W below one another)
-      const uint64_t adesc0 = smem_desc(a0, 16, 1024);
-      const uint64_t bdesc0 = KIND == FWD ? smem_desc(b0, 16, 1024) : smem_desc(b0, 16384, 1024);
-      constexpr uint64_t a_step = 32 >> 4, b_step = KIND == FWD ? (32 >> 4) : (4096 >> 4);
+      // a row of the swizzle is 128 bytes: of K (rows of x and W), or of columns (DX: W's rows below one another)
+      const uint64_t adesc0 = smem_desc(a0, 16, 1024), bdesc0 = smem_desc(b0, 16, 1024);
+      constexpr uint64_t a_step = 32 >> 4, b_step = KIND == FWD ? (32 >> 4) : (32 * 128 >> 4);
       uint32_t st = 0, sph = 0, acc = 0, aph = 0;  // operand stage and accumulator, with their phases
       bool ok = true;
       for (int i = 0, t; i < rounds && ok; ++i) {
@@ -255,116 +368,166 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
       if (elect_one()) mma_commit_pair(drain);
     }
     __syncwarp();
-    mbar_wait(drain, 0, abortv, p.status, false);  // all MMAs into this CTA's TMEM are done before it is freed
-  } else {
-    // ---------------------------------------------------------------- epilogue --------
-    constexpr int NO = GLU ? 1 : 2;  // 32-column chunks of output of a warp
-    const int ew = warp - 2, q = warp & 3, group = ew >> 2;
-    uint8_t* boxes = smem + C::kEpi + ew * kBoxBytes;
-    Out<1> out{boxes, smem_u32(boxes), 0};
-    // TMEM column of the warp's chunk c (SwiGLU: gate, up)
-    const uint32_t col0 = GLU ? group * 32 : group * 64, col1 = GLU ? BN / 2 + group * 32 : group * 64 + 32;
-    const int NP = GLU ? 2 * p.N : p.N;
-    uint32_t a = 0, aph = 0;
+    mbar_wait_ahead(drain, 0, abortv, p.status, true);  // all MMAs into this CTA's TMEM are done before it is freed
+  } else if (warp < 4) {
+    // ---------------------------------------------------------------- scales ----------
+    // each of the two warps loads 64 rows, eight slices of four rows at a time (whole sectors where rows allow)
+    const int part = warp - 2, lk = lane & 7, lr = lane >> 3;
+    uint32_t b = 0, bph = 0;
     bool ok = true;
     for (int i = 0, t; i < rounds && ok; ++i) {
       t = nth_tile(i, pair, n_pairs);
       if (t >= n_tiles) continue;
       const Tile d = decode<BN, GLU>(p, prefix, t, rank);
-      const int row_base = d.row0 + q * 32;
+      // the block of W's columns that this lane brings (columns past the last have any)
+      const int blk = min(d.n0 / kQBlock + (lr & 1), p.w_rows - 1);
+      for (int k0 = 0; k0 < p.slices; k0 += kRun) {
+        if (!mbar_wait_ahead(se0 + 8 * b, bph ^ 1u, abortv, p.status, false)) { ok = false; break; }
+        const int k = k0 + lk;
+        float v[kBM / 8];
+        const float* sx = p.x_scale + (int64_t)(d.row0 + part * (kBM / 2) + lr) * p.slices + k;
+#pragma unroll
+        for (int j = 0; j < kBM / 8; ++j) {
+          const int row = d.row0 + part * (kBM / 2) + lr + 4 * j;
+          v[j] = k < p.slices && row < d.row_end ? __ldg(sx + (int64_t)(4 * j) * p.slices) : 0.f;
+        }
+        float w = 0.f;
+        if (part == 0 && (GLU || lr < 2) && k < p.slices) {
+          if (KIND == DX)
+            w = __ldg(p.w_scale + ((int64_t)d.e * p.slices + k) * p.w_rows + blk);
+          else
+            w = __ldg(p.w_scale + ((int64_t)(GLU ? d.e * 2 + (lr >> 1) : d.e) * p.w_rows + blk) * p.slices + k);
+        }
+        Scales& to = scales[b];
+#pragma unroll
+        for (int j = 0; j < kBM / 8; ++j) to.x[lk][part * (kBM / 2) + lr + 4 * j] = v[j];
+        if (part == 0) to.w[lk][lr] = w;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sf0 + 8 * b);
+        b ^= 1u;
+        if (b == 0) bph ^= 1u;
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue --------
+    constexpr int NO = GLU ? 1 : 2;  // 32-column chunks of output of a warp
+    const int ew = warp - 4, q = warp & 3, group = ew >> 2;
+    uint8_t* boxes = smem + C::kEpi + ew * C::kBoxes * kBoxBytes;
+    const uint32_t res_bar = res0 + 8 * ew;
+    // TMEM columns of the warp's two chunks (SwiGLU: gate, up)
+    const uint32_t col0 = group * NO * 32, col1 = GLU ? BN / 2 + group * 32 : col0 + 32;
+    const uint32_t quarter = tmem_base + ((uint32_t)(q * 32) << 16);
+    const int NP = GLU ? 2 * p.N : p.N;
+    const uint32_t scales_s = smem_u32(scales);
+    uint32_t a = 0, aph = 0, b = 0, bph = 0, rph = 0;  // accumulator, scales and residual, with their phases
+    bool ok = true;
+    for (int i = 0, t; i < rounds && ok; ++i) {
+      t = nth_tile(i, pair, n_pairs);
+      if (t >= n_tiles) continue;
+      const Tile d = decode<BN, GLU>(p, prefix, t, rank);
+      const int row_base = d.row0 + q * 32, n_first = d.n0 + group * NO * 32;
       // (the check, where it is on, covers what this warp's stores address: the expert, and its first and last row)
       const int nrows = d.has_rows && LRM_DCHECK(d.e >= 0 && d.e < p.E && row_base >= 0 && d.row_end <= p.R, p.status,
                                                  LRM_ERR_BAD_INDEX)
                             ? min(32, d.row_end - row_base)
                             : 0;
-      // without segments the output map ends where the rows end, so TMA clips a partial block
-      const bool whole = nrows == 32 || (nrows > 0 && p.seg == nullptr);
-      const bool live = lane < nrows;
-      const int64_t row = row_base + lane;
-      const int n_first = d.n0 + group * NO * 32;
-      // this row's scales, and those of the warp's block of columns (rows and columns past the last have any)
-      const float* sx = p.x_scale + (live ? row : 0) * p.slices;
-      const int blk = min(n_first / kQBlock, p.w_rows - 1);
-      const float *sw0, *sw1 = nullptr;
-      int64_t w_step = 1;
-      if (KIND == DX) {
-        sw0 = p.w_scale + (int64_t)d.e * p.slices * p.w_rows + blk;
-        w_step = p.w_rows;
-      } else {
-        sw0 = p.w_scale + ((int64_t)d.e * p.halves * p.w_rows + blk) * p.slices;
-        if (GLU) sw1 = sw0 + (int64_t)p.w_rows * p.slices;
+      const bool mine = nrows > 0 && n_first < p.N;  // warp-uniform: this warp has output
+      if (RES && mine && lane == 0) {  // the residual comes into the boxes meanwhile
+        bulk_wait_read<0>();
+        mbar_expect_tx(res_bar, NO * kBoxBytes);
+#pragma unroll
+        for (int c = 0; c < NO; ++c)
+          tma_load_3d_cta(smem_u32(boxes) + c * kBoxBytes, &tmR, n_first + c * 32, row_base, 0, res_bar);
       }
+      const int blk = n_first / kQBlock - d.n0 / kQBlock;  // 0 or 1
       float acc[2][32];
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
-      // scales one slice ahead
-      float nx = __ldg(sx), n0 = __ldg(sw0), n1 = GLU ? __ldg(sw1) : 0.f;
       for (int kb = 0; kb < p.slices; ++kb) {
-        const float s0 = nx * n0, s1 = GLU ? nx * n1 : s0;
-        if (kb + 1 < p.slices) {
-          nx = __ldg(sx + kb + 1);
-          n0 = __ldg(sw0 + (kb + 1) * w_step);
-          if (GLU) n1 = __ldg(sw1 + kb + 1);
+        const int kr = kb % kRun;
+        if (kr == 0 && !mbar_wait_here(sf0 + 8 * b, bph, abortv, p.status)) { ok = false; break; }
+        const uint32_t at = scales_s + b * (uint32_t)sizeof(Scales);
+        const uint32_t wa = at + (uint32_t)offsetof(Scales, w) + kr * 16 + blk * 4;
+        const float sx = lds(at + (kr * (kBM + 4) + q * 32 + lane) * 4);
+        const float s0 = sx * lds(wa), s1 = GLU ? sx * lds(wa + 8) : s0;
+        if (kr == kRun - 1 || kb + 1 == p.slices) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(se0 + 8 * b);
+          b ^= 1u;
+          if (b == 0) bph ^= 1u;
         }
-        if (!mbar_wait(accf0 + 8 * a, aph, abortv, p.status)) { ok = false; break; }
+        if (!mbar_wait_here(accf0 + 8 * a, aph, abortv, p.status)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t tbase = tmem_base + a * BN + ((uint32_t)(q * 32) << 16);
-        uint32_t r0[16], r1[16];
         __syncwarp();
-        tmem_start16(tbase + col0, r0);
-        tmem_wait16(r0);
-        tmem_start16(tbase + col0 + 16, r1);
-        add_scaled16(acc[0], 0, r0, s0);
-        tmem_wait16(r1);
-        tmem_start16(tbase + col1, r0);
-        add_scaled16(acc[0], 16, r1, s0);
-        tmem_wait16(r0);
-        tmem_start16(tbase + col1 + 16, r1);
-        add_scaled16(acc[1], 0, r0, s1);
-        tmem_wait16(r1);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acce_lead + 8 * a);
-        add_scaled16(acc[1], 16, r1, s1);
+        const uint32_t tbase = quarter + a * BN;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float r[16];
+          tmem_take16(tbase + (c < 2 ? col0 : col1) + (c & 1) * 16, r);
+          if (c == 3) {  // the accumulator goes back before its last columns are added
+            tc_fence_before();
+            mbar_arrive_one(acce_lead + 8 * a);
+          }
+          add_scaled(acc[c >> 1] + (c & 1) * 16, r, c < 2 ? s0 : s1);
+        }
         if (++a == (uint32_t)ACCS) { a = 0; aph ^= 1u; }
       }
-      if (!ok) break;
+      if (!ok) {  // (the residual's copy lands before the CTA exits)
+        if (RES && mine) mbar_wait(res_bar, rph, abortv, p.status, false);
+        break;
+      }
       __syncwarp();
-      const B16* res =
-          KIND == FWD && p.residual != nullptr && live ? static_cast<const B16*>(p.residual) + row * p.N : nullptr;
-      B16* y_row = static_cast<B16*>(p.y) + row * p.N;
+      if (!mine) continue;
+      // without segments the output map ends where the rows end, so TMA clips a partial block
+      const bool whole = nrows == 32 || p.seg == nullptr;
+      const bool live = lane < nrows;
+      const int64_t row = row_base + lane;
+      if (RES) {
+        if (!mbar_wait_here(res_bar, rph, abortv, p.status)) break;
+        rph ^= 1u;
+        __syncwarp();
+      }
 #pragma unroll
       for (int c = 0; c < NO; ++c) {
         const int n = n_first + c * 32;
-        if (nrows <= 0 || n >= p.N) continue;  // warp-uniform
+        if (n >= p.N) break;  // warp-uniform
         float(&v)[32] = acc[c];
+        const Box box{boxes + (C::kBoxes > 1 ? c * kBoxBytes : 0), lane};
         if (KIND == FWD) {
           if (p.bias != nullptr) {
-            const B16* b = static_cast<const B16*>(p.bias) + (int64_t)d.e * NP;
-            add_row(v, b, n, p.N);
-            if (GLU) add_row(acc[1], b + p.N, n, p.N);
+            const B16* bias = static_cast<const B16*>(p.bias) + (int64_t)d.e * NP + n;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (n + 8 * j < p.N) {
+                add8(v + 8 * j, ldg16(bias + 8 * j));
+                if (GLU) add8(acc[1] + 8 * j, ldg16(bias + p.N + 8 * j));
+              }
           }
-          if (p.z != nullptr) {
-            B16* z_row = static_cast<B16*>(p.z) + row * NP;
-            out.put(v, &tmZ, lane, n, p.N, row_base, 0, whole, live, z_row);
-            if (GLU) out.put(acc[1], &tmZ, lane, n, p.N, row_base, 1, whole, live, z_row + p.N);
+          if (p.z != nullptr) {  // (where the box holds the residual, from the registers)
+            const bool boxed = whole && !RES;
+            const bool z_live = live || (whole && row < d.row_end);
+            B16* z_row = static_cast<B16*>(p.z) + row * NP + n;
+            box.put(v, &tmZ, n, p.N, row_base, 0, boxed, z_live, z_row);
+            if (GLU) Box{boxes + (C::kBoxes - 1) * kBoxBytes, lane}.put(acc[1], &tmZ, n, p.N, row_base, 1, boxed, z_live, z_row + p.N);
           }
           if (GLU) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = act_value<LRM_ACT_SWIGLU>(v[j]) * acc[1][j];
           } else {
             switch (p.act) {
-              case LRM_ACT_RELU: act32<LRM_ACT_RELU>(v); break;
-              case LRM_ACT_GELU: act32<LRM_ACT_GELU>(v); break;
-              case LRM_ACT_SILU: act32<LRM_ACT_SILU>(v); break;
+              case LRM_ACT_RELU: act_all<LRM_ACT_RELU>(v); break;
+              case LRM_ACT_GELU: act_all<LRM_ACT_GELU>(v); break;
+              case LRM_ACT_SILU: act_all<LRM_ACT_SILU>(v); break;
               default: break;
             }
           }
-          if (res != nullptr) add_row(v, res, n, p.N);
+          if (RES)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) add8(v + 8 * j, *box.piece(j));
         }
-        out.put(v, &tmY, lane, n, p.N, row_base, 0, whole, live, y_row);
+        box.put(v, &tmY, n, p.N, row_base, 0, whole, live, static_cast<B16*>(p.y) + row * p.N + n);
       }
     }
     if (lane == 0) bulk_wait_all();  // stores complete before the CTA exits
@@ -384,11 +547,21 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
 bool fp8_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b1, uint32_t b2) {
   const cuuint64_t dims[3] = {d0, d1, d2};
   const cuuint64_t strides[2] = {d0, d0 * d1};
-  const cuuint32_t box[3] = {kBK, b1, b2};
+  const cuuint32_t box[3] = {128, b1, b2};
   const cuuint32_t estr[3] = {1, 1, 1};
   return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// bf16 rows [rows][halves][cols] in boxes of 32 rows and 32 columns of one half.
+bool rows_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t halves) {
+  const cuuint64_t dims[3] = {cols, rows, halves};
+  const cuuint64_t strides[2] = {cols * halves * 2, halves > 1 ? cols * 2 : cols * rows * 2};
+  const cuuint32_t box[3] = {32, 32, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int blocks_of(int n) { return (n + kQBlock - 1) / kQBlock; }
@@ -398,7 +571,6 @@ int blocks_of(int n) { return (n + kQBlock - 1) / kQBlock; }
 lrm_status launch_fp8_tc(const Fp8Args& a, cudaStream_t s) {
   if (!device_ok() || encode_fn() == nullptr) return LRM_ERR_UNSUPPORTED;
   const bool glu = a.act == LRM_ACT_SWIGLU;
-  const int NP = glu ? 2 * a.N : a.N;
   Params p{};
   p.E = a.E;
   p.R = a.R;
@@ -411,31 +583,35 @@ lrm_status launch_fp8_tc(const Fp8Args& a, cudaStream_t s) {
   p.seg = a.seg_offsets;
   p.act = a.act;
   p.bias = a.bias;
-  p.residual = a.residual;
   p.y = a.y;
   p.z = a.z;
   p.status = a.status;
-  CUtensorMap mA, mB, mY, mZ;
-  if (!fp8_map(&mA, a.x, a.K, 1, a.R, 1, kBM) || !output_map(&mY, a.y, false, a.N, a.R, 1)) return LRM_ERR_CUDA;
-  mZ = mY;
-  if (a.z != nullptr && !output_map(&mZ, a.z, false, a.N, a.R, glu ? 2 : 1, glu)) return LRM_ERR_CUDA;
-  auto go = [&](auto bn, auto glu_tag) {
+  CUtensorMap mA, mB, mY, mZ, mR;
+  if (!fp8_map(&mA, a.x, a.K, 1, a.R, 1, kBM) || !rows_map(&mY, a.y, a.N, a.R, 1)) return LRM_ERR_CUDA;
+  mZ = mR = mY;
+  if (a.z != nullptr && !rows_map(&mZ, a.z, a.N, a.R, p.halves)) return LRM_ERR_CUDA;
+  if (a.residual != nullptr && !rows_map(&mR, a.residual, a.N, a.R, 1)) return LRM_ERR_CUDA;
+  auto tiles = [&](auto bn, auto glu_tag, auto res_tag) {
     constexpr int BN = decltype(bn)::value;
-    constexpr bool GLU = decltype(glu_tag)::value != 0;
+    constexpr bool GLU = decltype(glu_tag)::value != 0, RES = decltype(res_tag)::value != 0;
     constexpr int cols = GLU ? BN / 2 : BN;
+    using C = Cfg<FWD, BN, RES>;
     p.tiles_n = (a.N + cols - 1) / cols;
     if (!fp8_map(&mB, a.w, a.K, a.N, (uint64_t)a.E * p.halves, BN / 2, 1)) return LRM_ERR_CUDA;
-    return launch_pairs<fp8_tc_kernel<FWD, BN, GLU>>(Cfg<BN>::smem(), Cfg<BN>::kThreads,
-                                                     row_tiles(a.seg_offsets, a.R, a.E) * p.tiles_n, s, mA, mB, mY, mZ,
-                                                     p);
+    return launch_pairs<fp8_tc_kernel<FWD, BN, GLU, RES>>(
+        C::smem(), C::kThreads, row_tiles(a.seg_offsets, a.R, a.E) * p.tiles_n, s, mA, mB, mY, mZ, mR, p);
+  };
+  auto go = [&](auto bn, auto glu_tag) {
+    return a.residual != nullptr ? tiles(bn, glu_tag, IntTag<1>{}) : tiles(bn, glu_tag, IntTag<0>{});
   };
   const int64_t likely = likely_row_tiles(a.seg_offsets, a.R, a.E);
-  if (glu) return with_width(likely, NP, 64, [&](auto bn) { return go(bn, IntTag<1>{}); });
-  return with_width(likely, NP, 64, [&](auto bn) { return go(bn, IntTag<0>{}); });
+  if (glu) return with_width(likely, p.halves * a.N, 64, [&](auto bn) { return go(bn, IntTag<1>{}); });
+  return with_width(likely, a.N, 64, [&](auto bn) { return go(bn, IntTag<0>{}); });
 }
 
 lrm_status launch_fp8_dx(const Fp8GradArgs& a, cudaStream_t s) {
   if (!device_ok() || encode_fn() == nullptr) return LRM_ERR_UNSUPPORTED;
+  using C = Cfg<DX, 256, false>;
   Params p{};
   p.E = a.E;
   p.R = a.R;
@@ -452,11 +628,10 @@ lrm_status launch_fp8_dx(const Fp8GradArgs& a, cudaStream_t s) {
   p.status = a.status;
   CUtensorMap mA, mB, mY;
   if (!fp8_map(&mA, a.dz, a.N, p.halves, a.R, 1, kBM) ||
-      !fp8_map(&mB, a.w, a.K, a.N, (uint64_t)a.E * p.halves, 128, 1) || !output_map(&mY, a.dx, false, a.K, a.R, 1))
+      !fp8_map(&mB, a.w, a.K, a.N, (uint64_t)a.E * p.halves, kBK, 1) || !rows_map(&mY, a.dx, a.K, a.R, 1))
     return LRM_ERR_CUDA;
-  return launch_pairs<fp8_tc_kernel<DX, 256, false>>(Cfg<256>::smem(), Cfg<256>::kThreads,
-                                                     row_tiles(a.seg_offsets, a.R, a.E) * p.tiles_n, s, mA, mB, mY, mY,
-                                                     p);
+  return launch_pairs<fp8_tc_kernel<DX, 256, false, false>>(
+      C::smem(), C::kThreads, row_tiles(a.seg_offsets, a.R, a.E) * p.tiles_n, s, mA, mB, mY, mY, mY, p);
 }
 
 }  // namespace lrm
