@@ -509,6 +509,67 @@ lrm_status lrm_fp8_linear_backward(const int32_t* seg_offsets, const void* dz, c
                                    const float* w_scale, int64_t R, int32_t E, int32_t N, int32_t K, int32_t glu,
                                    void* dx, int32_t* dev_status, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The optimiser that applies the layer's gradients.  The pages stop at the gradients; these calls end the
+ * training step.
+ * ------------------------------------------------------------------------------------------- */
+
+/* One tensor of lrm_adamw and lrm_grad_norm (the array of them is HOST memory, read before the call returns).  The
+ * tensors of a call do not overlap. */
+typedef struct lrm_adamw_tensor {
+  void* w;        /* [n] weights, updated                                                              */
+  void* copy;     /* [n] bf16, written with the new weights' values: fp32 weights only; NULL for none  */
+  const void* g;  /* [n] gradient                                                                      */
+  void* m;        /* [n] first moment: fp32, or e4m3 with state_bits 8                                  */
+  void* v;        /* [n] second moment: v in fp32, or sqrt(v) in e4m3 with state_bits 8                 */
+  float* m_scale; /* [ceil(n / 256)] scales of 256 elements each (state_bits 8), zeros at the start     */
+  float* v_scale;
+  int64_t n;          /* elements, 0 or more                                                           */
+  float weight_decay; /* of this tensor                                                                */
+  float lr_scale;     /* factor of the rate for this tensor, usually 1                                 */
+  int32_t id;         /* a number of its own: the random bits of 8-bit states differ by it             */
+} lrm_adamw_tensor;
+
+/* Values of a step of lrm_adamw. */
+typedef struct lrm_adamw_hyper {
+  double lr, beta1, beta2, eps; /* 0 <= beta < 1, eps >= 0                                              */
+  int64_t step;                 /* 1 for the first step, up to INT32_MAX                                */
+  uint32_t seed;                /* of the random bits of 8-bit states                                   */
+  double max_norm;              /* with grad_norm: gradients are scaled by min(1, max_norm / (norm + 1e-6)) */
+  const float* grad_norm;       /* DEVICE, from lrm_grad_norm, or NULL; not finite: nothing is changed     */
+  const float* lr_dev;          /* DEVICE, or NULL: the rate in place of lr (for captured steps)           */
+  const int32_t* step_dev;      /* DEVICE, or NULL: the step in place of step (less than 1 counts as 1)    */
+} lrm_adamw_hyper;
+
+/* Bytes of scratch of lrm_grad_norm for these tensors (only their n is read).  Host-only. */
+lrm_status lrm_grad_norm_workspace_size(const lrm_adamw_tensor* tensors, int32_t count, size_t* bytes);
+
+/*
+ * The 2-norm of all gradients together:  norm [1] fp32 = sqrt(sum over the tensors of sum g^2).  Squares are fp32
+ * (|g| above 1.8e19 gives infinity), sums fp64 beyond 32 values and in a fixed order.  A norm that is not finite sets
+ * LRM_ERR_NONFINITE.  Of the tensors only g and n are read.  No tensors, or none with elements: 0.
+ * Errors: LRM_ERR_INVALID_ARG, LRM_ERR_SHAPE, LRM_ERR_DTYPE, LRM_ERR_WORKSPACE, LRM_ERR_CUDA.
+ */
+lrm_status lrm_grad_norm(const lrm_adamw_tensor* tensors, int32_t count, lrm_dtype g_dt, float* norm, void* ws,
+                         size_t ws_bytes, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * One AdamW step over `count` tensors, in place, all arithmetic in fp32:
+ *   g = gradient * factor (min(1, max_norm / (norm + 1e-6)) with grad_norm, else 1)
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   w = w (1 - lr wd) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * w_dt, g_dt: types of all weights and of all gradients.  copy: 1 where every tensor has a bf16 copy (w_dt
+ * LRM_F32), else 0.  state_bits 32, or 8: m and sqrt(v) are then e4m3 values, 256 elements of a tensor to a scale
+ * (their largest magnitude, at least 2^-120, over 448), rounded up or down at random with the odds that keep the mean:
+ * with h = mix(e * 0x9E3779B1 + (e >> 32) * 0xC2B2AE3D + mix(mix(seed + 0x9E3779B9 (id + 1)) ^ step)) for element
+ * e and MurmurHash3's finaliser mix, all modulo 2^32, m by the low and sqrt(v) by the high 16 bits of h.  The step's
+ * update uses m and v before that rounding; a sqrt(v) above 0 is held as 2^-9 of its scale at least.  A state of 8 bits
+ * that has become infinite or NaN makes its 256 elements NaN.  Zeroed states and scales are the start.
+ * Errors: LRM_ERR_INVALID_ARG, LRM_ERR_SHAPE (step), LRM_ERR_DTYPE, LRM_ERR_CUDA.
+ */
+lrm_status lrm_adamw(const lrm_adamw_tensor* tensors, int32_t count, lrm_dtype w_dt, lrm_dtype g_dt, int32_t state_bits,
+                     int32_t copy, const lrm_adamw_hyper* hyper, cudaStream_t stream);
+
 /*
  * Self-test of failure detection (no counterpart in the pages; part of this library's fault
  * handling).  The tensor-core kernels bound every wait on an mbarrier (about one second of

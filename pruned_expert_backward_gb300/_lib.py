@@ -26,6 +26,18 @@ LRM_MAX_EXPERTS, LRM_MAX_TOPK = 1024, 16
 
 _p, _i32, _i64, _sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
 
+class AdamwTensor(C.Structure):
+    """lrm_adamw_tensor: addresses, elements and factors of one tensor."""
+    _fields_ = [("w", _p), ("copy", _p), ("g", _p), ("m", _p), ("v", _p), ("m_scale", _p), ("v_scale", _p), ("n", _i64),
+                ("weight_decay", C.c_float), ("lr_scale", C.c_float), ("id", _i32)]
+
+
+class AdamwHyper(C.Structure):
+    """lrm_adamw_hyper: the values of a step."""
+    _fields_ = [("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_double), ("step", _i64),
+                ("seed", C.c_uint32), ("max_norm", C.c_double), ("grad_norm", _p), ("lr_dev", _p), ("step_dev", _p)]
+
+
 SIGNATURES = {
     "lrm_status_string": (C.c_char_p, [C.c_int]),
     "lrm_workspace_size": (C.c_int, [_i64, _i32, _i32, _i32, _i32, C.c_int, C.POINTER(_sz)]),
@@ -60,6 +72,9 @@ SIGNATURES = {
     "lrm_fp8_quantize_weight": (C.c_int, [_p, _i32, _i32, _i32, C.c_int, _p, _p, _p]),
     "lrm_fp8_linear": (C.c_int, [_p, _p, _p, _p, _p, _p, _p, _i64, _i32, _i32, _i32, C.c_int, _p, _p, _p, _p]),
     "lrm_fp8_linear_backward": (C.c_int, [_p, _p, _p, _p, _p, _i64, _i32, _i32, _i32, _i32, _p, _p, _p]),
+    "lrm_grad_norm_workspace_size": (C.c_int, [C.POINTER(AdamwTensor), _i32, C.POINTER(_sz)]),
+    "lrm_grad_norm": (C.c_int, [C.POINTER(AdamwTensor), _i32, C.c_int, _p, _p, _sz, _p, _p]),
+    "lrm_adamw": (C.c_int, [C.POINTER(AdamwTensor), _i32, C.c_int, C.c_int, _i32, _i32, C.POINTER(AdamwHyper), _p]),
     "lrm_score_mode": (C.c_int, [_p, _p, _p, _i64, _i32, _i32, _i32, C.c_int, C.c_int, _p, _p, _p]),
 }
 

@@ -791,6 +791,140 @@ class MoeLayer:
         return self.dx, self.dalpha, self.dw_gate_up, self.dw_down
 
 
+class AdamW:
+    """AdamW over many tensors at once (lrm_adamw): one or a few launches a step, whatever the number of tensors.
+
+    params: bf16 or fp32 tensors, updated in place.  grads: their gradients, read at every step where they are (the
+    layer's dw_gate_up and dw_down stay in place); step(grads=...) takes others.  copies: bf16 tensors that get the
+    fp32 params' new values as well.  state_bits 32 keeps both moments in fp32; 8 keeps m and sqrt(v) in e4m3 with a
+    scale for 256 elements, rounded at random by `seed`, the step and the element's place (lrm_adamw in lrm.h).
+    weight_decay and lr_scale: one value, or one for each tensor.  max_norm: gradients are scaled so that their
+    common norm is at most that; a step whose norm is not finite changes nothing and sets LRM_ERR_NONFINITE in
+    dev_status.  state: {"m": [...], "v": [...]} and, for 8 bits, "m_scale", "v_scale" to go on from; zeros without.
+    capturable: step and rate live on the device (step_dev, lr_dev), so that a captured step can be replayed."""
+
+    def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, copies=None, state_bits=32,
+                 state=None, max_norm=None, seed=0, lr_scale=1.0, capturable=False):
+        n = len(params)
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
+        if n == 0:
+            raise ValueError("AdamW needs at least one tensor")
+
+        def each(a, name):
+            a = list(a) if isinstance(a, (list, tuple)) else [a] * n
+            if len(a) != n:
+                raise ValueError(f"{name} must hold {n} values, got {len(a)}")
+            return a
+
+        self.params, self.copies, self.state_bits = list(params), each(copies, "copies"), state_bits
+        self.lr, self.betas, self.eps, self.seed, self.max_norm = lr, betas, eps, seed, max_norm
+        decay, scale = each(weight_decay, "weight_decay"), each(lr_scale, "lr_scale")
+        dev = self.params[0].device
+        for t in self.params:
+            _cuda(t, "param")
+            _dt(t)
+        if state is None:
+            kind = torch.float32 if state_bits == 32 else FP8
+            state = {key: [torch.zeros(t.shape, device=t.device).to(kind) for t in self.params] for key in ("m", "v")}
+            if state_bits == 8:
+                for key in ("m_scale", "v_scale"):
+                    state[key] = [torch.zeros(-(-t.numel() // 256), dtype=torch.float32, device=t.device) for t in self.params]
+        self.state = state
+        # the tensors by the types that share a launch, in order
+        self._groups = []
+        kinds = {}
+        for i, t in enumerate(self.params):
+            kinds.setdefault((_dt(t), self.copies[i] is not None), []).append(i)
+        for (w_dt, copy), members in kinds.items():
+            table = (L.AdamwTensor * len(members))()
+            for j, i in enumerate(members):
+                t, e = self.params[i], table[j]
+                e.w, e.n, e.weight_decay, e.lr_scale, e.id = t.data_ptr(), t.numel(), decay[i], scale[i], i
+                if copy:
+                    if w_dt != L.LRM_F32:
+                        raise TypeError("copies are of fp32 params")
+                    _same(self.copies[i], t.shape, "copy")
+                    e.copy = _cuda(self.copies[i], "copy", torch.bfloat16)
+                for key in ("m", "v"):
+                    s = state[key][i]
+                    if s.numel() != t.numel():
+                        raise ValueError(f"state {key} must hold {t.numel()} values, got {s.numel()}")
+                    setattr(e, key, _cuda(s, key, torch.float32 if state_bits == 32 else FP8))
+                    if state_bits == 8:
+                        s = state[key + "_scale"][i]
+                        if s.numel() != -(-t.numel() // 256):
+                            raise ValueError(f"state {key}_scale must hold a value for each 256, got {s.numel()}")
+                        setattr(e, key + "_scale", _cuda(s, key + "_scale", torch.float32))
+            self._groups.append((w_dt, copy, members, table))
+        # one table of all tensors for the common norm
+        self._all = self._groups[0][3] if len(self._groups) == 1 else (L.AdamwTensor * n)()
+        if len(self._groups) > 1:
+            for i, t in enumerate(self.params):
+                self._all[i].n = t.numel()
+        self.grads, self._g_dt = None, None
+        self.set_grads(grads)
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.norm = self._ws = None
+        if max_norm is not None:
+            if not max_norm > 0:
+                raise ValueError(f"max_norm must be positive, got {max_norm}")
+            out = C.c_size_t(0)
+            _ok(L.load().lrm_grad_norm_workspace_size(self._all, n, C.byref(out)), "lrm_grad_norm_workspace_size")
+            self.norm = torch.zeros((), dtype=torch.float32, device=dev)
+            self._ws = torch.empty(out.value, dtype=torch.uint8, device=dev)
+        self.steps = 0
+        self.step_dev = torch.zeros(1, dtype=torch.int32, device=dev) if capturable else None
+        self.lr_dev = torch.full((1,), lr, dtype=torch.float32, device=dev) if capturable else None
+
+    def set_grads(self, grads):
+        """The gradients that the next steps read: one type, bf16 or fp32, for all of them."""
+        grads = list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(self.params)} gradients expected, got {len(grads)}")
+        g_dt = _dt(grads[0])
+        at = []
+        for g, t in zip(grads, self.params):
+            if g.numel() != t.numel():
+                raise ValueError(f"a gradient of {g.numel()} values for a param of {t.numel()}")
+            at.append(_cuda(g, "gradient", grads[0].dtype))
+        for _, _, members, table in self._groups:
+            for j, i in enumerate(members):
+                table[j].g = at[i]
+        if len(self._groups) > 1:
+            for i, p in enumerate(at):
+                self._all[i].g = p
+        self.grads, self._g_dt = grads, g_dt
+
+    def step(self, step=None, lr=None, grads=None):
+        """One step; returns the gradients' norm (fp32 scalar on the device) with max_norm, else None.  step: its
+        number, one more than the last by default.  lr: this step's rate in place of the one given at first."""
+        if grads is not None:
+            self.set_grads(grads)
+        stream = _stream()
+        if self.step_dev is not None:
+            if step is not None or lr is not None:
+                raise ValueError("a capturable step takes step and rate from step_dev and lr_dev")
+            self.step_dev.add_(1)
+        else:
+            self.steps = self.steps + 1 if step is None else int(step)
+        h = L.AdamwHyper(self.lr if lr is None else lr, *self.betas, self.eps, max(self.steps, 1), self.seed & 0xFFFFFFFF,
+                         0.0 if self.max_norm is None else self.max_norm, None, None, None)
+        if self.step_dev is not None:
+            h.step_dev, h.lr_dev = self.step_dev.data_ptr(), self.lr_dev.data_ptr()
+        elif self.steps < 1:
+            raise ValueError(f"steps count from 1, got {self.steps}")
+        lib = L.load()
+        if self.max_norm is not None:
+            h.grad_norm = self.norm.data_ptr()
+            _ok(lib.lrm_grad_norm(self._all, len(self.params), self._g_dt, h.grad_norm, self._ws.data_ptr(),
+                                  self._ws.numel(), self.dev_status.data_ptr(), stream), "lrm_grad_norm")
+        for w_dt, copy, members, table in self._groups:
+            _ok(lib.lrm_adamw(table, len(members), w_dt, self._g_dt, self.state_bits, int(copy), C.byref(h), stream),
+                "lrm_adamw")
+        return self.norm
+
+
 class HostPipeline:
     """The pruned backward over batches held in pinned host memory.
 

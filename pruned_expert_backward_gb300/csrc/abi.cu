@@ -45,6 +45,15 @@ lrm_status check_fp8_width(int32_t K) {
   return K % 16 != 0 || K > (1 << 24) ? LRM_ERR_SHAPE : LRM_OK;
 }
 
+lrm_status check_tensors(const lrm_adamw_tensor* tensors, int32_t count) {
+  if (count < 0 || (count > 0 && !tensors)) return LRM_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < count; ++i) {
+    if (tensors[i].n < 0) return LRM_ERR_INVALID_ARG;
+    if (tensors[i].n > ((int64_t)1 << 40)) return LRM_ERR_SHAPE;
+  }
+  return LRM_OK;
+}
+
 // Scratch of lrm_sort_tokens: the counts of each chunk of pairs and the buckets' sizes.
 struct SortWs {
   size_t counts, loads, total;
@@ -668,6 +677,54 @@ lrm_status lrm_fp8_linear_backward(const int32_t* seg_offsets, const void* dz, c
   if (!al4(seg_offsets) || !al4(dz_scale) || !al4(w_scale)) return LRM_ERR_INVALID_ARG;
   if (R == 0) return LRM_OK;
   return launch_fp8_dx(Fp8GradArgs{seg_offsets, dz, dz_scale, w, w_scale, R, E, N, K, glu != 0, dx, dev_status}, stream);
+}
+
+lrm_status lrm_grad_norm_workspace_size(const lrm_adamw_tensor* tensors, int32_t count, size_t* bytes) {
+  LRM_NVTX_RANGE();
+  if (!bytes) return LRM_ERR_INVALID_ARG;
+  const lrm_status st = check_tensors(tensors, count);
+  if (st) return st;
+  *bytes = up(sizeof(double) * grad_norm_parts(tensors, count));
+  return LRM_OK;
+}
+
+lrm_status lrm_grad_norm(const lrm_adamw_tensor* tensors, int32_t count, lrm_dtype g_dt, float* norm, void* ws,
+                         size_t ws_bytes, int32_t* dev_status, cudaStream_t stream) {
+  LRM_NVTX_RANGE();
+  lrm_status st = check_tensors(tensors, count);
+  if (st) return st;
+  if ((st = check_dt(g_dt))) return st;
+  if (!norm || !al4(norm)) return LRM_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < count; ++i)
+    if (tensors[i].n > 0 && (!tensors[i].g || !al16(tensors[i].g))) return LRM_ERR_INVALID_ARG;
+  if (!ws || !al16(ws) || ws_bytes < sizeof(double) * grad_norm_parts(tensors, count)) return LRM_ERR_WORKSPACE;
+  launch_grad_norm(tensors, count, g_dt, norm, static_cast<double*>(ws), dev_status, stream);
+  return after_launch();
+}
+
+lrm_status lrm_adamw(const lrm_adamw_tensor* tensors, int32_t count, lrm_dtype w_dt, lrm_dtype g_dt, int32_t state_bits,
+                     int32_t copy, const lrm_adamw_hyper* hyper, cudaStream_t stream) {
+  LRM_NVTX_RANGE();
+  lrm_status st = check_tensors(tensors, count);
+  if (st) return st;
+  if ((st = check_dt(w_dt)) || (st = check_dt(g_dt))) return st;
+  if ((state_bits != 8 && state_bits != 32) || (copy != 0 && copy != 1) || !hyper) return LRM_ERR_INVALID_ARG;
+  if (copy && w_dt != LRM_F32) return LRM_ERR_DTYPE;
+  const lrm_adamw_hyper& h = *hyper;
+  // (written so that a NaN is refused)
+  if (!(h.beta1 >= 0 && h.beta1 < 1 && h.beta2 >= 0 && h.beta2 < 1 && h.eps >= 0 && h.lr >= 0)) return LRM_ERR_INVALID_ARG;
+  if (h.grad_norm && !(h.max_norm > 0)) return LRM_ERR_INVALID_ARG;
+  if (!h.step_dev && (h.step < 1 || h.step > INT32_MAX)) return LRM_ERR_SHAPE;
+  if (!al4(h.grad_norm) || !al4(h.lr_dev) || !al4(h.step_dev)) return LRM_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < count; ++i) {
+    const lrm_adamw_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    if (!t.w || !t.g || !t.m || !t.v || (copy && !t.copy)) return LRM_ERR_INVALID_ARG;
+    if (!al16(t.w) || !al16(t.copy) || !al16(t.g) || !al16(t.m) || !al16(t.v)) return LRM_ERR_INVALID_ARG;
+    if (state_bits == 8 && (!t.m_scale || !t.v_scale || !al4(t.m_scale) || !al4(t.v_scale))) return LRM_ERR_INVALID_ARG;
+  }
+  launch_adamw(tensors, count, w_dt, g_dt, state_bits, copy != 0, h, stream);
+  return after_launch();
 }
 
 lrm_status lrm_selftest_wait_timeout(int32_t* dev_status, int64_t limit_ns, cudaStream_t stream) {

@@ -236,4 +236,11 @@ struct Fp8GradArgs {
 };
 lrm_status launch_fp8_dx(const Fp8GradArgs& a, cudaStream_t s);
 
+// The optimiser.
+size_t grad_norm_parts(const lrm_adamw_tensor* tensors, int32_t count);  // partial sums (fp64) of lrm_grad_norm
+void launch_grad_norm(const lrm_adamw_tensor* tensors, int32_t count, lrm_dtype g_dt, float* norm, double* part,
+                      int32_t* status, cudaStream_t s);
+void launch_adamw(const lrm_adamw_tensor* tensors, int32_t count, lrm_dtype w_dt, lrm_dtype g_dt, int32_t state_bits,
+                  bool copy, const lrm_adamw_hyper& p, cudaStream_t s);
+
 }  // namespace lrm
