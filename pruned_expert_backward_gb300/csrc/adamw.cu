@@ -25,7 +25,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBlock = 256;                 // elements of a warp at a time, and of a state's scale
 constexpr int kChunk = 8192;                // elements of a CTA's task
-constexpr int kTable = 128;                 // tensors of a launch (10 KB of parameters)
+constexpr int kTable = 384;                 // tensors of a launch (32 KB of parameters, the most there can be)
+constexpr int kAdamCtas = 4, kNormCtas = 8;  // of a multiprocessor
 constexpr float kStateLeast = 0x1p-120f;    // blocks of smaller states are scaled as if this were their largest
 
 struct Table {
@@ -120,7 +121,13 @@ __device__ __forceinline__ void store4(uint8_t* p, int64_t i, int64_t n, uint32_
   }
 }
 
-// The root for the update alone, a unit in the last place off.
+// The larger magnitude, NaN above all.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %2;\n\tmax.NaN.f32 %0, %1, t;\n\t}" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// The root, a unit in the last place off.
 __device__ __forceinline__ float sqrt_f(float v) {
   float r;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -134,12 +141,40 @@ __host__ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
   return h ^ (h >> 16);
 }
 
-// A magnitude y (448 and a little at most) as an e4m3 value, up or down at random: 16 random bits below the 4-bit
-// significand.  Values below the normal ones have the smallest normal one's spacing, so they are rounded with it added.
-__device__ __forceinline__ float to_grid(float y, uint32_t rnd16) {
-  const float shift = y < 0x1p-6f ? 0x1p-6f : 0.f;
-  const uint32_t up = (__float_as_uint(y + shift) + (rnd16 << 4)) & 0xfff00000u;
-  return fminf(__uint_as_float(up) - shift, kQTop);
+// Random rounding of a magnitude y (448 and a little at most) to an e4m3 value: 16 random bits are added below the
+// 4-bit significand, what stays below it is cut.  Values below the normal ones have the smallest normal one's spacing:
+// they are rounded with that one added.
+__device__ __forceinline__ float raised(float y, uint32_t rnd16) {
+  return __uint_as_float((__float_as_uint(y) + (rnd16 << 4)) & 0xfff00000u);
+}
+
+// The 8-bit states of a lane's two runs: y is |m| and sqrt(v) over their scales.
+template <bool TAIL, bool SMALL>
+__device__ __forceinline__ void store_states(const lrm_adamw_tensor& t, const int64_t (&i)[2], int64_t n,
+                                             const float (&m)[2][4], const float2 (&y)[2][4], uint32_t key) {
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    float qm[4], qv[4];
+    const uint32_t base = (uint32_t)i[s] * 0x9E3779B1u + (uint32_t)((uint64_t)i[s] >> 32) * 0xC2B2AE3Du + key;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t rnd = mix32(base + (uint32_t)j * 0x9E3779B1u);
+      float2 z = y[s][j];
+      if (SMALL) {
+        const float2 shift = make_float2(z.x < 0x1p-6f ? 0x1p-6f : 0.f, z.y < 0x1p-6f ? 0x1p-6f : 0.f);
+        z = __fadd2_rn(z, shift);
+        z = make_float2(raised(z.x, rnd & 0xffffu), raised(z.y, rnd >> 16));
+        z = __fadd2_rn(z, make_float2(-shift.x, -shift.y));
+        if (y[s][j].y > 0.f) z.y = fmaxf(z.y, 0x1p-9f);
+      } else {
+        z = make_float2(raised(z.x, rnd & 0xffffu), raised(z.y, rnd >> 16));
+      }
+      qm[j] = copysignf(z.x, m[s][j]);
+      qv[j] = z.y;
+    }
+    store4<TAIL>(static_cast<uint8_t*>(t.m), i[s], n, e4m3x4(qm[0], qm[1], qm[2], qm[3]));
+    store4<TAIL>(static_cast<uint8_t*>(t.v), i[s], n, e4m3x4(qv[0], qv[1], qv[2], qv[3]));
+  }
 }
 
 struct Hyper {
@@ -180,29 +215,61 @@ __device__ __forceinline__ void update_block(const lrm_adamw_tensor& t, int64_t 
       from_e4m3x4(mq[s], m[s]);
       from_e4m3x4(vq[s], v[s]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        m[s][j] *= ms;
-        v[s][j] *= vs;
-        v[s][j] *= v[s][j];
+      for (int j = 0; j < 4; j += 2) {
+        const float2 mm = __fmul2_rn(make_float2(m[s][j], m[s][j + 1]), make_float2(ms, ms));
+        const float2 rr = __fmul2_rn(make_float2(v[s][j], v[s][j + 1]), make_float2(vs, vs));
+        const float2 vv = __fmul2_rn(rr, rr);
+        m[s][j] = mm.x;
+        m[s][j + 1] = mm.y;
+        v[s][j] = vv.x;
+        v[s][j + 1] = vv.y;
       }
     }
   }
-  uint32_t top_m = 0, top_v = 0;
+  float top_m = 0.f, top_v = 0.f;
+  const float2 f2 = make_float2(factor, factor), b1 = make_float2(h.b1, h.b1), b2 = make_float2(h.b2, h.b2),
+               c1 = make_float2(h.one_b1, h.one_b1), c2 = make_float2(h.one_b2, h.one_b2);
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {  // two at a time: half the instructions
+      // (each step rounded by itself, so that a host program's fp32 repeats the states to the bit)
+      const float2 gf = __fmul2_rn(make_float2(g[s][j], g[s][j + 1]), f2);
+      float2 mm = make_float2(m[s][j], m[s][j + 1]), vv = make_float2(v[s][j], v[s][j + 1]);
+      mm = __fadd2_rn(__fmul2_rn(mm, b1), __fmul2_rn(gf, c1));
+      vv = __fadd2_rn(__fmul2_rn(vv, b2), __fmul2_rn(__fmul2_rn(gf, gf), c2));
+      m[s][j] = mm.x;
+      m[s][j + 1] = mm.y;
+      v[s][j] = vv.x;
+      v[s][j + 1] = vv.y;
+      if (BITS8) {
+        top_m = max_abs(max_abs(top_m, mm.x), mm.y);
+        top_v = max_abs(max_abs(top_v, vv.x), vv.y);
+      }
+    }
+  float tm = 0.f, tv = 0.f, rv = 0.f;  // of the block: largest m, v and sqrt(v)
+  if (BITS8) {  // (as bits a NaN is above every value)
+    tm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_m)));
+    tv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_v)));
+    rv = __fsqrt_rn(tv);
+  }
+  float r[2][4];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float gf = g[s][j] * factor;
-      // (each step rounded by itself, so that a host program's fp32 repeats the states to the bit)
-      m[s][j] = __fadd_rn(__fmul_rn(m[s][j], h.b1), __fmul_rn(gf, h.one_b1));
-      v[s][j] = __fadd_rn(__fmul_rn(v[s][j], h.b2), __fmul_rn(__fmul_rn(gf, gf), h.one_b2));
-      const float r = BITS8 ? __fsqrt_rn(v[s][j]) : sqrt_f(v[s][j]);
-      w[s][j] = fmaf(w[s][j], decay, -rate * __fdividef(m[s][j], fmaf(r, inv_c2, h.eps)));
-      if (BITS8) {
-        v[s][j] = r;
-        top_m = max(top_m, abs_bits(m[s][j]));
-        top_v = max(top_v, abs_bits(r));
-      }
+      r[s][j] = sqrt_f(v[s][j]);
+      if (BITS8 && v[s][j] == tv) r[s][j] = rv;  // the largest has its own scale's root, so that it is held as 448
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      const float2 den = __ffma2_rn(make_float2(r[s][j], r[s][j + 1]), make_float2(inv_c2, inv_c2),
+                                    make_float2(h.eps, h.eps));
+      const float2 up = make_float2(__fdividef(m[s][j], den.x), __fdividef(m[s][j + 1], den.y));
+      const float2 ww = __ffma2_rn(up, make_float2(-rate, -rate),
+                                   __fmul2_rn(make_float2(w[s][j], w[s][j + 1]), make_float2(decay, decay)));
+      w[s][j] = ww.x;
+      w[s][j + 1] = ww.y;
     }
     store4<TAIL>(static_cast<W*>(t.w), i[s], n, w[s]);
     if (COPY) store4<TAIL>(static_cast<__nv_bfloat16*>(t.copy), i[s], n, w[s]);
@@ -212,33 +279,32 @@ __device__ __forceinline__ void update_block(const lrm_adamw_tensor& t, int64_t 
     }
   }
   if (BITS8) {
-    const uint32_t least = __float_as_uint(kStateLeast);  // (as bits a NaN is above every value)
-    const float tm = __uint_as_float(max(__reduce_max_sync(0xffffffffu, top_m), least));
-    const float tv = __uint_as_float(max(__reduce_max_sync(0xffffffffu, top_v), least));
+    if (tm < kStateLeast) tm = kStateLeast;  // (a NaN stays)
+    if (rv < kStateLeast) rv = kStateLeast;
     if (lane == 0) {
       t.m_scale[i0 / kBlock] = tm * (1.f / kQTop);
-      t.v_scale[i0 / kBlock] = tv * (1.f / kQTop);
+      t.v_scale[i0 / kBlock] = rv * (1.f / kQTop);
     }
-    const float im = kQTop * __frcp_rn(tm), iv = kQTop * __frcp_rn(tv);
+    const float im = kQTop * __frcp_rn(tm), iv = kQTop * __frcp_rn(rv);
+    float2 y[2][4];  // m and sqrt(v) side by side
+    float least = kQTop;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      float qm[4], qv[4];
-      const uint32_t high = (uint32_t)((uint64_t)i[s] >> 32) * 0xC2B2AE3Du + key;
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t rnd = mix32(((uint32_t)i[s] + j) * 0x9E3779B1u + high);
-        qm[j] = copysignf(to_grid(fabsf(m[s][j]) * im, rnd & 0xffffu), m[s][j]);
-        const float z = to_grid(v[s][j] * iv, rnd >> 16);
-        qv[j] = v[s][j] > 0.f ? fmaxf(z, 0x1p-9f) : z;
+        y[s][j] = __fmul2_rn(make_float2(fabsf(m[s][j]), r[s][j]), make_float2(im, iv));
+        least = fminf(fminf(y[s][j].x, y[s][j].y), least);
       }
-      store4<TAIL>(static_cast<uint8_t*>(t.m), i[s], n, e4m3x4(qm[0], qm[1], qm[2], qm[3]));
-      store4<TAIL>(static_cast<uint8_t*>(t.v), i[s], n, e4m3x4(qv[0], qv[1], qv[2], qv[3]));
-    }
+    // most blocks have no value below e4m3's normal ones
+    if (__all_sync(0xffffffffu, least >= 0x1p-6f))
+      store_states<TAIL, false>(t, i, n, m, y, key);
+    else
+      store_states<TAIL, true>(t, i, n, m, y, key);
   }
 }
 
 template <typename W, typename G, bool BITS8, bool COPY>
-__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ Table a, const Hyper h) {
+__global__ void __launch_bounds__(kThreads, kAdamCtas) adamw_kernel(const __grid_constant__ Table a, const Hyper h) {
   chain_wait();
   __shared__ float s_lr, s_c1, s_c2, s_factor;
   __shared__ uint32_t s_step;
@@ -265,11 +331,20 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
   const float inv_c2 = __frsqrt_rn(s_c2), lr_c1 = __fdiv_rn(s_lr, s_c1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t chunks = a.first[a.count];
+  int ti = -1;
+  uint32_t t_first = 0, t_end = 0, key = 0;
+  float decay = 0.f, rate = 0.f;
   for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const lrm_adamw_tensor& t = a.t[tensor_of(a, c)];
-    const int64_t begin = (int64_t)(c - a.first[&t - a.t]) * kChunk, end = min(t.n, begin + kChunk);
-    const float decay = 1.f - s_lr * t.lr_scale * t.weight_decay, rate = lr_c1 * t.lr_scale;
-    const uint32_t key = mix32(mix32(h.seed + 0x9E3779B9u * (uint32_t)(t.id + 1)) ^ s_step);
+    if (c >= t_end) {  // (always at first)
+      ti = tensor_of(a, c);
+      t_first = a.first[ti];
+      t_end = a.first[ti + 1];
+      decay = 1.f - s_lr * a.t[ti].lr_scale * a.t[ti].weight_decay;
+      rate = lr_c1 * a.t[ti].lr_scale;
+      key = mix32(mix32(h.seed + 0x9E3779B9u * (uint32_t)(a.t[ti].id + 1)) ^ s_step);
+    }
+    const lrm_adamw_tensor& t = a.t[ti];
+    const int64_t begin = (int64_t)(c - t_first) * kChunk, end = min(t.n, begin + kChunk);
     for (int64_t i = begin + warp * kBlock; i < end; i += (kThreads / 32) * kBlock) {
       if (i + kBlock <= t.n)
         update_block<W, G, BITS8, COPY, false>(t, i, lane, h, factor, decay, rate, inv_c2, key);
@@ -359,8 +434,8 @@ void for_tables(const lrm_adamw_tensor* tensors, int32_t count, F&& f) {
   flush();
 }
 
-constexpr int kNormCtas = 8;   // a multiprocessor
-constexpr int kAdamCtas = 4;
+
+
 
 unsigned ctas(uint32_t chunks, int per_sm) {
   const uint32_t room = (uint32_t)(per_sm * sm_count());
