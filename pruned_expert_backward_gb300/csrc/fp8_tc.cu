@@ -128,25 +128,42 @@ __device__ __forceinline__ void mbar_arrive_one(uint32_t cbar) {
       "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cbar)
       : "memory");
 }
-// mbar_wait without a call: what the epilogue holds in registers stays there.  (With a poll at once after the first,
-// plain 32768 x 4096 x 4096 463 us, with the pause 447 us: the polls take issue slots from the warps at work.)
-__device__ __forceinline__ bool mbar_wait_here(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+__device__ __forceinline__ void mbar_arrive_one_cta(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+// Polls by a whole warp with one answer.
+__device__ __forceinline__ bool mbar_try_all(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "vote.sync.all.pred q, p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// The epilogue's wait: no call (what it holds in registers stays there), and nothing to test afterwards.  A wait that
+// gives up raises the abort flag, which the caller looks at once a run of slices; later waits then return at once.
+__device__ __forceinline__ void mbar_wait_here(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                                int32_t* status) {
-  if (mbar_try(bar, parity)) return true;
-  __nanosleep(20);
+  if (mbar_try_all(bar, parity)) return;
   uint64_t t0 = 0;
   for (uint32_t it = 0; it < (1u << 30); ++it) {
-    if (mbar_try(bar, parity)) return true;
+    if (mbar_try_all(bar, parity)) return;
     if ((it & 255u) == 255u) {
-      if (*abort_flag) return false;
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) return;
       const uint64_t now = globaltimer();
       if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitNs) break;
+      if (__any_sync(0xffffffffu, now - t0 > kWaitNs)) break;
     }
   }
   *abort_flag = 1;
   set_status(status, LRM_ERR_TIMEOUT);
-  return false;
 }
 
 // The waits of warps that are ahead of the others: they sleep between polls.  `last`: the wait for everything this
@@ -182,7 +199,8 @@ __device__ __forceinline__ void add8(float* v, uint4 r) {
 struct Box {
   uint8_t* box;
   int lane;
-  __device__ __forceinline__ uint4* piece(int j) const {  // 64-byte swizzle: piece j of row r sits at j ^ ((r >> 1) & 3)
+  // 64-byte swizzle: piece j of row r sits at j ^ ((r >> 1) & 3)
+  __device__ __forceinline__ uint4* piece(int j) const {
     return reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
   }
   __device__ __forceinline__ void put(const float (&v)[32], const CUtensorMap* map, int n, int cols, int row, int half,
@@ -339,17 +357,19 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
       // a row of the swizzle is 128 bytes: of K (rows of x and W), or of columns (DX: W's rows below one another)
       const uint64_t adesc0 = smem_desc(a0, 16, 1024), bdesc0 = smem_desc(b0, 16, 1024);
       constexpr uint64_t a_step = 32 >> 4, b_step = KIND == FWD ? (32 >> 4) : (32 * 128 >> 4);
-      uint32_t st = 0, sph = 0, acc = 0, aph = 0;  // operand stage and accumulator, with their phases
+      uint32_t st = 0, sph = 0, aph = ~0u;  // operand stage and its phase; phases of the accumulators, a bit each
       bool ok = true;
       for (int i = 0, t; i < rounds && ok; ++i) {
         t = nth_tile(i, pair, n_pairs);
         if (t >= n_tiles) continue;
         for (int kb = 0; kb < p.slices; ++kb) {
-          if (!mbar_wait_warp(acce0 + 8 * acc, aph ^ 1u, abortv, p.status) ||
+          const uint32_t acc = kb % ACCS;
+          if (!mbar_wait_warp(acce0 + 8 * acc, (aph >> acc) & 1u, abortv, p.status) ||
               !mbar_wait_warp(full0 + 8 * st, sph, abortv, p.status)) {
             ok = false;
             break;
           }
+          aph ^= 1u << acc;
           tc_fence_after();
           if (elect_one()) {
             const uint64_t soff = (uint64_t)((st * C::kStage) >> 4);
@@ -362,7 +382,6 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
           }
           __syncwarp();
           if (++st == (uint32_t)S) { st = 0; sph ^= 1u; }
-          if (++acc == (uint32_t)ACCS) { acc = 0; aph ^= 1u; }
         }
       }
       if (elect_one()) mma_commit_pair(drain);
@@ -419,9 +438,8 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
     const uint32_t quarter = tmem_base + ((uint32_t)(q * 32) << 16);
     const int NP = GLU ? 2 * p.N : p.N;
     const uint32_t scales_s = smem_u32(scales);
-    uint32_t a = 0, aph = 0, b = 0, bph = 0, rph = 0;  // accumulator, scales and residual, with their phases
-    bool ok = true;
-    for (int i = 0, t; i < rounds && ok; ++i) {
+    uint32_t aph = 0, b = 0, bph = 0, rph = 0;  // phases of the accumulators (a bit each), the scales and the residual
+    for (int i = 0, t; i < rounds; ++i) {
       t = nth_tile(i, pair, n_pairs);
       if (t >= n_tiles) continue;
       const Tile d = decode<BN, GLU>(p, prefix, t, rank);
@@ -445,49 +463,52 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
-      for (int kb = 0; kb < p.slices; ++kb) {
-        const int kr = kb % kRun;
-        if (kr == 0 && !mbar_wait_here(sf0 + 8 * b, bph, abortv, p.status)) { ok = false; break; }
-        const uint32_t at = scales_s + b * (uint32_t)sizeof(Scales);
-        const uint32_t wa = at + (uint32_t)offsetof(Scales, w) + kr * 16 + blk * 4;
-        const float sx = lds(at + (kr * (kBM + 4) + q * 32 + lane) * 4);
-        const float s0 = sx * lds(wa), s1 = GLU ? sx * lds(wa + 8) : s0;
-        if (kr == kRun - 1 || kb + 1 == p.slices) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(se0 + 8 * b);
-          b ^= 1u;
-          if (b == 0) bph ^= 1u;
-        }
-        if (!mbar_wait_here(accf0 + 8 * a, aph, abortv, p.status)) { ok = false; break; }
-        tc_fence_after();
-        __syncwarp();
-        const uint32_t tbase = quarter + a * BN;
+      bool ok = true;
+      for (int k0 = 0; k0 < p.slices; k0 += kRun) {
+        mbar_wait_here(sf0 + 8 * b, bph, abortv, p.status);
+        const uint32_t xa = scales_s + b * (uint32_t)sizeof(Scales) + (q * 32 + lane) * 4;
+        const uint32_t wa = scales_s + b * (uint32_t)sizeof(Scales) + (uint32_t)offsetof(Scales, w) + blk * 4;
+#pragma unroll 2  // (eight at a time spill)
+        for (int kr = 0; kr < min(kRun, p.slices - k0); ++kr) {
+          constexpr int kPitch = (int)sizeof(scales[0].x[0]);
+          const int a = kr % ACCS;  // (a tile starts at the first accumulator)
+          const float sx = lds(xa + kr * kPitch);
+          const float s0 = sx * lds(wa + kr * 16), s1 = GLU ? sx * lds(wa + kr * 16 + 8) : s0;
+          mbar_wait_here(accf0 + 8 * a, (aph >> a) & 1u, abortv, p.status);
+          aph ^= 1u << a;
+          tc_fence_after();
+          const uint32_t tbase = quarter + a * BN;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float r[16];
-          tmem_take16(tbase + (c < 2 ? col0 : col1) + (c & 1) * 16, r);
-          if (c == 3) {  // the accumulator goes back before its last columns are added
-            tc_fence_before();
-            mbar_arrive_one(acce_lead + 8 * a);
+          for (int c = 0; c < 4; ++c) {
+            float r[16];
+            tmem_take16(tbase + (c < 2 ? col0 : col1) + (c & 1) * 16, r);
+            if (c == 3) {  // the accumulator goes back before its last columns are added
+              tc_fence_before();
+              mbar_arrive_one(acce_lead + 8 * a);
+            }
+            add_scaled(acc[c >> 1] + (c & 1) * 16, r, c < 2 ? s0 : s1);
           }
-          add_scaled(acc[c >> 1] + (c & 1) * 16, r, c < 2 ? s0 : s1);
         }
-        if (++a == (uint32_t)ACCS) { a = 0; aph ^= 1u; }
+        mbar_arrive_one_cta(se0 + 8 * b);
+        b ^= 1u;
+        if (b == 0) bph ^= 1u;
+        if (__any_sync(0xffffffffu, *abortv != 0)) {
+          ok = false;
+          break;
+        }
       }
       if (!ok) {  // (the residual's copy lands before the CTA exits)
         if (RES && mine) mbar_wait(res_bar, rph, abortv, p.status, false);
         break;
       }
-      __syncwarp();
       if (!mine) continue;
       // without segments the output map ends where the rows end, so TMA clips a partial block
       const bool whole = nrows == 32 || p.seg == nullptr;
       const bool live = lane < nrows;
       const int64_t row = row_base + lane;
       if (RES) {
-        if (!mbar_wait_here(res_bar, rph, abortv, p.status)) break;
+        mbar_wait_here(res_bar, rph, abortv, p.status);
         rph ^= 1u;
-        __syncwarp();
       }
 #pragma unroll
       for (int c = 0; c < NO; ++c) {
@@ -510,7 +531,10 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
             const bool z_live = live || (whole && row < d.row_end);
             B16* z_row = static_cast<B16*>(p.z) + row * NP + n;
             box.put(v, &tmZ, n, p.N, row_base, 0, boxed, z_live, z_row);
-            if (GLU) Box{boxes + (C::kBoxes - 1) * kBoxBytes, lane}.put(acc[1], &tmZ, n, p.N, row_base, 1, boxed, z_live, z_row + p.N);
+            if (GLU) {
+              const Box up{boxes + (C::kBoxes - 1) * kBoxBytes, lane};
+              up.put(acc[1], &tmZ, n, p.N, row_base, 1, boxed, z_live, z_row + p.N);
+            }
           }
           if (GLU) {
 #pragma unroll
