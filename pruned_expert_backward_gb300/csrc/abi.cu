@@ -621,7 +621,7 @@ lrm_status lrm_fp8_quantize(const void* x, const int32_t* row_of_pair, int64_t T
   if (st) return st;
   if ((st = check_fp8_width(K))) return st;
   if ((st = check_dt(dt))) return st;
-  if (cap < 0 || cap > INT32_MAX || (!row_of_pair && (k != 1 || cap < T))) return LRM_ERR_INVALID_ARG;
+  if (cap < 0 || cap > INT32_MAX || (T > 0 && !row_of_pair && (k != 1 || cap < T))) return LRM_ERR_INVALID_ARG;
   if (T > 0 && (!x || (cap > 0 && (!q || !scale)))) return LRM_ERR_INVALID_ARG;
   if (!al16(x) || !al16(q) || !al4(scale) || !al4(row_of_pair)) return LRM_ERR_INVALID_ARG;
   if (T == 0 || (cap == 0 && !row_of_pair)) return LRM_OK;
@@ -712,17 +712,22 @@ lrm_status lrm_adamw(const lrm_adamw_tensor* tensors, int32_t count, lrm_dtype w
   if (copy && w_dt != LRM_F32) return LRM_ERR_DTYPE;
   const lrm_adamw_hyper& h = *hyper;
   // (written so that a NaN is refused)
-  if (!(h.beta1 >= 0 && h.beta1 < 1 && h.beta2 >= 0 && h.beta2 < 1 && h.eps >= 0 && h.lr >= 0)) return LRM_ERR_INVALID_ARG;
+  if (!(h.beta1 >= 0 && h.beta1 < 1 && h.beta2 >= 0 && h.beta2 < 1 && h.eps >= 0 && h.lr >= 0))
+    return LRM_ERR_INVALID_ARG;
   if (h.grad_norm && !(h.max_norm > 0)) return LRM_ERR_INVALID_ARG;
   if (!h.step_dev && (h.step < 1 || h.step > INT32_MAX)) return LRM_ERR_SHAPE;
   if (!al4(h.grad_norm) || !al4(h.lr_dev) || !al4(h.step_dev)) return LRM_ERR_INVALID_ARG;
+  bool any = false;
   for (int32_t i = 0; i < count; ++i) {
     const lrm_adamw_tensor& t = tensors[i];
     if (t.n == 0) continue;
+    any = true;
     if (!t.w || !t.g || !t.m || !t.v || (copy && !t.copy)) return LRM_ERR_INVALID_ARG;
     if (!al16(t.w) || !al16(t.copy) || !al16(t.g) || !al16(t.m) || !al16(t.v)) return LRM_ERR_INVALID_ARG;
-    if (state_bits == 8 && (!t.m_scale || !t.v_scale || !al4(t.m_scale) || !al4(t.v_scale))) return LRM_ERR_INVALID_ARG;
+    if (state_bits == 8 && (!t.m_scale || !t.v_scale || !al4(t.m_scale) || !al4(t.v_scale)))
+      return LRM_ERR_INVALID_ARG;
   }
+  if (!any) return LRM_OK;
   launch_adamw(tensors, count, w_dt, g_dt, state_bits, copy != 0, h, stream);
   return after_launch();
 }

@@ -136,8 +136,8 @@ class Case:
 
 
 HYPER = dict(lr=3e-4, betas=(0.9, 0.95), eps=1e-8)
-TYPES = [(BF16, F32, 8, False), (BF16, BF16, 8, False), (F32, F32, 8, False), (F32, BF16, 8, True), (BF16, F32, 32, False),
-         (BF16, BF16, 32, False), (F32, F32, 32, True), (F32, BF16, 32, False)]
+TYPES = [(BF16, F32, 8, False), (BF16, BF16, 8, False), (F32, F32, 8, False), (F32, BF16, 8, True),
+         (BF16, F32, 32, False), (BF16, BF16, 32, False), (F32, F32, 32, True), (F32, BF16, 32, False)]
 
 
 @pytest.mark.parametrize("types", TYPES, ids=str)
@@ -164,8 +164,8 @@ def test_many_tensors_with_clipping_and_their_own_rates(bits):
     factor = 0.5 / (norm + 1e-6)
     want = []
     for i in range(301):
-        one = c.expect(3e-4, 0.9, 0.95, 1e-8, decay[i], 3, factor, scale[i], only=i)[0] if sizes[i] and i % 10 == 0 else None
-        want.append(one)
+        wanted = sizes[i] > 0 and i % 10 == 0
+        want.append(c.expect(3e-4, 0.9, 0.95, 1e-8, decay[i], 3, factor, scale[i], only=i)[0] if wanted else None)
     opt = c.optimiser(lrm, **HYPER, weight_decay=decay, lr_scale=scale, max_norm=0.5, seed=5)
     got = opt.step(step=3)
     assert abs(got.item() / norm - 1) < 1e-6
@@ -210,7 +210,8 @@ def test_same_bits_again():
         opt = c.optimiser(lrm, **HYPER, max_norm=0.1, seed=3)
         opt.step()
         opt.step()
-        out.append([*c.w, *[a.view(torch.uint8) for k in ("m", "v") for a in c.state[k]], *c.state["m_scale"], opt.norm])
+        codes = [a.view(torch.uint8) for k in ("m", "v") for a in c.state[k]]
+        out.append([*c.w, *codes, *c.state["m_scale"], opt.norm])
     assert all(torch.equal(a, b) for a, b in zip(*out))
 
 
@@ -223,13 +224,15 @@ def test_random_rounding_keeps_the_mean():
     r = torch.full((n,), 0.3, device="cuda")
     r[::256] = 1.0  # the largest of each block, whose scale follows it exactly
     state = {"m": [torch.zeros(n, device="cuda").to(FP8)], "v": [(r * 448).to(FP8)],
-             "m_scale": [torch.zeros(n // 256, device="cuda")], "v_scale": [torch.full((n // 256,), 1 / 448, device="cuda")]}
+             "m_scale": [torch.zeros(n // 256, device="cuda")],
+             "v_scale": [torch.full((n // 256,), 1 / 448, device="cuda")]}
     start = values(state["v"][0], state["v_scale"][0])
     g = torch.zeros(n, device="cuda")
     big = torch.zeros(n, dtype=torch.bool, device="cuda")
     big[::256] = True
     g[big] = 1.0  # the largest stay at 1, so that the others shrink against their scale
-    opt = lrm.AdamW([torch.zeros(n, device="cuda")], [g], lr=0.0, betas=(0.9, 0.999), state_bits=8, state=state, seed=11)
+    opt = lrm.AdamW([torch.zeros(n, device="cuda")], [g], lr=0.0, betas=(0.9, 0.999), state_bits=8, state=state,
+                    seed=11)
     for _ in range(400):
         opt.step()
     now = values(state["v"][0], state["v_scale"][0])
@@ -374,7 +377,8 @@ def test_refusals():
     import pruned_expert_backward_gb300 as lrm
     w, g = torch.zeros(64, device="cuda"), torch.zeros(64, device="cuda")
     for call in (lambda: lrm.AdamW([], []), lambda: lrm.AdamW([w], [g], state_bits=16), lambda: lrm.AdamW([w], [g, g]),
-                 lambda: lrm.AdamW([w], [g[:32]]), lambda: lrm.AdamW([w.cpu()], [g]), lambda: lrm.AdamW([w], [g], max_norm=0),
+                 lambda: lrm.AdamW([w], [g[:32]]), lambda: lrm.AdamW([w.cpu()], [g]),
+                 lambda: lrm.AdamW([w], [g], max_norm=0),
                  lambda: lrm.AdamW([w], [g], weight_decay=[0.1, 0.2]), lambda: lrm.AdamW([w[::2]], [g[:32]]),
                  lambda: lrm.AdamW([w], [g], state={"m": [w[:3]], "v": [g]}), lambda: lrm.AdamW([w], [g]).step(step=0),
                  lambda: lrm.AdamW([w], [g], copies=[w[:5].bfloat16()]),

@@ -125,8 +125,8 @@ def test_quantize_extremes(dt, status):
 
 def test_quantize_to_sorted_rows(status):
     import pruned_expert_backward_gb300 as lrm
-    for T, k, E, K, masked in ((1, 8, 16, 256, 0.0), (50, 3, 7, 144, 0.3), (700, 8, 128, 1040, 0.1), (40, 16, 16, 16, 0.5),
-                               (9, 1, 4, 128, 0.0)):
+    for T, k, E, K, masked in ((1, 8, 16, 256, 0.0), (50, 3, 7, 144, 0.3), (700, 8, 128, 1040, 0.1),
+                               (40, 16, 16, 16, 0.5), (9, 1, 4, 128, 0.0)):
         g = gen(T)
         idx, _ = routing(g, T, k, E, masked=masked)
         x = randn(g, T, K)
@@ -154,7 +154,8 @@ def test_quantize_bad_rows_are_skipped():
 
 
 @pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("shape", [(8, 16), (128, 128), (136, 144), (3, 264, 1040), (40, 72, 16), (2, 1536, 512)], ids=str)
+@pytest.mark.parametrize("shape", [(8, 16), (128, 128), (136, 144), (3, 264, 1040), (40, 72, 16), (2, 1536, 512)],
+                         ids=str)
 def test_quantize_weight(shape, dt, status):
     import pruned_expert_backward_gb300 as lrm
     g = gen(sum(shape))
@@ -182,12 +183,18 @@ DENSE = [  # R, N, K, act, bias, residual, save_z
     (2, 72, 4112, "gelu", True, True, True), (5, 776, 64, "relu", False, True, False),
     (8, 4096, 1408, "none", True, True, False), (9, 136, 2048, "silu", True, True, True),
     (17, 264, 1040, "swiglu", False, True, True), (32, 520, 144, "silu", True, True, True),
-    (33, 16, 32, "swiglu", True, True, True), (33, 256, 256, "gelu", True, False, True), (70, 8, 16, "gelu", True, True, True),
+    (33, 16, 32, "swiglu", True, True, True), (33, 256, 256, "gelu", True, False, True),
+    (70, 8, 16, "gelu", True, True, True),
     (128, 256, 64, "swiglu", True, True, True), (129, 136, 80, "gelu", True, True, True),
     (257, 776, 1040, "swiglu", True, True, True), (300, 72, 2048, "relu", True, False, False),
     (1537, 776, 1040, "gelu", True, True, True), (3001, 1416, 528, "swiglu", True, False, True),
     (4096, 1024, 144, "silu", True, True, True), (4090, 512, 80, "swiglu", True, True, True),
     (2300, 136, 8208, "none", True, True, False),
+    # tiles of 64, 128 and 256 columns, with a residual and without, SwiGLU and not (the rule of launch_fp8_tc)
+    (300, 72, 272, "swiglu", True, False, True), (1000, 704, 144, "swiglu", True, True, True),
+    (1000, 704, 400, "swiglu", False, False, True), (1500, 776, 144, "gelu", True, False, False),
+    (4096, 1024, 272, "none", False, False, True), (4096, 512, 1168, "swiglu", False, False, False),
+    (4001, 1000, 2064, "gelu", True, True, True),
 ]
 
 
@@ -211,7 +218,8 @@ GROUPED = [  # R, E, segments, N, K, act, bias, residual, save_z
     (512, 128, "ragged", 264, 528, "swiglu", True, False, True), (512, 16, "one", 72, 144, "none", True, True, False),
     (1000, 3, "even", 520, 80, "silu", True, True, True), (2000, 7, "short", 264, 336, "swiglu", True, True, True),
     (5000, 40, "ragged", 392, 208, "relu", True, False, False), (3000, 1, "even", 136, 64, "swiglu", False, True, True),
-    (6000, 1024, "ragged", 72, 64, "none", True, False, False), (3501, 5, "ragged", 1024, 144, "gelu", True, True, True),
+    (6000, 1024, "ragged", 72, 64, "none", True, False, False),
+    (3501, 5, "ragged", 1024, 144, "gelu", True, True, True), (3501, 5, "ragged", 1024, 400, "none", False, False, True),
     (3501, 5, "short", 512, 144, "swiglu", True, True, True), (9000, 2, "ragged", 136, 80, "gelu", True, True, True),
 ]
 
@@ -281,7 +289,8 @@ def test_gradient_against_differences(status):
     d64 = operand(dz, ds, 1)
     left = (d64 * (up.double() - down.double())).sum(1) / 2
     right = (dx.double() * h.double()).sum(1)
-    slack = 2.0 ** -8 * ((d64.abs() * (up.abs() + down.abs()).double()).sum(1) / 2 + (dx.abs() * h.abs()).double().sum(1))
+    ends = (d64.abs() * (up.abs() + down.abs()).double()).sum(1) / 2
+    slack = 2.0 ** -8 * (ends + (dx.abs() * h.abs()).double().sum(1))
     assert bool(((left - right).abs() <= slack).all())
 
 
@@ -395,7 +404,8 @@ def test_refusals():
                  lambda: lrm.lrm_fp8_quantize(x, row_of_pair=torch.zeros(7, dtype=torch.int32, device="cuda"), k=2),
                  lambda: lrm.lrm_fp8_quantize_weight(x.view(-1)), lambda: lrm.lrm_fp8_linear(q, s[:5], w, ws),
                  lambda: lrm.lrm_fp8_linear(q, s, w, ws[:, :0]), lambda: lrm.lrm_fp8_linear(q[:, :32], s, w, ws),
-                 lambda: lrm.lrm_fp8_linear(q, s, w, ws, bias=x[0]), lambda: lrm.lrm_fp8_linear(q, s, w, ws, act="tanh"),
+                 lambda: lrm.lrm_fp8_linear(q, s, w, ws, bias=x[0]),
+                 lambda: lrm.lrm_fp8_linear(q, s, w, ws, act="tanh"),
                  lambda: lrm.lrm_fp8_linear(q, s, w, ws, residual=x), lambda: lrm.lrm_fp8_linear_backward(q, s, w, ws)):
         with pytest.raises(ValueError):
             call()
