@@ -500,22 +500,26 @@ def lrm_act_backward(dy, z, act="none", seg_offsets=None, bias_grad=True, dz=Non
 def lrm_linear_backward(dz, x, w, seg_offsets=None, need_dx=True, need_dw=True, dx=None, dw=None, ws=None,
                         flags=L.LRM_GEMM_DEFAULT, dev_status=None):
     """Gradients of lrm_linear's product from dz [R,N]: dx [R,K] = dz w and dw fp32 [N,K] = dz^T x ([E,N,K]
-    with seg_offsets).  Rows of no segment are not written: uninitialised memory in a dx made here.  Returns
-    (dx or None, dw or None)."""
+    with seg_offsets).  w may be None where dw alone is wanted and given.  Rows of no segment are not written:
+    uninitialised memory in a dx made here.  Returns (dx or None, dw or None)."""
     R, N = dz.shape
-    E, Nw, K = _experts(w, seg_offsets, "w")
+    if w is None:
+        if need_dx or dw is None:
+            raise ValueError("w may be None only with need_dx=False and a dw that gives the sizes")
+    like = dw if w is None else w
+    E, Nw, K = _experts(like, seg_offsets, "w")
     dt, dev = dz.dtype, dz.device
     dz_p, dt_code = _cuda(dz, "dz"), _dt(dz)
     if Nw != N:
         raise ValueError(f"dz has {N} columns, w {Nw} rows")
     _same(x, (R, K), "x")
     dx, dx_p = _out(dx, (R, K), dt, dev, "dx") if need_dx else (None, None)
-    dw, dw_p = _out(dw, tuple(w.shape), torch.float32, dev, "dw") if need_dw else (None, None)
+    dw, dw_p = _out(dw, tuple(like.shape), torch.float32, dev, "dw") if need_dw else (None, None)
     uses = (L.LRM_LINEAR_USE_DX if need_dx else 0) | (L.LRM_LINEAR_USE_DW if need_dw else 0)
     need = lrm_linear_workspace_size(R, E, N, K, "none", dt, uses) if ws is None and uses else 0
     ws, ws_p, ws_n = _scratch(ws, need, dev)
     _ok(L.load().lrm_linear_backward(_opt(seg_offsets, "seg_offsets", torch.int32), dz_p, _cuda(x, "x", dt),
-                                     _cuda(w, "w", dt), R, E, N, K, dt_code, dx_p, dw_p, ws_p, ws_n, int(flags),
+                                     _opt(w, "w", dt), R, E, N, K, dt_code, dx_p, dw_p, ws_p, ws_n, int(flags),
                                      _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_linear_backward")
     return dx, dw
 
@@ -737,25 +741,40 @@ class MoeLayer:
     """The expert layer around the routing, forward and unpruned backward, for one fixed problem size with
     every buffer allocated once.  forward: sort by expert, SwiGLU product, down product, weighted way back;
     backward: the gradients of x, alpha and both weights.  Everything is queued on the current stream; no
-    host synchronisation.  train=False keeps no state for the backward (serving)."""
+    host synchronisation.  train=False keeps no state for the backward (serving).
+    fp8=True: the products and their rows' gradients run in 8 bits (bf16 in and out, H and I multiples of 16).  Each
+    weight is then the pair that lrm_fp8_quantize_weight returns (w_gate_up with glu=True); the weights' gradients
+    are taken from the bf16 rows."""
 
-    def __init__(self, T, k, E, H, I, dtype=torch.bfloat16, device="cuda", flags=L.LRM_GEMM_DEFAULT, train=True):
+    def __init__(self, T, k, E, H, I, dtype=torch.bfloat16, device="cuda", flags=L.LRM_GEMM_DEFAULT, train=True,
+                 fp8=False):
         self.T, self.k, self.E, self.H, self.I = T, k, E, H, I
-        self.dtype, self.flags, self.train = dtype, flags, train
+        self.dtype, self.flags, self.train, self.fp8 = dtype, flags, train, fp8
+        if fp8 and (dtype != torch.bfloat16 or flags != L.LRM_GEMM_DEFAULT or H % 16 or I % 16):
+            raise ValueError("fp8=True is for bf16 layers with H and I multiples of 16, on the tensor cores")
         dev, P = torch.device(device), T * k
         i32 = dict(dtype=torch.int32, device=dev)
         new = dict(dtype=dtype, device=dev)
         self.seg_offsets = torch.empty(E + 1, **i32)
         self.pair_of_row = torch.empty(P, **i32)
         self.row_of_pair = torch.empty(P, **i32)
-        self.x_s, self.phi_s = torch.empty(P, H, **new), torch.empty(P, I, **new)
+        self.x_s = torch.empty(P, H, **new) if train or not fp8 else None
+        self.phi_s = torch.empty(P, I, **new)
         self.y_s, self.y = torch.empty(P, H, **new), torch.empty(T, H, **new)
         self.dev_status = torch.zeros(1, **i32)
-        uses = L.LRM_LINEAR_USE_FORWARD
+        uses = 0 if fp8 else L.LRM_LINEAR_USE_FORWARD
         if train:
-            uses |= L.LRM_LINEAR_USE_DX | L.LRM_LINEAR_USE_DW
-        ws = max(_sort_ws(T, k, E), lrm_linear_workspace_size(P, E, I, H, "swiglu", dtype, uses),
-                 lrm_linear_workspace_size(P, E, H, I, "none", dtype, uses))
+            uses |= L.LRM_LINEAR_USE_DW | (0 if fp8 else L.LRM_LINEAR_USE_DX)
+        ws = _sort_ws(T, k, E)
+        if uses:
+            ws = max(ws, lrm_linear_workspace_size(P, E, I, H, "swiglu", dtype, uses),
+                     lrm_linear_workspace_size(P, E, H, I, "none", dtype, uses))
+        if fp8:
+            def rows(cols, halves=1):
+                return (torch.empty(P, halves * cols, dtype=FP8, device=dev),
+                        torch.empty(P, halves * _qblocks(cols), dtype=torch.float32, device=dev))
+
+            self.xq, self.phiq = rows(H), rows(I)
         if train:
             self.h_s, self.dh_s = torch.empty(P, 2 * I, **new), torch.empty(P, 2 * I, **new)
             self.dy_s, self.dphi_s = torch.empty(P, H, **new), torch.empty(P, I, **new)
@@ -763,31 +782,52 @@ class MoeLayer:
             self.dalpha = torch.empty(T, k, dtype=torch.float32, device=dev)
             self.dw_gate_up = torch.empty(E, 2 * I, H, dtype=torch.float32, device=dev)
             self.dw_down = torch.empty(E, H, I, dtype=torch.float32, device=dev)
+            if fp8:
+                self.dyq, self.dhq = rows(H), rows(I, 2)
         self.ws = torch.empty(ws, dtype=torch.uint8, device=dev)
 
     def forward(self, x, topk_idx, alpha, w_gate_up, w_down, residual=None):
         """y [T,H] = residual + sum_j alpha[t,j] * w_down[e] SwiGLU(w_gate_up[e] x_t), e = topk_idx[t,j] (-1: none)."""
-        lrm_sort_tokens(topk_idx, x, self.E, seg_offsets=self.seg_offsets, pair_of_row=self.pair_of_row,
-                        row_of_pair=self.row_of_pair, x_s=self.x_s, ws=self.ws, dev_status=self.dev_status)
-        lrm_linear(self.x_s, w_gate_up, act="swiglu", seg_offsets=self.seg_offsets, y=self.phi_s,
-                   z=self.h_s if self.train else None, ws=self.ws, flags=self.flags, dev_status=self.dev_status)
-        lrm_linear(self.phi_s, w_down, seg_offsets=self.seg_offsets, y=self.y_s, ws=self.ws, flags=self.flags,
-                   dev_status=self.dev_status)
-        return lrm_combine(self.row_of_pair, alpha, self.y_s, residual=residual, y=self.y, dev_status=self.dev_status)
+        seg, st = self.seg_offsets, dict(dev_status=self.dev_status)
+        # (serving in 8 bits, no row is copied in bf16: a token is rounded once, straight to its rows)
+        lrm_sort_tokens(topk_idx, x if self.x_s is not None else None, self.E, seg_offsets=seg,
+                        pair_of_row=self.pair_of_row, row_of_pair=self.row_of_pair, x_s=self.x_s, ws=self.ws, **st)
+        z = self.h_s if self.train else None
+        if self.fp8:
+            xq, phiq = self.xq, self.phiq
+            lrm_fp8_quantize(x, row_of_pair=self.row_of_pair, k=self.k, q=xq[0], scale=xq[1], **st)
+            lrm_fp8_linear(*xq, *w_gate_up, act="swiglu", seg_offsets=seg, y=self.phi_s, z=z, **st)
+            lrm_fp8_quantize(self.phi_s, q=phiq[0], scale=phiq[1], **st)
+            lrm_fp8_linear(*phiq, *w_down, seg_offsets=seg, y=self.y_s, **st)
+        else:
+            lrm_linear(self.x_s, w_gate_up, act="swiglu", seg_offsets=seg, y=self.phi_s, z=z, ws=self.ws,
+                       flags=self.flags, **st)
+            lrm_linear(self.phi_s, w_down, seg_offsets=seg, y=self.y_s, ws=self.ws, flags=self.flags, **st)
+        return lrm_combine(self.row_of_pair, alpha, self.y_s, residual=residual, y=self.y, **st)
 
     def backward(self, dy, alpha, w_gate_up, w_down):
         """Gradients of the last forward: dx [T,H], dalpha [T,k], dw_gate_up, dw_down (the residual's is dy)."""
         if not self.train:
             raise ValueError("MoeLayer(train=False) keeps no state for a backward")
-        seg, kw = self.seg_offsets, dict(ws=self.ws, dev_status=self.dev_status)
-        lrm_combine_backward(self.row_of_pair, alpha, dy, self.y_s, dy_s=self.dy_s, dalpha=self.dalpha,
-                             dev_status=self.dev_status)
-        lrm_linear_backward(self.dy_s, self.phi_s, w_down, seg_offsets=seg, dx=self.dphi_s, dw=self.dw_down,
-                            flags=self.flags, **kw)
+        seg, st, kw = self.seg_offsets, dict(dev_status=self.dev_status), dict(ws=self.ws, dev_status=self.dev_status)
+        lrm_combine_backward(self.row_of_pair, alpha, dy, self.y_s, dy_s=self.dy_s, dalpha=self.dalpha, **st)
+        if self.fp8:
+            dyq, dhq = self.dyq, self.dhq
+            lrm_linear_backward(self.dy_s, self.phi_s, None, seg_offsets=seg, need_dx=False, dw=self.dw_down, **kw)
+            lrm_fp8_quantize(self.dy_s, q=dyq[0], scale=dyq[1], **st)
+            lrm_fp8_linear_backward(*dyq, *w_down, seg_offsets=seg, dx=self.dphi_s, **st)
+        else:
+            lrm_linear_backward(self.dy_s, self.phi_s, w_down, seg_offsets=seg, dx=self.dphi_s, dw=self.dw_down,
+                                flags=self.flags, **kw)
         lrm_act_backward(self.dphi_s, self.h_s, act="swiglu", seg_offsets=seg, bias_grad=False, dz=self.dh_s, **kw)
-        lrm_linear_backward(self.dh_s, self.x_s, w_gate_up, seg_offsets=seg, dx=self.dx_s, dw=self.dw_gate_up,
-                            flags=self.flags, **kw)
-        lrm_scatter_dx(self.row_of_pair, self.dx_s, self.T, self.k, dx=self.dx, dev_status=self.dev_status)
+        if self.fp8:
+            lrm_linear_backward(self.dh_s, self.x_s, None, seg_offsets=seg, need_dx=False, dw=self.dw_gate_up, **kw)
+            lrm_fp8_quantize(self.dh_s, glu=True, q=dhq[0], scale=dhq[1], **st)
+            lrm_fp8_linear_backward(*dhq, *w_gate_up, glu=True, seg_offsets=seg, dx=self.dx_s, **st)
+        else:
+            lrm_linear_backward(self.dh_s, self.x_s, w_gate_up, seg_offsets=seg, dx=self.dx_s, dw=self.dw_gate_up,
+                                flags=self.flags, **kw)
+        lrm_scatter_dx(self.row_of_pair, self.dx_s, self.T, self.k, dx=self.dx, **st)
         return self.dx, self.dalpha, self.dw_gate_up, self.dw_down
 
 
