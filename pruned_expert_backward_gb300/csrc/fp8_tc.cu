@@ -9,8 +9,8 @@
 // at the next.
 //
 // CTA pairs and tiles are those of linear_tc.cu: 256 x BN tiles over a persistent grid.  Warp 0 issues the TMA loads,
-// warp 1 of the leader the MMAs, warps 2 and 3 bring the scales to shared memory, the rest are the epilogue: each has a
-// 32-row quarter of TMEM by 64 columns (SwiGLU: 32 gate columns and the 32 up columns that go with them), which lie in
+// warp 1 of the leader the MMAs, warps 2 and 3 bring the tile's place and its scales to shared memory, the rest are the
+// epilogue: each has a 32-row quarter of TMEM by 64 columns (SwiGLU: 32 gate columns and the 32 up columns that go with them), which lie in
 // one block of 128 columns of W.
 //
 // W stays as it was quantised: FWD reads its rows K-major, DX the same bytes with the columns contiguous (MN-major).
@@ -40,6 +40,7 @@ constexpr int kRun = 8;
 struct Scales {
   float x[kRun][kBM + 4];  // (the pad keeps the writing lanes' eight slices of four rows off each other's banks)
   float w[kRun][4];        // of the tile's two blocks of columns; SwiGLU: of the gate columns', then of the up columns'
+  int tile[4];             // e, row0, row_end, n0 of the tile
 };
 
 template <int KIND, int BN, bool RES>
@@ -119,6 +120,7 @@ __device__ __forceinline__ float lds(uint32_t at) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
   return v;
 }
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -148,16 +150,17 @@ __device__ __forceinline__ bool mbar_try_all(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// The epilogue's wait: no call (what it holds in registers stays there), and nothing to test afterwards.  A wait that
-// gives up raises the abort flag, which the caller looks at once a run of slices; later waits then return at once.
-__device__ __forceinline__ void mbar_wait_here(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+// The waits of the MMA warp and the epilogue: no call (what they hold in registers stays there), and no clock read
+// before the first 256 polls.  The epilogue does not test the answer: a wait that gives up raises the abort flag, which
+// it looks at once a run of slices; later waits then return at once.
+__device__ __forceinline__ bool mbar_wait_here(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                                int32_t* status) {
-  if (mbar_try_all(bar, parity)) return;
+  if (mbar_try_all(bar, parity)) return true;
   uint64_t t0 = 0;
   for (uint32_t it = 0; it < (1u << 30); ++it) {
-    if (mbar_try_all(bar, parity)) return;
+    if (mbar_try_all(bar, parity)) return true;
     if ((it & 255u) == 255u) {
-      if (__any_sync(0xffffffffu, *abort_flag != 0)) return;
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
       const uint64_t now = globaltimer();
       if (t0 == 0) t0 = now;
       if (__any_sync(0xffffffffu, now - t0 > kWaitNs)) break;
@@ -165,6 +168,7 @@ __device__ __forceinline__ void mbar_wait_here(uint32_t bar, uint32_t parity, vo
   }
   *abort_flag = 1;
   set_status(status, LRM_ERR_TIMEOUT);
+  return false;
 }
 
 // The waits of warps that are ahead of the others: they sleep between polls.  `last`: the wait for everything this
@@ -232,7 +236,16 @@ struct Box {
 template <int ACT>
 __device__ __forceinline__ void act_all(float (&v)[32]) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = act_value<ACT>(v[i]);
+  for (int i = 0; i < 32; i += 2) {
+    if (ACT == LRM_ACT_GELU) {
+      const float2 r = gelu2(make_float2(v[i], v[i + 1]));
+      v[i] = r.x;
+      v[i + 1] = r.y;
+    } else {
+      v[i] = act_value<ACT>(v[i]);
+      v[i + 1] = act_value<ACT>(v[i + 1]);
+    }
+  }
 }
 
 struct Tile {
@@ -365,8 +378,8 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
         if (t >= n_tiles) continue;
         for (int kb = 0; kb < p.slices; ++kb) {
           const uint32_t acc = kb % ACCS;
-          if (!mbar_wait_warp(acce0 + 8 * acc, (aph >> acc) & 1u, abortv, p.status) ||
-              !mbar_wait_warp(full0 + 8 * st, sph, abortv, p.status)) {
+          if (!mbar_wait_here(full0 + 8 * st, sph, abortv, p.status) ||
+              !mbar_wait_here(acce0 + 8 * acc, (aph >> acc) & 1u, abortv, p.status)) {
             ok = false;
             break;
           }
@@ -422,6 +435,8 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < kBM / 8; ++j) to.x[lk][part * (kBM / 2) + lr + 4 * j] = v[j];
         if (part == 0) to.w[lk][lr] = w;
+        if (part == 1 && lane == 0)
+          *reinterpret_cast<int4*>(to.tile) = make_int4(d.e, d.has_rows ? d.row0 : d.row_end, d.row_end, d.n0);
         __syncwarp();
         if (lane == 0) mbar_arrive(sf0 + 8 * b);
         b ^= 1u;
@@ -440,15 +455,20 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
     const int NP = GLU ? 2 * p.N : p.N;
     const uint32_t scales_s = smem_u32(scales);
     uint32_t aph = 0, b = 0, bph = 0, rph = 0;  // phases of the accumulators (a bit each), the scales and the residual
-    for (int i = 0, t; i < rounds; ++i) {
-      t = nth_tile(i, pair, n_pairs);
-      if (t >= n_tiles) continue;
-      const Tile d = decode<BN, GLU>(p, prefix, t, rank);
-      const int row_base = d.row0 + q * 32, n_first = d.n0 + group * NO * 32;
+    for (int i = 0; i < rounds; ++i) {
+      if (nth_tile(i, pair, n_pairs) >= n_tiles) continue;
+      float acc[2][32];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
+      // the tile comes with its first scales (segment bounds are a trip to memory, which the scale warps make ahead)
+      if (!mbar_wait_here(sf0 + 8 * b, bph, abortv, p.status)) break;
+      const int4 d = *reinterpret_cast<const int4*>(scales[b].tile);  // expert, first and last row, first column
+      const int row_base = d.y + q * 32, n_first = d.w + group * NO * 32;
       // (the check, where it is on, covers what this warp's stores address: the expert, and its first and last row)
-      const int nrows = d.has_rows && LRM_DCHECK(d.e >= 0 && d.e < p.E && row_base >= 0 && d.row_end <= p.R, p.status,
-                                                 LRM_ERR_BAD_INDEX)
-                            ? min(32, d.row_end - row_base)
+      const int nrows = LRM_DCHECK(d.x >= 0 && d.x < p.E && row_base >= 0 && d.z <= p.R, p.status, LRM_ERR_BAD_INDEX)
+                            ? min(32, d.z - row_base)
                             : 0;
       const bool mine = nrows > 0 && n_first < p.N;  // warp-uniform: this warp has output
       if (RES && mine && lane == 0) {  // the residual comes into the boxes meanwhile
@@ -458,15 +478,17 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
         for (int c = 0; c < NO; ++c)
           tma_load_3d_cta(smem_u32(boxes) + c * kBoxBytes, &tmR, n_first + c * 32, row_base, 0, res_bar);
       }
-      const int blk = n_first / kQBlock - d.n0 / kQBlock;  // 0 or 1
-      float acc[2][32];
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
+      const B16* bias = KIND == FWD && p.bias != nullptr
+                            ? static_cast<const B16*>(p.bias) + (int64_t)d.x * NP + n_first
+                            : nullptr;
+      if (bias != nullptr && mine) {  // on its way meanwhile
+        prefetch_l1(bias);
+        if (GLU) prefetch_l1(bias + p.N);
+      }
+      const int blk = n_first / kQBlock - d.w / kQBlock;  // 0 or 1
       bool ok = true;
       for (int k0 = 0; k0 < p.slices; k0 += kRun) {
-        mbar_wait_here(sf0 + 8 * b, bph, abortv, p.status);
+        if (k0 > 0) mbar_wait_here(sf0 + 8 * b, bph, abortv, p.status);
         const uint32_t xa = scales_s + b * (uint32_t)sizeof(Scales) + (q * 32 + lane) * 4;
         const uint32_t wa = scales_s + b * (uint32_t)sizeof(Scales) + (uint32_t)offsetof(Scales, w) + blk * 4;
 #pragma unroll 2  // (eight at a time spill)
@@ -518,18 +540,17 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
         float(&v)[32] = acc[c];
         const Box box{boxes + (C::kBoxes > 1 ? c * kBoxBytes : 0), lane};
         if (KIND == FWD) {
-          if (p.bias != nullptr) {
-            const B16* bias = static_cast<const B16*>(p.bias) + (int64_t)d.e * NP + n;
+          if (bias != nullptr) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (n + 8 * j < p.N) {
-                add8(v + 8 * j, ldg16(bias + 8 * j));
+                add8(v + 8 * j, ldg16(bias + c * 32 + 8 * j));
                 if (GLU) add8(acc[1] + 8 * j, ldg16(bias + p.N + 8 * j));
               }
           }
           if (p.z != nullptr) {  // (where the box holds the residual, from the registers)
             const bool boxed = whole && !RES;
-            const bool z_live = live || (whole && row < d.row_end);
+            const bool z_live = live || (whole && row < d.z);
             B16* z_row = static_cast<B16*>(p.z) + row * NP + n;
             box.put(v, &tmZ, n, p.N, row_base, 0, boxed, z_live, z_row);
             if (GLU) {
