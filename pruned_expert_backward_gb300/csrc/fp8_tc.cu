@@ -38,23 +38,27 @@ enum Kind { FWD = 0, DX = 1 };
 // The scales of a tile's rows and columns for the next kRun K slices, two of them in turn.
 constexpr int kRun = 8;
 struct Scales {
-  float x[kRun][kBM + 4];  // (the pad keeps the writing lanes' eight slices of four rows off each other's banks)
-  float w[kRun][4];        // of the tile's two blocks of columns; SwiGLU: of the gate columns', then of the up columns'
-  int tile[4];             // e, row0, row_end, n0 of the tile
+  // a row's scale times that of each of the tile's two blocks of columns; SwiGLU: of the gate's, then of the up columns'
+  // (the pad keeps the writing lanes' eight slices of four rows off each other's banks)
+  float xw[2][kRun][kBM + 4];
+  int tile[4];  // e, row0, row_end, n0 of the tile
 };
 
-template <int KIND, int BN, bool RES>
+template <int BN, bool GLU, bool RES>
 struct Cfg {
   static constexpr int kABytes = kBM * kBK;
   static constexpr int kBBytes = BN / 2 * kBK;  // this CTA's half of the columns
   static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kBoxes = BN == 256 && !RES ? 1 : 2;  // of an epilogue warp; the residual comes into both
-  static constexpr int kStages = BN == 256 ? (RES ? 4 : 5) : 6;
+  // SwiGLU's 32 columns a warp leave room for a fifth stage (65536 rows over 128 experts to 2 x 768, K = 2048: 246 us,
+  // with four and a second box 250 us; with z 280 and 290 us)
+  static constexpr bool kOneBox = BN == 256 && GLU && !RES;
+  static constexpr int kStages = BN == 256 ? (kOneBox ? 5 : 4) : 6;
+  static constexpr int kEpiBytes = kOneBox ? kBoxBytes : 2 * kBoxBytes;  // of an epilogue warp
   static constexpr int kEpiWarps = BN / 16;
   static constexpr int kThreads = 128 + 32 * kEpiWarps;
   static constexpr int kAccs = 512 / BN;  // all of TMEM
   static constexpr uint32_t kEpi = kStages * kStage;
-  static constexpr uint32_t kScales = kEpi + kEpiWarps * kBoxes * kBoxBytes;
+  static constexpr uint32_t kScales = kEpi + kEpiWarps * kEpiBytes;
   static constexpr uint32_t kBars = kScales + 2 * sizeof(Scales);
   // full, empty; accumulator full, empty; scales full[2], empty[2]; drain; residual of each epilogue warp
   static constexpr int kNBars = 2 * kStages + 2 * kAccs + 5 + kEpiWarps;
@@ -199,37 +203,40 @@ __device__ __forceinline__ void add8(float* v, uint4 r) {
   for (int i = 0; i < 8; ++i) v[i] += f[i];
 }
 
-// 32 columns of one row per lane go out in bf16: whole 32-row blocks through a swizzled box of the warp and TMA (which
-// clips columns past the tensor), others by each live lane.
-struct Box {
+// A warp's 32 rows of bf16 output, a row per lane: whole 32-row blocks go through shared memory and TMA (which clips
+// columns past the tensor), others by each live lane.  WIDE: in one box of 64 columns, else in boxes of 32.
+template <bool WIDE>
+struct Boxes {
   uint8_t* box;
   int lane;
-  // 64-byte swizzle: piece j of row r sits at j ^ ((r >> 1) & 3)
-  __device__ __forceinline__ uint4* piece(int j) const {
-    return reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
+  // 128-byte swizzle: piece j of row r sits at j ^ (r & 7); 64-byte swizzle: at j ^ ((r >> 1) & 3)
+  __device__ __forceinline__ uint4* piece(int c, int j) const {
+    return WIDE ? reinterpret_cast<uint4*>(box + lane * 128 + (((4 * c + j) ^ (lane & 7)) << 4))
+                : reinterpret_cast<uint4*>(box + c * kBoxBytes + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
   }
-  __device__ __forceinline__ void put(const float (&v)[32], const CUtensorMap* map, int n, int cols, int row, int half,
-                                      bool whole, bool live, B16* at) const {
-    if (whole) {  // warp-uniform
-      if (lane == 0) bulk_wait_read<0>();  // the last store has read the box
-      __syncwarp();
-    }
+  __device__ __forceinline__ void free() const {  // the last stores have read the boxes
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+  }
+  // 32 columns into chunk c, or to memory
+  __device__ __forceinline__ void put(const float (&v)[32], int c, int n, int cols, bool whole, bool live,
+                                      B16* at) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float f[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = v[8 * j + i];
       const uint4 q = pack(f);
-      if (whole)
-        *piece(j) = q;
+      if (whole)  // warp-uniform
+        *piece(c, j) = q;
       else if (live && n + 8 * j < cols)
         st16(at + 8 * j, q);
     }
-    if (whole) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tma_store_3d(map, smem_u32(box), n, row, half);
-    }
+  }
+  __device__ __forceinline__ void send(const CUtensorMap* map, int c, int n, int row, int half) const {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) tma_store_3d(map, smem_u32(box + c * kBoxBytes), n, row, half);
   }
 };
 
@@ -275,11 +282,11 @@ __device__ __forceinline__ Tile decode(const Params& p, const int* prefix, int t
 }
 
 template <int KIND, int BN, bool GLU, bool RES>
-__global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<BN, GLU, RES>::kThreads, 1)
     fp8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ,
                   const __grid_constant__ CUtensorMap tmR, const Params p) {
-  using C = Cfg<KIND, BN, RES>;
+  using C = Cfg<BN, GLU, RES>;
   constexpr int S = C::kStages, ACCS = C::kAccs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -412,29 +419,35 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
       t = nth_tile(i, pair, n_pairs);
       if (t >= n_tiles) continue;
       const Tile d = decode<BN, GLU>(p, prefix, t, rank);
-      // the block of W's columns that this lane brings (columns past the last have any)
-      const int blk = min(d.n0 / kQBlock + (lr & 1), p.w_rows - 1);
+      // the tile's blocks of W's columns (columns past the last have any)
+      const int blk0 = d.n0 / kQBlock, blk1 = min(blk0 + 1, p.w_rows - 1);
       for (int k0 = 0; k0 < p.slices; k0 += kRun) {
         if (!mbar_wait_ahead(se0 + 8 * b, bph ^ 1u, abortv, p.status, false)) { ok = false; break; }
         const int k = k0 + lk;
-        float v[kBM / 8];
+        float v[kBM / 8], w0 = 0.f, w1 = 0.f;
         const float* sx = p.x_scale + (int64_t)(d.row0 + part * (kBM / 2) + lr) * p.slices + k;
 #pragma unroll
         for (int j = 0; j < kBM / 8; ++j) {
           const int row = d.row0 + part * (kBM / 2) + lr + 4 * j;
           v[j] = k < p.slices && row < d.row_end ? __ldg(sx + (int64_t)(4 * j) * p.slices) : 0.f;
         }
-        float w = 0.f;
-        if (part == 0 && (GLU || lr < 2) && k < p.slices) {
-          if (KIND == DX)
-            w = __ldg(p.w_scale + ((int64_t)d.e * p.slices + k) * p.w_rows + blk);
-          else
-            w = __ldg(p.w_scale + ((int64_t)(GLU ? d.e * 2 + (lr >> 1) : d.e) * p.w_rows + blk) * p.slices + k);
+        if (k < p.slices) {
+          if (KIND == DX) {
+            const float* w = p.w_scale + ((int64_t)d.e * p.slices + k) * p.w_rows;
+            w0 = __ldg(w + blk0);
+            w1 = __ldg(w + blk1);
+          } else {
+            const float* w = p.w_scale + (int64_t)(GLU ? d.e * 2 : d.e) * p.w_rows * p.slices + k;
+            w0 = __ldg(w + (int64_t)blk0 * p.slices);
+            w1 = __ldg(w + (int64_t)(GLU ? p.w_rows + blk0 : blk1) * p.slices);
+          }
         }
         Scales& to = scales[b];
 #pragma unroll
-        for (int j = 0; j < kBM / 8; ++j) to.x[lk][part * (kBM / 2) + lr + 4 * j] = v[j];
-        if (part == 0) to.w[lk][lr] = w;
+        for (int j = 0; j < kBM / 8; ++j) {
+          to.xw[0][lk][part * (kBM / 2) + lr + 4 * j] = v[j] * w0;
+          to.xw[1][lk][part * (kBM / 2) + lr + 4 * j] = v[j] * w1;
+        }
         if (part == 1 && lane == 0)
           *reinterpret_cast<int4*>(to.tile) = make_int4(d.e, d.has_rows ? d.row0 : d.row_end, d.row_end, d.n0);
         __syncwarp();
@@ -446,8 +459,9 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
   } else {
     // ---------------------------------------------------------------- epilogue --------
     constexpr int NO = GLU ? 1 : 2;  // 32-column chunks of output of a warp
+    constexpr int kBlock = (int)sizeof(scales[0].xw[0]);
     const int ew = warp - 4, q = warp & 3, group = ew >> 2;
-    uint8_t* boxes = smem + C::kEpi + ew * C::kBoxes * kBoxBytes;
+    uint8_t* boxes = smem + C::kEpi + ew * C::kEpiBytes;
     const uint32_t res_bar = res0 + 8 * ew;
     // TMEM columns of the warp's two chunks (SwiGLU: gate, up)
     const uint32_t col0 = group * NO * 32, col1 = GLU ? BN / 2 + group * 32 : col0 + 32;
@@ -474,9 +488,7 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
       if (RES && mine && lane == 0) {  // the residual comes into the boxes meanwhile
         bulk_wait_read<0>();
         mbar_expect_tx(res_bar, NO * kBoxBytes);
-#pragma unroll
-        for (int c = 0; c < NO; ++c)
-          tma_load_3d_cta(smem_u32(boxes) + c * kBoxBytes, &tmR, n_first + c * 32, row_base, 0, res_bar);
+        tma_load_3d_cta(smem_u32(boxes), &tmR, n_first, row_base, 0, res_bar);
       }
       const B16* bias = KIND == FWD && p.bias != nullptr
                             ? static_cast<const B16*>(p.bias) + (int64_t)d.x * NP + n_first
@@ -489,14 +501,12 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
       bool ok = true;
       for (int k0 = 0; k0 < p.slices; k0 += kRun) {
         if (k0 > 0) mbar_wait_here(sf0 + 8 * b, bph, abortv, p.status);
-        const uint32_t xa = scales_s + b * (uint32_t)sizeof(Scales) + (q * 32 + lane) * 4;
-        const uint32_t wa = scales_s + b * (uint32_t)sizeof(Scales) + (uint32_t)offsetof(Scales, w) + blk * 4;
+        const uint32_t xa = scales_s + b * (uint32_t)sizeof(Scales) + (GLU ? 0 : blk * kBlock) + (q * 32 + lane) * 4;
 #pragma unroll 2  // (eight at a time spill)
         for (int kr = 0; kr < min(kRun, p.slices - k0); ++kr) {
-          constexpr int kPitch = (int)sizeof(scales[0].x[0]);
+          constexpr int kPitch = (int)sizeof(scales[0].xw[0][0]);
           const int a = kr % ACCS;  // (a tile starts at the first accumulator)
-          const float sx = lds(xa + kr * kPitch);
-          const float s0 = sx * lds(wa + kr * 16), s1 = GLU ? sx * lds(wa + kr * 16 + 8) : s0;
+          const float s0 = lds(xa + kr * kPitch), s1 = GLU ? lds(xa + kBlock + kr * kPitch) : s0;
           mbar_wait_here(accf0 + 8 * a, (aph >> a) & 1u, abortv, p.status);
           aph ^= 1u << a;
           tc_fence_after();
@@ -533,31 +543,32 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
         mbar_wait_here(res_bar, rph, abortv, p.status);
         rph ^= 1u;
       }
+      const Boxes<!GLU> out{boxes, lane};
+      if (KIND == FWD && bias != nullptr) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (n_first + (GLU ? 0 : c * 32) + 8 * j < p.N)
+              add8(acc[c] + 8 * j, ldg16(bias + (GLU ? c * p.N : c * 32) + 8 * j));
+      }
+      if (KIND == FWD && p.z != nullptr) {  // (where the boxes hold the residual, from the registers)
+        const bool boxed = whole && !RES;
+        const bool z_live = live || (whole && row < d.z);
+        B16* z_row = static_cast<B16*>(p.z) + row * NP + n_first;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int at = C::kOneBox ? 0 : c;
+          if (boxed && (c == 0 || C::kOneBox)) out.free();
+          out.put(acc[c], at, n_first + (GLU ? 0 : c * 32), p.N, boxed, z_live, z_row + (GLU ? c * p.N : c * 32));
+          if (boxed && (c == 1 || GLU)) out.send(&tmZ, GLU ? at : 0, n_first, row_base, GLU ? c : 0);
+        }
+      }
+      if (whole && !RES) out.free();
 #pragma unroll
       for (int c = 0; c < NO; ++c) {
-        const int n = n_first + c * 32;
-        if (n >= p.N) break;  // warp-uniform
         float(&v)[32] = acc[c];
-        const Box box{boxes + (C::kBoxes > 1 ? c * kBoxBytes : 0), lane};
         if (KIND == FWD) {
-          if (bias != nullptr) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (n + 8 * j < p.N) {
-                add8(v + 8 * j, ldg16(bias + c * 32 + 8 * j));
-                if (GLU) add8(acc[1] + 8 * j, ldg16(bias + p.N + 8 * j));
-              }
-          }
-          if (p.z != nullptr) {  // (where the box holds the residual, from the registers)
-            const bool boxed = whole && !RES;
-            const bool z_live = live || (whole && row < d.z);
-            B16* z_row = static_cast<B16*>(p.z) + row * NP + n;
-            box.put(v, &tmZ, n, p.N, row_base, 0, boxed, z_live, z_row);
-            if (GLU) {
-              const Box up{boxes + (C::kBoxes - 1) * kBoxBytes, lane};
-              up.put(acc[1], &tmZ, n, p.N, row_base, 1, boxed, z_live, z_row + p.N);
-            }
-          }
           if (GLU) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = act_value<LRM_ACT_SWIGLU>(v[j]) * acc[1][j];
@@ -571,10 +582,11 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, RES>::kThreads, 1)
           }
           if (RES)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) add8(v + 8 * j, *box.piece(j));
+            for (int j = 0; j < 4; ++j) add8(v + 8 * j, *out.piece(c, j));
         }
-        box.put(v, &tmY, n, p.N, row_base, 0, whole, live, static_cast<B16*>(p.y) + row * p.N + n);
+        out.put(v, c, n_first + c * 32, p.N, whole, live, static_cast<B16*>(p.y) + row * p.N + n_first + c * 32);
       }
+      if (whole) out.send(&tmY, 0, n_first, row_base, 0);
     }
     if (lane == 0) bulk_wait_all();  // stores complete before the CTA exits
   }
@@ -599,15 +611,16 @@ bool fp8_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// bf16 rows [rows][halves][cols] in boxes of 32 rows and 32 columns of one half.
-bool rows_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t halves) {
+// bf16 rows [rows][halves][cols] in boxes of 32 rows and `wide` (32 or 64) columns of one half.
+bool rows_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t halves, uint32_t wide) {
   const cuuint64_t dims[3] = {cols, rows, halves};
   const cuuint64_t strides[2] = {cols * halves * 2, halves > 1 ? cols * 2 : cols * rows * 2};
-  const cuuint32_t box[3] = {32, 32, 1};
+  const cuuint32_t box[3] = {wide, 32, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                     CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     wide == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // About how many row tiles there are: every expert with rows ends in half a tile, and has one at least.
@@ -625,6 +638,7 @@ int blocks_of(int n) { return (n + kQBlock - 1) / kQBlock; }
 lrm_status launch_fp8_tc(const Fp8Args& a, cudaStream_t s) {
   if (!device_ok() || encode_fn() == nullptr) return LRM_ERR_UNSUPPORTED;
   const bool glu = a.act == LRM_ACT_SWIGLU;
+  const uint32_t wide = glu ? 32 : 64;
   Params p{};
   p.E = a.E;
   p.R = a.R;
@@ -641,15 +655,15 @@ lrm_status launch_fp8_tc(const Fp8Args& a, cudaStream_t s) {
   p.z = a.z;
   p.status = a.status;
   CUtensorMap mA, mB, mY, mZ, mR;
-  if (!fp8_map(&mA, a.x, a.K, 1, a.R, 1, kBM) || !rows_map(&mY, a.y, a.N, a.R, 1)) return LRM_ERR_CUDA;
+  if (!fp8_map(&mA, a.x, a.K, 1, a.R, 1, kBM) || !rows_map(&mY, a.y, a.N, a.R, 1, wide)) return LRM_ERR_CUDA;
   mZ = mR = mY;
-  if (a.z != nullptr && !rows_map(&mZ, a.z, a.N, a.R, p.halves)) return LRM_ERR_CUDA;
-  if (a.residual != nullptr && !rows_map(&mR, a.residual, a.N, a.R, 1)) return LRM_ERR_CUDA;
+  if (a.z != nullptr && !rows_map(&mZ, a.z, a.N, a.R, p.halves, wide)) return LRM_ERR_CUDA;
+  if (a.residual != nullptr && !rows_map(&mR, a.residual, a.N, a.R, 1, wide)) return LRM_ERR_CUDA;
   auto tiles = [&](auto bn, auto glu_tag, auto res_tag) {
     constexpr int BN = decltype(bn)::value;
     constexpr bool GLU = decltype(glu_tag)::value != 0, RES = decltype(res_tag)::value != 0;
     constexpr int cols = GLU ? BN / 2 : BN;
-    using C = Cfg<FWD, BN, RES>;
+    using C = Cfg<BN, GLU, RES>;
     p.tiles_n = (a.N + cols - 1) / cols;
     if (!fp8_map(&mB, a.w, a.K, a.N, (uint64_t)a.E * p.halves, BN / 2, 1)) return LRM_ERR_CUDA;
     return launch_pairs<fp8_tc_kernel<FWD, BN, GLU, RES>>(
@@ -674,7 +688,7 @@ lrm_status launch_fp8_tc(const Fp8Args& a, cudaStream_t s) {
 
 lrm_status launch_fp8_dx(const Fp8GradArgs& a, cudaStream_t s) {
   if (!device_ok() || encode_fn() == nullptr) return LRM_ERR_UNSUPPORTED;
-  using C = Cfg<DX, 256, false>;
+  using C = Cfg<256, false, false>;
   Params p{};
   p.E = a.E;
   p.R = a.R;
@@ -691,7 +705,7 @@ lrm_status launch_fp8_dx(const Fp8GradArgs& a, cudaStream_t s) {
   p.status = a.status;
   CUtensorMap mA, mB, mY;
   if (!fp8_map(&mA, a.dz, a.N, p.halves, a.R, 1, kBM) ||
-      !fp8_map(&mB, a.w, a.K, a.N, (uint64_t)a.E * p.halves, kBK, 1) || !rows_map(&mY, a.dx, a.K, a.R, 1))
+      !fp8_map(&mB, a.w, a.K, a.N, (uint64_t)a.E * p.halves, kBK, 1) || !rows_map(&mY, a.dx, a.K, a.R, 1, 64))
     return LRM_ERR_CUDA;
   return launch_pairs<fp8_tc_kernel<DX, 256, false, false>>(
       C::smem(), C::kThreads, row_tiles(a.seg_offsets, a.R, a.E) * p.tiles_n, s, mA, mB, mY, mY, mY, p);
