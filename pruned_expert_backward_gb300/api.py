@@ -606,8 +606,9 @@ def lrm_fp8_linear(x, x_scale, w, w_scale, bias=None, residual=None, act="none",
     if save_z or z is not None:
         z, z_p = _out(z, (R, NP), b16, dev, "z")
     _same(residual, (R, N), "residual")
-    _ok(L.load().lrm_fp8_linear(_opt(seg_offsets, "seg_offsets", torch.int32), x_p, _cuda(x_scale, "x_scale", torch.float32),
-                                _cuda(w, "w", FP8), _cuda(w_scale, "w_scale", torch.float32), _opt(bias, "bias", b16),
+    _ok(L.load().lrm_fp8_linear(_opt(seg_offsets, "seg_offsets", torch.int32), x_p,
+                                _cuda(x_scale, "x_scale", torch.float32), _cuda(w, "w", FP8),
+                                _cuda(w_scale, "w_scale", torch.float32), _opt(bias, "bias", b16),
                                 _opt(residual, "residual", b16), R, E, N, K, code, y_p, z_p,
                                 _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_fp8_linear")
     return y, z
@@ -843,8 +844,8 @@ class AdamW:
     dev_status.  state: {"m": [...], "v": [...]} and, for 8 bits, "m_scale", "v_scale" to go on from; zeros without.
     capturable: step and rate live on the device (step_dev, lr_dev), so that a captured step can be replayed."""
 
-    def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, copies=None, state_bits=32,
-                 state=None, max_norm=None, seed=0, lr_scale=1.0, capturable=False):
+    def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, copies=None,
+                 state_bits=32, state=None, max_norm=None, seed=0, lr_scale=1.0, capturable=False):
         n = len(params)
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
@@ -869,7 +870,8 @@ class AdamW:
             state = {key: [torch.zeros(t.shape, device=t.device).to(kind) for t in self.params] for key in ("m", "v")}
             if state_bits == 8:
                 for key in ("m_scale", "v_scale"):
-                    state[key] = [torch.zeros(-(-t.numel() // 256), dtype=torch.float32, device=t.device) for t in self.params]
+                    state[key] = [torch.zeros(-(-t.numel() // 256), dtype=torch.float32, device=t.device)
+                                  for t in self.params]
         self.state = state
         # the tensors by the types that share a launch, in order
         self._groups = []
@@ -948,8 +950,8 @@ class AdamW:
             self.step_dev.add_(1)
         else:
             self.steps = self.steps + 1 if step is None else int(step)
-        h = L.AdamwHyper(self.lr if lr is None else lr, *self.betas, self.eps, max(self.steps, 1), self.seed & 0xFFFFFFFF,
-                         0.0 if self.max_norm is None else self.max_norm, None, None, None)
+        h = L.AdamwHyper(self.lr if lr is None else lr, *self.betas, self.eps, max(self.steps, 1),
+                         self.seed & 0xFFFFFFFF, 0.0 if self.max_norm is None else self.max_norm, None, None, None)
         if self.step_dev is not None:
             h.step_dev, h.lr_dev = self.step_dev.data_ptr(), self.lr_dev.data_ptr()
         elif self.steps < 1:

@@ -676,7 +676,8 @@ lrm_status lrm_fp8_linear_backward(const int32_t* seg_offsets, const void* dz, c
   if (!al16(dz) || !al16(w) || !al16(dx)) return LRM_ERR_INVALID_ARG;
   if (!al4(seg_offsets) || !al4(dz_scale) || !al4(w_scale)) return LRM_ERR_INVALID_ARG;
   if (R == 0) return LRM_OK;
-  return launch_fp8_dx(Fp8GradArgs{seg_offsets, dz, dz_scale, w, w_scale, R, E, N, K, glu != 0, dx, dev_status}, stream);
+  return launch_fp8_dx(Fp8GradArgs{seg_offsets, dz, dz_scale, w, w_scale, R, E, N, K, glu != 0, dx, dev_status},
+                       stream);
 }
 
 lrm_status lrm_grad_norm_workspace_size(const lrm_adamw_tensor* tensors, int32_t count, size_t* bytes) {

@@ -5,15 +5,15 @@
 //   w = w (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 //
 // Bound by memory: every tensor is read once and written once.  The tensors' addresses travel in the kernel's
-// parameters (no table on the device), a CTA takes chunks of 8192 elements in turn, a warp 256 of them at a time: lane l
-// has elements 4 l .. 4 l + 3 and 128 more on, so that loads of every type are whole sectors in a row.
+// parameters (no table on the device), a CTA takes chunks of 8192 elements in turn, a warp 256 of them at a time: lane
+// l has elements 4 l .. 4 l + 3 and 128 more on, so that loads of every type are whole sectors in a row.
 //
 // States in 8 bits: m and sqrt(v) in e4m3, the largest magnitude of each 256 elements of a tensor held as 448 with an
 // fp32 scale, one block to a warp.  They are rounded up or down at random, with the odds that keep the mean: to nearest
 // they would stand still (b2 = 0.999 moves sqrt(v) by 0.05 % a step at most where it shrinks, half a step of e4m3 is 3
-// to 6 %), and a block that once had a large gradient would keep its neighbours' sqrt(v) in proportion.  The random bits
-// are a hash of seed, step, tensor and element, so a step can be repeated.  The update itself uses the new m and v before
-// they are rounded.  A sqrt(v) that is not 0 is never held as 0: m / eps would follow when the gradient stops.
+// to 6 %), and a block that once had a large gradient would keep its neighbours' sqrt(v) in proportion.  The random
+// bits are a hash of seed, step, tensor and element, so a step can be repeated.  The update itself uses the new m and v
+// before they are rounded.  A sqrt(v) that is not 0 is never held as 0: m / eps would follow when the gradient stops.
 #include "fp8.cuh"
 #include "kernels.h"
 #include "tc_host.h"
@@ -127,7 +127,7 @@ __device__ __forceinline__ float max_abs(float a, float b) {
   asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %2;\n\tmax.NaN.f32 %0, %1, t;\n\t}" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// The root, a unit in the last place off.
+// The root, a unit in the last place off (32-bit states keep none).
 __device__ __forceinline__ float sqrt_f(float v) {
   float r;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -178,7 +178,7 @@ __device__ __forceinline__ void store_states(const lrm_adamw_tensor& t, const in
 }
 
 struct Hyper {
-  float lr, b1, b2, one_b1, one_b2, eps;
+  float lr, b1, b2, one_b1, one_b2, eps, one;
   float c1, c2;  // 1 - b^t, where the step is the host's
   double log_b1, log_b2;
   float max_norm;
@@ -189,8 +189,8 @@ struct Hyper {
 
 // One block of 256 elements from i0 of a tensor.
 template <typename W, typename G, bool BITS8, bool COPY, bool TAIL>
-__device__ __forceinline__ void update_block(const lrm_adamw_tensor& t, int64_t i0, int lane, const Hyper& h, float factor,
-                                             float decay, float rate, float inv_c2, uint32_t key) {
+__device__ __forceinline__ void update_block(const lrm_adamw_tensor& t, int64_t i0, int lane, const Hyper& h,
+                                             float factor, float decay, float rate, float inv_c2, uint32_t key) {
   const int64_t n = t.n, i[2] = {i0 + 4 * lane, i0 + 128 + 4 * lane};
   float g[2][4], w[2][4], m[2][4], v[2][4];
   uint32_t mq[2], vq[2];
@@ -228,16 +228,18 @@ __device__ __forceinline__ void update_block(const lrm_adamw_tensor& t, int64_t 
   }
   float top_m = 0.f, top_v = 0.f;
   const float2 f2 = make_float2(factor, factor), b1 = make_float2(h.b1, h.b1), b2 = make_float2(h.b2, h.b2),
-               c1 = make_float2(h.one_b1, h.one_b1), c2 = make_float2(h.one_b2, h.one_b2);
+               c1 = make_float2(h.one_b1, h.one_b1), c2 = make_float2(h.one_b2, h.one_b2),
+               one = make_float2(h.one, h.one);
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {  // two at a time: half the instructions
-      // (each step rounded by itself, so that a host program's fp32 repeats the states to the bit)
+      // Each step is rounded by itself, so that a host program's fp32 repeats the 8-bit states to the bit.  (The sum is
+      // x * 1 + y with a 1 that the compiler does not know: it would make a product and a plain sum one multiply-add.)
       const float2 gf = __fmul2_rn(make_float2(g[s][j], g[s][j + 1]), f2);
       float2 mm = make_float2(m[s][j], m[s][j + 1]), vv = make_float2(v[s][j], v[s][j + 1]);
-      mm = __fadd2_rn(__fmul2_rn(mm, b1), __fmul2_rn(gf, c1));
-      vv = __fadd2_rn(__fmul2_rn(vv, b2), __fmul2_rn(__fmul2_rn(gf, gf), c2));
+      mm = __ffma2_rn(__fmul2_rn(mm, b1), one, __fmul2_rn(gf, c1));
+      vv = __ffma2_rn(__fmul2_rn(vv, b2), one, __fmul2_rn(__fmul2_rn(gf, gf), c2));
       m[s][j] = mm.x;
       m[s][j + 1] = mm.y;
       v[s][j] = vv.x;
@@ -257,10 +259,7 @@ __device__ __forceinline__ void update_block(const lrm_adamw_tensor& t, int64_t 
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      r[s][j] = sqrt_f(v[s][j]);
-      if (BITS8 && v[s][j] == tv) r[s][j] = rv;  // the largest has its own scale's root, so that it is held as 448
-    }
+    for (int j = 0; j < 4; ++j) r[s][j] = BITS8 ? __fsqrt_rn(v[s][j]) : sqrt_f(v[s][j]);
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
       const float2 den = __ffma2_rn(make_float2(r[s][j], r[s][j + 1]), make_float2(inv_c2, inv_c2),
@@ -356,7 +355,8 @@ __global__ void __launch_bounds__(kThreads, kAdamCtas) adamw_kernel(const __grid
 
 // Sums of squares: each CTA's of its chunks, in fp64 beyond 32 values, to part[blockIdx].
 template <typename G>
-__global__ void __launch_bounds__(kThreads) norm_parts_kernel(const __grid_constant__ Table a, double* __restrict__ part) {
+__global__ void __launch_bounds__(kThreads)
+    norm_parts_kernel(const __grid_constant__ Table a, double* __restrict__ part) {
   chain_wait();
   __shared__ double s_sum[kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -473,6 +473,7 @@ void launch_adamw(const lrm_adamw_tensor* tensors, int32_t count, lrm_dtype w_dt
   h.one_b1 = (float)(1. - p.beta1);
   h.one_b2 = (float)(1. - p.beta2);
   h.eps = (float)p.eps;
+  h.one = 1.f;
   h.log_b1 = log(p.beta1);
   h.log_b2 = log(p.beta2);
   h.c1 = (float)-expm1((double)p.step * h.log_b1);

@@ -6,11 +6,11 @@
 // whole block NaN.  (2^-100 keeps 448 / top finite; all-zero blocks need no branch.)
 //
 // Rows: 16 lanes take a block of 128 columns of one row, 8 values each, and write its 128 bytes to every row of the
-// sorted batch that the token has: a token's row is read and rounded once, whatever k is.  Bound by memory (mostly the k
-// writes): 8192 tokens of 2048 bf16 to 65536 rows 28 us, 0.90 of the copy rate.
+// sorted batch that the token has: a token's row is read and rounded once, whatever k is.  Bound by memory (mostly the
+// k writes): 8192 tokens of 2048 bf16 to 65536 rows 28 us, 0.90 of the copy rate.
 // Weights: a CTA takes a block of 128 x 128, 16 lanes a row, 8 rows in flight each; the maximum goes through
-// shared memory while the block stays in registers.  Bound by reading W: 128 x 1536 x 2048 bf16 186 us, 0.96 of the copy
-// rate with three CTAs a multiprocessor (two 222 us, five, which spill, 231 us).
+// shared memory while the block stays in registers.  Bound by reading W: 128 x 1536 x 2048 bf16 186 us, 0.96 of the
+// copy rate with three CTAs a multiprocessor (two 222 us, five, which spill, 231 us).
 #include "fp8.cuh"
 #include "kernels.h"
 
@@ -146,8 +146,8 @@ void launch_fp8_quantize(const void* x, const int32_t* row_of_pair, int64_t T, i
   const int nb = (K + kQBlock - 1) / kQBlock;
   const int64_t units = T * nb, blocks = (units + kGroups - 1) / kGroups;
   auto go = [&](auto kernel, auto* at) {
-    launch_chained(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, at, row_of_pair, units, (int)k, (int)K, nb, cap,
-                   static_cast<uint8_t*>(q), scale, status);
+    launch_chained(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, at, row_of_pair, units, (int)k, (int)K, nb,
+                   cap, static_cast<uint8_t*>(q), scale, status);
   };
   auto typed = [&](auto* at) {
     using T_ = std::remove_cv_t<std::remove_pointer_t<decltype(at)>>;

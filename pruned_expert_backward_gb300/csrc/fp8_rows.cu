@@ -8,8 +8,8 @@
 //
 // Little is in flight a warp (one block), but three CTAs share a multiprocessor and hide one another's latencies: with
 // four blocks and two CTAs a token's 8 rows over 8 of 128 experts of (768+768) x 2048 took 12.2 us, not 7.9 (25 MB of
-// weights: 3.7 us at the copy rate), and 2048 x 768 13.9 us, not 6.3.  GB300, dense, 1 to 8 rows: (1408+1408) x 4096 6.0
-// to 6.3 us, 4096 x 4096 6.6 to 6.8 us, (768+768) x 2048 2.7 us.
+// weights: 3.7 us at the copy rate), and 2048 x 768 13.9 us, not 6.3.  GB300, dense, 1 to 8 rows: (1408+1408) x 4096
+// 6.0 to 6.3 us, 4096 x 4096 6.6 to 6.8 us, (768+768) x 2048 2.7 us.
 #include "fp8.cuh"
 #include "kernels.h"
 #include "linear.cuh"

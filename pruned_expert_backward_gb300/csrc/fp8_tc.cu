@@ -9,9 +9,18 @@
 // at the next.
 //
 // CTA pairs and tiles are those of linear_tc.cu: 256 x BN tiles over a persistent grid.  Warp 0 issues the TMA loads,
-// warp 1 of the leader the MMAs, warps 2 and 3 bring the tile's place and its scales to shared memory, the rest are the
-// epilogue: each has a 32-row quarter of TMEM by 64 columns (SwiGLU: 32 gate columns and the 32 up columns that go with them), which lie in
-// one block of 128 columns of W.
+// warp 1 of the leader the MMAs, warps 2 and 3 bring the tile's place and its scales to shared memory (segment bounds
+// and scales are trips to memory that the epilogue would wait for), the rest are the epilogue: each has a 32-row quarter
+// of TMEM by 64 columns (SwiGLU: 32 gate columns and the 32 up columns that go with them), which lie in one block of 128
+// columns of W.
+//
+// A 256-column slice costs the tensor core 557 cycles and the 16 epilogue warps' loads and sums 300 (one multiply-add
+// an element and slice, two an instruction), but 830 in all: TMEM holds two accumulators, so that a slice's products
+// wait until all 32 warps of the pair have taken out the one before the last, and the signals both ways are as long as
+// the sums.  Four accumulators of 128 columns each bring half as many products for three quarters of the operands
+// (bound by L2: 0.25 us a slice, 256 columns 0.43 us); eight epilogue warps of 128 columns hide less.
+// GB300: 32768 x 4096 x 4096 412 us (2.7 PFLOP/s), with bias, GELU and residual 530 us; 65536 rows over 128 experts to
+// 2 x 768, K = 2048, SwiGLU 247 us (with z 284 us), its rows' gradient 267 us, 768 to 2048 180 us.
 //
 // W stays as it was quantised: FWD reads its rows K-major, DX the same bytes with the columns contiguous (MN-major).
 #include "fp8.cuh"
@@ -38,7 +47,7 @@ enum Kind { FWD = 0, DX = 1 };
 // The scales of a tile's rows and columns for the next kRun K slices, two of them in turn.
 constexpr int kRun = 8;
 struct Scales {
-  // a row's scale times that of each of the tile's two blocks of columns; SwiGLU: of the gate's, then of the up columns'
+  // a row's scale times that of each of the tile's two blocks of columns; SwiGLU: of the gate's, then of the up's
   // (the pad keeps the writing lanes' eight slices of four rows off each other's banks)
   float xw[2][kRun][kBM + 4];
   int tile[4];  // e, row0, row_end, n0 of the tile
@@ -619,8 +628,8 @@ bool rows_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, ui
   const cuuint32_t estr[3] = {1, 1, 1};
   return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     wide == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                     wide == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // About how many row tiles there are: every expert with rows ends in half a tile, and has one at least.
@@ -672,13 +681,13 @@ lrm_status launch_fp8_tc(const Fp8Args& a, cudaStream_t s) {
   auto go = [&](auto bn, auto glu_tag) {
     return a.residual != nullptr ? tiles(bn, glu_tag, IntTag<1>{}) : tiles(bn, glu_tag, IntTag<0>{});
   };
-  // Tile width by the waves of tiles over the CTA pairs; a K slice of a 256-column tile takes 0.45 us (its sums out of
+  // Tile width by the waves of tiles over the CTA pairs; a K slice of a 256-column tile takes 0.43 us (its sums out of
   // TMEM), of a 128-column one 0.25 us, of a 64-column one 0.22 us.  E.g. 256 rows over 8 experts to 2 x 1408, K = 4096:
-  // 88, 176 or 352 tiles, 36, 31 and 44 us; 8192 x 4096 x 4096 116, 127 and 214 us.
+  // 88, 176 or 352 tiles, 35, 31 and 44 us; 8192 x 4096 x 4096 110, 123 and 211 us; 32 rows, 17, 12 and 11 us.
   const double rows = likely_tiles(a.seg_offsets != nullptr, a.R, a.E);
   const int pairs = sm_count() / 2, per = glu ? 2 : 1;
   auto cost = [&](int bn, double slice) { return ceil(rows * ((a.N * per + bn - 1) / bn) / pairs) * slice; };
-  const double c256 = cost(256, 0.45), c128 = cost(128, 0.25), c64 = cost(64, 0.22);
+  const double c256 = cost(256, 0.43), c128 = cost(128, 0.25), c64 = cost(64, 0.22);
   auto width = [&](auto glu_tag) {
     if (c64 <= c128 && c64 <= c256) return go(IntTag<64>{}, glu_tag);
     return c128 <= c256 ? go(IntTag<128>{}, glu_tag) : go(IntTag<256>{}, glu_tag);

@@ -216,13 +216,13 @@ struct Fp8Args {
   int32_t* status;
 };
 // Whether one pass over the weights by plain loads takes a product of so few rows, not the tensor cores' tiles of 256
-// rows.  GB300, us, rows kernel : tiles.  Dense, (1408+1408) x 4096, 4096 x 4096, (768+768) x 2048: 7.9 : 12.4, 8.1 :
-// 14.1, 4.0 : 6.9 at 16 rows, 12.7 : 12.4, 13.2 : 14.7, 6.1 : 7.0 at 17, 14.3 : 11.4, 14.4 : 12.0, 6.8 : 7.1 at 32.
-// Per expert, up to 128 rows in all, and 16 a mean expert: 128 experts of (768+768) x 2048, popularity even and zipf 1,
-// 58 : 68 and 28 : 33 at 128 rows, 93 : 98 and 73 : 52 at 512; of 2048 x 768 45 : 54 and 20 : 24 at 128; 8 experts of
-// (1408+1408) x 4096 22 : 36 at 64 rows, 35 : 36 at 128, 61 : 36 at 256.
+// rows.  GB300, us, rows kernel : tiles.  Dense, (1408+1408) x 4096, 4096 x 4096, (768+768) x 2048: 7.8 : 13.3, 8.1 :
+// 14.0, 3.7 : 6.9 at 16 rows, 12.8 : 11.4, 12.9 : 11.8, 5.8 : 6.9 at 32.
+// Per expert, up to 128 rows in all, and 8 a mean expert: 128 experts of (768+768) x 2048, popularity even and zipf 1,
+// 38 : 39 and 21 : 28 at 64 rows, 61 : 62 and 32 : 31 at 128, 80 : 80 and 46 : 39 at 256; of 2048 x 768 26 : 29 and 15 :
+// 17 at 64, 57 : 53 and 29 : 24 at 256; 8 experts of (1408+1408) x 4096 22 : 30 at 64 rows, 35 : 30 at 128.
 inline bool fp8_few_rows(int64_t R, int32_t E, bool grouped) {
-  return grouped ? R <= 128 && R <= 16 * (int64_t)E : R <= 16;
+  return R <= 16 || (grouped && R <= 128 && R <= 8 * (int64_t)E);
 }
 void launch_fp8_rows(const Fp8Args& a, cudaStream_t s);
 lrm_status launch_fp8_tc(const Fp8Args& a, cudaStream_t s);

@@ -40,8 +40,8 @@ __device__ __forceinline__ int last_at_most(const int* prefix, int n, int v) {
 // run of experts, a scan over the threads (scan [THREADS / 32]) gives the prefix.  Returns the number of row tiles, 0
 // for segments that are not valid.
 template <int THREADS>
-__device__ __forceinline__ int segment_tiles(const int32_t* seg, int E, int64_t R, int tile_rows, int* prefix, int* scan,
-                                             int32_t* status) {
+__device__ __forceinline__ int segment_tiles(const int32_t* seg, int E, int64_t R, int tile_rows, int* prefix,
+                                             int* scan, int32_t* status) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (E + THREADS - 1) / THREADS, e0 = threadIdx.x * per, e1 = min(E, e0 + per);
   int sum = 0, ok = 1;

@@ -215,6 +215,38 @@ def test_same_bits_again():
     assert all(torch.equal(a, b) for a, b in zip(*out))
 
 
+def test_states_repeat_in_a_host_programs_fp32():
+    """Two steps' 8-bit states, bit for bit from fp32 operations that are each rounded by themselves."""
+    import pruned_expert_backward_gb300 as lrm
+    f, n = np.float32, 256 * 500 + 77
+    c = Case([n], F32, F32, 8, seed=8)
+    opt = c.optimiser(lrm, **HYPER, max_norm=0.01, seed=21)
+
+    def host(a):
+        return a.float().cpu().numpy()
+
+    def state(a, rnd, least):
+        top = np.maximum(np.abs(np.pad(a, (0, -n % 256))).reshape(-1, 256).max(1), f(2.0 ** -120))
+        y = np.abs(a) * np.repeat(f(448) * (f(1) / top), 256)[:n]
+        shift = np.where(y < f(2.0 ** -6), f(2.0 ** -6), f(0))
+        up = ((y + shift).view(np.uint32) + (rnd.astype(np.uint32) << np.uint32(4))) & np.uint32(0xFFF00000)
+        y = up.view(f) - shift
+        y = np.where((a != 0) & (y < least), f(least), y)
+        return np.copysign(y, a), top * (f(1) / f(448))
+
+    for step in (1, 2):
+        m, r = (host(c.state[k][0]) * np.repeat(host(c.state[k + "_scale"][0]), 256)[:n] for k in ("m", "v"))
+        v = r * r
+        norm = f(opt.step().item())
+        g = host(c.g[0]) * (f(1) / (norm + f(1e-6)) * f(0.01))
+        m = m * f(0.9) + g * f(1 - 0.9)
+        v = v * f(0.95) + g * g * f(1 - 0.95)
+        bits = random_bits(torch.arange(n), 21, step, 0).numpy()
+        for key, a, rnd, least in (("m", m, bits & 0xFFFF, 0.0), ("v", np.sqrt(v), bits >> 16, 2.0 ** -9)):
+            q, scale = state(a, rnd, least)
+            assert np.array_equal(host(c.state[key][0]), q) and np.array_equal(host(c.state[key + "_scale"][0]), scale)
+
+
 def test_random_rounding_keeps_the_mean():
     """A sqrt(v) that shrinks by 0.05 % a step does so in 8 bits too; to nearest it would stand still (half a step is 3
     to 6 %).  100000 equal values after 400 steps of no gradient: the mean's deviation, a walk of 400 steps of at most

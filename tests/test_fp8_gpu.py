@@ -219,7 +219,8 @@ GROUPED = [  # R, E, segments, N, K, act, bias, residual, save_z
     (1000, 3, "even", 520, 80, "silu", True, True, True), (2000, 7, "short", 264, 336, "swiglu", True, True, True),
     (5000, 40, "ragged", 392, 208, "relu", True, False, False), (3000, 1, "even", 136, 64, "swiglu", False, True, True),
     (6000, 1024, "ragged", 72, 64, "none", True, False, False),
-    (3501, 5, "ragged", 1024, 144, "gelu", True, True, True), (3501, 5, "ragged", 1024, 400, "none", False, False, True),
+    (3501, 5, "ragged", 1024, 144, "gelu", True, True, True),
+    (3501, 5, "ragged", 1024, 400, "none", False, False, True),
     (3501, 5, "short", 512, 144, "swiglu", True, True, True), (9000, 2, "ragged", 136, 80, "gelu", True, True, True),
 ]
 
