@@ -253,8 +253,8 @@ template <int ACT>
 __device__ __forceinline__ void act_all(float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
-    if (ACT == LRM_ACT_GELU) {
-      const float2 r = gelu2(make_float2(v[i], v[i + 1]));
+    if (ACT == LRM_ACT_GELU || ACT == LRM_ACT_SILU) {
+      const float2 z = make_float2(v[i], v[i + 1]), r = ACT == LRM_ACT_GELU ? gelu2(z) : silu2(z);
       v[i] = r.x;
       v[i + 1] = r.y;
     } else {
@@ -580,7 +580,11 @@ __global__ void __launch_bounds__(Cfg<BN, GLU, RES>::kThreads, 1)
         if (KIND == FWD) {
           if (GLU) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = act_value<LRM_ACT_SWIGLU>(v[j]) * acc[1][j];
+            for (int j = 0; j < 32; j += 2) {
+              const float2 r = __fmul2_rn(silu2(make_float2(v[j], v[j + 1])), make_float2(acc[1][j], acc[1][j + 1]));
+              v[j] = r.x;
+              v[j + 1] = r.y;
+            }
           } else {
             switch (p.act) {
               case LRM_ACT_RELU: act_all<LRM_ACT_RELU>(v); break;

@@ -29,22 +29,22 @@ __device__ __forceinline__ float norm_cdf(float z, float* exp_out) {
   return z < 0.f ? tail : 1.f - tail;
 }
 
+__device__ __forceinline__ float fast_recip(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float fast_exp2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 // Two GELUs at once, two sums or products an instruction (about half the time of two norm_cdf, which the pipe of the
 // single ones bounds): max(z, 0) - |z| erfc(|z| / sqrt 2) / 2, the tail by norm_cdf's polynomial (halved here).
 __device__ __forceinline__ float2 gelu2(float2 z) {
   auto both = [](float v) { return make_float2(v, v); };
-  auto recip = [](float v) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-  };
-  auto exp_2 = [](float v) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-  };
-  const float2 t = make_float2(recip(fmaf(0.45f * 0.70710678118654752f, fabsf(z.x), 1.f)),
-                               recip(fmaf(0.45f * 0.70710678118654752f, fabsf(z.y), 1.f)));
+  const float2 t = make_float2(fast_recip(fmaf(0.45f * 0.70710678118654752f, fabsf(z.x), 1.f)),
+                               fast_recip(fmaf(0.45f * 0.70710678118654752f, fabsf(z.y), 1.f)));
   const float2 x = __fmul2_rn(__fmul2_rn(z, both(-0.5f * 1.4426950408889634f)), z);
   float2 p = both(0.5f * 0.06631968915462494f);
   p = __ffma2_rn(p, t, both(0.5f * -0.23788957297801971f));
@@ -54,8 +54,15 @@ __device__ __forceinline__ float2 gelu2(float2 z) {
   p = __ffma2_rn(p, t, both(0.5f * 0.22879089415073395f));
   p = __ffma2_rn(p, t, both(0.5f * 0.2535184919834137f));
   p = __ffma2_rn(p, t, both(0.5f * 0.25391680002212524f));
-  const float2 tail = __fmul2_rn(__fmul2_rn(p, t), make_float2(exp_2(x.x), exp_2(x.y)));
+  const float2 tail = __fmul2_rn(__fmul2_rn(p, t), make_float2(fast_exp2(x.x), fast_exp2(x.y)));
   return __ffma2_rn(make_float2(-fabsf(z.x), -fabsf(z.y)), tail, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
+}
+
+// Two SiLUs at once.
+__device__ __forceinline__ float2 silu2(float2 z) {
+  const float2 x = __fmul2_rn(z, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+  const float2 d = __fadd2_rn(make_float2(fast_exp2(x.x), fast_exp2(x.y)), make_float2(1.f, 1.f));
+  return __fmul2_rn(z, make_float2(fast_recip(d.x), fast_recip(d.y)));
 }
 
 // act(z) of the one-input activations (SwiGLU takes two: SiLU(gate) * up).
