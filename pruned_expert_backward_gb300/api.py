@@ -832,6 +832,12 @@ class MoeLayer:
         return self.dx, self.dalpha, self.dw_gate_up, self.dw_down
 
 
+def _on16(n, *addresses):
+    """The 16-byte starts that lrm_adamw asks for, looked at before any of several launches."""
+    if n and any(p is not None and p % 16 for p in addresses):
+        raise LrmError(1, "lrm_adamw")
+
+
 class AdamW:
     """AdamW over many tensors at once (lrm_adamw): one or a few launches a step, whatever the number of tensors.
 
@@ -866,8 +872,9 @@ class AdamW:
             _cuda(t, "param")
             _dt(t)
         if state is None:
-            kind = torch.float32 if state_bits == 32 else FP8
-            state = {key: [torch.zeros(t.shape, device=t.device).to(kind) for t in self.params] for key in ("m", "v")}
+            kind = (torch.float32, torch.float32) if state_bits == 32 else (torch.uint8, FP8)
+            state = {key: [torch.zeros(t.shape, dtype=kind[0], device=t.device).view(kind[1]) for t in self.params]
+                     for key in ("m", "v")}
             if state_bits == 8:
                 for key in ("m_scale", "v_scale"):
                     state[key] = [torch.zeros(-(-t.numel() // 256), dtype=torch.float32, device=t.device)
@@ -899,6 +906,16 @@ class AdamW:
                             raise ValueError(f"state {key}_scale must hold a value for each 256, got {s.numel()}")
                         setattr(e, key + "_scale", _cuda(s, key + "_scale", torch.float32))
             self._groups.append((w_dt, copy, members, table))
+        # what a step writes: two tensors on the same bytes would race
+        held = [state[key] for key in (("m", "v") if state_bits == 32 else ("m", "v", "m_scale", "v_scale"))]
+        spans = sorted((t.data_ptr(), t.numel() * t.element_size()) for own in (self.params, self.copies, *held)
+                       for t in own if t is not None and t.numel())
+        for (a, n_bytes), (b, _) in zip(spans, spans[1:]):
+            if a + n_bytes > b:
+                raise ValueError("params, copies and states must not share memory")
+        for _, _, _, table in self._groups:
+            for e in table:
+                _on16(e.n, e.w, e.copy, e.m, e.v)
         # one table of all tensors for the common norm
         self._all = self._groups[0][3] if len(self._groups) == 1 else (L.AdamwTensor * n)()
         if len(self._groups) > 1:
@@ -930,6 +947,7 @@ class AdamW:
             if g.numel() != t.numel():
                 raise ValueError(f"a gradient of {g.numel()} values for a param of {t.numel()}")
             at.append(_cuda(g, "gradient", grads[0].dtype))
+        _on16(1, *(p for p, t in zip(at, self.params) if t.numel()))
         for _, _, members, table in self._groups:
             for j, i in enumerate(members):
                 table[j].g = at[i]
@@ -947,16 +965,15 @@ class AdamW:
         if self.step_dev is not None:
             if step is not None or lr is not None:
                 raise ValueError("a capturable step takes step and rate from step_dev and lr_dev")
-            self.step_dev.add_(1)
-        else:
-            self.steps = self.steps + 1 if step is None else int(step)
-        h = L.AdamwHyper(self.lr if lr is None else lr, *self.betas, self.eps, max(self.steps, 1),
-                         self.seed & 0xFFFFFFFF, 0.0 if self.max_norm is None else self.max_norm, None, None, None)
-        if self.step_dev is not None:
-            h.step_dev, h.lr_dev = self.step_dev.data_ptr(), self.lr_dev.data_ptr()
-        elif self.steps < 1:
-            raise ValueError(f"steps count from 1, got {self.steps}")
+        number = self.steps + 1 if step is None else int(step)
+        if number < 1:
+            raise ValueError(f"steps count from 1, got {number}")
+        h = L.AdamwHyper(self.lr if lr is None else lr, *self.betas, self.eps, number, self.seed & 0xFFFFFFFF,
+                         0.0 if self.max_norm is None else self.max_norm, None, None, None)
         lib = L.load()
+        if self.step_dev is not None:
+            self.step_dev.add_(1)
+            h.step_dev, h.lr_dev = self.step_dev.data_ptr(), self.lr_dev.data_ptr()
         if self.max_norm is not None:
             h.grad_norm = self.norm.data_ptr()
             _ok(lib.lrm_grad_norm(self._all, len(self.params), self._g_dt, h.grad_norm, self._ws.data_ptr(),
@@ -964,6 +981,8 @@ class AdamW:
         for w_dt, copy, members, table in self._groups:
             _ok(lib.lrm_adamw(table, len(members), w_dt, self._g_dt, self.state_bits, int(copy), C.byref(h), stream),
                 "lrm_adamw")
+        if self.step_dev is None:
+            self.steps = number
         return self.norm
 
 

@@ -414,6 +414,8 @@ def test_refusals():
                  lambda: lrm.AdamW([w], [g], weight_decay=[0.1, 0.2]), lambda: lrm.AdamW([w[::2]], [g[:32]]),
                  lambda: lrm.AdamW([w], [g], state={"m": [w[:3]], "v": [g]}), lambda: lrm.AdamW([w], [g]).step(step=0),
                  lambda: lrm.AdamW([w], [g], copies=[w[:5].bfloat16()]),
+                 lambda: lrm.AdamW([w, w], [g, g]), lambda: lrm.AdamW([w, w[32:]], [g, g[32:]]),
+                 lambda: lrm.AdamW([w], [g], state={"m": [w], "v": [g]}),
                  lambda: lrm.AdamW([w], [g], capturable=True).step(step=3)):
         with pytest.raises(ValueError):
             call()
@@ -428,4 +430,10 @@ def test_refusals():
             lrm.AdamW([w], [g], **kw).step()
     with pytest.raises(lrm.LrmError):
         lrm.AdamW([w[1:33]], [g[1:33]]).step()  # off the 16 bytes
+    opt = lrm.AdamW([w, w.bfloat16()], [g, g.clone()])
+    with pytest.raises(lrm.LrmError):
+        opt.step(grads=[g, torch.zeros(65, device="cuda")[1:]])
+    with pytest.raises(ValueError):
+        opt.step(step=0)
+    assert opt.steps == 0 and opt.step() is None and opt.steps == 1
     assert torch.count_nonzero(w) == 0
