@@ -40,7 +40,7 @@ def _cuda(t: torch.Tensor, name: str, dtype=None) -> int:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     return t.data_ptr()
 
@@ -575,12 +575,26 @@ def lrm_fp8_quantize_weight(w, glu=False, q=None, scale=None):
     return q, scale
 
 
-def _fp8_weight(w, w_scale, per, seg_offsets):
-    """(E, rows, columns) of an 8-bit weight whose scales have been checked."""
-    E, NP, K = _experts(w, seg_offsets, "w")
+@functools.lru_cache(maxsize=1024)
+def _fp8_sizes(w, w_scale, per, seg_offsets, x_scale, R, columns, across):
+    """(E, rows, columns) of an 8-bit weight from the operands' shapes, once they have been checked (for each set of
+    shapes once: a small call is bound by the host).  The other operand has R rows of `columns`, which are w's columns
+    or, across, its rows."""
+    if len(w) != (2 if seg_offsets is None else 3):
+        raise ValueError(f"w must be {'[N,K] without' if seg_offsets is None else '[E,N,K] with'} seg_offsets, "
+                         f"got {list(w)}")
+    E, NP, K = (1, *w) if seg_offsets is None else w
+    if seg_offsets is not None and seg_offsets != (E + 1,):
+        raise ValueError(f"seg_offsets must be {[E + 1]}, got {list(seg_offsets)}")
     if NP % per:
         raise ValueError(f"w has {NP} rows: gate and up rows in equal number expected")
-    _same(w_scale, (*w.shape[:-2], per * _qblocks(NP // per), _qblocks(K)), "w_scale")
+    if columns != (NP if across else K):
+        raise ValueError(f"{'dz' if across else 'x'} has {columns} columns, w {f'{NP} rows' if across else K}")
+    blocks = per * _qblocks(NP // per)
+    for name, got, want in (("w_scale", w_scale, (*w[:-2], blocks, _qblocks(K))),
+                            ("dz_scale" if across else "x_scale", x_scale, (R, blocks if across else _qblocks(K)))):
+        if got != want:
+            raise ValueError(f"{name} must be {list(want)}, got {list(got)}")
     return E, NP, K
 
 
@@ -593,24 +607,23 @@ def lrm_fp8_linear(x, x_scale, w, w_scale, bias=None, residual=None, act="none",
     R, K = x.shape
     code, dev, b16 = _act_code(act), x.device, torch.bfloat16
     per = 2 if act == "swiglu" else 1
-    x_p = _cuda(x, "x", FP8)
-    E, NP, Kw = _fp8_weight(w, w_scale, per, seg_offsets)
+    E, NP, _ = _fp8_sizes(w.shape, w_scale.shape, per, None if seg_offsets is None else seg_offsets.shape,
+                          x_scale.shape, R, K, False)
     N = NP // per
-    if Kw != K:
-        raise ValueError(f"x has {K} columns, w {Kw}")
-    _same(x_scale, (R, _qblocks(K)), "x_scale")
     if bias is not None and bias.numel() != E * NP:
         raise ValueError(f"bias must hold {E * NP} values, got {bias.numel()}")
     y, y_p = _out(y, (R, N), b16, dev, "y")
     z_p = None
     if save_z or z is not None:
         z, z_p = _out(z, (R, NP), b16, dev, "z")
-    _same(residual, (R, N), "residual")
-    _ok(L.load().lrm_fp8_linear(_opt(seg_offsets, "seg_offsets", torch.int32), x_p,
-                                _cuda(x_scale, "x_scale", torch.float32), _cuda(w, "w", FP8),
-                                _cuda(w_scale, "w_scale", torch.float32), _opt(bias, "bias", b16),
-                                _opt(residual, "residual", b16), R, E, N, K, code, y_p, z_p,
-                                _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_fp8_linear")
+    if residual is not None:
+        _same(residual, (R, N), "residual")
+    _ok(L.load().lrm_fp8_linear(
+        None if seg_offsets is None else _cuda(seg_offsets, "seg_offsets", torch.int32), _cuda(x, "x", FP8),
+        _cuda(x_scale, "x_scale", torch.float32), _cuda(w, "w", FP8), _cuda(w_scale, "w_scale", torch.float32),
+        None if bias is None else _cuda(bias, "bias", b16),
+        None if residual is None else _cuda(residual, "residual", b16), R, E, N, K, code, y_p, z_p,
+        None if dev_status is None else _cuda(dev_status, "dev_status", torch.int32), _stream()), "lrm_fp8_linear")
     return y, z
 
 
@@ -620,15 +633,14 @@ def lrm_fp8_linear_backward(dz, dz_scale, w, w_scale, glu=False, seg_offsets=Non
     rows.  Rows of no segment are not written: uninitialised memory in a dx made here."""
     R, NP = dz.shape
     per = 2 if glu else 1
-    E, Nw, K = _fp8_weight(w, w_scale, per, seg_offsets)
-    if Nw != NP:
-        raise ValueError(f"dz has {NP} columns, w {Nw} rows")
-    _same(dz_scale, (R, per * _qblocks(NP // per)), "dz_scale")
+    E, _, K = _fp8_sizes(w.shape, w_scale.shape, per, None if seg_offsets is None else seg_offsets.shape,
+                         dz_scale.shape, R, NP, True)
     dx, dx_p = _out(dx, (R, K), torch.bfloat16, dz.device, "dx")
     _ok(L.load().lrm_fp8_linear_backward(
-        _opt(seg_offsets, "seg_offsets", torch.int32), _cuda(dz, "dz", FP8), _cuda(dz_scale, "dz_scale", torch.float32),
-        _cuda(w, "w", FP8), _cuda(w_scale, "w_scale", torch.float32), R, E, NP // per, K, per - 1, dx_p,
-        _opt(dev_status, "dev_status", torch.int32), _stream()), "lrm_fp8_linear_backward")
+        None if seg_offsets is None else _cuda(seg_offsets, "seg_offsets", torch.int32), _cuda(dz, "dz", FP8),
+        _cuda(dz_scale, "dz_scale", torch.float32), _cuda(w, "w", FP8), _cuda(w_scale, "w_scale", torch.float32), R, E,
+        NP // per, K, per - 1, dx_p, None if dev_status is None else _cuda(dev_status, "dev_status", torch.int32),
+        _stream()), "lrm_fp8_linear_backward")
     return dx
 
 
