@@ -127,6 +127,12 @@ __device__ __forceinline__ float max_abs(float a, float b) {
   asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %2;\n\tmax.NaN.f32 %0, %1, t;\n\t}" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+// A unit in the last place off; roots of fp32 values and what is added to them stay clear of what it flushes.
+__device__ __forceinline__ float recip(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 // The root, a unit in the last place off (32-bit states keep none).
 __device__ __forceinline__ float sqrt_f(float v) {
   float r;
@@ -141,36 +147,45 @@ __host__ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
   return h ^ (h >> 16);
 }
 
-// Random rounding of a magnitude y (448 and a little at most) to an e4m3 value: 16 random bits are added below the
-// 4-bit significand, what stays below it is cut.  Values below the normal ones have the smallest normal one's spacing:
-// they are rounded with that one added.
+// The finaliser's halves without its last exclusive or in full: m takes the low 16 bits, sqrt(v) the high ones.
+__device__ __forceinline__ uint2 mix_halves(uint32_t h) {
+  h = (h ^ (h >> 16)) * 0x85EBCA6Bu;
+  h = (h ^ (h >> 13)) * 0xC2B2AE35u;
+  const uint32_t high = h >> 16;
+  return make_uint2((h ^ high) & 0xffffu, high);
+}
+
+// Random rounding of y (448 and a little in magnitude at most, of either sign) to an e4m3 value: 16 random bits are
+// added below the 4-bit significand, what stays below it is cut.  Values below the normal ones have the smallest normal
+// one's spacing: they are rounded with that one added.
 __device__ __forceinline__ float raised(float y, uint32_t rnd16) {
   return __uint_as_float((__float_as_uint(y) + (rnd16 << 4)) & 0xfff00000u);
 }
 
-// The 8-bit states of a lane's two runs: y is |m| and sqrt(v) over their scales.
+// The 8-bit states of a lane's two runs: y is m and sqrt(v) over their scales.
 template <bool TAIL, bool SMALL>
 __device__ __forceinline__ void store_states(const lrm_adamw_tensor& t, const int64_t (&i)[2], int64_t n,
-                                             const float (&m)[2][4], const float2 (&y)[2][4], uint32_t key) {
+                                             const float2 (&y)[2][4], uint32_t key) {
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     float qm[4], qv[4];
     const uint32_t base = (uint32_t)i[s] * 0x9E3779B1u + (uint32_t)((uint64_t)i[s] >> 32) * 0xC2B2AE3Du + key;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t rnd = mix32(base + (uint32_t)j * 0x9E3779B1u);
-      float2 z = y[s][j];
+      const uint2 rnd = mix_halves(base + (uint32_t)j * 0x9E3779B1u);
       if (SMALL) {
+        float2 z = make_float2(fabsf(y[s][j].x), y[s][j].y);
         const float2 shift = make_float2(z.x < 0x1p-6f ? 0x1p-6f : 0.f, z.y < 0x1p-6f ? 0x1p-6f : 0.f);
         z = __fadd2_rn(z, shift);
-        z = make_float2(raised(z.x, rnd & 0xffffu), raised(z.y, rnd >> 16));
+        z = make_float2(raised(z.x, rnd.x), raised(z.y, rnd.y));
         z = __fadd2_rn(z, make_float2(-shift.x, -shift.y));
         if (y[s][j].y > 0.f) z.y = fmaxf(z.y, 0x1p-9f);
+        qm[j] = copysignf(z.x, y[s][j].x);
+        qv[j] = z.y;
       } else {
-        z = make_float2(raised(z.x, rnd & 0xffffu), raised(z.y, rnd >> 16));
+        qm[j] = raised(y[s][j].x, rnd.x);
+        qv[j] = raised(y[s][j].y, rnd.y);
       }
-      qm[j] = copysignf(z.x, m[s][j]);
-      qv[j] = z.y;
     }
     store4<TAIL>(static_cast<uint8_t*>(t.m), i[s], n, e4m3x4(qm[0], qm[1], qm[2], qm[3]));
     store4<TAIL>(static_cast<uint8_t*>(t.v), i[s], n, e4m3x4(qv[0], qv[1], qv[2], qv[3]));
@@ -264,7 +279,7 @@ __device__ __forceinline__ void update_block(const lrm_adamw_tensor& t, int64_t 
     for (int j = 0; j < 4; j += 2) {
       const float2 den = __ffma2_rn(make_float2(r[s][j], r[s][j + 1]), make_float2(inv_c2, inv_c2),
                                     make_float2(h.eps, h.eps));
-      const float2 up = make_float2(__fdividef(m[s][j], den.x), __fdividef(m[s][j + 1], den.y));
+      const float2 up = __fmul2_rn(make_float2(m[s][j], m[s][j + 1]), make_float2(recip(den.x), recip(den.y)));
       const float2 ww = __ffma2_rn(up, make_float2(-rate, -rate),
                                    __fmul2_rn(make_float2(w[s][j], w[s][j + 1]), make_float2(decay, decay)));
       w[s][j] = ww.x;
@@ -291,14 +306,14 @@ __device__ __forceinline__ void update_block(const lrm_adamw_tensor& t, int64_t 
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        y[s][j] = __fmul2_rn(make_float2(fabsf(m[s][j]), r[s][j]), make_float2(im, iv));
-        least = fminf(fminf(y[s][j].x, y[s][j].y), least);
+        y[s][j] = __fmul2_rn(make_float2(m[s][j], r[s][j]), make_float2(im, iv));
+        least = fminf(fminf(fabsf(y[s][j].x), y[s][j].y), least);
       }
     // most blocks have no value below e4m3's normal ones
     if (__all_sync(0xffffffffu, least >= 0x1p-6f))
-      store_states<TAIL, false>(t, i, n, m, y, key);
+      store_states<TAIL, false>(t, i, n, y, key);
     else
-      store_states<TAIL, true>(t, i, n, m, y, key);
+      store_states<TAIL, true>(t, i, n, y, key);
   }
 }
 
