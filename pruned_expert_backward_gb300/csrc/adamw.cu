@@ -7,6 +7,8 @@
 // Bound by memory: every tensor is read once and written once.  The tensors' addresses travel in the kernel's
 // parameters (no table on the device), a CTA takes chunks of 8192 elements in turn, a warp 256 of them at a time: lane
 // l has elements 4 l .. 4 l + 3 and 128 more on, so that loads of every type are whole sectors in a row.
+// GB300, 100M bf16 weights with fp32 gradients: 32-bit states 392 us (0.95 of the copy rate), 8-bit ones 251 us (0.74:
+// 474 instructions a block of 256, issued in 61 % of the cycles); 429M of them in 8 bits with the norm 1219 us.
 //
 // States in 8 bits: m and sqrt(v) in e4m3, the largest magnitude of each 256 elements of a tensor held as 448 with an
 // fp32 scale, one block to a warp.  They are rounded up or down at random, with the odds that keep the mean: to nearest
@@ -317,6 +319,22 @@ __device__ __forceinline__ void update_block(const lrm_adamw_tensor& t, int64_t 
   }
 }
 
+// Asks L2 for the lines of a block with 8-bit states, a line to a lane.
+template <typename W, typename G>
+__device__ __forceinline__ void ahead(const lrm_adamw_tensor& t, int64_t i, int lane) {
+  constexpr int kG = kBlock * sizeof(G) / 128, kW = kBlock * sizeof(W) / 128, kS = kBlock / 128;
+  const char* p = nullptr;
+  if (lane < kG)
+    p = static_cast<const char*>(t.g) + i * (int64_t)sizeof(G) + lane * 128;
+  else if (lane < kG + kW)
+    p = static_cast<const char*>(t.w) + i * (int64_t)sizeof(W) + (lane - kG) * 128;
+  else if (lane < kG + kW + kS)
+    p = static_cast<const char*>(t.m) + i + (lane - kG - kW) * 128;
+  else if (lane < kG + kW + 2 * kS)
+    p = static_cast<const char*>(t.v) + i + (lane - kG - kW - kS) * 128;
+  if (p != nullptr) asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 template <typename W, typename G, bool BITS8, bool COPY>
 __global__ void __launch_bounds__(kThreads, kAdamCtas) adamw_kernel(const __grid_constant__ Table a, const Hyper h) {
   chain_wait();
@@ -359,7 +377,11 @@ __global__ void __launch_bounds__(kThreads, kAdamCtas) adamw_kernel(const __grid
     }
     const lrm_adamw_tensor& t = a.t[ti];
     const int64_t begin = (int64_t)(c - t_first) * kChunk, end = min(t.n, begin + kChunk);
-    for (int64_t i = begin + warp * kBlock; i < end; i += (kThreads / 32) * kBlock) {
+    constexpr int64_t kNext = (kThreads / 32) * kBlock;
+    for (int64_t i = begin + warp * kBlock; i < end; i += kNext) {
+      // 8-bit states: the warp's next block of the chunk is fetched under this one's arithmetic (100M fp32 weights 265
+      // us, 301 without; bf16 ones 251 and 270; across chunks, or a fifth CTA instead, less; 32-bit states gain nothing)
+      if (BITS8 && i + kNext + kBlock <= end) ahead<W, G>(t, i + kNext, lane);
       if (i + kBlock <= t.n)
         update_block<W, G, BITS8, COPY, false>(t, i, lane, h, factor, decay, rate, inv_c2, key);
       else
