@@ -465,8 +465,8 @@ lrm_status lrm_linear_backward(const int32_t* seg_offsets, const void* dz, const
  * ------------------------------------------------------------------------------------------- */
 
 /*
- * Rows in 8 bits, in place (row_of_pair NULL, k = 1: row t to row t), or each token's row to the rows of its pairs in
- * the sorted batch (lrm_sort_tokens without x, then this, in place of the rows it would copy).
+ * Rows in 8 bits: row t to row t (row_of_pair NULL, k = 1), or each token's row to the rows of its pairs in the sorted
+ * batch (lrm_sort_tokens without x, then this, instead of the rows it would copy).
  *   x [T,K] dt, row_of_pair [T*k] int32 or NULL  ->  q [cap,K] e4m3, scale [cap,nk] fp32
  * A row outside [-1, cap) is not followed and sets LRM_ERR_BAD_INDEX.  Rows that no pair names are not written.
  * Without row_of_pair cap >= T.  For a gradient of SwiGLU's columns [R,2N] call it on 2R rows of N columns.

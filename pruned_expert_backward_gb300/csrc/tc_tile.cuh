@@ -1,5 +1,4 @@
-// What the tile kernels of a CTA pair share: the order of tiles, the way of an epilogue's columns out of registers,
-// tensor maps of outputs, and the launch.
+// What the tile kernels of a CTA pair share: the order of tiles, the row tiles of segments, and the launch.
 #pragma once
 
 #include "kernels.h"
@@ -71,123 +70,10 @@ __device__ __forceinline__ int segment_tiles(const int32_t* seg, int E, int64_t 
   return valid ? prefix[E] : 0;
 }
 
-// 32 columns of one row per lane go out: whole 32-row blocks through the warp's next box(es) and TMA
-// (which clips columns past the tensor), others by each live lane.
-template <int BOXES>
-struct Out {
-  uint8_t* boxes;
-  uint32_t boxes_s;
-  int next;
-  __device__ __forceinline__ void box(const uint4 (&q)[4], const CUtensorMap* map, int lane, int n, int row, int e) {
-    if (lane == 0) bulk_wait_read<BOXES - 1>();  // the store that used this box has read it
-    __syncwarp();
-    uint8_t* line = boxes + next * kBoxBytes + lane * 64;
-    const int swz = (lane >> 1) & 3;  // 64-byte swizzle: piece j of row r sits at j ^ ((r >> 1) & 3)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(line + ((j ^ swz) << 4)) = q[j];
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) tma_store_3d(map, boxes_s + next * kBoxBytes, n, row, e);
-    next = next + 1 == BOXES ? 0 : next + 1;
-  }
-  template <typename T>
-  __device__ __forceinline__ void put(const float (&v)[32], const CUtensorMap* map, int lane, int n, int cols, int row,
-                                      int e, bool whole, bool live, T* row_ptr) {
-    constexpr int VN = VecTraits<T>::N;
-    constexpr int PC = 4 * VN;  // columns of a box
-#pragma unroll
-    for (int h = 0; h < 32 / PC; ++h) {
-      uint4 q[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float f[VN];
-#pragma unroll
-        for (int i = 0; i < VN; ++i) f[i] = v[h * PC + j * VN + i];
-        q[j] = pack(f);
-      }
-      const int c0 = n + h * PC;
-      if (whole) {
-        if (c0 < cols) box(q, map, lane, c0, row, e);  // warp-uniform
-      } else if (live) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (c0 + j * VN < cols) st16(row_ptr + c0 + j * VN, q[j]);
-      }
-    }
-  }
-};
-
-// v += 32 values of a row of T at column n (columns past `cols` are left alone).
-template <typename T>
-__device__ __forceinline__ void add_row(float (&v)[32], const T* row, int n, int cols) {
-  constexpr int VN = VecTraits<T>::N;
-#pragma unroll
-  for (int j = 0; j < 32 / VN; ++j)
-    if (n + j * VN < cols) {
-      float f[VN];
-      unpack(*reinterpret_cast<const uint4*>(row + n + j * VN), f);
-#pragma unroll
-      for (int i = 0; i < VN; ++i) v[j * VN + i] += f[i];
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ void add_vectors(float (&v)[32], const uint4* r) {
-  constexpr int VN = VecTraits<T>::N;
-#pragma unroll
-  for (int j = 0; j < 32 / VN; ++j) {
-    float f[VN];
-    unpack(r[j], f);
-#pragma unroll
-    for (int i = 0; i < VN; ++i) v[j * VN + i] += f[i];
-  }
-}
-
-template <int ACT>
-__device__ __forceinline__ void act32(float (&v)[32]) {
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = act_value<ACT>(v[i]);
-}
-
 // ---------------------------------------------------------------- host side ----------
-// [d2][d1][d0] of 2- or 4-byte elements, d0 contiguous (a multiple of 16 bytes), with a {b0, b1, 1} box.
-bool make_map(CUtensorMap* m, const void* base, bool f32, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
-              uint64_t stride2, uint32_t b0, uint32_t b1, bool operand) {
-  const cuuint64_t dims[3] = {d0, d1, d2};
-  const cuuint64_t strides[2] = {stride1, stride2};
-  const cuuint32_t box[3] = {b0, b1, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return encode_fn()(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                     const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     operand ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                     operand ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-// An output [groups][rows][cols] in 32-row boxes of 64 bytes; halves: [rows][2][cols] seen as two groups.
-bool output_map(CUtensorMap* m, const void* base, bool f32, uint64_t cols, uint64_t rows, uint64_t groups,
-                bool halves = false) {
-  const uint64_t b = f32 ? 4 : 2, line = cols * b * (halves ? 2 : 1);
-  return make_map(m, base, f32, cols, rows, groups, line, halves ? cols * b : rows * line, f32 ? 16 : 32, 32, false);
-}
-
-// Most row tiles there can be, and about how many (every segment ends in half a tile).
+// Most row tiles there can be.
 int64_t row_tiles(const int32_t* seg, int64_t R, int E) {
   return (R + kTileRows - 1) / kTileRows + (seg != nullptr ? E : 0);
-}
-int64_t likely_row_tiles(const int32_t* seg, int64_t R, int E) {
-  return (R + kTileRows - 1) / kTileRows + (seg != nullptr ? (R < E ? R : E) / 2 : 0);
-}
-
-// Tile width by the waves of tiles over the CTA pairs: a K slice of a 256-column tile takes 0.26 us (its
-// products), one of a 128- or 64-column tile 0.155 us (the operands' way in).  On a tie the narrower: more
-// SMs then share the reading of the weights.
-template <typename F>
-lrm_status with_width(int64_t tiles_m, int N, int least, F&& f) {
-  const int64_t pairs = sm_count() / 2;
-  auto cost = [&](int bn, int slice) { return (tiles_m * ((N + bn - 1) / bn) + pairs - 1) / pairs * slice; };
-  const int64_t c256 = cost(256, 5), c128 = cost(128, 3), c64 = least > 64 ? INT64_MAX : cost(64, 3);
-  if (c64 <= c128 && c64 <= c256) return f(IntTag<64>{});
-  return c128 <= c256 ? f(IntTag<128>{}) : f(IntTag<256>{});
 }
 
 // `kernel` over `tiles_bound` tiles at most: persistent CTA pairs, as many as fit the GPU.
