@@ -10,17 +10,17 @@
 //
 // CTA pairs and tiles are those of linear_tc.cu: 256 x BN tiles over a persistent grid.  Warp 0 issues the TMA loads,
 // warp 1 of the leader the MMAs, warps 2 and 3 bring the tile's place and its scales to shared memory (segment bounds
-// and scales are trips to memory that the epilogue would wait for), the rest are the epilogue: each has a 32-row quarter
-// of TMEM by 64 columns (SwiGLU: 32 gate columns and the 32 up columns that go with them), which lie in one block of 128
-// columns of W.
+// and scales are trips to memory that the epilogue would wait for), the rest are the epilogue: each has a 32-row
+// quarter of TMEM by 64 columns (SwiGLU: 32 gate columns and the 32 up columns that go with them), which lie in one
+// block of 128 columns of W.
 //
 // A 256-column slice costs the tensor core 557 cycles and the 16 epilogue warps' loads and sums 300 (one multiply-add
 // an element and slice, two an instruction), but 830 in all: TMEM holds two accumulators, so that a slice's products
 // wait until all 32 warps of the pair have taken out the one before the last, and the signals both ways are as long as
 // the sums.  Four accumulators of 128 columns each bring half as many products for three quarters of the operands
 // (bound by L2: 0.25 us a slice, 256 columns 0.43 us); eight epilogue warps of 128 columns hide less.
-// GB300: 32768 x 4096 x 4096 412 us (2.7 PFLOP/s), with bias, GELU and residual 530 us; 65536 rows over 128 experts to
-// 2 x 768, K = 2048, SwiGLU 247 us (with z 284 us), its rows' gradient 267 us, 768 to 2048 180 us.
+// GB300: 32768 x 4096 x 4096 412 us (2.7 PFLOP/s), with bias, GELU and residual 514 us; 65536 rows over 128 experts to
+// 2 x 768, K = 2048, SwiGLU 244 us (with z 281 us), its rows' gradient 266 us, 768 to 2048 180 us.
 //
 // W stays as it was quantised: FWD reads its rows K-major, DX the same bytes with the columns contiguous (MN-major).
 #include "fp8.cuh"
@@ -53,7 +53,8 @@ struct Scales {
   int tile[4];  // e, row0, row_end, n0 of the tile
 };
 
-template <int BN, bool GLU, bool RES>
+// RES: 0 without a residual, 1 with one, 2 with one and outputs that go straight to memory.
+template <int BN, bool GLU, int RES>
 struct Cfg {
   static constexpr int kABytes = kBM * kBK;
   static constexpr int kBBytes = BN / 2 * kBK;  // this CTA's half of the columns
@@ -212,9 +213,14 @@ __device__ __forceinline__ void add8(float* v, uint4 r) {
   for (int i = 0; i < 8; ++i) v[i] += f[i];
 }
 
+__device__ __forceinline__ void st32(void* p, uint4 a, uint4 b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
 // A warp's 32 rows of bf16 output, a row per lane: whole 32-row blocks go through shared memory and TMA (which clips
 // columns past the tensor), others by each live lane.  WIDE: in one box of 64 columns, else in boxes of 32.
-template <bool WIDE>
+template <bool WIDE, bool SECTORS>
 struct Boxes {
   uint8_t* box;
   int lane;
@@ -227,19 +233,24 @@ struct Boxes {
     if (lane == 0) bulk_wait_read<0>();
     __syncwarp();
   }
-  // 32 columns into chunk c, or to memory
+  // 32 columns into chunk c, or to memory (SECTORS: always, in whole sectors)
   __device__ __forceinline__ void put(const float (&v)[32], int c, int n, int cols, bool whole, bool live,
                                       B16* at) const {
+    uint4 last;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float f[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = v[8 * j + i];
       const uint4 q = pack(f);
-      if (whole)  // warp-uniform
+      if constexpr (SECTORS) {
+        if ((j & 1) && live && n + 8 * j < cols) st32(at + 8 * j - 8, last, q);
+        last = q;
+      } else if (whole) {  // warp-uniform
         *piece(c, j) = q;
-      else if (live && n + 8 * j < cols)
+      } else if (live && n + 8 * j < cols) {
         st16(at + 8 * j, q);
+      }
     }
   }
   __device__ __forceinline__ void send(const CUtensorMap* map, int c, int n, int row, int half) const {
@@ -290,7 +301,7 @@ __device__ __forceinline__ Tile decode(const Params& p, const int* prefix, int t
   return d;
 }
 
-template <int KIND, int BN, bool GLU, bool RES>
+template <int KIND, int BN, bool GLU, int RES>
 __global__ void __launch_bounds__(Cfg<BN, GLU, RES>::kThreads, 1)
     fp8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ,
@@ -545,14 +556,14 @@ __global__ void __launch_bounds__(Cfg<BN, GLU, RES>::kThreads, 1)
       }
       if (!mine) continue;
       // without segments the output map ends where the rows end, so TMA clips a partial block
-      const bool whole = nrows == 32 || p.seg == nullptr;
+      const bool whole = RES != 2 && (nrows == 32 || p.seg == nullptr);
       const bool live = lane < nrows;
       const int64_t row = row_base + lane;
       if (RES) {
         mbar_wait_here(res_bar, rph, abortv, p.status);
         rph ^= 1u;
       }
-      const Boxes<!GLU> out{boxes, lane};
+      const Boxes<!GLU, RES == 2> out{boxes, lane};
       if (KIND == FWD && bias != nullptr) {
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -600,6 +611,7 @@ __global__ void __launch_bounds__(Cfg<BN, GLU, RES>::kThreads, 1)
         out.put(v, c, n_first + c * 32, p.N, whole, live, static_cast<B16*>(p.y) + row * p.N + n_first + c * 32);
       }
       if (whole) out.send(&tmY, 0, n_first, row_base, 0);
+      if (RES == 2) __syncwarp();  // every lane has read its residual: the next may come
     }
     if (lane == 0) bulk_wait_all();  // stores complete before the CTA exits
   }
@@ -674,7 +686,8 @@ lrm_status launch_fp8_tc(const Fp8Args& a, cudaStream_t s) {
   if (a.residual != nullptr && !rows_map(&mR, a.residual, a.N, a.R, 1, wide)) return LRM_ERR_CUDA;
   auto tiles = [&](auto bn, auto glu_tag, auto res_tag) {
     constexpr int BN = decltype(bn)::value;
-    constexpr bool GLU = decltype(glu_tag)::value != 0, RES = decltype(res_tag)::value != 0;
+    constexpr bool GLU = decltype(glu_tag)::value != 0;
+    constexpr int RES = decltype(res_tag)::value;
     constexpr int cols = GLU ? BN / 2 : BN;
     using C = Cfg<BN, GLU, RES>;
     p.tiles_n = (a.N + cols - 1) / cols;
@@ -682,12 +695,18 @@ lrm_status launch_fp8_tc(const Fp8Args& a, cudaStream_t s) {
     return launch_pairs<fp8_tc_kernel<FWD, BN, GLU, RES>>(
         C::smem(), C::kThreads, row_tiles(a.seg_offsets, a.R, a.E) * p.tiles_n, s, mA, mB, mY, mZ, mR, p);
   };
+  // Where the boxes hold the residual and pieces of 32 bytes are aligned, outputs go straight to memory (32768 x 4096 x
+  // 4096 with bias, GELU and residual 514 us, through the boxes 521; without a residual the boxes are faster, 768 to
+  // 2048 180 us and 190).
+  const uintptr_t starts = reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.z);
+  const bool sectors = a.N % 16 == 0 && (starts & 31) == 0;
   auto go = [&](auto bn, auto glu_tag) {
-    return a.residual != nullptr ? tiles(bn, glu_tag, IntTag<1>{}) : tiles(bn, glu_tag, IntTag<0>{});
+    if (a.residual == nullptr) return tiles(bn, glu_tag, IntTag<0>{});
+    return sectors ? tiles(bn, glu_tag, IntTag<2>{}) : tiles(bn, glu_tag, IntTag<1>{});
   };
   // Tile width by the waves of tiles over the CTA pairs; a K slice of a 256-column tile takes 0.43 us (its sums out of
-  // TMEM), of a 128-column one 0.25 us, of a 64-column one 0.22 us.  E.g. 256 rows over 8 experts to 2 x 1408, K = 4096:
-  // 88, 176 or 352 tiles, 35, 31 and 44 us; 8192 x 4096 x 4096 110, 123 and 211 us; 32 rows, 17, 12 and 11 us.
+  // TMEM), of a 128-column one 0.25 us, of a 64-column one 0.22 us.  E.g. 256 rows over 8 experts to 2 x 1408, K =
+  // 4096: 88, 176 or 352 tiles, 35, 31 and 44 us; 8192 x 4096 x 4096 110, 123 and 211 us; 32 rows, 17, 12 and 11 us.
   const double rows = likely_tiles(a.seg_offsets != nullptr, a.R, a.E);
   const int pairs = sm_count() / 2, per = glu ? 2 : 1;
   auto cost = [&](int bn, double slice) { return ceil(rows * ((a.N * per + bn - 1) / bn) / pairs) * slice; };
@@ -701,7 +720,7 @@ lrm_status launch_fp8_tc(const Fp8Args& a, cudaStream_t s) {
 
 lrm_status launch_fp8_dx(const Fp8GradArgs& a, cudaStream_t s) {
   if (!device_ok() || encode_fn() == nullptr) return LRM_ERR_UNSUPPORTED;
-  using C = Cfg<256, false, false>;
+  using C = Cfg<256, false, 0>;
   Params p{};
   p.E = a.E;
   p.R = a.R;
@@ -720,7 +739,7 @@ lrm_status launch_fp8_dx(const Fp8GradArgs& a, cudaStream_t s) {
   if (!fp8_map(&mA, a.dz, a.N, p.halves, a.R, 1, kBM) ||
       !fp8_map(&mB, a.w, a.K, a.N, (uint64_t)a.E * p.halves, kBK, 1) || !rows_map(&mY, a.dx, a.K, a.R, 1, 64))
     return LRM_ERR_CUDA;
-  return launch_pairs<fp8_tc_kernel<DX, 256, false, false>>(
+  return launch_pairs<fp8_tc_kernel<DX, 256, false, 0>>(
       C::smem(), C::kThreads, row_tiles(a.seg_offsets, a.R, a.E) * p.tiles_n, s, mA, mB, mY, mY, mY, p);
 }
 
