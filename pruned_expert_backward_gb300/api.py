@@ -799,8 +799,13 @@ class MoeLayer:
                 self.dyq, self.dhq = rows(H), rows(I, 2)
         self.ws = torch.empty(ws, dtype=torch.uint8, device=dev)
 
+    def _check_weights(self, *weights):
+        if any(isinstance(w, torch.Tensor) == self.fp8 for w in weights):
+            raise ValueError("fp8=True takes the pairs of lrm_fp8_quantize_weight, fp8=False the weights")
+
     def forward(self, x, topk_idx, alpha, w_gate_up, w_down, residual=None):
         """y [T,H] = residual + sum_j alpha[t,j] * w_down[e] SwiGLU(w_gate_up[e] x_t), e = topk_idx[t,j] (-1: none)."""
+        self._check_weights(w_gate_up, w_down)
         seg, st = self.seg_offsets, dict(dev_status=self.dev_status)
         # (serving in 8 bits, no row is copied in bf16: a token is rounded once, straight to its rows)
         lrm_sort_tokens(topk_idx, x if self.x_s is not None else None, self.E, seg_offsets=seg,
@@ -822,6 +827,7 @@ class MoeLayer:
         """Gradients of the last forward: dx [T,H], dalpha [T,k], dw_gate_up, dw_down (the residual's is dy)."""
         if not self.train:
             raise ValueError("MoeLayer(train=False) keeps no state for a backward")
+        self._check_weights(w_gate_up, w_down)
         seg, st, kw = self.seg_offsets, dict(dev_status=self.dev_status), dict(ws=self.ws, dev_status=self.dev_status)
         lrm_combine_backward(self.row_of_pair, alpha, dy, self.y_s, dy_s=self.dy_s, dalpha=self.dalpha, **st)
         if self.fp8:

@@ -163,6 +163,47 @@ def test_layer_without_tokens_and_refusals():
         lrm.MoeLayer(4, 2, 4, 72, 32, fp8=True)
     with pytest.raises(ValueError):
         lrm.lrm_linear_backward(dy, x, None)
+    for other, a, b in ((layer, w1, w2), (layer, q1, w2), (lrm.MoeLayer(4, 2, 4, 64, 32), q1, q2)):
+        with pytest.raises(ValueError):
+            other.forward(x, idx, alpha, a, b)
+        with pytest.raises(ValueError):
+            other.backward(dy, alpha, a, b)
+
+
+def test_two_layers_captured_side_by_side():
+    """Two layers and their optimisers, each captured into a graph of its own, replayed at once on two streams: they
+    share no memory, so each repeats its own bits."""
+    import pruned_expert_backward_gb300 as lrm
+    T, k, E, H, I = 700, 4, 8, 256, 128
+    made = []
+    for n in range(2):
+        x, dy, idx, alpha, w1, w2 = make(T + n, k, E, H, I)
+        q1, q2 = lrm.lrm_fp8_quantize_weight(w1, glu=True), lrm.lrm_fp8_quantize_weight(w2)
+        layer = lrm.MoeLayer(T + n, k, E, H, I, fp8=True)
+        opt = lrm.AdamW([w1, w2], [layer.dw_gate_up, layer.dw_down], lr=0.0, weight_decay=0.0, state_bits=8,
+                        max_norm=1.0, seed=n, capturable=True)
+
+        def step(x=x, dy=dy, idx=idx, alpha=alpha, q1=q1, q2=q2, layer=layer, opt=opt):
+            layer.forward(x, idx, alpha, q1, q2)
+            layer.backward(dy, alpha, q1, q2)
+            opt.step()
+
+        step()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (layer.y, layer.dx, layer.dw_gate_up, layer.dw_down, opt.norm)]
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph):
+            step()
+        made.append((graph, stream, layer, opt, want, step))
+    for _ in range(5):
+        for graph, stream, *_rest in made:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, layer, opt, want, _ in made:
+        for got, w in zip((layer.y, layer.dx, layer.dw_gate_up, layer.dw_down, opt.norm), want):
+            assert torch.equal(got, w)
+        assert int(layer.dev_status.item()) == 0 and int(opt.step_dev.item()) == 6
 
 
 _EVERY_CALL = r"""
