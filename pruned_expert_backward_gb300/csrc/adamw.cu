@@ -471,9 +471,6 @@ void for_tables(const lrm_adamw_tensor* tensors, int32_t count, F&& f) {
   flush();
 }
 
-
-
-
 unsigned ctas(uint32_t chunks, int per_sm) {
   const uint32_t room = (uint32_t)(per_sm * sm_count());
   return chunks < room ? chunks : room;
