@@ -560,7 +560,7 @@ lrm_status lrm_grad_norm(const lrm_adamw_tensor* tensors, int32_t count, lrm_dty
  *   w = w (1 - lr wd) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
  * w_dt, g_dt: types of all weights and of all gradients.  copy: 1 where every tensor has a bf16 copy (w_dt
  * LRM_F32), else 0.  state_bits 32, or 8: m and sqrt(v) are then e4m3 values, 256 elements of a tensor to a scale
- * (their largest magnitude, at least 2^-120, over 448), rounded up or down at random with the odds that keep the mean:
+ * (their largest magnitude, at least 2^-119, over 448), rounded up or down at random with the odds that keep the mean:
  * with h = mix(e * 0x9E3779B1 + (e >> 32) * 0xC2B2AE3D + mix(mix(seed + 0x9E3779B9 (id + 1)) ^ step)) for element
  * e and MurmurHash3's finaliser mix, all modulo 2^32, m by the low and sqrt(v) by the high 16 bits of h.  The step's
  * update uses m and v before that rounding; a sqrt(v) above 0 is held as 2^-9 of its scale at least.  A state of 8 bits

@@ -29,7 +29,9 @@ constexpr int kBlock = 256;                 // elements of a warp at a time, and
 constexpr int kChunk = 8192;                // elements of a CTA's task
 constexpr int kTable = 384;                 // tensors of a launch (32 KB of parameters, the most there can be)
 constexpr int kAdamCtas = 4, kNormCtas = 8;  // of a multiprocessor
-constexpr float kStateLeast = 0x1p-120f;    // blocks of smaller states are scaled as if this were their largest
+// Blocks of smaller states, all zeros among them, are scaled as if this were their largest.  448 over it has to be an
+// fp32 value: over 2^-120 it is infinite, and 0 times that a NaN.
+constexpr float kStateLeast = 0x1p-119f;
 
 struct Table {
   lrm_adamw_tensor t[kTable];

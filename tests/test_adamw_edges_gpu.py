@@ -1,0 +1,107 @@
+"""Edges of lrm_adamw and AdamW: blocks of 8-bit states that are zero or near the floor of their scale."""
+import pytest
+import torch
+
+from helpers import ensure_built
+from test_adamw_gpu import BF16, F32, FP8, Case, gen, values
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    ensure_built()
+
+
+FLOOR = 2.0 ** -119  # of the largest magnitude of 256 elements' states: 448 / FLOOR is an fp32 value
+
+
+def all_finite(opt):
+    return all(bool(torch.isfinite(t.float()).all()) for key in opt.state for t in opt.state[key])
+
+
+@pytest.mark.parametrize("g_dt", [BF16, F32], ids=["bf16", "f32"])
+def test_zero_blocks_stay_zero(g_dt):
+    """An expert without a token: zero states and zero gradients for some steps, then gradients for a part of it."""
+    import pruned_expert_backward_gb300 as lrm
+    n = (1 << 20) + 77
+    w = (torch.randn(n, generator=gen(3), device="cuda") * 0.1).bfloat16()
+    start, g = w.clone(), torch.zeros(n, dtype=g_dt, device="cuda")
+    opt = lrm.AdamW([w], [g], lr=1e-2, betas=(0.9, 0.95), weight_decay=0.0, state_bits=8, max_norm=1.0)
+    for _ in range(3):
+        opt.step()
+        assert all_finite(opt)
+        for key in ("m", "v"):
+            assert int(torch.count_nonzero(opt.state[key][0].float())) == 0
+            scale = opt.state[key + "_scale"][0].double()
+            assert bool(((scale - FLOOR / 448).abs() <= 2.0 ** -149).all())  # (a subnormal's spacing)
+    assert torch.equal(w, start) and opt.norm.item() == 0.0
+    live = torch.zeros(n, dtype=torch.bool, device="cuda")
+    live[:5000] = live[-1] = True
+    g[live] = 1e-3
+    for _ in range(3):
+        opt.step()
+        assert all_finite(opt) and bool(torch.isfinite(w).all())
+    assert torch.equal(w[~live], start[~live])
+    assert bool((w[live].float() < start[live].float()).all())
+    for key in ("m", "v"):
+        held = opt.state[key][0].float()
+        assert int(torch.count_nonzero(held[~live])) == 0 and bool((held[live] > 0).all())
+    assert int(opt.dev_status.item()) == 0
+
+
+def test_states_near_the_floor_of_their_scale():
+    """Halved first moments whose largest is 2^-110 to 2^-140, and none: held within a step of e4m3 (2^-3 of the value,
+    2^-9 of the scale for the smallest), with the scale within its own spacing (2^-149, on 448 steps)."""
+    import pruned_expert_backward_gb300 as lrm
+    powers = [-110, -116, -117, -118, -118.25, -118.5, -118.75, -119, -119.5, -120, -125, -130, -140, None]
+    n = 256 * len(powers)
+    q = torch.rand(n, generator=gen(5), device="cuda") * 446 + 1
+    q[::256] = 448
+    q[1::256] = -448
+    q[2::256] = 2.0 ** -9
+    q[3::256] = 0
+    m = q.to(FP8)
+    for i, p in enumerate(powers):
+        if p is None:
+            m[256 * i:256 * (i + 1)] = torch.zeros(256, device="cuda").to(FP8)
+    scale = torch.tensor([0.0 if p is None else 2.0 ** p / 448 for p in powers], device="cuda")
+    state = {"m": [m], "m_scale": [scale], "v": [torch.zeros(n, device="cuda").to(FP8)],
+             "v_scale": [torch.zeros(len(powers), device="cuda")]}
+    want = values(m, scale) / 2
+    w, g = torch.ones(n, device="cuda"), torch.zeros(n, device="cuda")
+    opt = lrm.AdamW([w], [g], lr=1e-2, betas=(0.5, 0.9), weight_decay=0.0, state_bits=8, state=state, seed=3)
+    opt.step()
+    assert all_finite(opt)
+    top = want.abs().view(-1, 256).amax(1).clamp_min(FLOOR)
+    new = opt.state["m_scale"][0].double()
+    assert bool(((new - top / 448).abs() <= 2.0 ** -20 * top / 448 + 2.0 ** -148).all())
+    held, spacing = values(opt.state["m"][0], opt.state["m_scale"][0]), new.repeat_interleave(256)
+    assert bool(((held - want).abs() <= 2.0 ** -3 * want.abs() + 2.0 ** -9 * spacing + 448 * 2.0 ** -148).all())
+    assert bool((held[want == 0] == 0).all())
+    assert torch.equal(w, torch.ones_like(w))  # m / eps is below 2^-80
+    for _ in range(3):
+        opt.step()
+        assert all_finite(opt) and bool(torch.isfinite(w).all())
+
+
+def test_zero_elements_past_32_bits():
+    """Every state of a tensor whose element numbers pass 32 bits, without gradient but for its end."""
+    import pruned_expert_backward_gb300 as lrm
+    n = 2 ** 32 + 777
+    if torch.cuda.mem_get_info()[0] < 40e9:
+        pytest.skip("needs 40 GB")
+    w, g = torch.zeros(n, dtype=BF16, device="cuda"), torch.zeros(n, dtype=BF16, device="cuda")
+    g[-300:] = 0.5
+    opt = lrm.AdamW([w], [g], lr=1e-2, betas=(0.9, 0.95), weight_decay=0.0, state_bits=8, seed=21)
+    for _ in range(2):
+        opt.step()
+        for key in ("m", "v"):
+            codes = opt.state[key][0].view(torch.uint8)
+            for part in codes[:-300].split(1 << 30):
+                assert int(torch.count_nonzero(part & 0x7F)) == 0
+            assert bool(torch.isfinite(codes[-300:].view(FP8).float()).all())
+            assert bool(torch.isfinite(opt.state[key + "_scale"][0]).all())
+    assert int(torch.count_nonzero(w[:-300].view(torch.int16))) == 0 and bool((w[-300:] < 0).all())
