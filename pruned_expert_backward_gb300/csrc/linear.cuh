@@ -40,7 +40,8 @@ __device__ __forceinline__ float fast_exp2(float v) {
   return r;
 }
 // Two GELUs at once, two sums or products an instruction (about half the time of two norm_cdf, which the pipe of the
-// single ones bounds): max(z, 0) - |z| erfc(|z| / sqrt 2) / 2, the tail by norm_cdf's polynomial (halved here).
+// single ones bounds): max(z, 0) - |z| erfc(|z| / sqrt 2) / 2, the tail by norm_cdf's polynomial (halved here).  The
+// tail is 0 from 14 on, and its factor is held below infinity there: +inf stays +inf, -inf is NaN as in act_value.
 __device__ __forceinline__ float2 gelu2(float2 z) {
   auto both = [](float v) { return make_float2(v, v); };
   const float2 t = make_float2(fast_recip(fmaf(0.45f * 0.70710678118654752f, fabsf(z.x), 1.f)),
@@ -55,7 +56,8 @@ __device__ __forceinline__ float2 gelu2(float2 z) {
   p = __ffma2_rn(p, t, both(0.5f * 0.2535184919834137f));
   p = __ffma2_rn(p, t, both(0.5f * 0.25391680002212524f));
   const float2 tail = __fmul2_rn(__fmul2_rn(p, t), make_float2(fast_exp2(x.x), fast_exp2(x.y)));
-  return __ffma2_rn(make_float2(-fabsf(z.x), -fabsf(z.y)), tail, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
+  return __ffma2_rn(make_float2(-fabsf(fminf(z.x, 0x1p100f)), -fabsf(fminf(z.y, 0x1p100f))), tail,
+                    make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
 }
 
 // Two SiLUs at once.

@@ -1,0 +1,56 @@
+"""Edges of the 8-bit operators: infinite and NaN pre-activations, whichever kernel a call takes."""
+import pytest
+import torch
+
+from helpers import ensure_built
+from test_fp8_gpu import BF16, F32, operand, plain_blocks, same_bits, status  # noqa: F401
+from test_moe_layer_gpu import check_linear, gen, randn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    ensure_built()
+
+
+def act64(z, act):
+    if act == "swiglu":
+        gate, up = z.chunk(2, 1)
+        return gate * torch.special.expit(gate) * up
+    return {"none": lambda v: v, "relu": lambda v: torch.where(v < 0, torch.zeros_like(v), v),
+            "gelu": lambda v: v * torch.special.ndtr(v), "silu": lambda v: v * torch.special.expit(v)}[act](z)
+
+
+@pytest.mark.parametrize("residual", [False, True], ids=["", "residual"])
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu", "swiglu"])
+@pytest.mark.parametrize("R", [4, 16, 40, 200, 3000])
+def test_infinite_pre_activations(R, act, residual, status):  # noqa: F811
+    """+inf, -inf and NaN by the bias: the outputs' kinds are the 64-bit formula's for any number of rows (0 * inf is
+    NaN there too), their neighbours are as ever."""
+    import pruned_expert_backward_gb300 as lrm
+    per, N, K, g = 2 if act == "swiglu" else 1, 520, 144, gen(R)
+    x, xs = lrm.lrm_fp8_quantize(randn(g, R, K), dev_status=status)
+    w, ws = lrm.lrm_fp8_quantize_weight(randn(g, per * N, K, std=K ** -0.5), glu=act == "swiglu")
+    b = randn(g, per * N, std=0.3)
+    inf, nan = float("inf"), float("nan")
+    b[3], b[40], b[77], b[300] = inf, -inf, nan, inf
+    if per == 2:
+        b[N + 3], b[N + 40], b[N + 100], b[N + 101] = -inf, inf, inf, nan
+    res = randn(g, R, N) if residual else None
+    y, z = lrm.lrm_fp8_linear(x, xs, w, ws, bias=b, residual=res, act=act, save_z=True, dev_status=status)
+    z64 = operand(x, xs, 1) @ operand(w, ws, 128, per).t() + b.double()
+    want = act64(z64, act) + (res.double() if residual else 0)
+    for got, ref in ((z, z64), (y, want)):
+        got = got.double()
+        assert torch.equal(torch.isnan(got), torch.isnan(ref))
+        assert torch.equal(torch.isposinf(got), torch.isposinf(ref))
+        assert torch.equal(torch.isneginf(got), torch.isneginf(ref))
+    usual = torch.isfinite(b.view(per, N)).all(0)
+    cols = torch.nonzero(usual).flatten()
+    rows = torch.cat([cols + i * N for i in range(per)])
+    # (a column's operand does not depend on its neighbours: the usual columns, checked as a product of their own)
+    check_linear(operand(x, xs, 1), operand(w, ws, 128, per)[rows], b[rows], res[:, cols] if residual else None, act,
+                 None, y[:, cols], z[:, rows])
