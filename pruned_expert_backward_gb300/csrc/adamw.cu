@@ -344,11 +344,11 @@ __global__ void __launch_bounds__(kThreads, kAdamCtas) adamw_kernel(const __grid
   __shared__ uint32_t s_step;
   if (threadIdx.x == 0) {
     s_lr = h.lr_dev != nullptr ? *h.lr_dev : h.lr;
-    s_step = h.step_dev != nullptr ? (uint32_t)*h.step_dev : h.step;
+    s_step = h.step_dev != nullptr ? (uint32_t)max(*h.step_dev, 1) : h.step;
     s_c1 = h.c1;
     s_c2 = h.c2;
     if (h.step_dev != nullptr) {
-      const double t = (double)max((int)s_step, 1);
+      const double t = (double)s_step;
       s_c1 = (float)-expm1(t * h.log_b1);
       s_c2 = (float)-expm1(t * h.log_b2);
     }

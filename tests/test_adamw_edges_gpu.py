@@ -1,4 +1,5 @@
-"""Edges of lrm_adamw and AdamW: blocks of 8-bit states that are zero or near the floor of their scale."""
+"""Edges of lrm_adamw and AdamW: blocks of 8-bit states that are zero or near the floor of their scale, steps counted on
+the device."""
 import pytest
 import torch
 
@@ -105,3 +106,18 @@ def test_zero_elements_past_32_bits():
             assert bool(torch.isfinite(codes[-300:].view(FP8).float()).all())
             assert bool(torch.isfinite(opt.state[key + "_scale"][0]).all())
     assert int(torch.count_nonzero(w[:-300].view(torch.int16))) == 0 and bool((w[-300:] < 0).all())
+
+
+def test_a_device_step_below_1_counts_as_1():
+    """Bias corrections and random bits alike."""
+    import pruned_expert_backward_gb300 as lrm
+    out = []
+    for first in (0, -1, -1000):
+        c = Case([5000], F32, F32, 8)
+        opt = c.optimiser(lrm, lr=3e-4, seed=7, capturable=True)
+        opt.step_dev.fill_(first)
+        opt.step()
+        assert int(opt.step_dev.item()) == first + 1
+        out.append([c.w[0], *(c.state[k][0].view(torch.uint8) for k in c.state)])
+    for other in out[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(out[0], other))
