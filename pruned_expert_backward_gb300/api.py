@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+from collections import OrderedDict
 
 import torch
 
@@ -856,6 +857,23 @@ def _on16(n, *addresses):
         raise LrmError(1, "lrm_adamw")
 
 
+class _Frozen(dict):
+    """Lists of tensors that a launch table holds by address: to be read, not assigned to.  Pickles as an ordinary
+    (ordered) dict of lists."""
+
+    def _refuse(self, *args, **kw):
+        raise TypeError("AdamW's state is not assigned to: load_state() takes values into it")
+
+    __setitem__ = __delitem__ = __ior__ = clear = pop = popitem = setdefault = update = _refuse
+
+    def __reduce__(self):
+        return OrderedDict, ([(key, list(held)) for key, held in self.items()],)
+
+
+def _storages(tensors):
+    return [t.untyped_storage() for t in tensors if t is not None]
+
+
 class AdamW:
     """AdamW over many tensors at once (lrm_adamw): one or a few launches a step, whatever the number of tensors.
 
@@ -866,6 +884,9 @@ class AdamW:
     weight_decay and lr_scale: one value, or one for each tensor.  max_norm: gradients are scaled so that their
     common norm is at most that; a step whose norm is not finite changes nothing and sets LRM_ERR_NONFINITE in
     dev_status.  state: {"m": [...], "v": [...]} and, for 8 bits, "m_scale", "v_scale" to go on from; zeros without.
+    The tensors given are the ones that are used, by their addresses: params, copies, grads and state are read-only
+    here, load_state takes other values, set_grads other gradients, and a step is refused where a copy, or a param
+    without one, lies elsewhere since (param.data = ..., a module moved): make a new AdamW then, with state=opt.state.
     capturable: step and rate live on the device (step_dev, lr_dev), so that a captured step can be replayed."""
 
     def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, copies=None,
@@ -882,7 +903,7 @@ class AdamW:
                 raise ValueError(f"{name} must hold {n} values, got {len(a)}")
             return a
 
-        self.params, self.copies, self.state_bits = list(params), each(copies, "copies"), state_bits
+        self._params, self._copies, self._state_bits = tuple(params), tuple(each(copies, "copies")), state_bits
         self.lr, self.betas, self.eps, self.seed, self.max_norm = lr, betas, eps, seed, max_norm
         decay, scale = each(weight_decay, "weight_decay"), each(lr_scale, "lr_scale")
         dev = self.params[0].device
@@ -897,7 +918,10 @@ class AdamW:
                 for key in ("m_scale", "v_scale"):
                     state[key] = [torch.zeros(-(-t.numel() // 256), dtype=torch.float32, device=t.device)
                                   for t in self.params]
-        self.state = state
+        self._state = _Frozen({key: tuple(state[key]) for key in self._state_keys()})
+        for key, held in self._state.items():
+            if len(held) != n:
+                raise ValueError(f"state {key} must hold {n} tensors, got {len(held)}")
         # the tensors by the types that share a launch, in order
         self._groups = []
         kinds = {}
@@ -914,32 +938,35 @@ class AdamW:
                     _same(self.copies[i], t.shape, "copy")
                     e.copy = _cuda(self.copies[i], "copy", torch.bfloat16)
                 for key in ("m", "v"):
-                    s = state[key][i]
+                    s = self._state[key][i]
                     if s.numel() != t.numel():
                         raise ValueError(f"state {key} must hold {t.numel()} values, got {s.numel()}")
                     setattr(e, key, _cuda(s, key, torch.float32 if state_bits == 32 else FP8))
                     if state_bits == 8:
-                        s = state[key + "_scale"][i]
+                        s = self._state[key + "_scale"][i]
                         if s.numel() != -(-t.numel() // 256):
                             raise ValueError(f"state {key}_scale must hold a value for each 256, got {s.numel()}")
                         setattr(e, key + "_scale", _cuda(s, key + "_scale", torch.float32))
             self._groups.append((w_dt, copy, members, table))
         # what a step writes: two tensors on the same bytes would race
-        held = [state[key] for key in (("m", "v") if state_bits == 32 else ("m", "v", "m_scale", "v_scale"))]
-        spans = sorted((t.data_ptr(), t.numel() * t.element_size()) for own in (self.params, self.copies, *held)
-                       for t in own if t is not None and t.numel())
+        written = [t for own in (self.params, self.copies, *self._state.values()) for t in own if t is not None]
+        spans = sorted((t.data_ptr(), t.numel() * t.element_size()) for t in written if t.numel())
         for (a, n_bytes), (b, _) in zip(spans, spans[1:]):
             if a + n_bytes > b:
                 raise ValueError("params, copies and states must not share memory")
         for _, _, _, table in self._groups:
             for e in table:
                 _on16(e.n, e.w, e.copy, e.m, e.v)
+        # the tables hold addresses: their memory lives as long as they do, whatever becomes of the tensors, and a step
+        # looks whether what a model reads, copies or else params, still lies there (54 ns a tensor)
+        self._held = _storages(written)
+        self._watched = [t if copy is None else copy for t, copy in zip(self.params, self.copies)]
+        self._watched_at = list(map(torch.Tensor.data_ptr, self._watched))
         # one table of all tensors for the common norm
         self._all = self._groups[0][3] if len(self._groups) == 1 else (L.AdamwTensor * n)()
         if len(self._groups) > 1:
             for i, t in enumerate(self.params):
                 self._all[i].n = t.numel()
-        self.grads, self._g_dt = None, None
         self.set_grads(grads)
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.norm = self._ws = None
@@ -972,7 +999,33 @@ class AdamW:
         if len(self._groups) > 1:
             for i, p in enumerate(at):
                 self._all[i].g = p
-        self.grads, self._g_dt = grads, g_dt
+        self._grads, self._g_dt, self._held_grads = tuple(grads), g_dt, _storages(grads)
+
+    def load_state(self, state):
+        """Takes the values of a state like `state` (tensors on any device) into the tensors held here, where captured
+        steps read them too."""
+        pairs = []
+        for key, held in self._state.items():
+            given = list(state[key])
+            if len(given) != len(held):
+                raise ValueError(f"state {key} must hold {len(held)} tensors, got {len(given)}")
+            for own, t in zip(held, given):
+                if t.numel() != own.numel():
+                    raise ValueError(f"state {key} must hold {own.numel()} values, got {t.numel()}")
+                if t.dtype != own.dtype:
+                    raise TypeError(f"state {key} must be {own.dtype}, got {t.dtype}")
+                pairs.append((own, t))
+        for own, t in pairs:
+            own.copy_(t.reshape(own.shape))
+
+    def _state_keys(self):
+        return ("m", "v") if self._state_bits == 32 else ("m", "v", "m_scale", "v_scale")
+
+    params = property(lambda self: self._params)
+    copies = property(lambda self: self._copies)
+    grads = property(lambda self: self._grads)
+    state = property(lambda self: self._state)
+    state_bits = property(lambda self: self._state_bits)
 
     def step(self, step=None, lr=None, grads=None):
         """One step; returns the gradients' norm (fp32 scalar on the device) with max_norm, else None.  step: its
@@ -983,6 +1036,8 @@ class AdamW:
         if self.step_dev is not None:
             if step is not None or lr is not None:
                 raise ValueError("a capturable step takes step and rate from step_dev and lr_dev")
+        if list(map(torch.Tensor.data_ptr, self._watched)) != self._watched_at:
+            raise ValueError("a copy, or a param without one, lies elsewhere than when this AdamW was made: make another")
         number = self.steps + 1 if step is None else int(step)
         if number < 1:
             raise ValueError(f"steps count from 1, got {number}")

@@ -1,5 +1,5 @@
 """Edges of lrm_adamw and AdamW: blocks of 8-bit states that are zero or near the floor of their scale, steps counted on
-the device."""
+the device, tensors that moved and states that are loaded."""
 import pytest
 import torch
 
@@ -121,3 +121,77 @@ def test_a_device_step_below_1_counts_as_1():
         out.append([c.w[0], *(c.state[k][0].view(torch.uint8) for k in c.state)])
     for other in out[1:]:
         assert all(torch.equal(a, b) for a, b in zip(out[0], other))
+
+
+def moved(t):
+    """The tensor's values elsewhere, as a module that is moved leaves it; where they were."""
+    old = t.data_ptr()
+    t.data = t.data.clone()
+    assert t.data_ptr() != old
+    return old
+
+
+def test_memory_that_the_tables_address_stays():
+    """A param, copy, gradient or state whose tensor got other memory: nobody else gets the old, and where a copy, or a
+    param without one, moved, a step is refused before it changes anything."""
+    import pruned_expert_backward_gb300 as lrm
+    for which, copy in (("w", False), ("copy", True), ("w", True), ("g", False), ("m", True), ("v", False)):
+        c = Case([70001, 300], F32, F32, 32, copy=copy)
+        other = Case([70001, 300], F32, F32, 32, copy=copy)
+        opt, twin = c.optimiser(lrm, lr=1e-3), other.optimiser(lrm, lr=1e-3)
+        t = c.state[which][0] if which in c.state else getattr(c, which)[0]
+        old = moved(t)
+        taken = [torch.full_like(t, 9.0) for _ in range(64)]
+        assert all(a.data_ptr() != old for a in taken)
+        if which == "copy" or (which == "w" and not copy):
+            with pytest.raises(ValueError):
+                opt.step()
+            assert opt.steps == 0
+            assert all(torch.equal(a, b) for k in c.state for a, b in zip(c.state[k], other.state[k]))
+        else:  # the step goes on where the tables point
+            opt.step()
+            twin.step()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(c.copy if copy else c.w, other.copy if copy else other.w))
+        assert all(bool((a == 9.0).all()) for a in taken)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_state_is_read_only_and_loaded(bits):
+    import io
+
+    import pruned_expert_backward_gb300 as lrm
+    sizes, kw = [5000, 300, 1], dict(lr=1e-3, seed=4, max_norm=1.0)
+    a, b = Case(sizes, BF16, F32, bits, seed=1), Case(sizes, BF16, F32, bits, seed=2)
+    first = a.optimiser(lrm, **kw)
+    first.step()
+    saved = io.BytesIO()
+    torch.save(first.state, saved)
+    saved.seek(0)
+    state = torch.load(saved, map_location="cpu")
+    second = b.optimiser(lrm, **kw)
+    for name in ("params", "copies", "grads", "state", "state_bits"):
+        with pytest.raises(AttributeError):
+            setattr(second, name, getattr(second, name))
+    for call in (lambda: second.state.update(state), lambda: second.state.pop("m"),
+                 lambda: second.state.__setitem__("m", state["m"]), lambda: second.state["m"].__setitem__(0, None),
+                 lambda: second.params.__setitem__(0, None),
+                 lambda: second.load_state(dict(state, m=[t.double() for t in state["m"]]))):
+        with pytest.raises((TypeError, AttributeError)):
+            call()
+    for bad in (state["m"][:2], state["m"][::-1]):
+        with pytest.raises(ValueError):
+            second.load_state(dict(state, m=bad))
+    b.state["m"][0] = None  # (the caller's own list)
+    second.load_state(state)
+    for own, t, g, u in zip(second.params, first.params, second.grads, first.grads):
+        own.copy_(t)
+        g.copy_(u)
+    second.steps = first.steps
+    first.step()
+    second.step()
+    for t, u in zip((*first.params, *(t for k in first.state for t in first.state[k])),
+                    (*second.params, *(t for k in second.state for t in second.state[k]))):
+        assert torch.equal(t.view(torch.uint8) if t.dtype == FP8 else t, u.view(torch.uint8) if u.dtype == FP8 else u)
+    with pytest.raises(ValueError):
+        lrm.AdamW(b.w, b.g, state_bits=bits, state={k: second.state[k][:2] for k in second.state})
