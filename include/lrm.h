@@ -536,7 +536,8 @@ typedef struct lrm_adamw_hyper {
   int64_t step;                 /* 1 for the first step, up to INT32_MAX                                */
   uint32_t seed;                /* of the random bits of 8-bit states                                   */
   double max_norm;              /* with grad_norm: gradients are scaled by min(1, max_norm / (norm + 1e-6)) */
-  const float* grad_norm;       /* DEVICE, from lrm_grad_norm, or NULL; not finite: nothing is changed     */
+  const float* grad_norm;       /* DEVICE, from lrm_grad_norm, or NULL; not finite: nothing is changed (whether such */
+                                /* a step counts is the caller's: step, step_dev)                         */
   const float* lr_dev;          /* DEVICE, or NULL: the rate in place of lr (for captured steps)           */
   const int32_t* step_dev;      /* DEVICE, or NULL: the step in place of step (less than 1 counts as 1)    */
 } lrm_adamw_hyper;

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import math
 from collections import OrderedDict
 
 import torch
@@ -883,7 +884,8 @@ class AdamW:
     scale for 256 elements, rounded at random by `seed`, the step and the element's place (lrm_adamw in lrm.h).
     weight_decay and lr_scale: one value, or one for each tensor.  max_norm: gradients are scaled so that their
     common norm is at most that; a step whose norm is not finite changes nothing and sets LRM_ERR_NONFINITE in
-    dev_status.  state: {"m": [...], "v": [...]} and, for 8 bits, "m_scale", "v_scale" to go on from; zeros without.
+    dev_status (it is not counted in step_dev; in `steps` it is: the host does not learn the norm).
+    state: {"m": [...], "v": [...]} and, for 8 bits, "m_scale", "v_scale" to go on from; zeros without.
     The tensors given are the ones that are used, by their addresses: params, copies, grads and state are read-only
     here, load_state takes other values, set_grads other gradients, and a step is refused where a copy, or a param
     without one, lies elsewhere since (param.data = ..., a module moved): make a new AdamW then, with state=opt.state.
@@ -1028,8 +1030,9 @@ class AdamW:
     state_bits = property(lambda self: self._state_bits)
 
     def step(self, step=None, lr=None, grads=None):
-        """One step; returns the gradients' norm (fp32 scalar on the device) with max_norm, else None.  step: its
-        number, one more than the last by default.  lr: this step's rate in place of the one given at first."""
+        """One step; returns the gradients' norm (fp32 scalar on the device, the same tensor at every step: clone what
+        is to be kept) with max_norm, else None.  step: its number, one more than the last by default.  lr: this step's
+        rate in place of the one given at first."""
         if grads is not None:
             self.set_grads(grads)
         stream = _stream()
@@ -1037,7 +1040,7 @@ class AdamW:
             if step is not None or lr is not None:
                 raise ValueError("a capturable step takes step and rate from step_dev and lr_dev")
         if list(map(torch.Tensor.data_ptr, self._watched)) != self._watched_at:
-            raise ValueError("a copy, or a param without one, lies elsewhere than when this AdamW was made: make another")
+            raise ValueError("a copy, or a param without one, lies elsewhere than when AdamW was made: make another")
         number = self.steps + 1 if step is None else int(step)
         if number < 1:
             raise ValueError(f"steps count from 1, got {number}")
@@ -1045,12 +1048,16 @@ class AdamW:
                          0.0 if self.max_norm is None else self.max_norm, None, None, None)
         lib = L.load()
         if self.step_dev is not None:
-            self.step_dev.add_(1)
             h.step_dev, h.lr_dev = self.step_dev.data_ptr(), self.lr_dev.data_ptr()
         if self.max_norm is not None:
             h.grad_norm = self.norm.data_ptr()
+        # values that are refused are so before anything is launched or counted
+        _ok(lib.lrm_adamw(None, 0, L.LRM_F32, self._g_dt, self.state_bits, 0, C.byref(h), stream), "lrm_adamw")
+        if self.max_norm is not None:
             _ok(lib.lrm_grad_norm(self._all, len(self.params), self._g_dt, h.grad_norm, self._ws.data_ptr(),
                                   self._ws.numel(), self.dev_status.data_ptr(), stream), "lrm_grad_norm")
+        if self.step_dev is not None:
+            self.step_dev.add_(1 if self.max_norm is None else self.norm < math.inf)
         for w_dt, copy, members, table in self._groups:
             _ok(lib.lrm_adamw(table, len(members), w_dt, self._g_dt, self.state_bits, int(copy), C.byref(h), stream),
                 "lrm_adamw")

@@ -195,3 +195,41 @@ def test_state_is_read_only_and_loaded(bits):
         assert torch.equal(t.view(torch.uint8) if t.dtype == FP8 else t, u.view(torch.uint8) if u.dtype == FP8 else u)
     with pytest.raises(ValueError):
         lrm.AdamW(b.w, b.g, state_bits=bits, state={k: second.state[k][:2] for k in second.state})
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_steps_on_the_device_that_are_skipped_or_refused_do_not_count(captured):
+    """A first step whose norm is not finite, then two as if it had not been; a refused one changes no count."""
+    import pruned_expert_backward_gb300 as lrm
+    for bad in (float("inf"), float("nan")):
+        a, b = Case([5000, 33], F32, F32, 8), Case([5000, 33], F32, F32, 8)
+        kw = dict(lr=1e-3, max_norm=0.5, seed=7, capturable=True)
+        opt, plain = a.optimiser(lrm, **kw), b.optimiser(lrm, **kw)
+        for name, value in (("lr", -1.0), ("betas", (0.9, 1.0)), ("eps", float("nan"))):
+            good = getattr(opt, name)
+            setattr(opt, name, value)
+            with pytest.raises(lrm.LrmError):
+                opt.step()
+            setattr(opt, name, good)
+        assert int(opt.step_dev.item()) == 0 and opt.norm.item() == 0.0
+        run = opt.step
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                opt.step()
+            run = graph.replay
+        kept = a.g[0][7].clone()
+        a.g[0][7] = bad
+        run()
+        assert int(opt.step_dev.item()) == 0 and int(opt.dev_status.item()) == 7
+        a.g[0][7] = kept
+        for count in (1, 2):
+            run()
+            plain.step()
+            assert int(opt.step_dev.item()) == int(plain.step_dev.item()) == count
+        for t, u in zip((*a.w, *sum(a.state.values(), [])), (*b.w, *sum(b.state.values(), []))):
+            assert torch.equal(t.view(torch.uint8), u.view(torch.uint8))
+    opt = Case([100], F32, F32, 32).optimiser(lrm, lr=1e-3, capturable=True)  # without a norm every step counts
+    opt.step()
+    opt.step()
+    assert int(opt.step_dev.item()) == 2
