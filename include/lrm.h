@@ -532,7 +532,8 @@ typedef struct lrm_adamw_tensor {
 
 /* Values of a step of lrm_adamw. */
 typedef struct lrm_adamw_hyper {
-  double lr, beta1, beta2, eps; /* 0 <= beta < 1, eps >= 0                                              */
+  double lr, beta1, beta2, eps; /* 0 <= beta < 1; eps 0 (then m / 0 where v is 0, NaN without a gradient) */
+                                /* or at least 2^-126                                                   */
   int64_t step;                 /* 1 for the first step, up to INT32_MAX                                */
   uint32_t seed;                /* of the random bits of 8-bit states                                   */
   double max_norm;              /* with grad_norm: gradients are scaled by min(1, max_norm / (norm + 1e-6)) */

@@ -1,6 +1,7 @@
 // C ABI of the LRM-pruned expert backward: argument validation, workspace layout, dispatch.
 // Every entry point only queues work on the caller's stream; nothing here allocates or
 // synchronises.
+#include <float.h>
 #include <stdint.h>
 #include <stdlib.h>
 #include <string.h>
@@ -715,6 +716,7 @@ lrm_status lrm_adamw(const lrm_adamw_tensor* tensors, int32_t count, lrm_dtype w
   // (written so that a NaN is refused)
   if (!(h.beta1 >= 0 && h.beta1 < 1 && h.beta2 >= 0 && h.beta2 < 1 && h.eps >= 0 && h.lr >= 0))
     return LRM_ERR_INVALID_ARG;
+  if (h.eps > 0 && h.eps < FLT_MIN) return LRM_ERR_INVALID_ARG;  // the kernel's reciprocal would take it for 0
   if (h.grad_norm && !(h.max_norm > 0)) return LRM_ERR_INVALID_ARG;
   if (!h.step_dev && (h.step < 1 || h.step > INT32_MAX)) return LRM_ERR_SHAPE;
   if (!al4(h.grad_norm) || !al4(h.lr_dev) || !al4(h.step_dev)) return LRM_ERR_INVALID_ARG;

@@ -233,3 +233,18 @@ def test_steps_on_the_device_that_are_skipped_or_refused_do_not_count(captured):
     opt.step()
     opt.step()
     assert int(opt.step_dev.item()) == 2
+
+
+def test_the_smallest_eps():
+    """2^-126, with zero and tiny gradients: 0 where there is none, the formula's quotient elsewhere."""
+    import pruned_expert_backward_gb300 as lrm
+    for bits in (8, 32):
+        w, g = torch.zeros(600, device="cuda"), torch.zeros(600, device="cuda")
+        g[300:] = 1e-3
+        opt = lrm.AdamW([w], [g], lr=1e-2, eps=2.0 ** -126, weight_decay=0.0, state_bits=bits)
+        opt.step()
+        assert int(torch.count_nonzero(w[:300])) == 0
+        assert bool(((w[300:] + 1e-2).abs() <= 1e-2 * 2.0 ** -18).all())
+        for bad in (1e-40, 1.17e-38):
+            with pytest.raises(lrm.LrmError):
+                lrm.AdamW([w], [g], eps=bad).step()
