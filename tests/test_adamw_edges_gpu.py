@@ -248,3 +248,24 @@ def test_the_smallest_eps():
         for bad in (1e-40, 1.17e-38):
             with pytest.raises(lrm.LrmError):
                 lrm.AdamW([w], [g], eps=bad).step()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_tensors_of_several_launches(bits):
+    """More tensors than two launches hold (384 each), of two types: every state, random bit and weight, and the norm
+    over all launches' sums."""
+    import pruned_expert_backward_gb300 as lrm
+    a = Case([1 + (i * 37) % 700 if i % 50 else 0 for i in range(800)] + [20000], BF16, F32, bits, seed=1)
+    b = Case([1 + (i * 53) % 300 for i in range(400)], F32, F32, bits, seed=2)
+    wa, wb = (c.expect(3e-4, 0.9, 0.95, 1e-8, 0.1, 3) for c in (a, b))
+    state = {k: a.state[k] + b.state[k] for k in a.state}
+    opt = lrm.AdamW(a.w + b.w, a.g + b.g, lr=3e-4, betas=(0.9, 0.95), weight_decay=0.1, state_bits=bits, state=state,
+                    max_norm=1e6, seed=5)
+    norm = opt.step(step=3).item()
+    want = torch.cat([g.double() for g in a.g + b.g]).norm().item()
+    assert abs(norm / want - 1) < 1e-6
+    whole = Case.__new__(Case)
+    whole.bits, whole.copy, whole.state = bits, None, state
+    whole.w, whole.sizes = a.w + b.w, a.sizes + b.sizes
+    whole.check(wa + wb, 3, 5)
+    assert int(opt.dev_status.item()) == 0
