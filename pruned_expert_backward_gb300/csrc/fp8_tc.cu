@@ -185,26 +185,6 @@ __device__ __forceinline__ bool mbar_wait_here(uint32_t bar, uint32_t parity, vo
   return false;
 }
 
-// The waits of warps that are ahead of the others: they sleep between polls.  `last`: the wait for everything this
-// CTA has under way, which may take as long as the kernel does and outlives an abort; its limit counts from one.
-__device__ __noinline__ bool mbar_wait_ahead(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status,
-                                             bool last) {
-  uint64_t t0 = globaltimer();
-  for (uint32_t it = 1; it < (1u << 30); ++it) {
-    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
-    __nanosleep(20);
-    if ((it & 63u) == 0) {
-      const bool stop = __any_sync(0xffffffffu, *abort_flag != 0);
-      if (stop && !last) return false;
-      if (last && !stop) t0 = globaltimer();
-      if (__any_sync(0xffffffffu, globaltimer() - t0 > kWaitNs)) break;
-    }
-  }
-  *abort_flag = 1;
-  set_status(status, LRM_ERR_TIMEOUT);
-  return false;
-}
-
 // v += 8 bf16 values
 __device__ __forceinline__ void add8(float* v, uint4 r) {
   float f[8];

@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) mma_commit_pair(drain);
     }
     __syncwarp();
-    mbar_wait(drain, 0, abortv, p.status, false);  // all MMAs into this CTA's TMEM are done before it is freed
+    mbar_wait_ahead(drain, 0, abortv, p.status, true);  // all MMAs into this CTA's TMEM are done before it is freed
   } else {
     // ---------------------------------------------------------------- epilogue --------
     // a warp reads one 32-row quarter of TMEM and its group's half of the columns
