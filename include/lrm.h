@@ -491,7 +491,9 @@ lrm_status lrm_fp8_quantize_weight(const void* w, int32_t G, int32_t N, int32_t 
  *   bias [E,N'] bf16 or NULL, residual [R,N] bf16 or NULL  ->  y [R,N] bf16, z [R,N'] bf16 or NULL
  * N' = 2N for SwiGLU, else N; N a multiple of 8.  Segments, activations, limits and rows that are not written as
  * for lrm_linear.  The 128 products of a block are summed by the tensor core, the blocks in fp32; bias,
- * activation and residual are in fp32 and each output is rounded once.  Needs no scratch.
+ * activation and residual are in fp32 and each output is rounded once.  The two scales are multiplied first, in fp32:
+ * below 2^-126 that product loses bits (a row's and a weight's block whose largest magnitudes have a product below
+ * 2.4e-33), beyond fp32's range it is infinite.  Needs no scratch.
  * A NaN in x spoils its own row's outputs, one in w its own column's.
  */
 lrm_status lrm_fp8_linear(const int32_t* seg_offsets, const void* x, const float* x_scale, const void* w,
@@ -567,6 +569,7 @@ lrm_status lrm_grad_norm(const lrm_adamw_tensor* tensors, int32_t count, lrm_dty
  * e and MurmurHash3's finaliser mix, all modulo 2^32, m by the low and sqrt(v) by the high 16 bits of h.  The step's
  * update uses m and v before that rounding; a sqrt(v) above 0 is held as 2^-9 of its scale at least.  A state of 8 bits
  * that has become infinite or NaN makes its 256 elements NaN.  Zeroed states and scales are the start.
+ * Gradients may be shared by tensors, but lie apart from all that is written.
  * Errors: LRM_ERR_INVALID_ARG, LRM_ERR_SHAPE (step), LRM_ERR_DTYPE, LRM_ERR_CUDA.
  */
 lrm_status lrm_adamw(const lrm_adamw_tensor* tensors, int32_t count, lrm_dtype w_dt, lrm_dtype g_dt, int32_t state_bits,

@@ -8,7 +8,8 @@
 // parameters (no table on the device), a CTA takes chunks of 8192 elements in turn, a warp 256 of them at a time: lane
 // l has elements 4 l .. 4 l + 3 and 128 more on, so that loads of every type are whole sectors in a row.
 // GB300, 100M bf16 weights with fp32 gradients: 32-bit states 392 us (0.95 of the copy rate), 8-bit ones 251 us (0.74:
-// 474 instructions a block of 256, issued in 61 % of the cycles); 429M of them in 8 bits with the norm 1219 us.
+// neither the 474 instructions a block of 256, issued in 61 % of the cycles, nor DRAM, at 59 % of its peak, is full: the
+// latency of a block's loads shows); 429M of them in 8 bits with the norm 1219 us.
 //
 // States in 8 bits: m and sqrt(v) in e4m3, the largest magnitude of each 256 elements of a tensor held as 448 with an
 // fp32 scale, one block to a warp.  They are rounded up or down at random, with the odds that keep the mean: to nearest
@@ -144,7 +145,8 @@ __device__ __forceinline__ float sqrt_f(float v) {
   return r;
 }
 
-// The finaliser of MurmurHash3 (A. Appleby).
+// The finaliser of MurmurHash3 (A. Appleby).  The multipliers of what goes into it, 0x9E3779B1 and 0xC2B2AE3D, are two
+// of the 32-bit primes of xxHash (Y. Collet); 0x9E3779B9 is 2^32 over the golden ratio.
 __host__ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
   h = (h ^ (h >> 16)) * 0x85EBCA6Bu;
   h = (h ^ (h >> 13)) * 0xC2B2AE35u;

@@ -1,4 +1,5 @@
-// lrm_fp8_linear for few rows (tokens being generated): bound by reading W once.
+// lrm_fp8_linear for few rows (tokens being generated): bound by reading W, once for each 8 rows of an expert (dense:
+// 16).
 //
 // The form of linear_rows.cu in 8 bits: a CTA takes 16 rows of W (SwiGLU: 8 gate rows and their 8 up rows) over the
 // whole K, its 8 warps the blocks of 128 columns in turn, and their sums meet in shared memory in a fixed order.
@@ -6,10 +7,12 @@
 // mma.sync m16n8k32 with K in the order the lanes hold it.  A block's products are summed on their own, then scaled
 // by the row's and the weight's scale and added up in fp32.
 //
-// Little is in flight a warp (one block), but three CTAs share a multiprocessor and hide one another's latencies: with
-// four blocks and two CTAs a token's 8 rows over 8 of 128 experts of (768+768) x 2048 took 12.2 us, not 7.9 (25 MB of
-// weights: 3.7 us at the copy rate), and 2048 x 768 13.9 us, not 6.3.  GB300, dense, 1 to 8 rows: (1408+1408) x 4096
-// 6.0 to 6.3 us, 4096 x 4096 6.6 to 6.8 us, (768+768) x 2048 2.7 us.
+// Little is in flight a warp (one block), but where tasks fill the GPU three CTAs share a multiprocessor and hide one
+// another's latencies: with four blocks and two CTAs a token's 8 rows over 8 of 128 experts of (768+768) x 2048 (768
+// tasks, 1.7 waves) took 12.2 us, not 7.9 (25 MB of weights: 3.7 us at the copy rate), and 2048 x 768 13.9 us, not 6.3.
+// A dense token has fewer tasks ((1408+1408) x 4096: 176, one CTA on most multiprocessors) and is bound by its warps'
+// trips to memory one after the other.  GB300, dense, 1 to 8 rows: (1408+1408) x 4096 6.0 to 6.3 us, 4096 x 4096 6.6 to
+// 6.8 us, (768+768) x 2048 2.7 us.
 #include "fp8.cuh"
 #include "kernels.h"
 #include "linear.cuh"
